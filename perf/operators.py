@@ -142,6 +142,9 @@ def prepare(case, seed):
 
     T, H, I, E, k = (c[n] for n in ("T", "H", "I", "E", "k"))
     s = {"case": c, "M": T * k}
+    if own:
+        import block_scaled_fp4_permute_amd as m
+        s["m"] = m
     if c["kind"] == "quantize":
         # activations with a few large channels, as after a norm
         x = normal((T, H), torch.float32)
@@ -178,11 +181,8 @@ def prepare(case, seed):
             part = normal((min(32, E - e0), N, K), torch.float32, 0.02)
             b[e0:e0 + 32], bs[e0:e0 + 32] = _row_quantized(part)
         s["b"] = (b, bs)
-    if own:
-        import block_scaled_fp4_permute_amd as m
-        s["m"] = m
-        if "b" in s and isinstance(s["b"], tuple):
-            s["a8"], s["b8"] = m.INT8Tensor(*s["a"]), m.INT8Tensor(*s["b"])
+    if own and c["kind"].startswith("int8"):
+        s["a8"], s["b8"] = m.INT8Tensor(*s["a"]), m.INT8Tensor(*s["b"])
     return s
 
 
