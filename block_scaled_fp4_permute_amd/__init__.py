@@ -11,7 +11,8 @@ C entry points (include/nvfp4moe.h): moe_route_permute, nvfp4_quantize,
 nvfp4_grouped_gemm, moe_swiglu, moe_unpermute_combine, moe_route_quantize
 (routing and activation quantisation in shared launches) and moe_expert_ffn
 (gate_up + SwiGLU requant + down for all experts, one persistent launch at
-decode sizes).
+decode sizes); mxfp4_* and fp8_* variants; moe_gated_ffn and moe_grouped_gemm
+with their gradients (16-bit experts); int8_quantize and int8_grouped_gemm.
 """
 from __future__ import annotations
 
@@ -23,8 +24,9 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libnvfp4moe.so")
 
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_HIP = range(5)
-F32, BF16 = 0, 1
-EPI_F32, EPI_BF16, EPI_SWIGLU_NVFP4, EPI_COMBINE_F32 = range(4)
+F32, BF16, F16 = 0, 1, 2
+EPI_F32, EPI_BF16, EPI_SWIGLU_NVFP4, EPI_COMBINE_F32, EPI_SWIGLU_BF16 = range(5)
+ACT_SILU, ACT_GELU = 0, 1
 
 
 class NVFP4MoEError(RuntimeError):
@@ -77,6 +79,30 @@ class Fp8GemmArgs(ctypes.Structure):
     ]
 
 
+def _struct(name, doc, fields):
+    kinds = {"p": ctypes.c_void_p, "i": ctypes.c_int32, "l": ctypes.c_int64}
+    return type(name, (ctypes.Structure,), {"__doc__": doc, "_fields_": [(n, kinds[k]) for n, k in fields]})
+
+
+GatedArgs = _struct("GatedArgs", "Mirror of nvfp4moe_gated_args.", [
+    ("x", "p"), ("dtype", "i"), ("a_rows", "p"), ("x_rows", "l"), ("w", "p"), ("offsets", "p"), ("E", "i"), ("H", "i"),
+    ("I", "i"), ("m_total", "l"), ("activation", "i"), ("max_rows_per_expert_hint", "i"), ("h", "p"), ("gu", "p")])
+GatedGradArgs = _struct("GatedGradArgs", "Mirror of nvfp4moe_gated_grad_args.", [
+    ("x", "p"), ("dtype", "i"), ("a_rows", "p"), ("x_rows", "l"), ("w", "p"), ("offsets", "p"), ("E", "i"), ("H", "i"),
+    ("I", "i"), ("m_total", "l"), ("activation", "i"), ("max_rows_per_expert_hint", "i"), ("gu", "p"), ("dh", "p"),
+    ("dx", "p"), ("dw", "p")])
+ProductArgs = _struct("ProductArgs", "Mirror of nvfp4moe_product_args.", [
+    ("a", "p"), ("dtype", "i"), ("a_rows", "p"), ("a_rows_total", "l"), ("b", "p"), ("offsets", "p"), ("E", "i"),
+    ("N", "i"), ("K", "i"), ("m_total", "l"), ("out_dtype", "i"), ("max_rows_per_expert_hint", "i"), ("out", "p")])
+ProductGradArgs = _struct("ProductGradArgs", "Mirror of nvfp4moe_product_grad_args.", [
+    ("a", "p"), ("dtype", "i"), ("a_rows", "p"), ("a_rows_total", "l"), ("b", "p"), ("offsets", "p"), ("E", "i"),
+    ("N", "i"), ("K", "i"), ("m_total", "l"), ("max_rows_per_expert_hint", "i"), ("dy", "p"), ("da", "p"), ("db", "p")])
+Int8GemmArgs = _struct("Int8GemmArgs", "Mirror of nvfp4moe_int8_gemm_args.", [
+    ("a_codes", "p"), ("a_scales", "p"), ("a_rows", "p"), ("a_rows_total", "l"), ("b_codes", "p"), ("b_scales", "p"),
+    ("offsets", "p"), ("E", "i"), ("N", "i"), ("K", "i"), ("m_total", "l"), ("epilogue", "i"),
+    ("max_rows_per_expert_hint", "i"), ("out", "p")])
+
+
 _lib = None
 
 _SIGNATURES = {
@@ -121,6 +147,17 @@ _SIGNATURES = {
     "fp8_weight_repack": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                          ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "fp8_grouped_gemm": (ctypes.c_int, [ctypes.POINTER(Fp8GemmArgs), ctypes.c_void_p]),
+    "moe_gated_ffn": (ctypes.c_int, [ctypes.POINTER(GatedArgs), ctypes.c_void_p]),
+    "moe_gated_ffn_backward_workspace_size": (ctypes.c_size_t, [ctypes.c_int32] * 3 + [ctypes.c_int64]),
+    "moe_gated_ffn_backward": (ctypes.c_int, [ctypes.POINTER(GatedGradArgs), ctypes.c_void_p, ctypes.c_size_t,
+                                              ctypes.c_void_p]),
+    "moe_grouped_gemm": (ctypes.c_int, [ctypes.POINTER(ProductArgs), ctypes.c_void_p]),
+    "moe_grouped_gemm_backward_workspace_size": (ctypes.c_size_t, [ctypes.c_int32] * 3 + [ctypes.c_int64]),
+    "moe_grouped_gemm_backward": (ctypes.c_int, [ctypes.POINTER(ProductGradArgs), ctypes.c_void_p, ctypes.c_size_t,
+                                                 ctypes.c_void_p]),
+    "int8_quantize": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_void_p]),
+    "int8_grouped_gemm": (ctypes.c_int, [ctypes.POINTER(Int8GemmArgs), ctypes.c_void_p]),
     "nvfp4moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "nvfp4moe_last_error_detail": (ctypes.c_char_p, []),
     "nvfp4moe_version": (ctypes.c_int, []),
@@ -708,6 +745,256 @@ def fp8_grouped_gemm(a: FP8Tensor, b_packed, b_scales, offsets, *, N: int, m_tot
     return out
 
 
+# ----------------------------------------------------------------- 16-bit expert FFN
+def _call(dev, stream, fn, *args):
+    """A C call on ``stream`` (None: the current stream of the operands' device)
+    with that device current."""
+    import torch
+    if torch.cuda.current_device() == dev.index:
+        st = torch.cuda.current_stream() if stream is None else stream
+        _check(fn(*args, st.cuda_stream))
+        return
+    with torch.cuda.device(dev):
+        st = torch.cuda.current_stream(dev) if stream is None else stream
+        _check(fn(*args, st.cuda_stream))
+
+
+def _dtype16(t, name):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return BF16
+    if t.dtype == torch.float16:
+        return F16
+    raise TypeError(f"{name}: expected bfloat16 or float16, got {t.dtype}")
+
+
+def _rows_of(a_rows, source, m_total, dev, name):
+    """Checks of a gathered (a_rows given) or direct row operand."""
+    import torch
+    if m_total < 0:
+        raise ValueError("m_total must be >= 0")
+    if a_rows is not None:
+        _need(a_rows, torch.int32, "a_rows", dev)
+        if a_rows.numel() < m_total:
+            raise ValueError(f"a_rows: {a_rows.numel()} values, expected m_total = {m_total}")
+    elif source.shape[0] < m_total:
+        raise ValueError(f"{name}: {source.shape[0]} rows, expected m_total = {m_total}")
+
+
+def _group(b, offsets, dev):
+    """E of weights [E, ...] with their offsets."""
+    import torch
+    _need(offsets, torch.int32, "offsets", dev)
+    E = b.shape[0]
+    if offsets.numel() < E + 1:
+        raise ValueError(f"offsets: {offsets.numel()} values, expected E+1 = {E + 1}")
+    return E
+
+
+def _result(out, shape, dtype, dev, name):
+    import torch
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(out, dtype, name, dev)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected {list(shape)}, got {list(out.shape)}")
+    return out
+
+
+def _scratch(workspace, need, dev):
+    import torch
+    if workspace is None:
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    _need(workspace, torch.uint8, "workspace", dev)
+    return workspace
+
+
+def moe_gated_ffn(x, w, offsets, *, m_total: int, a_rows=None, activation: int = ACT_SILU, save_gu: bool = False,
+                  out=None, gu=None, max_rows_per_expert_hint: int = 0, stream=None):
+    """h = act(x Wg^T) * (x Wu^T) per expert (see include/nvfp4moe.h): x bf16/f16
+    [rows, H], w [E, 2I, H] (rows [0, I) gate), offsets int32 [E+1] -> h
+    [m_total, I].  save_gu (or a float32 gu [m_total, 2I]): returns (h, gu) with
+    the pre-activations that moe_gated_ffn_backward reads."""
+    import torch
+    if x.dim() != 2 or w.dim() != 3:
+        raise ValueError("x must be [rows, H] and w [E, 2I, H]")
+    dev = w.device
+    code = _dtype16(w, "w")
+    _need(w, w.dtype, "w", dev)
+    _need(x, w.dtype, "x", dev)
+    E = _group(w, offsets, dev)
+    H, I = w.shape[2], w.shape[1] // 2
+    if x.shape[1] != H or w.shape[1] != 2 * I:
+        raise ValueError("operand shapes disagree")
+    _rows_of(a_rows, x, m_total, dev, "x")
+    h = _result(out, (m_total, I), w.dtype, dev, "out")
+    if save_gu or gu is not None:
+        gu = _result(gu, (m_total, 2 * I), torch.float32, dev, "gu")
+    args = GatedArgs(x=x.data_ptr(), dtype=code, a_rows=_ptr(a_rows), x_rows=x.shape[0], w=w.data_ptr(),
+                     offsets=offsets.data_ptr(), E=E, H=H, I=I, m_total=m_total, activation=activation,
+                     max_rows_per_expert_hint=max_rows_per_expert_hint, h=h.data_ptr(), gu=_ptr(gu))
+    _call(dev, stream, lib().moe_gated_ffn, ctypes.byref(args))
+    return h if gu is None else (h, gu)
+
+
+def moe_gated_ffn_backward(dh, gu, x, w, offsets, *, a_rows=None, activation: int = ACT_SILU, need_dx: bool = True,
+                           need_dw: bool = True, dx=None, dw=None, workspace=None, max_rows_per_expert_hint: int = 0,
+                           stream=None):
+    """Gradients of moe_gated_ffn: dh [m_total, I], gu as saved -> (dx
+    [m_total, H] one row per GEMM row, dw [E, 2I, H]); None where not needed.
+    For gathered x the gradient of the tokens is
+    moe_unpermute_combine(dx, perm_of_assignment, None, T, k)."""
+    import torch
+    if x.dim() != 2 or w.dim() != 3 or dh.dim() != 2:
+        raise ValueError("x must be [rows, H], w [E, 2I, H] and dh [m_total, I]")
+    if not (need_dx or need_dw):
+        raise ValueError("neither dx nor dw is needed")
+    dev = w.device
+    code = _dtype16(w, "w")
+    _need(w, w.dtype, "w", dev)
+    _need(x, w.dtype, "x", dev)
+    _need(dh, w.dtype, "dh", dev)
+    _need(gu, torch.float32, "gu", dev)
+    E = _group(w, offsets, dev)
+    H, I, m_total = w.shape[2], w.shape[1] // 2, dh.shape[0]
+    if x.shape[1] != H or w.shape[1] != 2 * I or dh.shape[1] != I or tuple(gu.shape) != (m_total, 2 * I):
+        raise ValueError("operand shapes disagree")
+    _rows_of(a_rows, x, m_total, dev, "x")
+    dx = _result(dx, (m_total, H), w.dtype, dev, "dx") if need_dx else None
+    dw = _result(dw, w.shape, w.dtype, dev, "dw") if need_dw else None
+    if m_total == 0 and not need_dw:
+        return dx, dw
+    ws = _scratch(workspace, lib().moe_gated_ffn_backward_workspace_size(E, H, I, m_total), dev)
+    args = GatedGradArgs(x=x.data_ptr(), dtype=code, a_rows=_ptr(a_rows), x_rows=x.shape[0], w=w.data_ptr(),
+                         offsets=offsets.data_ptr(), E=E, H=H, I=I, m_total=m_total, activation=activation,
+                         max_rows_per_expert_hint=max_rows_per_expert_hint, gu=gu.data_ptr(), dh=dh.data_ptr(),
+                         dx=_ptr(dx), dw=_ptr(dw))
+    _call(dev, stream, lib().moe_gated_ffn_backward, ctypes.byref(args), ws.data_ptr(), ws.numel())
+    return dx, dw
+
+
+def moe_grouped_gemm(a, b, offsets, *, m_total: int, a_rows=None, out=None, out_dtype=None,
+                     max_rows_per_expert_hint: int = 0, stream=None):
+    """y[p] = a[r] b[e]^T per expert (see include/nvfp4moe.h): a bf16/f16 [rows, K],
+    b [E, N, K], offsets int32 [E+1] -> [m_total, N] in a's dtype or float32."""
+    import torch
+    if a.dim() != 2 or b.dim() != 3:
+        raise ValueError("a must be [rows, K] and b [E, N, K]")
+    dev = b.device
+    code = _dtype16(b, "b")
+    _need(b, b.dtype, "b", dev)
+    _need(a, b.dtype, "a", dev)
+    E = _group(b, offsets, dev)
+    N, K = b.shape[1], b.shape[2]
+    if a.shape[1] != K:
+        raise ValueError("operand shapes disagree")
+    _rows_of(a_rows, a, m_total, dev, "a")
+    want = out.dtype if out is not None and out_dtype is None else (out_dtype or b.dtype)
+    if want not in (b.dtype, torch.float32):
+        raise TypeError(f"out: {b.dtype} or float32, got {want}")
+    out = _result(out, (m_total, N), want, dev, "out")
+    args = ProductArgs(a=a.data_ptr(), dtype=code, a_rows=_ptr(a_rows), a_rows_total=a.shape[0], b=b.data_ptr(),
+                       offsets=offsets.data_ptr(), E=E, N=N, K=K, m_total=m_total,
+                       out_dtype=F32 if want == torch.float32 else code,
+                       max_rows_per_expert_hint=max_rows_per_expert_hint, out=out.data_ptr())
+    _call(dev, stream, lib().moe_grouped_gemm, ctypes.byref(args))
+    return out
+
+
+def moe_grouped_gemm_backward(dy, a, b, offsets, *, a_rows=None, need_da: bool = True, need_db: bool = True, da=None,
+                              db=None, workspace=None, max_rows_per_expert_hint: int = 0, stream=None):
+    """Gradients of moe_grouped_gemm: dy [m_total, N] in b's dtype -> (da
+    [m_total, K] one row per GEMM row, db [E, N, K]); None where not needed."""
+    if a.dim() != 2 or b.dim() != 3 or dy.dim() != 2:
+        raise ValueError("a must be [rows, K], b [E, N, K] and dy [m_total, N]")
+    if not (need_da or need_db):
+        raise ValueError("neither da nor db is needed")
+    dev = b.device
+    code = _dtype16(b, "b")
+    _need(b, b.dtype, "b", dev)
+    _need(a, b.dtype, "a", dev)
+    _need(dy, b.dtype, "dy", dev)
+    E = _group(b, offsets, dev)
+    N, K, m_total = b.shape[1], b.shape[2], dy.shape[0]
+    if a.shape[1] != K or dy.shape[1] != N:
+        raise ValueError("operand shapes disagree")
+    _rows_of(a_rows, a, m_total, dev, "a")
+    da = _result(da, (m_total, K), b.dtype, dev, "da") if need_da else None
+    db = _result(db, b.shape, b.dtype, dev, "db") if need_db else None
+    if m_total == 0 and not need_db:
+        return da, db
+    need = lib().moe_grouped_gemm_backward_workspace_size(E, N, K, m_total)
+    ws = _scratch(workspace, need, dev) if need else None
+    args = ProductGradArgs(a=a.data_ptr(), dtype=code, a_rows=_ptr(a_rows), a_rows_total=a.shape[0], b=b.data_ptr(),
+                           offsets=offsets.data_ptr(), E=E, N=N, K=K, m_total=m_total,
+                           max_rows_per_expert_hint=max_rows_per_expert_hint, dy=dy.data_ptr(), da=_ptr(da),
+                           db=_ptr(db))
+    _call(dev, stream, lib().moe_grouped_gemm_backward, ctypes.byref(args), _ptr(ws), ws.numel() if need else 0)
+    return da, db
+
+
+# --------------------------------------------------------------------------- INT8
+@dataclass
+class INT8Tensor:
+    codes: "object"     # int8 [..., rows, cols]
+    scales: "object"    # float32 [..., rows]
+
+
+def int8_quantize(x, out: INT8Tensor | None = None, stream=None) -> INT8Tensor:
+    """x bf16/float32 [..., rows, cols] -> INT8Tensor with one scale per row
+    (tokens of activations, output channels of weights)."""
+    import torch
+    code = _dtype_code(x)
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    dev = x.device
+    _need(x, x.dtype, "x", dev)
+    cols = x.shape[-1]
+    if out is None:
+        out = INT8Tensor(torch.empty(x.shape, dtype=torch.int8, device=dev),
+                         torch.empty(x.shape[:-1], dtype=torch.float32, device=dev))
+    else:
+        _need(out.codes, torch.int8, "out.codes", dev)
+        _need(out.scales, torch.float32, "out.scales", dev)
+        if out.codes.shape != x.shape or out.scales.shape != x.shape[:-1]:
+            raise ValueError("out codes/scales do not match x")
+    if x.numel() == 0:
+        return out
+    _call(dev, stream, lib().int8_quantize, x.data_ptr(), code, x.numel() // cols, cols, out.codes.data_ptr(),
+          out.scales.data_ptr())
+    return out
+
+
+def int8_grouped_gemm(a: INT8Tensor, b: INT8Tensor, offsets, *, m_total: int, a_rows=None, epilogue: int = EPI_BF16,
+                      out=None, max_rows_per_expert_hint: int = 0, stream=None):
+    """Grouped INT8 GEMM (see include/nvfp4moe.h): a [rows, K], b [E, N, K] with
+    scales [E, N], offsets int32 [E+1].  Epilogues F32, BF16, or EPI_SWIGLU_BF16
+    (N = 2I: returns bf16 h [m_total, I])."""
+    import torch
+    if a.codes.dim() != 2 or b.codes.dim() != 3:
+        raise ValueError("a must be [rows, K] and b [E, N, K]")
+    dev = b.codes.device
+    _need(b.codes, torch.int8, "b.codes", dev)
+    _need(b.scales, torch.float32, "b.scales", dev)
+    _need(a.codes, torch.int8, "a.codes", dev)
+    _need(a.scales, torch.float32, "a.scales", dev)
+    E = _group(b.codes, offsets, dev)
+    N, K = b.codes.shape[1], b.codes.shape[2]
+    if a.codes.shape[1] != K or tuple(b.scales.shape) != (E, N) or tuple(a.scales.shape) != (a.codes.shape[0],):
+        raise ValueError("operand shapes disagree")
+    _rows_of(a_rows, a.codes, m_total, dev, "a")
+    if epilogue not in (EPI_F32, EPI_BF16, EPI_SWIGLU_BF16):
+        raise ValueError("int8_grouped_gemm: epilogue F32, BF16 or SWIGLU_BF16")
+    out = _result(out, (m_total, N // 2 if epilogue == EPI_SWIGLU_BF16 else N),
+                  torch.float32 if epilogue == EPI_F32 else torch.bfloat16, dev, "out")
+    args = Int8GemmArgs(a_codes=a.codes.data_ptr(), a_scales=a.scales.data_ptr(), a_rows=_ptr(a_rows),
+                        a_rows_total=a.codes.shape[0], b_codes=b.codes.data_ptr(), b_scales=b.scales.data_ptr(),
+                        offsets=offsets.data_ptr(), E=E, N=N, K=K, m_total=m_total, epilogue=epilogue,
+                        max_rows_per_expert_hint=max_rows_per_expert_hint, out=out.data_ptr())
+    _call(dev, stream, lib().int8_grouped_gemm, ctypes.byref(args))
+    return out
+
+
 # -------------------------------------------------------------------------- swiglu
 def moe_swiglu(gate_up, g=None, out: NVFP4Tensor | None = None, workspace=None, stream=None) -> NVFP4Tensor:
     """gate_up float32/bf16 [M, 2I] -> NVFP4 h = silu(gate) * up."""
@@ -758,4 +1045,6 @@ __all__ = ["lib", "moe_route_permute", "moe_route_quantize", "moe_route_quantize
            "moe_unpermute_combine", "moe_expert_ffn", "moe_expert_ffn_workspace", "mxfp4_quantize",
            "mxfp4_grouped_gemm", "mxfp4_weight_repack", "MXFP4Tensor", "fp8_quantize", "fp8_swiglu_quantize", "fp8_weight_repack",
            "fp8_grouped_gemm", "FP8Tensor", "Fp8GemmArgs", "NVFP4Tensor", "Routing", "GemmArgs", "NVFP4MoEError",
+           "moe_gated_ffn", "moe_gated_ffn_backward", "moe_grouped_gemm", "moe_grouped_gemm_backward", "int8_quantize",
+           "int8_grouped_gemm", "INT8Tensor", "ACT_SILU", "ACT_GELU", "F16", "EPI_SWIGLU_BF16",
            "F32", "BF16", "EPI_F32", "EPI_BF16", "EPI_SWIGLU_NVFP4", "EPI_COMBINE_F32"]

@@ -682,6 +682,270 @@ int fp8_grouped_gemm(const nvfp4moe_fp8_gemm_args* a, void* stream) {
                     "fp8_grouped_gemm");
 }
 
+// ------------------------------------------------------------------ 16-bit expert FFN
+namespace {
+
+// the checks that the calls on plain operands share; `row_ptrs` is whether
+// every row operand is there (needed once there are rows)
+int check_plain(const char* fn, int32_t dtype, const int32_t* offsets, int32_t E, int32_t N, int32_t K, int64_t m_total,
+                const int32_t* a_rows, int64_t rows_total, bool row_ptrs, bool needs_rows) {
+  if (dtype != NVFP4MOE_BF16 && dtype != NVFP4MOE_F16)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: dtype %d (bf16 or f16)", fn, dtype);
+  if (!offsets) return fail(NVFP4MOE_ERR_INVALID, "%s: null offsets", fn);
+  if (E <= 0 || N <= 0 || K <= 0 || m_total < 0 || rows_total < 0)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: sizes must be > 0 and row counts >= 0", fn);
+  if (N % 8 != 0 || K % 8 != 0) return fail(NVFP4MOE_ERR_INVALID, "%s: sizes %d and %d must be multiples of 8", fn, N, K);
+  if (E > 4096) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: E=%d > 4096", fn, E);
+  if (m_total >= (int64_t(1) << 31) || rows_total >= (int64_t(1) << 31))
+    return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: 2^31 rows or more", fn);
+  if (N > (1 << 30) || K > (1 << 30)) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: a dimension above 2^30", fn);
+  if (!aligned(offsets, 4) || !aligned(a_rows, 4)) return fail(NVFP4MOE_ERR_INVALID, "%s: misaligned index array", fn);
+  if (m_total > 0) {
+    if (!row_ptrs) return fail(NVFP4MOE_ERR_INVALID, "%s: null row operand", fn);
+    if (needs_rows && (a_rows ? rows_total == 0 : rows_total < m_total))
+      return fail(NVFP4MOE_ERR_INVALID, "%s: %lld source rows for %lld GEMM rows", fn, static_cast<long long>(rows_total),
+                  static_cast<long long>(m_total));
+  }
+  // one grid dimension holds every tile of the smallest tile shape
+  const int64_t chunks = m_total / 16 + (E < m_total ? E : m_total);
+  if (prod_ge(chunks, N / 64 + 1, int64_t(1) << 31) || prod_ge(chunks, K / 64 + 1, int64_t(1) << 31) ||
+      prod_ge(E, N / 64 + 1, K / 64 + 1, int64_t(1) << 31))
+    return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: 2^31 tiles or more", fn);
+  return NVFP4MOE_OK;
+}
+
+int debug_plain(const char* fn, const int32_t* offsets, int32_t E, int64_t m_total, const int32_t* a_rows,
+                int64_t rows_total, hipStream_t s) {
+  if (!debug_checks()) return NVFP4MOE_OK;
+  return debug_check_gemm(fn, offsets, E, m_total, a_rows, rows_total, nullptr, 0, s);
+}
+
+hipError_t launch16(int32_t dtype, const nvfp4::TileParams& p, int layout, int epilogue, hipStream_t s) {
+  return dtype == NVFP4MOE_F16 ? nvfp4::launch_tile_gemm_f16(p, layout, epilogue, s)
+                               : nvfp4::launch_tile_gemm_bf16(p, layout, epilogue, s);
+}
+
+// layouts and epilogues of tile_gemm.h
+enum : int { L_NT = 0, L_NN = 1, L_TN = 2, O_16 = 0, O_F32 = 1, O_GATED = 2 };
+
+// da = dy b and db = dy^T a of one grouped product: dy [m_total, n], b [E, n, k]
+int product_grad(const char* fn, int32_t dtype, const void* dy, const void* a, const int32_t* a_rows, int64_t rows_total,
+                 const void* b, const int32_t* offsets, int32_t E, int32_t n, int32_t k, int64_t m_total, int32_t hint,
+                 void* da, void* db, hipStream_t s) {
+  nvfp4::TileParams p{};
+  p.a = dy;
+  p.offsets = offsets;
+  p.E = E;
+  p.N = k;
+  p.m_total = static_cast<int>(m_total);
+  p.rows_hint = hint > 0 ? hint : static_cast<int>(m_total / E);
+  if (da && m_total > 0) {
+    p.b = b;
+    p.K = n;
+    p.out = da;
+    const hipError_t err = launch16(dtype, p, L_NN, O_16, s);
+    if (err != hipSuccess) return hip_status(err, fn);
+  }
+  if (db) {
+    p.b = a;
+    p.K = 0;
+    p.R = n;
+    p.a_rows = a_rows;
+    p.src_rows = static_cast<int>(rows_total);
+    p.out = db;
+    const hipError_t err = launch16(dtype, p, L_TN, O_16, s);
+    if (err != hipSuccess) return hip_status(err, fn);
+  }
+  return ok();
+}
+
+}  // namespace
+
+int moe_gated_ffn(const nvfp4moe_gated_args* a, void* stream) {
+  const char* fn = "moe_gated_ffn";
+  if (!a) return fail(NVFP4MOE_ERR_INVALID, "%s: args is NULL", fn);
+  if (a->I > (1 << 29)) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: I=%d above 2^29", fn, a->I);
+  if (a->I <= 0 || a->I % 8 != 0) return fail(NVFP4MOE_ERR_INVALID, "%s: I=%d must be a positive multiple of 8", fn, a->I);
+  const int bad = check_plain(fn, a->dtype, a->offsets, a->E, 2 * a->I, a->H, a->m_total, a->a_rows, a->x_rows,
+                              a->x && a->h, true);
+  if (bad != NVFP4MOE_OK) return bad;
+  if (!a->w) return fail(NVFP4MOE_ERR_INVALID, "%s: null w", fn);
+  if (a->activation != NVFP4MOE_ACT_SILU && a->activation != NVFP4MOE_ACT_GELU)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: activation %d", fn, a->activation);
+  if (!aligned(a->x, 16) || !aligned(a->w, 16) || !aligned(a->h, 16) || !aligned(a->gu, 16))
+    return fail(NVFP4MOE_ERR_INVALID, "%s: x, w, h and gu must be 16-byte aligned", fn);
+  if (a->m_total == 0) return ok();
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const int st = debug_plain(fn, a->offsets, a->E, a->m_total, a->a_rows, a->x_rows, s);
+  if (st != NVFP4MOE_OK) return st;
+  nvfp4::TileParams p{};
+  p.a = a->x;
+  p.b = a->w;
+  p.a_rows = a->a_rows;
+  p.offsets = a->offsets;
+  p.E = a->E;
+  p.N = 2 * a->I;
+  p.K = a->H;
+  p.m_total = static_cast<int>(a->m_total);
+  p.src_rows = static_cast<int>(a->x_rows);
+  p.act = a->activation;
+  p.rows_hint = a->max_rows_per_expert_hint > 0 ? a->max_rows_per_expert_hint : static_cast<int>(a->m_total / a->E);
+  p.out = a->h;
+  p.gu = a->gu;
+  return hip_status(launch16(a->dtype, p, L_NT, O_GATED, s), fn);
+}
+
+size_t moe_gated_ffn_backward_workspace_size(int32_t E, int32_t H, int32_t I, int64_t m_total) {
+  if (E <= 0 || E > 4096 || H <= 0 || I <= 0 || m_total < 0 || H % 8 != 0 || I % 8 != 0 || m_total >= (int64_t(1) << 31) ||
+      I > (1 << 29))
+    return 0;
+  return static_cast<size_t>(m_total > 0 ? m_total : 1) * 2 * static_cast<size_t>(I) * 2;   // dg and du in 16 bits
+}
+
+int moe_gated_ffn_backward(const nvfp4moe_gated_grad_args* a, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_gated_ffn_backward";
+  if (!a) return fail(NVFP4MOE_ERR_INVALID, "%s: args is NULL", fn);
+  if (a->I > (1 << 29)) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: I=%d above 2^29", fn, a->I);
+  if (a->I <= 0 || a->I % 8 != 0) return fail(NVFP4MOE_ERR_INVALID, "%s: I=%d must be a positive multiple of 8", fn, a->I);
+  if (!a->dx && !a->dw && a->m_total > 0) return fail(NVFP4MOE_ERR_INVALID, "%s: neither dx nor dw", fn);
+  const int bad = check_plain(fn, a->dtype, a->offsets, a->E, 2 * a->I, a->H, a->m_total, a->a_rows, a->x_rows,
+                              a->gu && a->dh && (a->x || !a->dw), a->dw != nullptr);
+  if (bad != NVFP4MOE_OK) return bad;
+  if (a->dx && !a->w) return fail(NVFP4MOE_ERR_INVALID, "%s: dx needs w", fn);
+  if (a->activation != NVFP4MOE_ACT_SILU && a->activation != NVFP4MOE_ACT_GELU)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: activation %d", fn, a->activation);
+  if (!aligned(a->x, 16) || !aligned(a->w, 16) || !aligned(a->gu, 16) || !aligned(a->dh, 16) || !aligned(a->dx, 16) ||
+      !aligned(a->dw, 16))
+    return fail(NVFP4MOE_ERR_INVALID, "%s: pointers must be 16-byte aligned", fn);
+  const size_t need = moe_gated_ffn_backward_workspace_size(a->E, a->H, a->I, a->m_total);
+  if (!workspace || workspace_bytes < need)
+    return fail(NVFP4MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes, need);
+  if (!aligned(workspace, 256)) return fail(NVFP4MOE_ERR_INVALID, "%s: workspace not 256-byte aligned", fn);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (a->m_total > 0) {
+    const int st = debug_plain(fn, a->offsets, a->E, a->m_total, a->dw ? a->a_rows : nullptr, a->x_rows, s);
+    if (st != NVFP4MOE_OK) return st;
+    const hipError_t err = nvfp4::launch_gated_grad(a->gu, a->dh, a->dtype == NVFP4MOE_F16, a->I, a->m_total, a->offsets,
+                                                    a->E, a->activation, workspace, s);
+    if (err != hipSuccess) return hip_status(err, fn);
+  }
+  return product_grad(fn, a->dtype, workspace, a->x, a->a_rows, a->x_rows, a->w, a->offsets, a->E, 2 * a->I, a->H,
+                      a->m_total, a->max_rows_per_expert_hint, a->dx, a->dw, s);
+}
+
+int moe_grouped_gemm(const nvfp4moe_product_args* a, void* stream) {
+  const char* fn = "moe_grouped_gemm";
+  if (!a) return fail(NVFP4MOE_ERR_INVALID, "%s: args is NULL", fn);
+  const int bad = check_plain(fn, a->dtype, a->offsets, a->E, a->N, a->K, a->m_total, a->a_rows, a->a_rows_total,
+                              a->a && a->out, true);
+  if (bad != NVFP4MOE_OK) return bad;
+  if (!a->b) return fail(NVFP4MOE_ERR_INVALID, "%s: null b", fn);
+  if (a->out_dtype != a->dtype && a->out_dtype != NVFP4MOE_F32)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: out_dtype %d (the operands' dtype or f32)", fn, a->out_dtype);
+  if (!aligned(a->a, 16) || !aligned(a->b, 16) || !aligned(a->out, 16))
+    return fail(NVFP4MOE_ERR_INVALID, "%s: a, b and out must be 16-byte aligned", fn);
+  if (a->m_total == 0) return ok();
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const int st = debug_plain(fn, a->offsets, a->E, a->m_total, a->a_rows, a->a_rows_total, s);
+  if (st != NVFP4MOE_OK) return st;
+  nvfp4::TileParams p{};
+  p.a = a->a;
+  p.b = a->b;
+  p.a_rows = a->a_rows;
+  p.offsets = a->offsets;
+  p.E = a->E;
+  p.N = a->N;
+  p.K = a->K;
+  p.m_total = static_cast<int>(a->m_total);
+  p.src_rows = static_cast<int>(a->a_rows_total);
+  p.rows_hint = a->max_rows_per_expert_hint > 0 ? a->max_rows_per_expert_hint : static_cast<int>(a->m_total / a->E);
+  p.out = a->out;
+  return hip_status(launch16(a->dtype, p, L_NT, a->out_dtype == NVFP4MOE_F32 ? O_F32 : O_16, s), fn);
+}
+
+size_t moe_grouped_gemm_backward_workspace_size(int32_t E, int32_t N, int32_t K, int64_t m_total) { return 0; }
+
+int moe_grouped_gemm_backward(const nvfp4moe_product_grad_args* a, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_grouped_gemm_backward";
+  if (!a) return fail(NVFP4MOE_ERR_INVALID, "%s: args is NULL", fn);
+  if (!a->da && !a->db && a->m_total > 0) return fail(NVFP4MOE_ERR_INVALID, "%s: neither da nor db", fn);
+  const int bad = check_plain(fn, a->dtype, a->offsets, a->E, a->N, a->K, a->m_total, a->a_rows, a->a_rows_total,
+                              a->dy && (a->a || !a->db), a->db != nullptr);
+  if (bad != NVFP4MOE_OK) return bad;
+  if (a->da && !a->b) return fail(NVFP4MOE_ERR_INVALID, "%s: da needs b", fn);
+  if (!aligned(a->a, 16) || !aligned(a->b, 16) || !aligned(a->dy, 16) || !aligned(a->da, 16) || !aligned(a->db, 16))
+    return fail(NVFP4MOE_ERR_INVALID, "%s: pointers must be 16-byte aligned", fn);
+  const size_t need = moe_grouped_gemm_backward_workspace_size(a->E, a->N, a->K, a->m_total);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(NVFP4MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes, need);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (a->m_total > 0) {
+    const int st = debug_plain(fn, a->offsets, a->E, a->m_total, a->db ? a->a_rows : nullptr, a->a_rows_total, s);
+    if (st != NVFP4MOE_OK) return st;
+  }
+  return product_grad(fn, a->dtype, a->dy, a->a, a->a_rows, a->a_rows_total, a->b, a->offsets, a->E, a->N, a->K,
+                      a->m_total, a->max_rows_per_expert_hint, a->da, a->db, s);
+}
+
+// ------------------------------------------------------------------ INT8
+int int8_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int8_t* codes, float* scales, void* stream) {
+  if (!x || !codes || !scales) return fail(NVFP4MOE_ERR_INVALID, "int8_quantize: null pointer argument");
+  if (x_dtype != NVFP4MOE_F32 && x_dtype != NVFP4MOE_BF16)
+    return fail(NVFP4MOE_ERR_INVALID, "int8_quantize: x_dtype %d", x_dtype);
+  if (rows <= 0 || cols <= 0 || cols % 8 != 0)
+    return fail(NVFP4MOE_ERR_INVALID, "int8_quantize: rows > 0 and cols a positive multiple of 8 needed");
+  if (rows >= (int64_t(1) << 31) || cols >= (int64_t(1) << 31))
+    return fail(NVFP4MOE_ERR_UNSUPPORTED, "int8_quantize: 2^31 rows or columns");
+  if (!aligned(x, 16) || !aligned(codes, 8) || !aligned(scales, 4))
+    return fail(NVFP4MOE_ERR_INVALID, "int8_quantize: x must be 16-byte, codes 8-byte, scales 4-byte aligned");
+  return hip_status(nvfp4::launch_int8_quantize(x, x_dtype, rows, cols, codes, scales, static_cast<hipStream_t>(stream)),
+                    "int8_quantize");
+}
+
+int int8_grouped_gemm(const nvfp4moe_int8_gemm_args* a, void* stream) {
+  const char* fn = "int8_grouped_gemm";
+  if (!a) return fail(NVFP4MOE_ERR_INVALID, "%s: args is NULL", fn);
+  const int bad = check_plain(fn, NVFP4MOE_BF16, a->offsets, a->E, a->N, a->K, a->m_total, a->a_rows, a->a_rows_total,
+                              a->a_codes && a->a_scales && a->out, true);
+  if (bad != NVFP4MOE_OK) return bad;
+  if (!a->b_codes || !a->b_scales) return fail(NVFP4MOE_ERR_INVALID, "%s: null b_codes or b_scales", fn);
+  if (a->K % 16 != 0) return fail(NVFP4MOE_ERR_INVALID, "%s: K=%d not a multiple of 16", fn, a->K);
+  if (a->K > 131056) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: K=%d: the 32-bit sum covers K <= 131056", fn, a->K);
+  if (!aligned(a->a_codes, 16) || !aligned(a->a_scales, 4) || !aligned(a->b_codes, 16) || !aligned(a->b_scales, 16) ||
+      !aligned(a->out, 16))
+    return fail(NVFP4MOE_ERR_INVALID, "%s: codes, b_scales and out must be 16-byte, a_scales 4-byte aligned", fn);
+  int epi;
+  switch (a->epilogue) {
+    case NVFP4MOE_EPI_F32: epi = O_F32; break;
+    case NVFP4MOE_EPI_BF16: epi = O_16; break;
+    case NVFP4MOE_EPI_SWIGLU_BF16:
+      if (a->N % 16 != 0) return fail(NVFP4MOE_ERR_INVALID, "%s: SwiGLU needs N = 2I with I %% 8 == 0", fn);
+      epi = O_GATED;
+      break;
+    default: return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: epilogue %d (F32, BF16 or SWIGLU_BF16)", fn, a->epilogue);
+  }
+  if (a->m_total == 0) return ok();
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const int st = debug_plain(fn, a->offsets, a->E, a->m_total, a->a_rows, a->a_rows_total, s);
+  if (st != NVFP4MOE_OK) return st;
+  nvfp4::TileParams p{};
+  p.a = a->a_codes;
+  p.b = a->b_codes;
+  p.a_rows = a->a_rows;
+  p.sa = a->a_scales;
+  p.sb = a->b_scales;
+  p.offsets = a->offsets;
+  p.E = a->E;
+  p.N = a->N;
+  p.K = a->K;
+  p.m_total = static_cast<int>(a->m_total);
+  p.src_rows = static_cast<int>(a->a_rows_total);
+  p.act = nvfp4::TG_ACT_SILU;
+  p.rows_hint = a->max_rows_per_expert_hint > 0 ? a->max_rows_per_expert_hint : static_cast<int>(a->m_total / a->E);
+  p.out = a->out;
+  return hip_status(nvfp4::launch_tile_gemm_i8(p, epi, s), fn);
+}
+
 // ------------------------------------------------------------------ packed weights
 size_t nvfp4_weight_packed_size(int32_t E, int32_t N, int32_t K) {
   if (E <= 0 || N <= 0 || K <= 0 || K % 32 != 0 || prod_ge(E, N, int64_t(1) << 31)) return 0;

@@ -66,8 +66,15 @@ typedef enum nvfp4moe_status {
 
 typedef enum nvfp4moe_dtype {
   NVFP4MOE_F32 = 0,
-  NVFP4MOE_BF16 = 1
+  NVFP4MOE_BF16 = 1,
+  NVFP4MOE_F16 = 2               /* moe_gated_ffn, moe_grouped_gemm and their gradients only */
 } nvfp4moe_dtype;
+
+/* activation of the gated feed-forward block */
+typedef enum nvfp4moe_activation {
+  NVFP4MOE_ACT_SILU = 0,         /* g / (1 + exp(-g)) */
+  NVFP4MOE_ACT_GELU = 1          /* g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+} nvfp4moe_activation;
 
 typedef enum nvfp4moe_epilogue {
   /* y[p, n] = acc * (g_a * g_b[e]) written as float32 to out[p*N + n], p < m_total */
@@ -85,7 +92,11 @@ typedef enum nvfp4moe_epilogue {
    * out is float32 [out_rows, N] and must be zeroed by the caller; the order of
    * the additions is not fixed, so results may differ in the last bits between
    * runs). */
-  NVFP4MOE_EPI_COMBINE_F32 = 3
+  NVFP4MOE_EPI_COMBINE_F32 = 3,
+  /* int8_grouped_gemm only: SwiGLU of the gate_up output (N = 2I, halves as
+   * above), h = silu(y[:, :I]) * y[:, I:] rounded to bfloat16 into out
+   * [m_total, I] (nearest even). */
+  NVFP4MOE_EPI_SWIGLU_BF16 = 4
 } nvfp4moe_epilogue;
 
 /* Arguments of nvfp4_grouped_gemm (a struct keeps the ABI stable). */
@@ -396,6 +407,145 @@ typedef struct nvfp4moe_fp8_gemm_args {
   float* out_scales;          /* SwiGLU: h block scales [m_total, N/256], 4-byte aligned */
 } nvfp4moe_fp8_gemm_args;
 int fp8_grouped_gemm(const nvfp4moe_fp8_gemm_args* args, void* stream);
+
+/* ---------------------------------------------------------------- 16-bit expert FFN
+ * The experts' feed-forward block on bfloat16 or float16 operands, with its
+ * gradients: the form the experts are trained in before they are quantised
+ * for the calls above (same grouping, gate_up row order and layer shape: "From
+ * Empirical Limits ...", section "Sections 5-6: Algorithmic Techniques").  All
+ * operands row-major; `dtype` (NVFP4MOE_BF16 or NVFP4MOE_F16) is the type of
+ * every 16-bit operand and result of a call.  Sums run in float32 in a fixed
+ * order (no atomics: results are the same from run to run) and are rounded
+ * once, nearest even.  The grouping rules of nvfp4_grouped_gemm hold: rows
+ * [offsets[e], offsets[e+1]) belong to expert e, rows p >= offsets[E] of a
+ * result are not written, E = 1 is a dense product.  m_total may be 0 (then
+ * the row operands may be NULL; a weight gradient is still written, as zeros).
+ * Pointers 16-byte aligned; H, I, N and K multiples of 8; E <= 4096; an
+ * operand or result may exceed 4 GiB.  A hint is the rows per expert the
+ * caller expects (0: m_total / E): it picks the tile, never the result's
+ * definition. */
+
+/* h[p, i] = act(g[p, i]) * u[p, i] with g = x[r] w[e, :I]^T, u = x[r] w[e, I:]^T
+ * and r = a_rows ? a_rows[p] : p; gate and up projection, activation and
+ * product in one kernel.  gu (nullable) receives g and u in float32
+ * [m_total, 2I] for moe_gated_ffn_backward. */
+typedef struct nvfp4moe_gated_args {
+  const void* x;              /* [x_rows, H] */
+  int32_t dtype;
+  const int32_t* a_rows;      /* device [m_total] or NULL; entries in [0, x_rows) */
+  int64_t x_rows;             /* without a_rows: at least m_total */
+  const void* w;              /* [E, 2I, H]: rows [0, I) gate, [I, 2I) up */
+  const int32_t* offsets;     /* device [E+1] */
+  int32_t E, H, I;
+  int64_t m_total;
+  int32_t activation;         /* nvfp4moe_activation */
+  int32_t max_rows_per_expert_hint;
+  void* h;                    /* out [m_total, I] */
+  float* gu;                  /* out [m_total, 2I] or NULL */
+} nvfp4moe_gated_args;
+int moe_gated_ffn(const nvfp4moe_gated_args* args, void* stream);
+
+/* Gradients of moe_gated_ffn from dh, the gradient of h, and the gu it saved:
+ *   dg = dh * u * act'(g), du = dh * act(g)   (float32, rounded to dtype: the
+ *                                              operand of both products)
+ *   dx[p, :] = dg[p] w[e, :I] + du[p] w[e, I:]         one row per row p
+ *   dw[e, :I] = sum_p dg[p]^T x[r_p], dw[e, I:] = sum_p du[p]^T x[r_p]
+ * dx rows are per GEMM row: for gathered x, the gradient of a token is the sum
+ * of its rows, moe_unpermute_combine(dx, perm_of_assignment, NULL, ...).
+ * Either of dx and dw may be NULL (not wanted).  dw of an expert without rows
+ * is zero.  workspace: moe_gated_ffn_backward_workspace_size bytes, 256-byte
+ * aligned, caller-owned; calls sharing one must not overlap. */
+typedef struct nvfp4moe_gated_grad_args {
+  const void* x;              /* as in the forward call (not read when dw is NULL) */
+  int32_t dtype;
+  const int32_t* a_rows;
+  int64_t x_rows;
+  const void* w;              /* not read when dx is NULL */
+  const int32_t* offsets;
+  int32_t E, H, I;
+  int64_t m_total;
+  int32_t activation;
+  int32_t max_rows_per_expert_hint;
+  const float* gu;            /* [m_total, 2I] */
+  const void* dh;             /* [m_total, I] */
+  void* dx;                   /* out [m_total, H] or NULL */
+  void* dw;                   /* out [E, 2I, H] or NULL */
+} nvfp4moe_gated_grad_args;
+size_t moe_gated_ffn_backward_workspace_size(int32_t E, int32_t H, int32_t I, int64_t m_total);
+int moe_gated_ffn_backward(const nvfp4moe_gated_grad_args* args, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* y[p, n] = sum_k a[r, k] b[e, n, k], the down projection (r = a_rows ? a_rows[p]
+ * : p); out in dtype, or float32. */
+typedef struct nvfp4moe_product_args {
+  const void* a;              /* [a_rows_total, K] */
+  int32_t dtype;
+  const int32_t* a_rows;      /* device [m_total] or NULL; entries in [0, a_rows_total) */
+  int64_t a_rows_total;       /* without a_rows: at least m_total */
+  const void* b;              /* [E, N, K] */
+  const int32_t* offsets;     /* device [E+1] */
+  int32_t E, N, K;
+  int64_t m_total;
+  int32_t out_dtype;          /* dtype or NVFP4MOE_F32 */
+  int32_t max_rows_per_expert_hint;
+  void* out;                  /* [m_total, N] */
+} nvfp4moe_product_args;
+int moe_grouped_gemm(const nvfp4moe_product_args* args, void* stream);
+
+/* Gradients of moe_grouped_gemm from dy [m_total, N]:
+ *   da[p, :] = dy[p] b[e]  (one row per row p, as dx above),  db[e] = sum_p dy[p]^T a[r_p]
+ * in dtype.  Either may be NULL; db of an expert without rows is zero.
+ * workspace as above (moe_grouped_gemm_backward_workspace_size; may be NULL
+ * where that is 0). */
+typedef struct nvfp4moe_product_grad_args {
+  const void* a;              /* as in the forward call (not read when db is NULL) */
+  int32_t dtype;
+  const int32_t* a_rows;
+  int64_t a_rows_total;
+  const void* b;              /* not read when da is NULL */
+  const int32_t* offsets;
+  int32_t E, N, K;
+  int64_t m_total;
+  int32_t max_rows_per_expert_hint;
+  const void* dy;             /* [m_total, N] */
+  void* da;                   /* out [m_total, K] or NULL */
+  void* db;                   /* out [E, N, K] or NULL */
+} nvfp4moe_product_grad_args;
+size_t moe_grouped_gemm_backward_workspace_size(int32_t E, int32_t N, int32_t K, int64_t m_total);
+int moe_grouped_gemm_backward(const nvfp4moe_product_grad_args* args, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* ---------------------------------------------------------------- INT8 variant
+ * Symmetric 8-bit integers with one float32 scale per row: per token for
+ * activations, per output channel for weights (value = code * scale).
+ * int8_quantize: x [rows, cols] (bf16 or float32, finite) -> codes int8 in
+ * [-127, 127] and scales [rows]: s = absmax / 127 (float32 division; 1 where
+ * that is zero), code = nearest-even integer of the correctly rounded float32
+ * quotient x / s.  Reproducible bit for bit.  cols % 8 == 0; x 16-byte, codes
+ * 8-byte, scales 4-byte aligned; rows < 2^31. */
+int int8_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int8_t* codes, float* scales,
+                  void* stream);
+/* Grouped INT8 GEMM, rows and experts as in nvfp4_grouped_gemm:
+ *   y[p, n] = (a_scales[r] * b_scales[e, n]) * sum_k a[r, k] b[e, n, k]
+ * with an exact 32-bit integer sum, scaled in float32.  Epilogues EPI_F32,
+ * EPI_BF16 and EPI_SWIGLU_BF16 (N = 2I, I % 8 == 0).  Weights row-major, as
+ * int8_quantize writes them.  K % 16 == 0, K <= 131056 (the sum's range),
+ * N % 8 == 0, E <= 4096. */
+typedef struct nvfp4moe_int8_gemm_args {
+  const int8_t* a_codes;      /* [a_rows_total, K], 16-byte aligned */
+  const float* a_scales;      /* [a_rows_total] */
+  const int32_t* a_rows;      /* device [m_total] or NULL; entries in [0, a_rows_total) */
+  int64_t a_rows_total;       /* without a_rows: at least m_total */
+  const int8_t* b_codes;      /* [E, N, K], 16-byte aligned */
+  const float* b_scales;      /* [E, N], 16-byte aligned */
+  const int32_t* offsets;     /* device [E+1] */
+  int32_t E, N, K;
+  int64_t m_total;
+  int32_t epilogue;
+  int32_t max_rows_per_expert_hint;
+  void* out;                  /* float or bf16 [m_total, N], or bf16 [m_total, N/2]; 16-byte aligned */
+} nvfp4moe_int8_gemm_args;
+int int8_grouped_gemm(const nvfp4moe_int8_gemm_args* args, void* stream);
 
 /* ---------------------------------------------------------------- packed weights
  * Weights are static, so they can be repacked once into a tile layout that the
