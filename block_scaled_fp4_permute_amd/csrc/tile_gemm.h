@@ -10,9 +10,11 @@
 // An operand stored [x][k] is K-contiguous, one stored [k][x] is K-major.
 //
 // The matrix instruction gets C as its first operand and R as its second, so a
-// lane's four results are four neighbouring columns of one output row (one
-// 8- or 16-byte store).
+// lane's four results are four columns of one output row; two column tiles are
+// interleaved so that they make eight neighbouring ones (one 16-byte store).
 #pragma once
+
+#include <type_traits>
 
 #include "gemm_device.h"
 
@@ -92,11 +94,19 @@ constexpr int kTgStep = 128;                // a K step: 128 bytes of each K-con
 // bytes in lane order, so the layout's permutation is made by choosing which
 // 16 bytes of memory each lane fetches.
 //
-// K-contiguous: row r is 128 bytes, its 16-byte chunk ch at chunk ch ^ ((r >> 1) & 7).
-//   The 16 rows that a fragment read touches at one chunk cover all 64 banks.
-// K-major: row k is 2 X bytes, its 32-byte unit u (16 values) at unit u ^ f(k),
-//   f(k) = (k & 3) + 4 ((k >> 3) & 1): the 8 rows that half a wave's transposing
-//   read touches (4 of lane groups 2q and 2q + 1 each) lie in distinct units.
+// Fragments are tiles of 16 rows or columns.  Row tile i holds rows 16 i + n.
+// Column tiles 2 i and 2 i + 1 share 32 columns: tile 2 i + b holds columns
+// 32 i + 8 (n / 4) + 4 b + n % 4, which puts eight neighbouring columns into
+// one lane's results of the pair.
+//
+// K-contiguous: row r is 128 bytes, its 16-byte chunk ch at chunk ch ^ f(r), f =
+//   (r >> 1) & 7 for rows, ((r >> 1) & 1) + 2 ((r >> 3) & 3) for columns: the 16
+//   rows that a fragment read touches at one chunk cover all 64 banks.
+// K-major: row k is 2 X bytes.  Rows operand: its 32-byte unit u (16 values) at
+//   unit u ^ f(k), f(k) = (k & 3) + 4 ((k >> 3) & 1): the 8 rows that half a
+//   wave's transposing read touches (4 of lane groups 2q and 2q + 1 each) lie in
+//   distinct units.  Columns operand: a fragment takes every other 8 bytes of a
+//   64-byte unit, so there the 64-byte units are permuted.
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 #define TG_LDS __attribute__((address_space(3)))
 
@@ -110,8 +120,8 @@ __device__ __forceinline__ void tg_dma(const uint8_t* src, uint32_t lds_wave) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_wave), "v"(src) : "memory");
 }
 
-// all but the N youngest loads of this wave have landed, its LDS reads are
-// done, and so for every wave of the workgroup
+// all but the N youngest memory operations of this wave are done, its LDS
+// reads too, and so for every wave of the workgroup
 template <int N>
 __device__ __forceinline__ void tg_wait() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
@@ -121,84 +131,104 @@ __device__ __forceinline__ uint32_t tg_lds_addr(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const TG_LDS uint8_t*)(p)));
 }
 
-// K-contiguous tile of X rows: thread t fetches chunk ch of rows t / 8 + i TH / 8
-template <int X, int TH>
+// the thread's index, opaque to the compiler: what a task's start or end derives
+// from it is then computed there and holds no registers during the steps
+__device__ __forceinline__ int tg_thread() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+
+template <bool COL>
+__device__ __forceinline__ int tg_chunk_perm(int r) {
+  return COL ? ((r >> 1) & 1) + 2 * ((r >> 3) & 3) : (r >> 1) & 7;
+}
+
+// K-contiguous tile of X rows: thread t fetches one chunk of rows t / 8 + i TH / 8
+template <int X, int TH, bool COL>
 struct TgRows {
   static constexpr int N = X * 8 / TH;
-  const uint8_t* p[N];
+  static constexpr int STEP = TH / 8;       // rows between the thread's loads
+  static_assert(STEP % 32 == 0, "the chunk permutation repeats every 32 rows");
+  const uint8_t* p[N];                      // of the next step
   int ch16;                                 // byte of the thread's chunk in the step
-  template <class F>                        // row_ptr(r): first byte of tile row r (any row of the operand for a dead one)
+  template <class F>                        // row_ptr(r): first byte of the operand row of tile row r (any row for a dead one)
   __device__ __forceinline__ void setup(F row_ptr) {
-    const int r = threadIdx.x >> 3;
-    ch16 = 16 * ((threadIdx.x & 7) ^ ((r >> 1) & 7));
+    const int t = tg_thread(), r = t >> 3;
+    ch16 = 16 * ((t & 7) ^ tg_chunk_perm<COL>(r));
 #pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = row_ptr(r + i * (TH / 8)) + ch16;
+    for (int i = 0; i < N; ++i) p[i] = row_ptr(r + i * STEP) + ch16;
   }
-  __device__ __forceinline__ void issue(int step, int64_t kbytes, uint32_t lds_wave) {
-    const int64_t o = static_cast<int64_t>(step) * kTgStep;
-    const bool dead = o + ch16 >= kbytes;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      tg_dma(dead ? reinterpret_cast<const uint8_t*>(&tg_zero) : p[i] + o, lds_wave + i * TH * 16);
+  // left: bytes of the reduction from this step on
+  __device__ __forceinline__ void issue(int i, int left, uint32_t lds_wave) {
+    tg_dma(ch16 < left ? p[i] : reinterpret_cast<const uint8_t*>(&tg_zero), lds_wave + i * TH * 16);
+    p[i] += kTgStep;
   }
 };
 
 // K-major tile of X columns of 2 bytes: thread t fetches one chunk of rows
 // t / (X / 8) + i TH / (X / 8).  Columns at or behind `cols` repeat the last
 // chunk (their results are not stored).
-template <int X, int TH>
+template <int X, int TH, bool COL>
 struct TgCols {
   static constexpr int PER = X / 8;         // chunks of a row
   static constexpr int N = 64 * PER / TH;
   static constexpr int STEP = TH / PER;     // rows between the thread's loads
-  static_assert(X >= 128 && STEP % 16 == 0, "the unit permutation repeats every 16 rows and needs 8 units");
-  const uint8_t* base;                      // the thread's chunk of row 0
+  static constexpr int ROWS = 64 / PER;     // rows of a wave's load
+  static_assert(X >= 128 && STEP % 16 == 0, "the unit permutation repeats every 16 rows");
+  const uint8_t* p[N];                      // of the next step; gathered: p[0] is the thread's chunk of row 0
   int64_t ld;                               // bytes of a row
   int k0;                                   // the thread's first row of a step
-  int idx[N];                               // gathered: source rows of the next step
-  __device__ __forceinline__ void setup(const uint8_t* mem, int64_t ld_bytes, int c0, int cols) {
-    k0 = threadIdx.x / PER;
+  __device__ __forceinline__ void setup(const uint8_t* mem, int64_t ld_bytes, int c0, int cols, bool gathered) {
+    const int t = tg_thread();
+    k0 = t / PER;
     const int f = (k0 & 3) + 4 * ((k0 >> 3) & 1);
-    const int c = c0 + 8 * ((threadIdx.x % PER) ^ (2 * f));
+    const int c = c0 + 8 * ((t % PER) ^ ((COL ? 4 : 2) * f & (PER - 1)));
     ld = ld_bytes;
-    base = mem + 2 * static_cast<int64_t>(min(c, cols - 8));
-  }
-  template <class F>                        // source(k): memory row of reduction row k, any valid one where k >= kt
-  __device__ __forceinline__ void fetch_rows(int step, F source) {
+    p[0] = mem + 2 * static_cast<int64_t>(min(c, cols - 8));
+    if (!gathered) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) idx[i] = source(step * 64 + k0 + i * STEP);
-  }
-  __device__ __forceinline__ void issue_gathered(int step, int kt, uint32_t lds_wave) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const bool dead = step * 64 + k0 + i * STEP >= kt;
-      tg_dma(dead ? reinterpret_cast<const uint8_t*>(&tg_zero) : base + idx[i] * ld, lds_wave + i * TH * 16);
+      for (int i = N - 1; i >= 0; --i) p[i] = p[0] + (k0 + i * STEP) * ld;
     }
   }
-  __device__ __forceinline__ void issue(int step, int kt, uint32_t lds_wave) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int k = step * 64 + k0 + i * STEP;
-      tg_dma(k >= kt ? reinterpret_cast<const uint8_t*>(&tg_zero) : base + k * ld, lds_wave + i * TH * 16);
-    }
+  // left: rows of the reduction from this step on
+  __device__ __forceinline__ void issue(int i, int left, uint32_t lds_wave) {
+    tg_dma(k0 < left - i * STEP ? p[i] : reinterpret_cast<const uint8_t*>(&tg_zero), lds_wave + i * TH * 16);
+    p[i] += 64 * ld;
+  }
+  __device__ __forceinline__ void issue_row(int i, int left, int64_t source, uint32_t lds_wave) {
+    tg_dma(k0 < left - i * STEP ? p[0] + source * ld : reinterpret_cast<const uint8_t*>(&tg_zero), lds_wave + i * TH * 16);
   }
 };
 
-// A wave's fragments of NT 16-row tiles, the first at tile t0: lane (lg, lr)
-// holds row lr of the tile, 16 bytes of k from 16 lg (+ 64 with sub-step 1)
-template <bool KM, int X, int NT>
+// NT fragments of a tile from fragment t0 on: lane (lg, lr) holds entry lr of
+// each, 16 bytes of k from 16 lg (+ 64 with sub-step 1)
+template <bool KM, bool COL, int X, int NT>
 __device__ __forceinline__ void tg_frags(const uint8_t* tile, int t0, int s, u32x4 (&f)[NT]) {
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   if constexpr (!KM) {
-    const uint8_t* b = tile + t0 * 16 * kTgStep + lr * kTgStep + 16 * ((4 * s + lg) ^ (lr >> 1));
+    const int r = COL ? 8 * (lr >> 2) + (lr & 3) : lr;       // row of the lane in tile t0 (an even one)
+    if constexpr (COL) {
+      // tile 2 i + b: rows 32 i + r + 4 b, the same permutation for both (bits 1, 3 and 4 of r)
+      const uint8_t* b = tile + t0 * 16 * kTgStep + r * kTgStep + 16 * ((4 * s + lg) ^ tg_chunk_perm<true>(r));
 #pragma unroll
-    for (int i = 0; i < NT; ++i) f[i] = *reinterpret_cast<const u32x4*>(b + i * 16 * kTgStep);
+      for (int i = 0; i < NT; ++i)
+        f[i] = *reinterpret_cast<const u32x4*>(b + ((i >> 1) * 32 + (i & 1) * 4) * kTgStep);
+    } else {
+      const uint8_t* b = tile + t0 * 16 * kTgStep + r * kTgStep + 16 * ((4 * s + lg) ^ tg_chunk_perm<false>(r));
+#pragma unroll
+      for (int i = 0; i < NT; ++i) f[i] = *reinterpret_cast<const u32x4*>(b + i * 16 * kTgStep);
+    }
   } else {
     const int perm = (lr >> 2) + 4 * (lg & 1);
-    const uint8_t* b = tile + (32 * s + 8 * lg + (lr >> 2)) * 2 * X + 8 * (lr & 3);
+    const uint8_t* b = tile + (32 * s + 8 * lg + (lr >> 2)) * 2 * X;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const uint8_t* q = b + 32 * ((t0 + i) ^ perm);
+      const uint8_t* q;
+      if constexpr (COL)
+        q = b + 64 * ((((t0 + i) >> 1) ^ perm) & (X / 32 - 1)) + 16 * (lr & 3) + 8 * (i & 1);
+      else
+        q = b + 32 * (((t0 + i) ^ perm) & (X / 16 - 1)) + 8 * (lr & 3);
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TG_LDS s16x4*)(q));
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TG_LDS s16x4*)(q + 4 * 2 * X));
       const uint2 l = __builtin_bit_cast(uint2, lo), h = __builtin_bit_cast(uint2, hi);
@@ -207,13 +237,115 @@ __device__ __forceinline__ void tg_frags(const uint8_t* tile, int t0, int s, u32
   }
 }
 
+// ------------------------------------------------------------------ tasks
+// A task is one output tile.  NT and NN: row chunk by row chunk, column tile by
+// column tile within one, experts in order; a prefix sum of the experts'
+// chunks lies in LDS.  TN: every expert has the same tiles.  Each XCD gets an
+// equal contiguous range of the tasks (workgroups go to XCDs round-robin), so
+// that the tiles side by side in its L2 share rows and weights; a workgroup
+// takes every (workgroups per XCD)th task of its XCD's range.
+constexpr int kTgMaxExperts = 4096;
+
+struct TgTask {
+  int e, m0, nt;
+  int row0;       // first row of the expert
+  int rows;       // live rows of the tile
+  int kt;         // length of the reduction
+  int nsteps;     // at least 2: the loads run two steps ahead, short reductions get steps of zeros
+};
+
+// uniform reads that must not wait for the loads in flight go through scalar loads
+typedef const int __attribute__((address_space(4)))* tg_const_ints;
+
+template <int BM>
+__device__ __forceinline__ int tg_prefix(const TileParams& p, int* pre) {
+  const int lane = threadIdx.x & 63;
+  if (threadIdx.x < 64) {
+    int base = 0;
+    for (int g = 0; g < p.E; g += 64) {
+      int c = 0;
+      if (g + lane < p.E) {
+        const int a = min(max(p.offsets[g + lane], 0), p.m_total);
+        const int b = min(max(p.offsets[g + lane + 1], 0), p.m_total);
+        c = (max(b - a, 0) + BM - 1) / BM;
+      }
+      int total;
+      const int before = base + wave_excl_scan(c, total);
+      if (g + lane < p.E) pre[g + lane] = before;
+      base += total;
+    }
+    if (lane == 0) pre[0] = base;           // the place of the first expert's zero holds the total
+  }
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(pre[0]);
+}
+
+template <int L, int BM, int SK>
+__device__ __forceinline__ void tg_decode(const TileParams& p, const int* pre, int u, int e_from, TgTask& t) {
+  const tg_const_ints off = (tg_const_ints)(p.offsets);
+  if constexpr (L == TG_TN) {
+    const int per = p.r_tiles * p.n_tiles;
+    t.e = u / per;
+    const int v = u - t.e * per;
+    // groups of 4 row tiles, column tile by column tile
+    const int grp = v / (4 * p.n_tiles);
+    const int gq = min(4, p.r_tiles - 4 * grp);
+    const int w = v - 4 * grp * p.n_tiles;
+    t.m0 = (4 * grp + w % gq) * BM;
+    t.nt = w / gq;
+    t.row0 = min(max(off[t.e], 0), p.m_total);
+    t.kt = max(min(max(off[t.e + 1], 0), p.m_total) - t.row0, 0);
+    t.rows = min(BM, p.R - t.m0);
+  } else {
+    const int lane = threadIdx.x & 63;
+    const int c = u / p.n_tiles;
+    int e = e_from & ~63;                  // the experts whose chunks all lie before c, counted 64 at a time
+    for (;;) {
+      const bool past = e + lane + 1 < p.E && pre[e + lane + 1] <= c;
+      const int n = __popcll(__ballot(past));
+      e += n;
+      if (n < 64) break;
+    }
+    t.e = __builtin_amdgcn_readfirstlane(e);
+    t.row0 = min(max(off[t.e], 0), p.m_total);
+    const int Me = min(max(off[t.e + 1], 0), p.m_total) - t.row0;
+    const int nc = (Me + BM - 1) / BM;
+    // inside an expert, groups of 4 chunks run column tile by column tile
+    const int v = u - (t.e ? __builtin_amdgcn_readfirstlane(pre[t.e]) : 0) * p.n_tiles;
+    const int grp = v / (4 * p.n_tiles);
+    const int gq = max(1, min(4, nc - 4 * grp));
+    const int w = v - 4 * grp * p.n_tiles;
+    t.m0 = (4 * grp + w % gq) * BM;
+    t.nt = w / gq;
+    t.rows = min(BM, Me - t.m0);
+    t.kt = p.K;
+  }
+  t.nsteps = max(2, (t.kt + SK - 1) / SK);
+}
+
 // ------------------------------------------------------------------ the tile kernel
 // A workgroup of WR x WC waves computes BM rows x BN columns (gated: BN / 2
-// gate columns and the same BN / 2 of up); wave (wr, wc) holds BM / WR rows and
-// BN / WC columns.  ST stages of both operand tiles in LDS: while step s is
-// multiplied, the loads of steps s + 1 .. s + ST - 1 are in flight; one barrier
-// per step.
-template <int T, int L, int EPI, int BM, int BN, int WR, int WC, int ST>
+// gate columns and the same BN / 2 of up) per task; wave (wr, wc) holds
+// BM / WR rows and BN / WC columns.  The steps of all its tasks form one
+// stream through two LDS stages.
+//
+// A step is four units of (half h of the wave's row tiles) x (half s of the
+// step's k); while a unit is multiplied, the next unit's fragments are read
+// from LDS.  The workgroup meets twice a step, before units 1 and 3:
+//   before 1  the fragments of units 0 and 1 are in registers, so the parts of
+//             the stage that no later unit reads are free; the loads X of step
+//             + 2 go into them during units 1 and 2
+//   before 3  all fragments are in registers; the loads Y of step + 2 go into
+//             the rest during unit 3, and the next step's first fragments are
+//             read
+// With the units in the order (h, s) = 00 01 10 11 the columns operand and the
+// h = 0 rows are free first (X), the h = 1 rows later (Y).  Two K-major
+// operands (TN) are split by k instead: order 00 10 01 11, X the s = 0 halves.
+// A load is waited for 1.25 steps or more after it went out, and never more
+// than a step's loads are waited for at once.  Loads are spread over a unit's
+// products: in one burst they would hold up the products behind them.  A
+// finished tile is stored while the next one's loads are in flight.
+template <int T, int L, int EPI, int BM, int BN, int WR, int WC>
 __global__ __launch_bounds__(64 * WR * WC) void k_tile_gemm(const TileParams p) {
   using TT = TgType<T>;
   using acc_t = typename TT::acc_t;
@@ -223,223 +355,325 @@ __global__ __launch_bounds__(64 * WR * WC) void k_tile_gemm(const TileParams p) 
   constexpr bool RKM = L == TG_TN, CKM = L != TG_NT;
   constexpr bool GATED = EPI == TG_OUT_GATED;
   constexpr int RT = BM / WR / 16, CT = BN / WC / 16;     // 16-row and 16-column tiles of a wave
+  constexpr int RH = RT / 2;
   constexpr int kStage = (BM + BN) * kTgStep;
-  constexpr int kLoads = kStage / 16 / TH;
+  using Rows = TgRows<BM, TH, false>;
+  using Cols = TgRows<BN, TH, true>;
+  using RowsK = TgCols<BM, TH, false>;
+  using ColsK = TgCols<BN, TH, true>;
+  constexpr int NR = Rows::N, NC = Cols::N;               // loads of a thread per step and operand
+  constexpr int NX = RKM ? NR / 2 + NC / 2 : NC + NR / 2, NY = NR + NC - NX;
   static_assert(T != TG_I8 || L == TG_NT, "int8 has the forward product only");
-  static_assert(!GATED || CT % 2 == 0, "a gated wave holds as many gate as up tiles");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[ST * kStage];
-  static_assert(fits_lds(sizeof(lds), 1), "tile stages exceed the LDS of a CU");
+  static_assert(CT % (GATED ? 4 : 2) == 0 && RT % 2 == 0, "column tiles come in pairs, row tiles in halves");
+  static_assert(RowsK::N == NR && ColsK::N == NC && NR % 2 == 0 && NC % 2 == 0, "halves of the loads");
+  static_assert(RKM || Rows::STEP * WR * 2 <= BM, "a load holds rows of one half");
+  constexpr int kMap = L == TG_TN ? 1 : kTgMaxExperts;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
+  __shared__ int pre[kMap];
+  static_assert(fits_lds(sizeof(lds) + sizeof(pre), 1), "tile stages exceed the LDS of a CU");
 
-  int e, m0, nt;
-  int row0, Me;
-  if constexpr (L == TG_TN) {
-    // equal contiguous ranges of the tiles per XCD, as find_task gives
-    const int per = p.r_tiles * p.n_tiles;
-    const int n = p.E * per;
-    const int share = (n + 7) >> 3;
-    const int u = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
-    if ((blockIdx.x >> 3) >= share || u >= n) return;
-    e = u / per;
-    const int v = u - e * per;
-    m0 = (v / p.n_tiles) * BM;
-    nt = v % p.n_tiles;
-    row0 = min(max(p.offsets[e], 0), p.m_total);
-    Me = max(min(max(p.offsets[e + 1], 0), p.m_total) - row0, 0);
-  } else {
-    bool narrow;
-    GemmParams map{};
-    map.offsets = p.offsets;
-    map.E = p.E;
-    map.m_total = p.m_total;
-    map.n_tiles = p.n_tiles;
-    map.slots = 1 << 30;
-    if (!find_task<BM / 16, false, 0>(map, e, m0, nt, narrow)) return;
-    row0 = min(max(p.offsets[e], 0), p.m_total);
-    Me = min(max(p.offsets[e + 1], 0), p.m_total) - row0;
-    // inside an expert, groups of 4 row chunks run column tile by column tile:
-    // workgroups side by side on an XCD share row chunks and weight tiles in its L2
-    const int nc = (Me + BM - 1) / BM;
-    const int u = (m0 / BM) * p.n_tiles + nt;
-    const int grp = (m0 / BM) / 4;
-    const int gq = min(4, nc - 4 * grp);
-    const int w = u - 4 * grp * p.n_tiles;
-    m0 = (4 * grp + w % gq) * BM;
-    nt = w / gq;
-  }
-  const int rows = L == TG_TN ? min(BM, p.R - m0) : min(BM, Me - m0);
-  const int kt = L == TG_TN ? Me : p.K;     // length of the reduction
-  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  int n;
+  if constexpr (L == TG_TN) n = p.E * p.r_tiles * p.n_tiles;
+  else n = tg_prefix<BM>(p, pre) * p.n_tiles;
+  const int share = (n + 7) >> 3;
+  const int lo = (blockIdx.x & 7) * share, hi = min(lo + share, n);
+  const int stride = gridDim.x >> 3;
+  int u = lo + (blockIdx.x >> 3);
+  if (u >= hi) return;
+
+  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / WC, wc = wave % WC;
-  const int c0 = nt * (GATED ? BN / 2 : BN);
   const int half = p.N / 2;
-
   const uint8_t* A = static_cast<const uint8_t*>(p.a);
   const uint8_t* B = static_cast<const uint8_t*>(p.b);
-  if constexpr (L != TG_TN) B += static_cast<size_t>(e) * p.N * p.K * EB;
-  // row q of the expert's rows in the operand that may be gathered; the index
-  // array's entries are clamped, so that bad ones give wrong rows only
-  auto src_row = [&](int q) -> int {
-    int r = row0 + q;
-    if (p.a_rows) {
-      r = p.a_rows[r];
-      r = (r >= 0 && r < p.src_rows) ? r : 0;
-    }
-    return r;
-  };
+  // an entry of the index array, clamped, so that a bad one gives wrong rows only
+  auto valid_row = [&](int r) __attribute__((always_inline)) -> int { return (r >= 0 && r < p.src_rows) ? r : 0; };
 
-  TgRows<BM, TH> ra;
-  TgRows<BN, TH> ca;
-  TgCols<(BM < 128 ? 128 : BM), TH> rk;
-  TgCols<(BN < 128 ? 128 : BN), TH> ck;
-  if constexpr (!RKM) {
-    ra.setup([&](int r) {
-      const int q = m0 + (r < rows ? r : 0);
-      const int64_t sr = L == TG_NT ? src_row(q) : row0 + q;
-      return A + sr * p.K * EB;
-    });
-  } else {
-    rk.setup(A + static_cast<int64_t>(row0) * p.R * 2, static_cast<int64_t>(p.R) * 2, m0, p.R);
-  }
-  if constexpr (!CKM) {
-    ca.setup([&](int c) {
-      int col;
-      if constexpr (GATED)
-        col = min(c0 + (c & (BN / 2 - 1)), half - 1) + (c >= BN / 2 ? half : 0);
-      else
-        col = min(c0 + c, p.N - 1);
-      return B + static_cast<int64_t>(col) * p.K * EB;
-    });
-  } else {
-    ck.setup(B, static_cast<int64_t>(p.N) * 2, c0, p.N);
-  }
+  // ---- the loads
+  TgTask pt = {};                           // their task
+  int ps = 0;                               // their step in it
+  int pg = 0;                               // their step in the stream
+  bool idle = false;                        // no task is left: zeros are loaded, which nothing reads
+  Rows ra;
+  Cols ca;
+  RowsK rk;
+  ColsK ck;
+  auto begin = [&]() __attribute__((always_inline)) {
+    const int c0 = pt.nt * (GATED ? BN / 2 : BN);
+    const uint8_t* Be = B;
+    if constexpr (L != TG_TN) Be += static_cast<size_t>(pt.e) * p.N * p.K * EB;
+    if constexpr (L == TG_TN) {
+      rk.setup(A + static_cast<int64_t>(pt.row0) * p.R * 2, static_cast<int64_t>(p.R) * 2, pt.m0, p.R, false);
+    } else {
+      ra.setup([&](int r) __attribute__((always_inline)) {
+        int q = pt.row0 + pt.m0 + (r < pt.rows ? r : 0);
+        if (L == TG_NT && p.a_rows) q = valid_row(p.a_rows[q]);
+        return A + static_cast<int64_t>(q) * p.K * EB;
+      });
+    }
+    if constexpr (L == TG_NT)
+      ca.setup([&](int c) __attribute__((always_inline)) {
+        int col;
+        if constexpr (GATED)
+          col = min(c0 + (c & (BN / 2 - 1)), half - 1) + (c >= BN / 2 ? half : 0);
+        else
+          col = min(c0 + c, p.N - 1);
+        return Be + static_cast<int64_t>(col) * p.K * EB;
+      });
+    else
+      ck.setup(Be, static_cast<int64_t>(p.N) * 2, c0, p.N, L == TG_TN);
+  };
   const uint32_t lds0 = tg_lds_addr(lds) + wave * 1024;
-  auto fetch = [&](int step) {              // the gathered rows of a K-major step
-    if constexpr (L == TG_TN) ck.fetch_rows(step, [&](int k) { return src_row(min(k, kt - 1)); });
-  };
-  auto issue = [&](int step) {
-    const uint32_t l = lds0 + (step % ST) * kStage;
-    if constexpr (!RKM) ra.issue(step, static_cast<int64_t>(kt) * EB, l);
-    else rk.issue(step, kt, l);
-    if constexpr (!CKM) ca.issue(step, static_cast<int64_t>(kt) * EB, l + BM * kTgStep);
-    else if constexpr (L == TG_TN) ck.issue_gathered(step, kt, l + BM * kTgStep);
-    else ck.issue(step, kt, l + BM * kTgStep);
-  };
-
-  acc_t acc[RT][CT];
+  int left = 0;                             // of the reduction from the loads' step on: bytes (K-contiguous) and rows
+  int left_k = 0;
+  int src[NC][L == TG_TN ? ColsK::ROWS : 1];  // TN: source rows of the wave's loads
+  auto open = [&]() __attribute__((always_inline)) {        // before a step's loads
+    left_k = pt.kt - ps * 64;
+    left = idle ? 0 : pt.kt * EB - ps * kTgStep;
+    if (idle) left_k = 0;
+    if constexpr (L == TG_TN) {
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+      for (int j = 0; j < NC; ++j)
 #pragma unroll
-    for (int j = 0; j < CT; ++j) acc[i][j] = acc_t{0, 0, 0, 0};
-
-  const int nsteps = (kt + SK - 1) / SK;
-  if (nsteps > 0) {
-    fetch(0);
-#pragma unroll
-    for (int s = 0; s < ST - 1; ++s)
-      if (s < nsteps) {
-        issue(s);
-        if (s + 1 < nsteps) fetch(s + 1);
-      }
-  }
-  const bool live = wr * (BM / WR) < rows;  // the wave has rows
-  for (int step = 0; step < nsteps; ++step) {
-    if (step + ST - 1 <= nsteps) tg_wait<(ST - 2) * kLoads>();
-    else tg_wait<0>();
-    if (step + ST - 1 < nsteps) {
-      issue(step + ST - 1);
-      if (step + ST < nsteps) fetch(step + ST);
-    }
-    const uint8_t* cur = lds + (step % ST) * kStage;
-    if (live) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        u32x4 fc[CT], fr[RT];
-        if constexpr (GATED) {
-          u32x4 g[CT / 2], u[CT / 2];
-          tg_frags<CKM, BN, CT / 2>(cur + BM * kTgStep, wc * (CT / 2), s, g);
-          tg_frags<CKM, BN, CT / 2>(cur + BM * kTgStep, BN / 32 + wc * (CT / 2), s, u);
-#pragma unroll
-          for (int j = 0; j < CT / 2; ++j) {
-            fc[j] = g[j];
-            fc[CT / 2 + j] = u[j];
-          }
-        } else {
-          tg_frags<CKM, BN, CT>(cur + BM * kTgStep, wc * CT, s, fc);
+        for (int w = 0; w < ColsK::ROWS; ++w) {
+          const int k = pt.row0 + max(min(ps * 64 + wave * ColsK::ROWS + j * ColsK::STEP + w, pt.kt - 1), 0);
+          src[j][w] = p.a_rows && pt.kt > 0 ? ((tg_const_ints)(p.a_rows))[k] : k;
         }
-        tg_frags<RKM, BM, RT>(cur, wr * RT, s, fr);
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int j = 0; j < CT; ++j) acc[i][j] = TT::mfma(fc[j], fr[i], acc[i][j]);
-      }
     }
-  }
-
-  // lane: output row lr of a 16-row tile, columns 4 lg .. 4 lg + 3 of a 16-column tile
+  };
+  auto issue_row = [&](int i, uint32_t l) __attribute__((always_inline)) {
+    if constexpr (RKM) rk.issue(i, left_k, l);
+    else ra.issue(i, left, l);
+  };
+  auto issue_col = [&](int j, uint32_t l) __attribute__((always_inline)) {
+    if constexpr (L == TG_NT) {
+      ca.issue(j, left, l + BM * kTgStep);
+    } else if constexpr (L == TG_NN) {
+      ck.issue(j, left_k, l + BM * kTgStep);
+    } else {
+      int v = src[j][0];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    const int r = (BM / WR) * wr + 16 * i + lr;
-    if (r >= rows) continue;
-    const int64_t orow = L == TG_TN ? static_cast<int64_t>(e) * p.R + m0 + r : static_cast<int64_t>(row0) + m0 + r;
-    float sa = 1.0f;
-    if constexpr (T == TG_I8) sa = p.sa[src_row(m0 + r)];
-#pragma unroll
-    for (int j = 0; j < (GATED ? CT / 2 : CT); ++j) {
-      const int c = c0 + (GATED ? BN / 2 : BN) / WC * wc + 16 * j + 4 * lg;
-      if (c >= (GATED ? half : p.N)) continue;
-      float4v v, w;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = static_cast<float>(acc[i][j][q]);
-      if constexpr (T == TG_I8) v = v * (*reinterpret_cast<const float4v*>(p.sb + static_cast<size_t>(e) * p.N + c) * sa);
-      if constexpr (GATED) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) w[q] = static_cast<float>(acc[i][j + CT / 2][q]);
-        if constexpr (T == TG_I8) w = w * (*reinterpret_cast<const float4v*>(p.sb + static_cast<size_t>(e) * p.N + half + c) * sa);
-        if (p.gu) {
-          *reinterpret_cast<float4v*>(p.gu + orow * p.N + c) = v;
-          *reinterpret_cast<float4v*>(p.gu + orow * p.N + half + c) = w;
-        }
-        float4v h;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) h[q] = tg_act(v[q], p.act) * w[q];
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + orow * half + c) = TT::pack(h);
-      } else if constexpr (EPI == TG_OUT_F32) {
-        *reinterpret_cast<float4v*>(static_cast<float*>(p.out) + orow * p.N + c) = v;
+      for (int w = 1; w < ColsK::ROWS; ++w) v = lane / (64 / ColsK::ROWS) == w ? src[j][w] : v;
+      if (p.a_rows) v = valid_row(v);
+      ck.issue_row(j, left_k, v, l + BM * kTgStep);
+    }
+  };
+  auto issue_x = [&](int q) __attribute__((always_inline)) {   // load q of X
+    const uint32_t l = lds0 + (pg & 1) * kStage;
+    if constexpr (RKM) {
+      if (q < NC / 2) issue_col(q, l);
+      else issue_row(q - NC / 2, l);
+    } else {
+      if (q < NC) issue_col(q, l);
+      else issue_row(2 * (q - NC), l);
+    }
+  };
+  auto issue_y = [&](int q) __attribute__((always_inline)) {
+    const uint32_t l = lds0 + (pg & 1) * kStage;
+    if constexpr (RKM) {
+      if (q < NC / 2) issue_col(NC / 2 + q, l);
+      else issue_row(NR / 2 + q - NC / 2, l);
+    } else {
+      issue_row(2 * q + 1, l);
+    }
+  };
+  auto advance = [&]() __attribute__((always_inline)) {     // after a step's loads
+    ++pg;
+    if (++ps == pt.nsteps) {
+      u += stride;
+      ps = 0;
+      if (u < hi) {
+        tg_decode<L, BM, SK>(p, pre, u, pt.e, pt);
+        begin();
       } else {
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + orow * p.N + c) = TT::pack(v);
+        idle = true;
+        pt.nsteps = 0;
       }
     }
+  };
+
+  // ---- the products
+  acc_t acc[RT][CT];
+  auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < CT; ++j) acc[i][j] = acc_t{0, 0, 0, 0};
+  };
+  auto read_rows = [&](const uint8_t* stage, int s, int h, u32x4 (&f)[RH]) __attribute__((always_inline)) {
+    tg_frags<RKM, false, BM, RH>(stage, wr * RT + h * RH, s, f);
+  };
+  auto read_cols = [&](const uint8_t* stage, int s, u32x4 (&f)[CT]) __attribute__((always_inline)) {
+    const uint8_t* c = stage + BM * kTgStep;
+    if constexpr (GATED) {                  // the gate tiles, then the same columns of up
+      u32x4 g[CT / 2], v[CT / 2];
+      tg_frags<CKM, true, BN, CT / 2>(c, wc * (CT / 2), s, g);
+      tg_frags<CKM, true, BN, CT / 2>(c, BN / 32 + wc * (CT / 2), s, v);
+#pragma unroll
+      for (int j = 0; j < CT / 2; ++j) {
+        f[j] = g[j];
+        f[CT / 2 + j] = v[j];
+      }
+    } else {
+      tg_frags<CKM, true, BN, CT>(c, wc * CT, s, f);
+    }
+  };
+  // the products of a unit, `loads` of load(0 ..) spread over them
+  auto unit = [&](int h, const u32x4 (&fc)[CT], const u32x4 (&fr)[RH], auto from, auto to, auto load) __attribute__((always_inline)) {
+    constexpr int F = decltype(from)::value, N = decltype(to)::value - F;
+#pragma unroll
+    for (int i = 0; i < RH; ++i) {
+#pragma unroll
+      for (int j = 0; j < CT; ++j) acc[h * RH + i][j] = TT::mfma(fc[j], fr[i], acc[h * RH + i][j]);
+      if constexpr (N > 0) {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int q = F + i * N / RH; q < F + (i + 1) * N / RH; ++q) load(q);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  TgTask ct = {};                           // their task
+
+  // lane: output row lr of a 16-row tile, 8 columns from 8 lg of a pair of column tiles
+  auto store = [&]() __attribute__((always_inline)) {
+    const int lr = tg_thread() & 15, lg = (tg_thread() >> 4) & 3;
+    const int c0 = ct.nt * (GATED ? BN / 2 : BN) + (GATED ? BN / 2 : BN) / WC * wc + 8 * lg;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int r = (BM / WR) * wr + 16 * i + lr;
+      if (r >= ct.rows) continue;
+      const int64_t orow = L == TG_TN ? static_cast<int64_t>(ct.e) * p.R + ct.m0 + r : static_cast<int64_t>(ct.row0) + ct.m0 + r;
+      float sa = 1.0f;
+      if constexpr (T == TG_I8) sa = p.sa[p.a_rows ? valid_row(p.a_rows[ct.row0 + ct.m0 + r]) : ct.row0 + ct.m0 + r];
+#pragma unroll
+      for (int j = 0; j < (GATED ? CT / 2 : CT); j += 2) {
+        const int c = c0 + 16 * j;
+        if (c >= (GATED ? half : p.N)) continue;
+        float4v v[2], w[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[b][q] = static_cast<float>(acc[i][j + b][q]);
+          if constexpr (T == TG_I8) v[b] = v[b] * (*reinterpret_cast<const float4v*>(p.sb + static_cast<size_t>(ct.e) * p.N + c + 4 * b) * sa);
+        }
+        if constexpr (GATED) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[b][q] = static_cast<float>(acc[i][j + b + CT / 2][q]);
+            if constexpr (T == TG_I8)
+              w[b] = w[b] * (*reinterpret_cast<const float4v*>(p.sb + static_cast<size_t>(ct.e) * p.N + half + c + 4 * b) * sa);
+            if (p.gu) {
+              *reinterpret_cast<float4v*>(p.gu + orow * p.N + c + 4 * b) = v[b];
+              *reinterpret_cast<float4v*>(p.gu + orow * p.N + half + c + 4 * b) = w[b];
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[b][q] = tg_act(v[b][q], p.act) * w[b][q];
+          }
+        }
+        if constexpr (EPI == TG_OUT_F32) {
+          float* o = static_cast<float*>(p.out) + orow * p.N + c;
+          *reinterpret_cast<float4v*>(o) = v[0];
+          *reinterpret_cast<float4v*>(o + 4) = v[1];
+        } else {
+          const uint2 a = TT::pack(v[0]), b = TT::pack(v[1]);
+          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + orow * (GATED ? half : p.N) + c) = u32x4{a.x, a.y, b.x, b.y};
+        }
+      }
+    }
+  };
+
+  constexpr std::integral_constant<int, 0> i0;
+  constexpr std::integral_constant<int, NX / 2> ix1;
+  constexpr std::integral_constant<int, NX> ix;
+  constexpr std::integral_constant<int, NY> iy;
+  tg_decode<L, BM, SK>(p, pre, u, 0, pt);
+  begin();
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    open();
+#pragma unroll
+    for (int q = 0; q < NX; ++q) issue_x(q);
+#pragma unroll
+    for (int q = 0; q < NY; ++q) issue_y(q);
+    if (s == 1) ct = pt;
+    advance();
   }
+  tg_wait<NX + NY>();
+  clear();
+  u32x4 c0[CT], c1[CT], ra_[RH], rb_[RH];
+  read_cols(lds, 0, c0);
+  read_rows(lds, 0, 0, ra_);
+  __builtin_amdgcn_sched_barrier(0);
+  int cs = 0;                               // step of the task
+  for (int cg = 0;; ++cg) {
+    const uint8_t* cur = lds + (cg & 1) * kStage;
+    const uint8_t* nxt = lds + ((cg + 1) & 1) * kStage;
+    open();
+    if constexpr (!RKM) {
+      read_cols(cur, 1, c1);
+      read_rows(cur, 1, 0, rb_);
+      unit(0, c0, ra_, i0, i0, issue_x);
+      tg_wait<NX + NY>();
+      read_rows(cur, 0, 1, ra_);
+      unit(0, c1, rb_, i0, ix1, issue_x);
+      read_rows(cur, 1, 1, rb_);
+      unit(1, c0, ra_, ix1, ix, issue_x);
+    } else {
+      read_rows(cur, 0, 1, rb_);
+      unit(0, c0, ra_, i0, i0, issue_x);
+      tg_wait<NX + NY>();
+      read_cols(cur, 1, c1);
+      read_rows(cur, 1, 0, ra_);
+      unit(1, c0, rb_, i0, ix1, issue_x);
+      read_rows(cur, 1, 1, rb_);
+      unit(0, c1, ra_, ix1, ix, issue_x);
+    }
+    tg_wait<NX + NY>();
+    read_cols(nxt, 0, c0);
+    read_rows(nxt, 0, 0, ra_);
+    unit(1, c1, rb_, i0, iy, issue_y);
+    if (++cs == ct.nsteps) {
+      store();
+      if (idle) break;
+      ct = pt;
+      cs = 0;
+      clear();
+    }
+    advance();
+  }
+  tg_wait<0>();                             // nothing may land in LDS after the workgroup is gone
 }
 
-template <int T, int L, int EPI, int BM, int BN, int WR, int WC, int ST>
-static hipError_t tg_start(TileParams p, hipStream_t stream) {
+// persistent workgroups: as many as are resident at once (256 CUs)
+template <int T, int L, int EPI, int BM, int BN, int WR, int WC>
+static hipError_t tg_start(TileParams p, int per_cu, hipStream_t stream) {
   const int cols = EPI == TG_OUT_GATED ? p.N / 2 : p.N;
   const int bn = EPI == TG_OUT_GATED ? BN / 2 : BN;
   p.n_tiles = (cols + bn - 1) / bn;
   p.r_tiles = (p.R + BM - 1) / BM;
-  int64_t blocks;
+  int64_t tasks;
   if (L == TG_TN) {
-    blocks = static_cast<int64_t>(p.E) * p.r_tiles * p.n_tiles;
+    tasks = static_cast<int64_t>(p.E) * p.r_tiles * p.n_tiles;
   } else {
     // at most min(E, m_total) experts have rows, each with one partial chunk
     const int64_t chunks = p.m_total / BM + (p.E < p.m_total ? p.E : p.m_total);
-    blocks = chunks * p.n_tiles;
+    tasks = chunks * p.n_tiles;
   }
-  blocks = (blocks + 7) / 8 * 8;
-  if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
-  if (blocks == 0) return hipSuccess;
-  hipLaunchKernelGGL((k_tile_gemm<T, L, EPI, BM, BN, WR, WC, ST>), dim3(static_cast<unsigned>(blocks)), dim3(64 * WR * WC), 0,
-                     stream, p);
+  if (tasks >= (int64_t(1) << 31) - 8) return hipErrorInvalidConfiguration;
+  if (tasks == 0) return hipSuccess;
+  const int64_t blocks = min(int64_t(256) * per_cu, (tasks + 7) / 8 * 8);
+  hipLaunchKernelGGL((k_tile_gemm<T, L, EPI, BM, BN, WR, WC>), dim3(static_cast<unsigned>(blocks)), dim3(64 * WR * WC), 0, stream, p);
   return hipGetLastError();
 }
 
 template <int T, int L, int EPI>
 static hipError_t tg_launch(const TileParams& p, hipStream_t stream) {
   const int64_t r = L == TG_TN ? p.R : p.rows_hint;
-  if (r >= 192) return tg_start<T, L, EPI, 256, 256, 2, 4, 2>(p, stream);
-  return tg_start<T, L, EPI, 128, 128, 2, 2, 2>(p, stream);
+  if (r >= 192) return tg_start<T, L, EPI, 256, 256, 2, 4>(p, 1, stream);
+  return tg_start<T, L, EPI, 128, 128, 2, 2>(p, 2, stream);
 }
 
 template <int T>
