@@ -698,7 +698,7 @@ int check_plain(const char* fn, int32_t dtype, const int32_t* offsets, int32_t E
   if (E > 4096) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: E=%d > 4096", fn, E);
   if (m_total >= (int64_t(1) << 31) || rows_total >= (int64_t(1) << 31))
     return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: 2^31 rows or more", fn);
-  if (N > (1 << 29) || K > (1 << 29)) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: a dimension above 2^29", fn);
+  if (N > (1 << 26) || K > (1 << 26)) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: a dimension above 2^26", fn);
   if (!aligned(offsets, 4) || !aligned(a_rows, 4)) return fail(NVFP4MOE_ERR_INVALID, "%s: misaligned index array", fn);
   if (m_total > 0) {
     if (!row_ptrs) return fail(NVFP4MOE_ERR_INVALID, "%s: null row operand", fn);
@@ -764,7 +764,7 @@ int product_grad(const char* fn, int32_t dtype, const void* dy, const void* a, c
 int moe_gated_ffn(const nvfp4moe_gated_args* a, void* stream) {
   const char* fn = "moe_gated_ffn";
   if (!a) return fail(NVFP4MOE_ERR_INVALID, "%s: args is NULL", fn);
-  if (a->I > (1 << 28)) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: I=%d above 2^28", fn, a->I);
+  if (a->I > (1 << 25)) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: I=%d above 2^25", fn, a->I);
   if (a->I <= 0 || a->I % 8 != 0) return fail(NVFP4MOE_ERR_INVALID, "%s: I=%d must be a positive multiple of 8", fn, a->I);
   const int bad = check_plain(fn, a->dtype, a->offsets, a->E, 2 * a->I, a->H, a->m_total, a->a_rows, a->x_rows,
                               a->x && a->h, true);
@@ -797,7 +797,7 @@ int moe_gated_ffn(const nvfp4moe_gated_args* a, void* stream) {
 
 size_t moe_gated_ffn_backward_workspace_size(int32_t E, int32_t H, int32_t I, int64_t m_total) {
   if (E <= 0 || E > 4096 || H <= 0 || I <= 0 || m_total < 0 || H % 8 != 0 || I % 8 != 0 || m_total >= (int64_t(1) << 31) ||
-      I > (1 << 28))
+      I > (1 << 25))
     return 0;
   return static_cast<size_t>(m_total > 0 ? m_total : 1) * 2 * static_cast<size_t>(I) * 2;   // dg and du in 16 bits
 }
@@ -805,7 +805,7 @@ size_t moe_gated_ffn_backward_workspace_size(int32_t E, int32_t H, int32_t I, in
 int moe_gated_ffn_backward(const nvfp4moe_gated_grad_args* a, void* workspace, size_t workspace_bytes, void* stream) {
   const char* fn = "moe_gated_ffn_backward";
   if (!a) return fail(NVFP4MOE_ERR_INVALID, "%s: args is NULL", fn);
-  if (a->I > (1 << 28)) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: I=%d above 2^28", fn, a->I);
+  if (a->I > (1 << 25)) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: I=%d above 2^25", fn, a->I);
   if (a->I <= 0 || a->I % 8 != 0) return fail(NVFP4MOE_ERR_INVALID, "%s: I=%d must be a positive multiple of 8", fn, a->I);
   if (!a->dx && !a->dw && a->m_total > 0) return fail(NVFP4MOE_ERR_INVALID, "%s: neither dx nor dw", fn);
   const int bad = check_plain(fn, a->dtype, a->offsets, a->E, 2 * a->I, a->H, a->m_total, a->a_rows, a->x_rows,

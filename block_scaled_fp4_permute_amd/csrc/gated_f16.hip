@@ -1,5 +1,5 @@
 // The grouped products of the 16-bit expert FFN on float16 operands.
-#include "tile_gemm.h"
+#include "skinny_gemm.h"
 
 namespace nvfp4 {
 

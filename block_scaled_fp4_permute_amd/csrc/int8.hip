@@ -1,41 +1,145 @@
 // INT8 products with one scale per row of each operand (tokens and output
 // channels), and the quantiser that makes such operands.
-#include "tile_gemm.h"
+#include "skinny_gemm.h"
 
 namespace nvfp4 {
 
 // s = absmax / 127 (float32 division, 1 where that is zero), code =
-// nearest-even integer of the correctly rounded float32 quotient x / s.  One
-// workgroup per row, two passes over it (the second from cache).
+// nearest-even integer of the correctly rounded float32 quotient x / s.
+//
+// One read of x: LPR lanes hold a row in registers (NV pieces of 8 values a
+// lane), reduce its maximum and write codes and scale.  Bound by memory; the
+// quotient is x * (1 / s) except where that lands within 2^-14 of a tie between
+// two codes: |x / s| <= 127 (1 + 2^-23), so the product's two roundings and the
+// quotient's own move it by less than 127 * 3 * 2^-24 < 2^-15, and only there
+// can they decide otherwise than the divided quotient.  Below 2^-100 the
+// reciprocal could leave float32's range, and the row is divided throughout.
 template <int DT>
-__global__ __launch_bounds__(256) void k_int8_quantize(const void* __restrict__ x, int64_t cols, int8_t* __restrict__ codes,
-                                                       float* __restrict__ scales) {
-  const int64_t row = blockIdx.x;
-  auto at = [&](int64_t c) -> float {
-    if constexpr (DT == 0) return static_cast<const float*>(x)[row * cols + c];
-    return bf16_to_f32(static_cast<const uint16_t*>(x)[row * cols + c]);
-  };
-  float top = 0.0f;
-  for (int64_t c = threadIdx.x; c < cols; c += 256) top = fmaxf(top, fabsf(at(c)));
+struct Q8Piece {
+  u32x4 w[DT == 0 ? 2 : 1];
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (DT == 0) return __uint_as_float(w[i >> 2][i & 3]);
+    return __uint_as_float((i & 1) ? w[0][i >> 1] & 0xFFFF0000u : w[0][i >> 1] << 16);
+  }
+};
+
+template <int DT>
+__device__ __forceinline__ Q8Piece<DT> q8_load(const void* __restrict__ x, int64_t first) {
+  Q8Piece<DT> r;
+  const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(x) + first * (DT == 0 ? 4 : 2));
+  r.w[0] = p[0];
+  if constexpr (DT == 0) r.w[1] = p[1];
+  return r;
+}
+
+__device__ __forceinline__ int q8_code(float x, float s, float inv, bool fast) {
+  float q = x * inv;
+  float k = rintf(q);
+  if (!fast || fabsf(fabsf(q - k) - 0.5f) < 0x1p-14f) k = rintf(x / s);
+  return static_cast<int>(fminf(fmaxf(k, -127.0f), 127.0f));
+}
+
+template <int DT>
+__device__ __forceinline__ void q8_store(const Q8Piece<DT>& v, float s, float inv, bool fast, int8_t* __restrict__ dst) {
+  uint32_t w[2];
 #pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-  __shared__ float part[4];
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+  for (int h = 0; h < 2; ++h) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r |= (static_cast<uint32_t>(q8_code(v.at(4 * h + i), s, inv, fast)) & 0xFFu) << (8 * i);
+    w[h] = r;
+  }
+  *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+}
+
+// the maximum over the LPR lanes of a row (64: the wave, 256: the workgroup)
+template <int LPR>
+__device__ __forceinline__ float q8_row_max(float m) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+  if constexpr (LPR == 256) {
+    __shared__ float part[4];
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+  }
+  return m;
+}
+
+// NV = 0: rows of any length, read a second time (from cache) for the codes
+template <int DT, int LPR, int NV>
+__global__ __launch_bounds__(256) void k_int8_quantize(const void* __restrict__ x, int64_t rows, int cols,
+                                                       int8_t* __restrict__ codes, float* __restrict__ scales) {
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / LPR) + threadIdx.x / LPR;
+  if (row >= rows) return;                  // whole waves (LPR 64) or no lane at all
+  const int l = threadIdx.x % LPR;
+  const int pieces = cols / 8;
+  const int64_t base = row * cols;
+  float top = 0.0f;
+  Q8Piece<DT> v[NV > 0 ? NV : 1];
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = l + i * LPR;
+      v[i] = q8_load<DT>(x, base + 8 * (c < pieces ? c : 0));
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) top = fmaxf(top, fabsf(v[i].at(q)));
+  } else {
+    for (int c = l; c < pieces; c += LPR) {
+      const Q8Piece<DT> w = q8_load<DT>(x, base + 8 * static_cast<int64_t>(c));
+#pragma unroll
+      for (int q = 0; q < 8; ++q) top = fmaxf(top, fabsf(w.at(q)));
+    }
+  }
+  top = q8_row_max<LPR>(top);
   float s = top / 127.0f;
   if (!(s > 0.0f)) s = 1.0f;
-  if (threadIdx.x == 0) scales[row] = s;
-  for (int64_t c = threadIdx.x; c < cols; c += 256)
-    codes[row * cols + c] = static_cast<int8_t>(fminf(fmaxf(rintf(at(c) / s), -127.0f), 127.0f));
+  const bool fast = s > 0x1p-100f;
+  const float inv = 1.0f / s;
+  if (l == 0) scales[row] = s;
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = l + i * LPR;
+      if (c < pieces) q8_store<DT>(v[i], s, inv, fast, codes + base + 8 * c);
+    }
+  } else {
+    for (int c = l; c < pieces; c += LPR) {
+      const int64_t o = base + 8 * static_cast<int64_t>(c);
+      q8_store<DT>(q8_load<DT>(x, o), s, inv, fast, codes + o);
+    }
+  }
+}
+
+template <int DT, int LPR, int NV>
+static hipError_t q8_start(const void* x, int64_t rows, int cols, int8_t* codes, float* scales, hipStream_t stream) {
+  const int64_t blocks = (rows + 256 / LPR - 1) / (256 / LPR);
+  hipLaunchKernelGGL((k_int8_quantize<DT, LPR, NV>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, x, rows, cols,
+                     codes, scales);
+  return hipGetLastError();
+}
+
+// a wave per row up to 1024 values (2 pieces a lane), a workgroup above, to 16384
+// values in registers (8 pieces: 64 registers of float32)
+template <int DT>
+static hipError_t q8_launch(const void* x, int64_t rows, int cols, int8_t* codes, float* scales, hipStream_t stream) {
+  if (cols <= 512) return q8_start<DT, 64, 1>(x, rows, cols, codes, scales, stream);
+  if (cols <= 1024) return q8_start<DT, 64, 2>(x, rows, cols, codes, scales, stream);
+  if (cols <= 2048) return q8_start<DT, 256, 1>(x, rows, cols, codes, scales, stream);
+  if (cols <= 4096) return q8_start<DT, 256, 2>(x, rows, cols, codes, scales, stream);
+  if (cols <= 6144) return q8_start<DT, 256, 3>(x, rows, cols, codes, scales, stream);
+  if (cols <= 8192) return q8_start<DT, 256, 4>(x, rows, cols, codes, scales, stream);
+  if (cols <= 16384) return q8_start<DT, 256, 8>(x, rows, cols, codes, scales, stream);
+  return q8_start<DT, 256, 0>(x, rows, cols, codes, scales, stream);
 }
 
 hipError_t launch_int8_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int8_t* codes, float* scales,
                                 hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(rows));
-  if (dtype == 0) hipLaunchKernelGGL((k_int8_quantize<0>), grid, dim3(256), 0, stream, x, cols, codes, scales);
-  else hipLaunchKernelGGL((k_int8_quantize<1>), grid, dim3(256), 0, stream, x, cols, codes, scales);
-  return hipGetLastError();
+  const int c = static_cast<int>(cols);
+  return dtype == 0 ? q8_launch<0>(x, rows, c, codes, scales, stream) : q8_launch<1>(x, rows, c, codes, scales, stream);
 }
 
 hipError_t launch_tile_gemm_i8(const TileParams& p, int epilogue, hipStream_t stream) {

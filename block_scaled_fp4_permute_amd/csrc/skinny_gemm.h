@@ -1,0 +1,180 @@
+// The forward products (NT in tile_gemm.h) for few rows per expert: decode
+// steps down to a single token.  Bound by the weight bytes; with at most 16
+// rows a weight is used in one matrix instruction, so nothing is gained by
+// staging it in LDS: every lane loads its fragments straight from the row-major
+// weights (16 bytes; a wave's two loads of a piece cover 128 bytes of 16 rows).
+//
+// A task is 16 rows of an expert times WC x NB column tiles of 16 (gated: NB / 2
+// of gate and the same of up).  WK waves share a task's columns and take every
+// WK-th 128-byte piece of the reduction, so that together they read contiguous
+// memory and few rows still keep a chip's worth of loads in flight; their sums
+// meet in LDS and are added in the order of the waves.
+#pragma once
+
+#include "tile_gemm.h"
+
+namespace nvfp4 {
+
+constexpr int kSkPiece = 128;              // bytes of k per wave and turn: two matrix instructions
+constexpr int kSkTurns = 4;                // pieces loaded ahead
+
+template <int T, int EPI, int NB, int WK, int WC>
+__global__ __launch_bounds__(64 * WK * WC) void k_skinny_gemm(const TileParams p) {
+  using TT = TgType<T>;
+  using acc_t = typename TT::acc_t;
+  constexpr int EB = TT::bytes;
+  constexpr bool GATED = EPI == TG_OUT_GATED;
+  constexpr int COLS = 16 * (GATED ? NB / 2 : NB);          // output columns of a wave
+  __shared__ acc_t red[WK][WC][NB][64];
+  int e, m0, nt;
+  bool narrow;
+  {
+    GemmParams map{};
+    map.offsets = p.offsets;
+    map.E = p.E;
+    map.m_total = p.m_total;
+    map.n_tiles = p.n_tiles;
+    map.slots = 1 << 30;
+    if (!find_task<1, false, 0>(map, e, m0, nt, narrow)) return;
+  }
+  const int row0 = min(max(p.offsets[e], 0), p.m_total);
+  const int rows = min(16, min(max(p.offsets[e + 1], 0), p.m_total) - row0 - m0);
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wk = wave % WK, wc = wave / WK;
+  const int width = GATED ? p.N / 2 : p.N;                  // columns of the output
+  const int c0 = nt * (WC * COLS);                          // of the task
+  const int64_t kb = static_cast<int64_t>(p.K) * EB;        // bytes of a row
+  auto src_row = [&](int r) __attribute__((always_inline)) -> int64_t {
+    if (p.a_rows) {
+      r = p.a_rows[r];
+      r = (r >= 0 && r < p.src_rows) ? r : 0;
+    }
+    return r;
+  };
+  const uint8_t* a = static_cast<const uint8_t*>(p.a) + src_row(row0 + m0 + (lr < rows ? lr : 0)) * kb + 16 * lg;
+  const uint8_t* b[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const int c = min(c0 + wc * COLS + (j * 16) % COLS + lr, width - 1) + (j * 16 >= COLS ? width : 0);
+    b[j] = static_cast<const uint8_t*>(p.b) + (static_cast<int64_t>(e) * p.N + c) * kb + 16 * lg;
+  }
+  acc_t acc[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) acc[j] = acc_t{0, 0, 0, 0};
+  const int pieces = static_cast<int>((kb + kSkPiece - 1) / kSkPiece);
+  for (int q0 = wk; q0 < pieces; q0 += WK * kSkTurns) {
+    u32x4 fa[kSkTurns][2], fb[kSkTurns][NB][2];
+#pragma unroll
+    for (int i = 0; i < kSkTurns; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int64_t o = static_cast<int64_t>(q0 + i * WK) * kSkPiece + 64 * s;
+        const bool in = o + 16 * lg < kb;                   // zeros behind the end of the reduction
+        fa[i][s] = u32x4{0, 0, 0, 0};
+        if (in) fa[i][s] = *reinterpret_cast<const u32x4*>(a + o);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          fb[i][j][s] = u32x4{0, 0, 0, 0};
+          if (in) fb[i][j][s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b[j] + o));
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < kSkTurns; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[j] = TT::mfma(fb[i][j][s], fa[i][s], acc[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < NB; ++j) red[wk][wc][j][lane] = acc[j];
+  __syncthreads();
+
+  // one thread per 4 neighbouring columns of a row
+  constexpr int OT = GATED ? NB / 2 : NB;                   // output tiles of a wave
+  for (int o = threadIdx.x; o < WC * OT * 64; o += 64 * WK * WC) {
+    const int w = o / (OT * 64), j = (o / 64) % OT, l = o & 63;
+    const int r = l & 15;
+    const int c = c0 + w * COLS + 16 * j + 4 * (l >> 4);
+    if (r >= rows || c >= width) continue;
+    acc_t sv = red[0][w][j][l], sw = {0, 0, 0, 0};
+    if constexpr (GATED) sw = red[0][w][j + OT][l];
+#pragma unroll
+    for (int k = 1; k < WK; ++k) {
+      sv += red[k][w][j][l];
+      if constexpr (GATED) sw += red[k][w][j + OT][l];
+    }
+    float4v v, g;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[q] = static_cast<float>(sv[q]);
+      g[q] = static_cast<float>(sw[q]);
+    }
+    const int64_t orow = static_cast<int64_t>(row0) + m0 + r;
+    if constexpr (T == TG_I8) {
+      const float sa = p.sa[src_row(row0 + m0 + r)];
+      const float* sb = p.sb + static_cast<size_t>(e) * p.N + c;
+      v = v * (*reinterpret_cast<const float4v*>(sb) * sa);
+      if constexpr (GATED) g = g * (*reinterpret_cast<const float4v*>(sb + width) * sa);
+    }
+    if constexpr (GATED) {
+      if (p.gu) {
+        *reinterpret_cast<float4v*>(p.gu + orow * p.N + c) = v;
+        *reinterpret_cast<float4v*>(p.gu + orow * p.N + width + c) = g;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = tg_act(v[q], p.act) * g[q];
+    }
+    if constexpr (EPI == TG_OUT_F32)
+      *reinterpret_cast<float4v*>(static_cast<float*>(p.out) + orow * p.N + c) = v;
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + orow * width + c) = TT::pack(v);
+  }
+}
+
+template <int T, int EPI, int NB, int WK, int WC>
+static hipError_t sk_start(TileParams p, hipStream_t stream) {
+  const int width = EPI == TG_OUT_GATED ? p.N / 2 : p.N;
+  const int per = 16 * (EPI == TG_OUT_GATED ? NB / 2 : NB) * WC;
+  p.n_tiles = (width + per - 1) / per;
+  const int64_t chunks = p.m_total / 16 + (p.E < p.m_total ? p.E : p.m_total);
+  const int64_t blocks = (chunks * p.n_tiles + 7) / 8 * 8;
+  if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
+  if (blocks == 0) return hipSuccess;
+  hipLaunchKernelGGL((k_skinny_gemm<T, EPI, NB, WK, WC>), dim3(static_cast<unsigned>(blocks)), dim3(64 * WK * WC), 0, stream, p);
+  return hipGetLastError();
+}
+
+// 8 waves on one set of columns for long reductions; from 1 KB of a row down
+// (8 pieces) pairs of waves, so that no wave is without a piece
+template <int T, int EPI>
+static hipError_t sk_launch(const TileParams& p, hipStream_t stream) {
+  if (static_cast<int64_t>(p.K) * TgType<T>::bytes > 8 * kSkPiece) return sk_start<T, EPI, 2, 8, 1>(p, stream);
+  return sk_start<T, EPI, 2, 2, 4>(p, stream);
+}
+
+// ------------------------------------------------------------------ choice of the kernel
+template <int T, int L, int EPI>
+static hipError_t tg_launch(const TileParams& p, hipStream_t stream) {
+  if constexpr (L == TG_NT) {
+    // few rows in few tiles: the tile kernel would leave most of the chip idle
+    const int64_t bn = EPI == TG_OUT_GATED ? 64 : 128, width = EPI == TG_OUT_GATED ? p.N / 2 : p.N;
+    const int64_t experts = p.E < p.m_total ? p.E : p.m_total;
+    if (p.rows_hint <= 16 && experts * ((width + bn - 1) / bn) < 256) return sk_launch<T, EPI>(p, stream);
+  }
+  const int64_t r = L == TG_TN ? p.R : p.rows_hint;
+  if (r >= 192) return tg_start<T, L, EPI, 256, 256, 2, 4>(p, 1, stream);
+  return tg_start<T, L, EPI, 128, 128, 2, 2>(p, 2, stream);
+}
+
+template <int T>
+static hipError_t tg_launch16(const TileParams& p, int layout, int epilogue, hipStream_t stream) {
+  if (layout == TG_NT)
+    return epilogue == TG_OUT_GATED ? tg_launch<T, TG_NT, TG_OUT_GATED>(p, stream)
+           : epilogue == TG_OUT_F32 ? tg_launch<T, TG_NT, TG_OUT_F32>(p, stream)
+                                    : tg_launch<T, TG_NT, TG_OUT_16>(p, stream);
+  if (layout == TG_NN) return tg_launch<T, TG_NN, TG_OUT_16>(p, stream);
+  return tg_launch<T, TG_TN, TG_OUT_16>(p, stream);
+}
+
+}  // namespace nvfp4

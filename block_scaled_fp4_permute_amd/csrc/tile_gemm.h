@@ -15,6 +15,7 @@
 #pragma once
 
 #include <type_traits>
+#include <utility>
 
 #include "gemm_device.h"
 
@@ -66,6 +67,16 @@ struct TgType<TG_I8> {
   static __device__ __forceinline__ uint2 pack(const float4v& v) { return TgType<TG_BF16>::pack(v); }
 };
 
+// f(0) .. f(N - 1) with constants
+template <class F, int... I>
+__device__ __forceinline__ void tg_for_each(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void tg_for(F f) {
+  tg_for_each(f, std::make_integer_sequence<int, N>{});
+}
+
 // act(g) and its derivative, float32
 __device__ __forceinline__ float tg_act(float g, int act) {
   if (act == TG_ACT_SILU) return g / (1.0f + __expf(-g));
@@ -110,8 +121,9 @@ constexpr int kTgStep = 128;                // a K step: 128 bytes of each K-con
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 #define TG_LDS __attribute__((address_space(3)))
 
-// zeros for the parts of a step behind the end of the reduction
-__device__ const u32x4 tg_zero = {0, 0, 0, 0};
+// zeros for the parts of a step behind the end of the reduction (as wide as a
+// row of the widest K-major tile)
+__device__ const u32x4 tg_zero[32] = {};
 
 // The load is written as assembly because the compiler, which cannot tell
 // which stage a read touches, would wait for every load in flight before each
@@ -161,7 +173,7 @@ struct TgRows {
   }
   // left: bytes of the reduction from this step on
   __device__ __forceinline__ void issue(int i, int left, uint32_t lds_wave) {
-    tg_dma(ch16 < left ? p[i] : reinterpret_cast<const uint8_t*>(&tg_zero), lds_wave + i * TH * 16);
+    tg_dma(ch16 < left ? p[i] : reinterpret_cast<const uint8_t*>(tg_zero), lds_wave + i * TH * 16);
     p[i] += kTgStep;
   }
 };
@@ -176,28 +188,39 @@ struct TgCols {
   static constexpr int STEP = TH / PER;     // rows between the thread's loads
   static constexpr int ROWS = 64 / PER;     // rows of a wave's load
   static_assert(X >= 128 && STEP % 16 == 0, "the unit permutation repeats every 16 rows");
-  const uint8_t* p[N];                      // of the next step; gathered: p[0] is the thread's chunk of row 0
+  const uint8_t* p[N];                      // of the next step
   int64_t ld;                               // bytes of a row
   int k0;                                   // the thread's first row of a step
-  __device__ __forceinline__ void setup(const uint8_t* mem, int64_t ld_bytes, int c0, int cols, bool gathered) {
+  uint32_t col;                             // gathered: byte of the thread's chunk in the tile's row
+  __device__ __forceinline__ void setup(const uint8_t* mem, int64_t ld_bytes, int c0, int cols) {
     const int t = tg_thread();
     k0 = t / PER;
     const int f = (k0 & 3) + 4 * ((k0 >> 3) & 1);
-    const int c = c0 + 8 * ((t % PER) ^ ((COL ? 4 : 2) * f & (PER - 1)));
+    const int c = 8 * ((t % PER) ^ ((COL ? 4 : 2) * f & (PER - 1)));
     ld = ld_bytes;
-    p[0] = mem + 2 * static_cast<int64_t>(min(c, cols - 8));
-    if (!gathered) {
+    col = 2 * min(c, cols - 8 - c0);
 #pragma unroll
-      for (int i = N - 1; i >= 0; --i) p[i] = p[0] + (k0 + i * STEP) * ld;
-    }
+    for (int i = 0; i < N; ++i) p[i] = mem + 2 * static_cast<int64_t>(c0) + col + (k0 + i * STEP) * ld;
   }
   // left: rows of the reduction from this step on
   __device__ __forceinline__ void issue(int i, int left, uint32_t lds_wave) {
-    tg_dma(k0 < left - i * STEP ? p[i] : reinterpret_cast<const uint8_t*>(&tg_zero), lds_wave + i * TH * 16);
+    tg_dma(k0 < left - i * STEP ? p[i] : reinterpret_cast<const uint8_t*>(tg_zero), lds_wave + i * TH * 16);
     p[i] += 64 * ld;
   }
-  __device__ __forceinline__ void issue_row(int i, int left, int64_t source, uint32_t lds_wave) {
-    tg_dma(k0 < left - i * STEP ? p[0] + source * ld : reinterpret_cast<const uint8_t*>(&tg_zero), lds_wave + i * TH * 16);
+  // gathered: rows of the wave's load, from the tile's first column on
+  __device__ __forceinline__ void issue_rows(int i, const uint64_t (&src)[ROWS], uint32_t lds_wave) {
+    const int w = (threadIdx.x & 63) / PER;
+    uint32_t lo = static_cast<uint32_t>(src[0]), hi = static_cast<uint32_t>(src[0] >> 32);
+    tg_for<ROWS - 1>([&](auto ic) __attribute__((always_inline)) {
+      constexpr int q = decltype(ic)::value + 1;
+      // moved to vector registers here: a plain choice among the array's entries becomes a table in memory
+      uint32_t a, b;
+      asm("v_mov_b32 %0, %1" : "=v"(a) : "s"(static_cast<uint32_t>(src[q])));
+      asm("v_mov_b32 %0, %1" : "=v"(b) : "s"(static_cast<uint32_t>(src[q] >> 32)));
+      lo = w == q ? a : lo;
+      hi = w == q ? b : hi;
+    });
+    tg_dma(reinterpret_cast<const uint8_t*>((static_cast<uint64_t>(hi) << 32 | lo) + col), lds_wave + i * TH * 16);
   }
 };
 
@@ -346,7 +369,7 @@ __device__ __forceinline__ void tg_decode(const TileParams& p, const int* pre, i
 // products: in one burst they would hold up the products behind them.  A
 // finished tile is stored while the next one's loads are in flight.
 template <int T, int L, int EPI, int BM, int BN, int WR, int WC>
-__global__ __launch_bounds__(64 * WR * WC) void k_tile_gemm(const TileParams p) {
+__global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_tile_gemm(const TileParams p) {
   using TT = TgType<T>;
   using acc_t = typename TT::acc_t;
   constexpr int EB = TT::bytes;
@@ -364,7 +387,7 @@ __global__ __launch_bounds__(64 * WR * WC) void k_tile_gemm(const TileParams p) 
   constexpr int NR = Rows::N, NC = Cols::N;               // loads of a thread per step and operand
   constexpr int NX = RKM ? NR / 2 + NC / 2 : NC + NR / 2, NY = NR + NC - NX;
   static_assert(T != TG_I8 || L == TG_NT, "int8 has the forward product only");
-  static_assert(CT % (GATED ? 4 : 2) == 0 && RT % 2 == 0, "column tiles come in pairs, row tiles in halves");
+  static_assert(CT % 4 == 0 && RT % 2 == 0, "column tiles come in pairs, row tiles in halves");
   static_assert(RowsK::N == NR && ColsK::N == NC && NR % 2 == 0 && NC % 2 == 0, "halves of the loads");
   static_assert(RKM || Rows::STEP * WR * 2 <= BM, "a load holds rows of one half");
   constexpr int kMap = L == TG_TN ? 1 : kTgMaxExperts;
@@ -404,7 +427,7 @@ __global__ __launch_bounds__(64 * WR * WC) void k_tile_gemm(const TileParams p) 
     const uint8_t* Be = B;
     if constexpr (L != TG_TN) Be += static_cast<size_t>(pt.e) * p.N * p.K * EB;
     if constexpr (L == TG_TN) {
-      rk.setup(A + static_cast<int64_t>(pt.row0) * p.R * 2, static_cast<int64_t>(p.R) * 2, pt.m0, p.R, false);
+      rk.setup(A + static_cast<int64_t>(pt.row0) * p.R * 2, static_cast<int64_t>(p.R) * 2, pt.m0, p.R);
     } else {
       ra.setup([&](int r) __attribute__((always_inline)) {
         int q = pt.row0 + pt.m0 + (r < pt.rows ? r : 0);
@@ -422,23 +445,40 @@ __global__ __launch_bounds__(64 * WR * WC) void k_tile_gemm(const TileParams p) 
         return Be + static_cast<int64_t>(col) * p.K * EB;
       });
     else
-      ck.setup(Be, static_cast<int64_t>(p.N) * 2, c0, p.N, L == TG_TN);
+      ck.setup(Be, static_cast<int64_t>(p.N) * 2, c0, p.N);
   };
   const uint32_t lds0 = tg_lds_addr(lds) + wave * 1024;
-  int left = 0;                             // of the reduction from the loads' step on: bytes (K-contiguous) and rows
-  int left_k = 0;
-  int src[NC][L == TG_TN ? ColsK::ROWS : 1];  // TN: source rows of the wave's loads
-  auto open = [&]() __attribute__((always_inline)) {        // before a step's loads
-    left_k = pt.kt - ps * 64;
-    left = idle ? 0 : pt.kt * EB - ps * kTgStep;
-    if (idle) left_k = 0;
+  int left = 0, left_k = 0;                 // of the reduction from the loads' step on: bytes (K-contiguous) and rows
+  // TN: source rows of the wave's loads.  They are the same for half a wave, so
+  // scalar loads fetch them (a vector load would wait for all loads in flight),
+  // half a step before they are needed.
+  constexpr int W = L == TG_TN ? ColsK::ROWS : 1;
+  int raw[NC][W];
+  uint64_t src[NC][W];
+  auto fetch = [&]() __attribute__((always_inline)) {
     if constexpr (L == TG_TN) {
 #pragma unroll
       for (int j = 0; j < NC; ++j)
 #pragma unroll
-        for (int w = 0; w < ColsK::ROWS; ++w) {
-          const int k = pt.row0 + max(min(ps * 64 + wave * ColsK::ROWS + j * ColsK::STEP + w, pt.kt - 1), 0);
-          src[j][w] = p.a_rows && pt.kt > 0 ? ((tg_const_ints)(p.a_rows))[k] : k;
+        for (int w = 0; w < W; ++w) {
+          raw[j][w] = pt.row0 + max(min(ps * 64 + wave * W + j * ColsK::STEP + w, pt.kt - 1), 0);
+          if (p.a_rows && pt.kt > 0) raw[j][w] = ((tg_const_ints)(p.a_rows))[raw[j][w]];
+        }
+    }
+  };
+  auto open = [&]() __attribute__((always_inline)) {        // before a step's loads
+    left_k = idle ? 0 : pt.kt - ps * 64;
+    left = idle ? 0 : pt.kt * EB - ps * kTgStep;
+    if constexpr (L == TG_TN) {
+      const uint8_t* tile = B + static_cast<int64_t>(pt.nt) * BN * 2;
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          int r = __builtin_amdgcn_readfirstlane(raw[j][w]);
+          if (p.a_rows) r = valid_row(r);
+          const int k = wave * W + j * ColsK::STEP + w;
+          src[j][w] = reinterpret_cast<uint64_t>(k < left_k ? tile + static_cast<int64_t>(r) * p.N * 2 : reinterpret_cast<const uint8_t*>(tg_zero));
         }
     }
   };
@@ -452,11 +492,7 @@ __global__ __launch_bounds__(64 * WR * WC) void k_tile_gemm(const TileParams p) 
     } else if constexpr (L == TG_NN) {
       ck.issue(j, left_k, l + BM * kTgStep);
     } else {
-      int v = src[j][0];
-#pragma unroll
-      for (int w = 1; w < ColsK::ROWS; ++w) v = lane / (64 / ColsK::ROWS) == w ? src[j][w] : v;
-      if (p.a_rows) v = valid_row(v);
-      ck.issue_row(j, left_k, v, l + BM * kTgStep);
+      ck.issue_rows(j, src[j], l + BM * kTgStep);
     }
   };
   auto issue_x = [&](int q) __attribute__((always_inline)) {   // load q of X
@@ -491,16 +527,11 @@ __global__ __launch_bounds__(64 * WR * WC) void k_tile_gemm(const TileParams p) 
         pt.nsteps = 0;
       }
     }
+    fetch();
   };
 
   // ---- the products
-  acc_t acc[RT][CT];
-  auto clear = [&]() __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int j = 0; j < CT; ++j) acc[i][j] = acc_t{0, 0, 0, 0};
-  };
+  acc_t acc[RT][CT] = {};
   auto read_rows = [&](const uint8_t* stage, int s, int h, u32x4 (&f)[RH]) __attribute__((always_inline)) {
     tg_frags<RKM, false, BM, RH>(stage, wr * RT + h * RH, s, f);
   };
@@ -519,78 +550,144 @@ __global__ __launch_bounds__(64 * WR * WC) void k_tile_gemm(const TileParams p) 
       tg_frags<CKM, true, BN, CT>(c, wc * CT, s, f);
     }
   };
-  // the products of a unit, `loads` of load(0 ..) spread over them
-  auto unit = [&](int h, const u32x4 (&fc)[CT], const u32x4 (&fr)[RH], auto from, auto to, auto load) __attribute__((always_inline)) {
-    constexpr int F = decltype(from)::value, N = decltype(to)::value - F;
+  // the products of a unit; work(i) goes between those of row tile i and the next
+  auto unit = [&](int h, bool fresh, const u32x4 (&fc)[CT], const u32x4 (&fr)[RH], auto work) __attribute__((always_inline)) {
+    tg_for<RH>([&](auto ic) __attribute__((always_inline)) {
+      constexpr int i = decltype(ic)::value;
 #pragma unroll
-    for (int i = 0; i < RH; ++i) {
-#pragma unroll
-      for (int j = 0; j < CT; ++j) acc[h * RH + i][j] = TT::mfma(fc[j], fr[i], acc[h * RH + i][j]);
-      if constexpr (N > 0) {
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int q = F + i * N / RH; q < F + (i + 1) * N / RH; ++q) load(q);
-      }
-    }
+      for (int j = 0; j < CT; ++j)
+        acc[h * RH + i][j] = TT::mfma(fc[j], fr[i], fresh ? acc_t{0, 0, 0, 0} : acc[h * RH + i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+      work(ic);
+    });
     __builtin_amdgcn_sched_barrier(0);
   };
   TgTask ct = {};                           // their task
 
-  // lane: output row lr of a 16-row tile, 8 columns from 8 lg of a pair of column tiles
-  auto store = [&]() __attribute__((always_inline)) {
-    const int lr = tg_thread() & 15, lg = (tg_thread() >> 4) & 3;
-    const int c0 = ct.nt * (GATED ? BN / 2 : BN) + (GATED ? BN / 2 : BN) / WC * wc + 8 * lg;
+  // ---- the results
+  // A lane holds output row lr of a 16-row tile, 8 columns from 8 lg of each pair
+  // of column tiles.  Lanes lr and lr ^ 8 exchange 16 bytes, so that a store
+  // instruction writes whole 128-byte lines: 8 rows of 8 neighbouring pieces.
+  // The stores are non-temporal: no product of the call reads them, and the
+  // operands keep the caches (weight gradients of 64 rows an expert: 543 -> 452 us).
+  constexpr int OB = EPI == TG_OUT_F32 ? 4 : 2;             // bytes of a result
+  constexpr int PAIRB = OB == 2 ? 32 : 4;                   // columns from a lane's piece a to its piece b
+  uint8_t* obase = static_cast<uint8_t*>(p.out);            // the wave's first result (gated: of h)
+  float* gbase = p.gu;                      // gated: of the gate pre-activations
+  uint32_t ooff = 0, goff = 0;              // bytes from there to the lane's piece of row tile 0
+  int orows = 0;                            // rows from row lr & 7 on; none where the piece lies behind the last column
+  int orows2 = 0;                           // float32: of the second pair
+  constexpr int kNoRows = -BM;
+  bool full = false;                        // every lane of the wave has all its results
+  auto aim = [&]() __attribute__((always_inline)) {         // before the first store of task ct
+    const int t = tg_thread(), lg = (t >> 4) & 3;
+    const int width = GATED ? half : p.N;
+    const int wave_cols = (GATED ? BN / 2 : BN) / WC;
+    const int c0 = ct.nt * (GATED ? BN / 2 : BN) + wave_cols * wc;
+    const int rows = ct.rows - (BM / WR) * wr;              // of the wave
+    const int64_t row0 = (L == TG_TN ? static_cast<int64_t>(ct.e) * p.R : static_cast<int64_t>(ct.row0)) + ct.m0 + (BM / WR) * wr;
+    full = rows >= BM / WR && c0 + wave_cols <= width;
+    if constexpr (GATED) {
+      const int c = 8 * lg;
+      obase = static_cast<uint8_t*>(p.out) + (row0 * half + c0) * 2;
+      ooff = ((t & 15) * half + c) * 2;
+      orows = c0 + c < width ? rows - (t & 7) : kNoRows;
+      if (p.gu) gbase = p.gu + row0 * p.N + c0;
+      goff = ((t & 7) * p.N + c + (t & 8 ? 4 : 0)) * 4;
+    } else {
+      const int c = 8 * lg + (t & 8 ? PAIRB : 0);
+      obase = static_cast<uint8_t*>(p.out) + (row0 * p.N + c0) * OB;
+      ooff = ((t & 7) * p.N + c) * OB;
+      orows = c0 + c < width ? rows - (t & 7) : kNoRows;
+      if constexpr (OB == 4) orows2 = c0 + c + 32 < width ? orows : kNoRows;
+    }
+  };
+  auto put = [&](uint8_t* base, uint32_t off, int64_t ld, int rows, u32x4 a, u32x4 b) __attribute__((always_inline)) {
+    const bool up = threadIdx.x & 8;        // the lanes that store the pieces b
+    u32x4 lo, hi;
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int r = (BM / WR) * wr + 16 * i + lr;
-      if (r >= ct.rows) continue;
-      const int64_t orow = L == TG_TN ? static_cast<int64_t>(ct.e) * p.R + ct.m0 + r : static_cast<int64_t>(ct.row0) + ct.m0 + r;
-      float sa = 1.0f;
-      if constexpr (T == TG_I8) sa = p.sa[p.a_rows ? valid_row(p.a_rows[ct.row0 + ct.m0 + r]) : ct.row0 + ct.m0 + r];
+    for (int d = 0; d < 4; ++d) {
+      const uint32_t x = __builtin_amdgcn_update_dpp(0u, up ? a[d] : b[d], 0x128, 0xF, 0xF, false);   // from lane lr ^ 8
+      lo[d] = up ? x : a[d];                // rows 0 .. 7
+      hi[d] = up ? b[d] : x;                // rows 8 .. 15
+    }
+    if (rows > 0) __builtin_nontemporal_store(lo, reinterpret_cast<u32x4*>(base + off));
+    if (rows > 8) __builtin_nontemporal_store(hi, reinterpret_cast<u32x4*>(base + 8 * ld + off));
+  };
+  constexpr int kStores = GATED ? 1 : 2 * CT / (OB == 2 ? 4 : 2);   // store instructions of a row tile, at least
+  float row_scale[T == TG_I8 ? RT : 1];     // INT8: scales of the lane's rows and columns
+  float4v col_scale[T == TG_I8 ? CT : 1];
+  auto scales = [&]() __attribute__((always_inline)) {
+    if constexpr (T == TG_I8) {
+      const int t = tg_thread();
+      const int c0 = ct.nt * (GATED ? BN / 2 : BN) + (GATED ? BN / 2 : BN) / WC * wc + 8 * ((t >> 4) & 3);
+      const float* sb = p.sb + static_cast<size_t>(ct.e) * p.N;
+      const int width = GATED ? half : p.N;
 #pragma unroll
-      for (int j = 0; j < (GATED ? CT / 2 : CT); j += 2) {
-        const int c = c0 + 16 * j;
-        if (c >= (GATED ? half : p.N)) continue;
+      for (int i = 0; i < RT; ++i) {
+        const int r = ct.row0 + ct.m0 + min((BM / WR) * wr + 16 * i + (t & 15), ct.rows - 1);
+        row_scale[i] = p.sa[p.a_rows ? valid_row(p.a_rows[r]) : r];
+      }
+#pragma unroll
+      for (int j = 0; j < CT; ++j) {
+        // scales behind the last column are not there; those results are not stored
+        const int q = GATED ? j % (CT / 2) : j;
+        const int c = min(c0 + 16 * (q & ~1), width - 8) + 4 * (q & 1) + (GATED && j >= CT / 2 ? half : 0);
+        col_scale[j] = *reinterpret_cast<const float4v*>(sb + c);
+      }
+    }
+  };
+  auto store = [&](int i) __attribute__((always_inline)) {  // row tile i
+    // 8 float32 values of column tiles j and j + 1, scaled
+    auto pair = [&](int j, float4v (&v)[2]) __attribute__((always_inline)) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[b][q] = static_cast<float>(acc[i][j + b][q]);
+        if constexpr (T == TG_I8) v[b] = v[b] * (col_scale[j + b] * row_scale[i]);
+      }
+    };
+    auto packed = [&](const float4v (&v)[2]) __attribute__((always_inline)) {
+      const uint2 a = TT::pack(v[0]), b = TT::pack(v[1]);
+      return u32x4{a.x, a.y, b.x, b.y};
+    };
+    if constexpr (GATED) {
+      static_assert(CT == 4, "one pair of h columns");
+      float4v g[2], w[2];
+      pair(0, g);
+      pair(2, w);
+      const int64_t ld = static_cast<int64_t>(p.N) * 4;
+      if (p.gu) {
+        uint8_t* o = reinterpret_cast<uint8_t*>(gbase) + 16 * i * ld;
+        put(o, goff, ld, orows - 16 * i, __builtin_bit_cast(u32x4, g[0]), __builtin_bit_cast(u32x4, g[1]));
+        put(o + 4 * static_cast<int64_t>(half), goff, ld, orows - 16 * i, __builtin_bit_cast(u32x4, w[0]), __builtin_bit_cast(u32x4, w[1]));
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) g[b][q] = tg_act(g[b][q], p.act) * w[b][q];
+      if (orows - static_cast<int>(threadIdx.x & 8) > 16 * i) *reinterpret_cast<u32x4*>(obase + 16 * i * static_cast<int64_t>(half) * 2 + ooff) = packed(g);
+    } else {
+      const int64_t ld = static_cast<int64_t>(p.N) * OB;
+      uint8_t* o = obase + 16 * i * ld;
+#pragma unroll
+      for (int j = 0; j < CT; j += OB == 2 ? 4 : 2) {
         float4v v[2], w[2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[b][q] = static_cast<float>(acc[i][j + b][q]);
-          if constexpr (T == TG_I8) v[b] = v[b] * (*reinterpret_cast<const float4v*>(p.sb + static_cast<size_t>(ct.e) * p.N + c + 4 * b) * sa);
-        }
-        if constexpr (GATED) {
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) w[b][q] = static_cast<float>(acc[i][j + b + CT / 2][q]);
-            if constexpr (T == TG_I8)
-              w[b] = w[b] * (*reinterpret_cast<const float4v*>(p.sb + static_cast<size_t>(ct.e) * p.N + half + c + 4 * b) * sa);
-            if (p.gu) {
-              *reinterpret_cast<float4v*>(p.gu + orow * p.N + c + 4 * b) = v[b];
-              *reinterpret_cast<float4v*>(p.gu + orow * p.N + half + c + 4 * b) = w[b];
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v[b][q] = tg_act(v[b][q], p.act) * w[b][q];
-          }
-        }
-        if constexpr (EPI == TG_OUT_F32) {
-          float* o = static_cast<float*>(p.out) + orow * p.N + c;
-          *reinterpret_cast<float4v*>(o) = v[0];
-          *reinterpret_cast<float4v*>(o + 4) = v[1];
+        pair(j, v);
+        if constexpr (OB == 4) {
+          put(o + 16 * j * OB, ooff, ld, (j ? orows2 : orows) - 16 * i, __builtin_bit_cast(u32x4, v[0]), __builtin_bit_cast(u32x4, v[1]));
         } else {
-          const uint2 a = TT::pack(v[0]), b = TT::pack(v[1]);
-          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + orow * (GATED ? half : p.N) + c) = u32x4{a.x, a.y, b.x, b.y};
+          pair(j + 2, w);
+          put(o + 16 * j * OB, ooff, ld, orows - 16 * i, packed(v), packed(w));
         }
       }
     }
   };
 
-  constexpr std::integral_constant<int, 0> i0;
-  constexpr std::integral_constant<int, NX / 2> ix1;
-  constexpr std::integral_constant<int, NX> ix;
-  constexpr std::integral_constant<int, NY> iy;
+  // ---- the stream
   tg_decode<L, BM, SK>(p, pre, u, 0, pt);
   begin();
+  fetch();
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     open();
@@ -602,47 +699,135 @@ __global__ __launch_bounds__(64 * WR * WC) void k_tile_gemm(const TileParams p) 
     advance();
   }
   tg_wait<NX + NY>();
-  clear();
   u32x4 c0[CT], c1[CT], ra_[RH], rb_[RH];
   read_cols(lds, 0, c0);
   read_rows(lds, 0, 0, ra_);
   __builtin_amdgcn_sched_barrier(0);
-  int cs = 0;                               // step of the task
-  for (int cg = 0;; ++cg) {
+
+  // A meeting lets the loads of one step stay in flight, and the stores of a
+  // full tile that are younger than the loads it waits for (`stores`: of so
+  // many row tiles), since memory operations complete in order.
+  auto meet = [&](bool may, auto stores) __attribute__((always_inline)) {
+    constexpr int S = decltype(stores)::value * kStores;
+    if constexpr (S > 0) {
+      if (may) {
+        tg_wait<NX + NY + S>();
+        return;
+      }
+    }
+    tg_wait<NX + NY>();
+  };
+  // INT8 results need scales from memory, whose loads wait for all others: they
+  // are stored at the end of the task in one go.  So are TN's, whose stores
+  // among the products cost more registers than there are.
+  constexpr bool kSpread = T != TG_I8 && L != TG_TN;
+  // One step.  FIRST of a task: the products start from zero, and the h = 1 half
+  // of the task before is stored before unit 2 overwrites it.  LAST: the h = 0
+  // half, complete after unit 1, is stored.
+  bool after_first = false;                 // the step follows a task's first one
+  auto step = [&](int cg, auto first, auto last) __attribute__((always_inline)) {
+    constexpr bool FIRST = decltype(first)::value, LAST = decltype(last)::value;
     const uint8_t* cur = lds + (cg & 1) * kStage;
     const uint8_t* nxt = lds + ((cg + 1) & 1) * kStage;
-    open();
+    // loads FROM .. FROM + N - 1, shared out over the row tiles of a unit
+    auto part = [&](auto ic, auto nc, auto fc, auto load) __attribute__((always_inline)) {
+      constexpr int i = decltype(ic)::value, n = decltype(nc)::value, from = decltype(fc)::value;
+      tg_for<(i + 1) * n / RH - i * n / RH>([&](auto k) __attribute__((always_inline)) {
+        load(from + i * n / RH + decltype(k)::value);
+      });
+    };
+    const std::integral_constant<int, 0> i0;
+    const std::integral_constant<int, NX / 2> nx1;
+    const std::integral_constant<int, NX - NX / 2> nx2;
+    const std::integral_constant<int, NY> ny;
+    auto none = [](auto) __attribute__((always_inline)) {};
+    // half a half's row tiles (q = 0, 1) are stored at every other row tile of a unit
+    auto store_half = [&](int h, int q, auto ic) __attribute__((always_inline)) {
+      constexpr int i = decltype(ic)::value;
+      if constexpr (kSpread && (i & 1)) store(h * RH + q * (RH / 2) + i / 2);
+    };
+    constexpr int kHalf = kSpread ? RH : 0;
     if constexpr (!RKM) {
       read_cols(cur, 1, c1);
       read_rows(cur, 1, 0, rb_);
-      unit(0, c0, ra_, i0, i0, issue_x);
-      tg_wait<NX + NY>();
+      unit(0, FIRST, c0, ra_, [&](auto i) __attribute__((always_inline)) { if constexpr (FIRST) store_half(1, 0, i); });
+      if constexpr (FIRST) meet(full, std::integral_constant<int, 3 * kHalf / 2>{});
+      else meet(full && after_first, std::integral_constant<int, kHalf>{});
+      open();
       read_rows(cur, 0, 1, ra_);
-      unit(0, c1, rb_, i0, ix1, issue_x);
+      unit(0, false, c1, rb_, [&](auto i) __attribute__((always_inline)) {
+        part(i, nx1, i0, issue_x);
+        if constexpr (FIRST) store_half(1, 1, i);
+      });
+      if constexpr (LAST) aim();
       read_rows(cur, 1, 1, rb_);
-      unit(1, c0, ra_, ix1, ix, issue_x);
+      unit(1, FIRST, c0, ra_, [&](auto i) __attribute__((always_inline)) {
+        part(i, nx2, nx1, issue_x);
+        if constexpr (LAST) store_half(0, 0, i);
+      });
+      if constexpr (FIRST) meet(full, std::integral_constant<int, 3 * kHalf / 2>{});
+      else meet(LAST && full, std::integral_constant<int, LAST ? kHalf / 2 : 0>{});
+      read_cols(nxt, 0, c0);
+      read_rows(nxt, 0, 0, ra_);
+      unit(1, false, c1, rb_, [&](auto i) __attribute__((always_inline)) {
+        part(i, ny, i0, issue_y);
+        if constexpr (LAST) store_half(0, 1, i);
+      });
     } else {
       read_rows(cur, 0, 1, rb_);
-      unit(0, c0, ra_, i0, i0, issue_x);
-      tg_wait<NX + NY>();
+      unit(0, false, c0, ra_, none);
+      meet(false, std::integral_constant<int, 0>{});
+      open();
       read_cols(cur, 1, c1);
       read_rows(cur, 1, 0, ra_);
-      unit(1, c0, rb_, i0, ix1, issue_x);
+      unit(1, false, c0, rb_, [&](auto i) __attribute__((always_inline)) { part(i, nx1, i0, issue_x); });
       read_rows(cur, 1, 1, rb_);
-      unit(0, c1, ra_, ix1, ix, issue_x);
+      unit(0, false, c1, ra_, [&](auto i) __attribute__((always_inline)) { part(i, nx2, nx1, issue_x); });
+      meet(false, std::integral_constant<int, 0>{});
+      read_cols(nxt, 0, c0);
+      read_rows(nxt, 0, 0, ra_);
+      unit(1, false, c1, rb_, [&](auto i) __attribute__((always_inline)) { part(i, ny, i0, issue_y); });
     }
-    tg_wait<NX + NY>();
-    read_cols(nxt, 0, c0);
-    read_rows(nxt, 0, 0, ra_);
-    unit(1, c1, rb_, i0, iy, issue_y);
-    if (++cs == ct.nsteps) {
-      store();
+    after_first = FIRST;
+  };
+  const std::true_type yes;
+  const std::false_type no;
+  if constexpr (kSpread) {
+    for (int cg = 0;;) {
+      step(cg, yes, no);
+      ++cg;
+      advance();
+      for (int cs = 2; cs < ct.nsteps; ++cs, ++cg) {
+        step(cg, no, no);
+        advance();
+      }
+      step(cg, no, yes);
+      ++cg;
       if (idle) break;
       ct = pt;
-      cs = 0;
-      clear();
+      advance();
     }
-    advance();
+#pragma unroll
+    for (int i = 0; i < RH; ++i) store(RH + i);
+  } else {
+    int cs = 0;                             // step of the task
+    for (int cg = 0;; ++cg) {
+      step(cg, no, no);
+      if (++cs == ct.nsteps) {
+        aim();
+        scales();
+#pragma unroll
+        for (int i = 0; i < RT; ++i) store(i);
+        if (idle) break;
+        ct = pt;
+        cs = 0;
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int j = 0; j < CT; ++j) acc[i][j] = acc_t{0, 0, 0, 0};
+      }
+      advance();
+    }
   }
   tg_wait<0>();                             // nothing may land in LDS after the workgroup is gone
 }
@@ -667,23 +852,6 @@ static hipError_t tg_start(TileParams p, int per_cu, hipStream_t stream) {
   const int64_t blocks = min(int64_t(256) * per_cu, (tasks + 7) / 8 * 8);
   hipLaunchKernelGGL((k_tile_gemm<T, L, EPI, BM, BN, WR, WC>), dim3(static_cast<unsigned>(blocks)), dim3(64 * WR * WC), 0, stream, p);
   return hipGetLastError();
-}
-
-template <int T, int L, int EPI>
-static hipError_t tg_launch(const TileParams& p, hipStream_t stream) {
-  const int64_t r = L == TG_TN ? p.R : p.rows_hint;
-  if (r >= 192) return tg_start<T, L, EPI, 256, 256, 2, 4>(p, 1, stream);
-  return tg_start<T, L, EPI, 128, 128, 2, 2>(p, 2, stream);
-}
-
-template <int T>
-static hipError_t tg_launch16(const TileParams& p, int layout, int epilogue, hipStream_t stream) {
-  if (layout == TG_NT)
-    return epilogue == TG_OUT_GATED ? tg_launch<T, TG_NT, TG_OUT_GATED>(p, stream)
-           : epilogue == TG_OUT_F32 ? tg_launch<T, TG_NT, TG_OUT_F32>(p, stream)
-                                    : tg_launch<T, TG_NT, TG_OUT_16>(p, stream);
-  if (layout == TG_NN) return tg_launch<T, TG_NN, TG_OUT_16>(p, stream);
-  return tg_launch<T, TG_TN, TG_OUT_16>(p, stream);
 }
 
 }  // namespace nvfp4
