@@ -4,11 +4,12 @@
 // staging it in LDS: every lane loads its fragments straight from the row-major
 // weights (16 bytes; a wave's two loads of a piece cover 128 bytes of 16 rows).
 //
-// A task is 16 rows of an expert times WC x NB column tiles of 16 (gated: NB / 2
-// of gate and the same of up).  WK waves share a task's columns and take every
-// WK-th 128-byte piece of the reduction, so that together they read contiguous
-// memory and few rows still keep a chip's worth of loads in flight; their sums
-// meet in LDS and are added in the order of the waves.
+// A task is 16 rows of an expert times WC column tiles of 16 weight rows (gated:
+// 8 of gate and the 8 of up for the same columns, so that one token's experts
+// make twice as many tasks).  WK waves share a tile and take every WK-th 128-byte
+// piece of the reduction, so that together they read contiguous memory and few
+// rows still keep a chip's worth of loads in flight; their sums meet in LDS and
+// are added in the order of the waves.
 #pragma once
 
 #include "tile_gemm.h"
@@ -16,16 +17,16 @@
 namespace nvfp4 {
 
 constexpr int kSkPiece = 128;              // bytes of k per wave and turn: two matrix instructions
-constexpr int kSkTurns = 4;                // pieces loaded ahead
+constexpr int kSkTurns = 6;                // pieces loaded ahead
 
-template <int T, int EPI, int NB, int WK, int WC>
-__global__ __launch_bounds__(64 * WK * WC) void k_skinny_gemm(const TileParams p) {
+template <int T, int EPI, int WK, int WC>
+__global__ __launch_bounds__(64 * WK * WC) __attribute__((amdgpu_waves_per_eu(2))) void k_skinny_gemm(const TileParams p) {
   using TT = TgType<T>;
   using acc_t = typename TT::acc_t;
   constexpr int EB = TT::bytes;
   constexpr bool GATED = EPI == TG_OUT_GATED;
-  constexpr int COLS = 16 * (GATED ? NB / 2 : NB);          // output columns of a wave
-  __shared__ acc_t red[WK][WC][NB][64];
+  constexpr int COLS = GATED ? 8 : 16;                      // output columns of a tile
+  __shared__ acc_t red[WK][WC][64];
   int e, m0, nt;
   bool narrow;
   {
@@ -53,56 +54,45 @@ __global__ __launch_bounds__(64 * WK * WC) void k_skinny_gemm(const TileParams p
     return r;
   };
   const uint8_t* a = static_cast<const uint8_t*>(p.a) + src_row(row0 + m0 + (lr < rows ? lr : 0)) * kb + 16 * lg;
-  const uint8_t* b[NB];
-#pragma unroll
-  for (int j = 0; j < NB; ++j) {
-    const int c = min(c0 + wc * COLS + (j * 16) % COLS + lr, width - 1) + (j * 16 >= COLS ? width : 0);
-    b[j] = static_cast<const uint8_t*>(p.b) + (static_cast<int64_t>(e) * p.N + c) * kb + 16 * lg;
-  }
-  acc_t acc[NB];
-#pragma unroll
-  for (int j = 0; j < NB; ++j) acc[j] = acc_t{0, 0, 0, 0};
+  const int wrow = min(c0 + wc * COLS + (lr % COLS), width - 1) + (lr >= COLS ? width : 0);
+  const uint8_t* b = static_cast<const uint8_t*>(p.b) + (static_cast<int64_t>(e) * p.N + wrow) * kb + 16 * lg;
+  acc_t acc = {0, 0, 0, 0};
   const int pieces = static_cast<int>((kb + kSkPiece - 1) / kSkPiece);
   for (int q0 = wk; q0 < pieces; q0 += WK * kSkTurns) {
-    u32x4 fa[kSkTurns][2], fb[kSkTurns][NB][2];
+    u32x4 fa[kSkTurns][2], fb[kSkTurns][2];
 #pragma unroll
     for (int i = 0; i < kSkTurns; ++i)
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const int64_t o = static_cast<int64_t>(q0 + i * WK) * kSkPiece + 64 * s;
         const bool in = o + 16 * lg < kb;                   // zeros behind the end of the reduction
+        fb[i][s] = u32x4{0, 0, 0, 0};
+        if (in) fb[i][s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b + o));
         fa[i][s] = u32x4{0, 0, 0, 0};
         if (in) fa[i][s] = *reinterpret_cast<const u32x4*>(a + o);
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          fb[i][j][s] = u32x4{0, 0, 0, 0};
-          if (in) fb[i][j][s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b[j] + o));
-        }
       }
 #pragma unroll
     for (int i = 0; i < kSkTurns; ++i)
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int j = 0; j < NB; ++j) acc[j] = TT::mfma(fb[i][j][s], fa[i][s], acc[j]);
+      for (int s = 0; s < 2; ++s) acc = TT::mfma(fb[i][s], fa[i][s], acc);
   }
-#pragma unroll
-  for (int j = 0; j < NB; ++j) red[wk][wc][j][lane] = acc[j];
+  red[wk][wc][lane] = acc;
   __syncthreads();
 
-  // one thread per 4 neighbouring columns of a row
-  constexpr int OT = GATED ? NB / 2 : NB;                   // output tiles of a wave
-  for (int o = threadIdx.x; o < WC * OT * 64; o += 64 * WK * WC) {
-    const int w = o / (OT * 64), j = (o / 64) % OT, l = o & 63;
+  // one thread per 4 neighbouring columns of a row; gated: lane groups 0, 1 hold
+  // gate columns, 2, 3 the same of up
+  for (int o = threadIdx.x; o < WC * 64; o += 64 * WK * WC) {
+    const int w = o >> 6, l = o & 63;
+    if (GATED && l >= 32) continue;
     const int r = l & 15;
-    const int c = c0 + w * COLS + 16 * j + 4 * (l >> 4);
+    const int c = c0 + w * COLS + 4 * (l >> 4);
     if (r >= rows || c >= width) continue;
-    acc_t sv = red[0][w][j][l], sw = {0, 0, 0, 0};
-    if constexpr (GATED) sw = red[0][w][j + OT][l];
+    acc_t sv = red[0][w][l], sw = {0, 0, 0, 0};
+    if constexpr (GATED) sw = red[0][w][l + 32];
 #pragma unroll
     for (int k = 1; k < WK; ++k) {
-      sv += red[k][w][j][l];
-      if constexpr (GATED) sw += red[k][w][j + OT][l];
+      sv += red[k][w][l];
+      if constexpr (GATED) sw += red[k][w][l + 32];
     }
     float4v v, g;
 #pragma unroll
@@ -132,25 +122,25 @@ __global__ __launch_bounds__(64 * WK * WC) void k_skinny_gemm(const TileParams p
   }
 }
 
-template <int T, int EPI, int NB, int WK, int WC>
+template <int T, int EPI, int WK, int WC>
 static hipError_t sk_start(TileParams p, hipStream_t stream) {
   const int width = EPI == TG_OUT_GATED ? p.N / 2 : p.N;
-  const int per = 16 * (EPI == TG_OUT_GATED ? NB / 2 : NB) * WC;
+  const int per = (EPI == TG_OUT_GATED ? 8 : 16) * WC;
   p.n_tiles = (width + per - 1) / per;
   const int64_t chunks = p.m_total / 16 + (p.E < p.m_total ? p.E : p.m_total);
   const int64_t blocks = (chunks * p.n_tiles + 7) / 8 * 8;
   if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
   if (blocks == 0) return hipSuccess;
-  hipLaunchKernelGGL((k_skinny_gemm<T, EPI, NB, WK, WC>), dim3(static_cast<unsigned>(blocks)), dim3(64 * WK * WC), 0, stream, p);
+  hipLaunchKernelGGL((k_skinny_gemm<T, EPI, WK, WC>), dim3(static_cast<unsigned>(blocks)), dim3(64 * WK * WC), 0, stream, p);
   return hipGetLastError();
 }
 
-// 8 waves on one set of columns for long reductions; from 1 KB of a row down
-// (8 pieces) pairs of waves, so that no wave is without a piece
+// 8 waves on one tile for long reductions; from 1 KB of a row down (8 pieces)
+// pairs of waves
 template <int T, int EPI>
 static hipError_t sk_launch(const TileParams& p, hipStream_t stream) {
-  if (static_cast<int64_t>(p.K) * TgType<T>::bytes > 8 * kSkPiece) return sk_start<T, EPI, 2, 8, 1>(p, stream);
-  return sk_start<T, EPI, 2, 2, 4>(p, stream);
+  if (static_cast<int64_t>(p.K) * TgType<T>::bytes > 8 * kSkPiece) return sk_start<T, EPI, 8, 1>(p, stream);
+  return sk_start<T, EPI, 2, 4>(p, stream);
 }
 
 // ------------------------------------------------------------------ choice of the kernel

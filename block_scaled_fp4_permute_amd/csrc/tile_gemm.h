@@ -10,8 +10,7 @@
 // An operand stored [x][k] is K-contiguous, one stored [k][x] is K-major.
 //
 // The matrix instruction gets C as its first operand and R as its second, so a
-// lane's four results are four columns of one output row; two column tiles are
-// interleaved so that they make eight neighbouring ones (one 16-byte store).
+// lane's four results are four neighbouring columns of one output row.
 #pragma once
 
 #include <type_traits>
@@ -105,19 +104,11 @@ constexpr int kTgStep = 128;                // a K step: 128 bytes of each K-con
 // bytes in lane order, so the layout's permutation is made by choosing which
 // 16 bytes of memory each lane fetches.
 //
-// Fragments are tiles of 16 rows or columns.  Row tile i holds rows 16 i + n.
-// Column tiles 2 i and 2 i + 1 share 32 columns: tile 2 i + b holds columns
-// 32 i + 8 (n / 4) + 4 b + n % 4, which puts eight neighbouring columns into
-// one lane's results of the pair.
-//
-// K-contiguous: row r is 128 bytes, its 16-byte chunk ch at chunk ch ^ f(r), f =
-//   (r >> 1) & 7 for rows, ((r >> 1) & 1) + 2 ((r >> 3) & 3) for columns: the 16
-//   rows that a fragment read touches at one chunk cover all 64 banks.
-// K-major: row k is 2 X bytes.  Rows operand: its 32-byte unit u (16 values) at
-//   unit u ^ f(k), f(k) = (k & 3) + 4 ((k >> 3) & 1): the 8 rows that half a
-//   wave's transposing read touches (4 of lane groups 2q and 2q + 1 each) lie in
-//   distinct units.  Columns operand: a fragment takes every other 8 bytes of a
-//   64-byte unit, so there the 64-byte units are permuted.
+// K-contiguous: row r is 128 bytes, its 16-byte chunk ch at chunk ch ^ ((r >> 1) & 7):
+//   the 16 rows that a fragment read touches at one chunk cover all 64 banks.
+// K-major: row k is 2 X bytes, its 32-byte unit u (16 values) at unit u ^ f(k),
+//   f(k) = (k & 3) + 4 ((k >> 3) & 1): the 8 rows that half a wave's transposing
+//   read touches (4 of lane groups 2q and 2q + 1 each) lie in distinct units.
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 #define TG_LDS __attribute__((address_space(3)))
 
@@ -151,23 +142,18 @@ __device__ __forceinline__ int tg_thread() {
   return t;
 }
 
-template <bool COL>
-__device__ __forceinline__ int tg_chunk_perm(int r) {
-  return COL ? ((r >> 1) & 1) + 2 * ((r >> 3) & 3) : (r >> 1) & 7;
-}
-
 // K-contiguous tile of X rows: thread t fetches one chunk of rows t / 8 + i TH / 8
-template <int X, int TH, bool COL>
+template <int X, int TH>
 struct TgRows {
   static constexpr int N = X * 8 / TH;
   static constexpr int STEP = TH / 8;       // rows between the thread's loads
-  static_assert(STEP % 32 == 0, "the chunk permutation repeats every 32 rows");
+  static_assert(STEP % 16 == 0, "the chunk permutation repeats every 16 rows");
   const uint8_t* p[N];                      // of the next step
   int ch16;                                 // byte of the thread's chunk in the step
   template <class F>                        // row_ptr(r): first byte of the operand row of tile row r (any row for a dead one)
   __device__ __forceinline__ void setup(F row_ptr) {
     const int t = tg_thread(), r = t >> 3;
-    ch16 = 16 * ((t & 7) ^ tg_chunk_perm<COL>(r));
+    ch16 = 16 * ((t & 7) ^ ((r >> 1) & 7));
 #pragma unroll
     for (int i = 0; i < N; ++i) p[i] = row_ptr(r + i * STEP) + ch16;
   }
@@ -181,7 +167,7 @@ struct TgRows {
 // K-major tile of X columns of 2 bytes: thread t fetches one chunk of rows
 // t / (X / 8) + i TH / (X / 8).  Columns at or behind `cols` repeat the last
 // chunk (their results are not stored).
-template <int X, int TH, bool COL>
+template <int X, int TH>
 struct TgCols {
   static constexpr int PER = X / 8;         // chunks of a row
   static constexpr int N = 64 * PER / TH;
@@ -196,7 +182,7 @@ struct TgCols {
     const int t = tg_thread();
     k0 = t / PER;
     const int f = (k0 & 3) + 4 * ((k0 >> 3) & 1);
-    const int c = 8 * ((t % PER) ^ ((COL ? 4 : 2) * f & (PER - 1)));
+    const int c = 8 * ((t % PER) ^ (2 * f));
     ld = ld_bytes;
     col = 2 * min(c, cols - 8 - c0);
 #pragma unroll
@@ -224,34 +210,21 @@ struct TgCols {
   }
 };
 
-// NT fragments of a tile from fragment t0 on: lane (lg, lr) holds entry lr of
-// each, 16 bytes of k from 16 lg (+ 64 with sub-step 1)
-template <bool KM, bool COL, int X, int NT>
-__device__ __forceinline__ void tg_frags(const uint8_t* tile, int t0, int s, u32x4 (&f)[NT]) {
+// NT fragments (16 rows or columns each) of a tile from fragment t0 on: lane
+// (lg, lr) holds entry lr of each, 16 bytes of k from 16 lg (+ 64 with sub-step 1)
+template <bool KM, int X, int NT>
+__device__ __forceinline__ void tg_frags(const uint8_t* tile, int t0, int s, u32x4* f) {
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   if constexpr (!KM) {
-    const int r = COL ? 8 * (lr >> 2) + (lr & 3) : lr;       // row of the lane in tile t0 (an even one)
-    if constexpr (COL) {
-      // tile 2 i + b: rows 32 i + r + 4 b, the same permutation for both (bits 1, 3 and 4 of r)
-      const uint8_t* b = tile + t0 * 16 * kTgStep + r * kTgStep + 16 * ((4 * s + lg) ^ tg_chunk_perm<true>(r));
+    const uint8_t* b = tile + t0 * 16 * kTgStep + lr * kTgStep + 16 * ((4 * s + lg) ^ (lr >> 1));
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-        f[i] = *reinterpret_cast<const u32x4*>(b + ((i >> 1) * 32 + (i & 1) * 4) * kTgStep);
-    } else {
-      const uint8_t* b = tile + t0 * 16 * kTgStep + r * kTgStep + 16 * ((4 * s + lg) ^ tg_chunk_perm<false>(r));
-#pragma unroll
-      for (int i = 0; i < NT; ++i) f[i] = *reinterpret_cast<const u32x4*>(b + i * 16 * kTgStep);
-    }
+    for (int i = 0; i < NT; ++i) f[i] = *reinterpret_cast<const u32x4*>(b + i * 16 * kTgStep);
   } else {
     const int perm = (lr >> 2) + 4 * (lg & 1);
-    const uint8_t* b = tile + (32 * s + 8 * lg + (lr >> 2)) * 2 * X;
+    const uint8_t* b = tile + (32 * s + 8 * lg + (lr >> 2)) * 2 * X + 8 * (lr & 3);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const uint8_t* q;
-      if constexpr (COL)
-        q = b + 64 * ((((t0 + i) >> 1) ^ perm) & (X / 32 - 1)) + 16 * (lr & 3) + 8 * (i & 1);
-      else
-        q = b + 32 * (((t0 + i) ^ perm) & (X / 16 - 1)) + 8 * (lr & 3);
+      const uint8_t* q = b + 32 * ((t0 + i) ^ perm);
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TG_LDS s16x4*)(q));
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TG_LDS s16x4*)(q + 4 * 2 * X));
       const uint2 l = __builtin_bit_cast(uint2, lo), h = __builtin_bit_cast(uint2, hi);
@@ -303,26 +276,19 @@ __device__ __forceinline__ int tg_prefix(const TileParams& p, int* pre) {
   return __builtin_amdgcn_readfirstlane(pre[0]);
 }
 
+// task (c, nt): row chunk c of all experts' chunks (TN: row tile c), column tile
+// nt.  Inside an expert, groups of 4 chunks run column tile by column tile.
 template <int L, int BM, int SK>
-__device__ __forceinline__ void tg_decode(const TileParams& p, const int* pre, int u, int e_from, TgTask& t) {
+__device__ __forceinline__ void tg_decode(const TileParams& p, const int* pre, int c, int nt, TgTask& t) {
   const tg_const_ints off = (tg_const_ints)(p.offsets);
+  int q, nc;                               // chunk of its expert, chunks of the expert
   if constexpr (L == TG_TN) {
-    const int per = p.r_tiles * p.n_tiles;
-    t.e = u / per;
-    const int v = u - t.e * per;
-    // groups of 4 row tiles, column tile by column tile
-    const int grp = v / (4 * p.n_tiles);
-    const int gq = min(4, p.r_tiles - 4 * grp);
-    const int w = v - 4 * grp * p.n_tiles;
-    t.m0 = (4 * grp + w % gq) * BM;
-    t.nt = w / gq;
-    t.row0 = min(max(off[t.e], 0), p.m_total);
-    t.kt = max(min(max(off[t.e + 1], 0), p.m_total) - t.row0, 0);
-    t.rows = min(BM, p.R - t.m0);
+    t.e = c / p.r_tiles;
+    q = c - t.e * p.r_tiles;
+    nc = p.r_tiles;
   } else {
     const int lane = threadIdx.x & 63;
-    const int c = u / p.n_tiles;
-    int e = e_from & ~63;                  // the experts whose chunks all lie before c, counted 64 at a time
+    int e = t.e & ~63;                     // the experts whose chunks all lie before c, counted 64 at a time
     for (;;) {
       const bool past = e + lane + 1 < p.E && pre[e + lane + 1] <= c;
       const int n = __popcll(__ballot(past));
@@ -330,19 +296,20 @@ __device__ __forceinline__ void tg_decode(const TileParams& p, const int* pre, i
       if (n < 64) break;
     }
     t.e = __builtin_amdgcn_readfirstlane(e);
-    t.row0 = min(max(off[t.e], 0), p.m_total);
-    const int Me = min(max(off[t.e + 1], 0), p.m_total) - t.row0;
-    const int nc = (Me + BM - 1) / BM;
-    // inside an expert, groups of 4 chunks run column tile by column tile
-    const int v = u - (t.e ? __builtin_amdgcn_readfirstlane(pre[t.e]) : 0) * p.n_tiles;
-    const int grp = v / (4 * p.n_tiles);
-    const int gq = max(1, min(4, nc - 4 * grp));
-    const int w = v - 4 * grp * p.n_tiles;
-    t.m0 = (4 * grp + w % gq) * BM;
-    t.nt = w / gq;
-    t.rows = min(BM, Me - t.m0);
-    t.kt = p.K;
+    q = c - (t.e ? __builtin_amdgcn_readfirstlane(pre[t.e]) : 0);
   }
+  t.row0 = min(max(off[t.e], 0), p.m_total);
+  const int Me = max(min(max(off[t.e + 1], 0), p.m_total) - t.row0, 0);
+  if constexpr (L != TG_TN) nc = (Me + BM - 1) / BM;
+  const int w = (q & 3) * p.n_tiles + nt, left = nc - (q & ~3);
+  int m = w >> 2, r = w & 3;               // w by the chunks of the group
+  if (left == 1) { m = w; r = 0; }
+  if (left == 2) { m = w >> 1; r = w & 1; }
+  if (left == 3) { m = w / 3; r = w - 3 * m; }
+  t.m0 = ((q & ~3) + r) * BM;
+  t.nt = m;
+  t.rows = min(BM, (L == TG_TN ? p.R : Me) - t.m0);
+  t.kt = L == TG_TN ? Me : p.K;
   t.nsteps = max(2, (t.kt + SK - 1) / SK);
 }
 
@@ -380,14 +347,14 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   constexpr int RT = BM / WR / 16, CT = BN / WC / 16;     // 16-row and 16-column tiles of a wave
   constexpr int RH = RT / 2;
   constexpr int kStage = (BM + BN) * kTgStep;
-  using Rows = TgRows<BM, TH, false>;
-  using Cols = TgRows<BN, TH, true>;
-  using RowsK = TgCols<BM, TH, false>;
-  using ColsK = TgCols<BN, TH, true>;
+  using Rows = TgRows<BM, TH>;
+  using Cols = TgRows<BN, TH>;
+  using RowsK = TgCols<BM, TH>;
+  using ColsK = TgCols<BN, TH>;
   constexpr int NR = Rows::N, NC = Cols::N;               // loads of a thread per step and operand
   constexpr int NX = RKM ? NR / 2 + NC / 2 : NC + NR / 2, NY = NR + NC - NX;
   static_assert(T != TG_I8 || L == TG_NT, "int8 has the forward product only");
-  static_assert(CT % 4 == 0 && RT % 2 == 0, "column tiles come in pairs, row tiles in halves");
+  static_assert(CT == 4 && RT % 4 == 0, "the store's exchange takes 4 column tiles; row tiles are stored in quarters");
   static_assert(RowsK::N == NR && ColsK::N == NC && NR % 2 == 0 && NC % 2 == 0, "halves of the loads");
   static_assert(RKM || Rows::STEP * WR * 2 <= BM, "a load holds rows of one half");
   constexpr int kMap = L == TG_TN ? 1 : kTgMaxExperts;
@@ -403,6 +370,9 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   const int stride = gridDim.x >> 3;
   int u = lo + (blockIdx.x >> 3);
   if (u >= hi) return;
+  // task u as (chunk, column tile), and the step to the workgroup's next one
+  int uc = u / p.n_tiles, un = u - uc * p.n_tiles;
+  const int dc = stride / p.n_tiles, dn = stride - dc * p.n_tiles;
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -518,9 +488,15 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
     ++pg;
     if (++ps == pt.nsteps) {
       u += stride;
+      uc += dc;
+      un += dn;
+      if (un >= p.n_tiles) {
+        un -= p.n_tiles;
+        ++uc;
+      }
       ps = 0;
       if (u < hi) {
-        tg_decode<L, BM, SK>(p, pre, u, pt.e, pt);
+        tg_decode<L, BM, SK>(p, pre, uc, un, pt);
         begin();
       } else {
         idle = true;
@@ -533,21 +509,15 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   // ---- the products
   acc_t acc[RT][CT] = {};
   auto read_rows = [&](const uint8_t* stage, int s, int h, u32x4 (&f)[RH]) __attribute__((always_inline)) {
-    tg_frags<RKM, false, BM, RH>(stage, wr * RT + h * RH, s, f);
+    tg_frags<RKM, BM, RH>(stage, wr * RT + h * RH, s, f);
   };
   auto read_cols = [&](const uint8_t* stage, int s, u32x4 (&f)[CT]) __attribute__((always_inline)) {
     const uint8_t* c = stage + BM * kTgStep;
     if constexpr (GATED) {                  // the gate tiles, then the same columns of up
-      u32x4 g[CT / 2], v[CT / 2];
-      tg_frags<CKM, true, BN, CT / 2>(c, wc * (CT / 2), s, g);
-      tg_frags<CKM, true, BN, CT / 2>(c, BN / 32 + wc * (CT / 2), s, v);
-#pragma unroll
-      for (int j = 0; j < CT / 2; ++j) {
-        f[j] = g[j];
-        f[CT / 2 + j] = v[j];
-      }
+      tg_frags<CKM, BN, CT / 2>(c, wc * (CT / 2), s, f);
+      tg_frags<CKM, BN, CT / 2>(c, BN / 32 + wc * (CT / 2), s, f + CT / 2);
     } else {
-      tg_frags<CKM, true, BN, CT>(c, wc * CT, s, f);
+      tg_frags<CKM, BN, CT>(c, wc * CT, s, f);
     }
   };
   // the products of a unit; work(i) goes between those of row tile i and the next
@@ -565,18 +535,19 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   TgTask ct = {};                           // their task
 
   // ---- the results
-  // A lane holds output row lr of a 16-row tile, 8 columns from 8 lg of each pair
-  // of column tiles.  Lanes lr and lr ^ 8 exchange 16 bytes, so that a store
-  // instruction writes whole 128-byte lines: 8 rows of 8 neighbouring pieces.
+  // A lane holds output row lr of a 16-row tile, 4 columns from 4 lg of each column
+  // tile.  Lane groups exchange 16-bit results of two tiles, so that each lane
+  // has 8 neighbouring columns, and lanes lr and lr ^ 8 exchange 16 bytes, so that
+  // a store instruction writes whole 128-byte lines: 8 rows of 8 pieces.
   // The stores are non-temporal: no product of the call reads them, and the
   // operands keep the caches (weight gradients of 64 rows an expert: 543 -> 452 us).
   constexpr int OB = EPI == TG_OUT_F32 ? 4 : 2;             // bytes of a result
-  constexpr int PAIRB = OB == 2 ? 32 : 4;                   // columns from a lane's piece a to its piece b
+  constexpr int PAIRB = OB == 2 ? 32 : 16;                  // columns from a lane's piece a to its piece b
   uint8_t* obase = static_cast<uint8_t*>(p.out);            // the wave's first result (gated: of h)
   float* gbase = p.gu;                      // gated: of the gate pre-activations
   uint32_t ooff = 0, goff = 0;              // bytes from there to the lane's piece of row tile 0
-  int orows = 0;                            // rows from row lr & 7 on; none where the piece lies behind the last column
-  int orows2 = 0;                           // float32: of the second pair
+  int orows = 0;                            // rows from the lane's on; none where its piece lies behind the last column
+  int orows2 = 0;                           // float32: the same for the second pair; gated: for the pre-activations
   constexpr int kNoRows = -BM;
   bool full = false;                        // every lane of the wave has all its results
   auto aim = [&]() __attribute__((always_inline)) {         // before the first store of task ct
@@ -587,15 +558,17 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
     const int rows = ct.rows - (BM / WR) * wr;              // of the wave
     const int64_t row0 = (L == TG_TN ? static_cast<int64_t>(ct.e) * p.R : static_cast<int64_t>(ct.row0)) + ct.m0 + (BM / WR) * wr;
     full = rows >= BM / WR && c0 + wave_cols <= width;
+    const int piece = 16 * (lg & 1) + 4 * (lg & 2);         // the lane's 8 columns of a pair of tiles after the exchange
     if constexpr (GATED) {
-      const int c = 8 * lg;
+      const int c = piece, cg = 4 * lg + (t & 8 ? 16 : 0);
       obase = static_cast<uint8_t*>(p.out) + (row0 * half + c0) * 2;
       ooff = ((t & 15) * half + c) * 2;
-      orows = c0 + c < width ? rows - (t & 7) : kNoRows;
+      orows = c0 + c < width ? rows - (t & 15) : kNoRows;
       if (p.gu) gbase = p.gu + row0 * p.N + c0;
-      goff = ((t & 7) * p.N + c + (t & 8 ? 4 : 0)) * 4;
+      goff = ((t & 7) * p.N + cg) * 4;
+      orows2 = c0 + cg < width ? rows - (t & 7) : kNoRows;
     } else {
-      const int c = 8 * lg + (t & 8 ? PAIRB : 0);
+      const int c = (OB == 2 ? piece : 4 * lg) + (t & 8 ? PAIRB : 0);
       obase = static_cast<uint8_t*>(p.out) + (row0 * p.N + c0) * OB;
       ooff = ((t & 7) * p.N + c) * OB;
       orows = c0 + c < width ? rows - (t & 7) : kNoRows;
@@ -620,7 +593,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   auto scales = [&]() __attribute__((always_inline)) {
     if constexpr (T == TG_I8) {
       const int t = tg_thread();
-      const int c0 = ct.nt * (GATED ? BN / 2 : BN) + (GATED ? BN / 2 : BN) / WC * wc + 8 * ((t >> 4) & 3);
+      const int c0 = ct.nt * (GATED ? BN / 2 : BN) + (GATED ? BN / 2 : BN) / WC * wc + 4 * ((t >> 4) & 3);
       const float* sb = p.sb + static_cast<size_t>(ct.e) * p.N;
       const int width = GATED ? half : p.N;
 #pragma unroll
@@ -632,60 +605,58 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
       for (int j = 0; j < CT; ++j) {
         // scales behind the last column are not there; those results are not stored
         const int q = GATED ? j % (CT / 2) : j;
-        const int c = min(c0 + 16 * (q & ~1), width - 8) + 4 * (q & 1) + (GATED && j >= CT / 2 ? half : 0);
+        const int c = min(c0 + 16 * q, width - 4) + (GATED && j >= CT / 2 ? half : 0);
         col_scale[j] = *reinterpret_cast<const float4v*>(sb + c);
       }
     }
   };
   auto store = [&](int i) __attribute__((always_inline)) {  // row tile i
-    // 8 float32 values of column tiles j and j + 1, scaled
-    auto pair = [&](int j, float4v (&v)[2]) __attribute__((always_inline)) {
+    auto value = [&](int j) __attribute__((always_inline)) {  // of column tile j, scaled
+      float4v v;
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[b][q] = static_cast<float>(acc[i][j + b][q]);
-        if constexpr (T == TG_I8) v[b] = v[b] * (col_scale[j + b] * row_scale[i]);
-      }
+      for (int q = 0; q < 4; ++q) v[q] = static_cast<float>(acc[i][j][q]);
+      if constexpr (T == TG_I8) v = v * (col_scale[j] * row_scale[i]);
+      return v;
     };
-    auto packed = [&](const float4v (&v)[2]) __attribute__((always_inline)) {
-      const uint2 a = TT::pack(v[0]), b = TT::pack(v[1]);
-      return u32x4{a.x, a.y, b.x, b.y};
+    // 16-bit results of two column tiles as 8 neighbouring columns: lane groups 0
+    // and 2 give their second tile to 1 and 3 and take those's first
+    auto packed = [&](const float4v& v, const float4v& w) __attribute__((always_inline)) {
+      const uint2 a = TT::pack(v), b = TT::pack(w);
+      const auto x = __builtin_amdgcn_permlane16_swap(a.x, b.x, false, false);
+      const auto y = __builtin_amdgcn_permlane16_swap(a.y, b.y, false, false);
+      return u32x4{x[0], y[0], x[1], y[1]};
     };
     if constexpr (GATED) {
-      static_assert(CT == 4, "one pair of h columns");
-      float4v g[2], w[2];
-      pair(0, g);
-      pair(2, w);
+      static_assert(CT == 4, "two tiles of h");
+      float4v g[2] = {value(0), value(1)}, w[2] = {value(2), value(3)};
       const int64_t ld = static_cast<int64_t>(p.N) * 4;
       if (p.gu) {
         uint8_t* o = reinterpret_cast<uint8_t*>(gbase) + 16 * i * ld;
-        put(o, goff, ld, orows - 16 * i, __builtin_bit_cast(u32x4, g[0]), __builtin_bit_cast(u32x4, g[1]));
-        put(o + 4 * static_cast<int64_t>(half), goff, ld, orows - 16 * i, __builtin_bit_cast(u32x4, w[0]), __builtin_bit_cast(u32x4, w[1]));
+        put(o, goff, ld, orows2 - 16 * i, __builtin_bit_cast(u32x4, g[0]), __builtin_bit_cast(u32x4, g[1]));
+        put(o + 4 * static_cast<int64_t>(half), goff, ld, orows2 - 16 * i, __builtin_bit_cast(u32x4, w[0]), __builtin_bit_cast(u32x4, w[1]));
       }
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int q = 0; q < 4; ++q) g[b][q] = tg_act(g[b][q], p.act) * w[b][q];
-      if (orows - static_cast<int>(threadIdx.x & 8) > 16 * i) *reinterpret_cast<u32x4*>(obase + 16 * i * static_cast<int64_t>(half) * 2 + ooff) = packed(g);
+      const u32x4 h = packed(g[0], g[1]);
+      if (orows > 16 * i) *reinterpret_cast<u32x4*>(obase + 16 * i * static_cast<int64_t>(half) * 2 + ooff) = h;
     } else {
       const int64_t ld = static_cast<int64_t>(p.N) * OB;
       uint8_t* o = obase + 16 * i * ld;
+      if constexpr (OB == 4) {
 #pragma unroll
-      for (int j = 0; j < CT; j += OB == 2 ? 4 : 2) {
-        float4v v[2], w[2];
-        pair(j, v);
-        if constexpr (OB == 4) {
-          put(o + 16 * j * OB, ooff, ld, (j ? orows2 : orows) - 16 * i, __builtin_bit_cast(u32x4, v[0]), __builtin_bit_cast(u32x4, v[1]));
-        } else {
-          pair(j + 2, w);
-          put(o + 16 * j * OB, ooff, ld, orows - 16 * i, packed(v), packed(w));
-        }
+        for (int j = 0; j < CT; j += 2)
+          put(o + 16 * j * OB, ooff, ld, (j ? orows2 : orows) - 16 * i, __builtin_bit_cast(u32x4, value(j)),
+              __builtin_bit_cast(u32x4, value(j + 1)));
+      } else {
+        put(o, ooff, ld, orows - 16 * i, packed(value(0), value(1)), packed(value(2), value(3)));
       }
     }
   };
 
   // ---- the stream
-  tg_decode<L, BM, SK>(p, pre, u, 0, pt);
+  tg_decode<L, BM, SK>(p, pre, uc, un, pt);
   begin();
   fetch();
 #pragma unroll

@@ -25,7 +25,9 @@ Choices:
                    two-launch regimes the combine kernel follows on the stream.
 
 Buffers are allocated once per layer object (torch device memory); a forward
-allocates nothing.
+allocates nothing.  Beside MoELayer: MXMoELayer, FP8MoELayer and INT8MoELayer
+on the other number formats, MoELayer16 on 16-bit weights with the experts'
+gradients.
 """
 from __future__ import annotations
 
@@ -386,3 +388,147 @@ class FP8MoELayer:
         moe_unpermute_combine(self.y2, r.perm_of_assignment, r.topk_w, T, k, out=self.out, stream=stream)
         mark(6)
         return self.out
+
+
+# ------------------------------------------------------------------ INT8 variant
+@dataclass
+class INT8ExpertWeights:
+    """Per-expert INT8 weights with one float32 scale per output channel:
+    gate_up codes [E, 2I, H] and scales [E, 2I], down [E, H, I] and [E, H],
+    row-major (no packed form)."""
+    gu: "object"
+    dn: "object"
+
+    @property
+    def E(self):
+        return self.gu.codes.shape[0]
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in (self.gu.codes, self.gu.scales, self.dn.codes, self.dn.scales))
+
+
+def quantize_expert_weights_int8(w_gu: torch.Tensor, w_dn: torch.Tensor) -> INT8ExpertWeights:
+    """Quantise float32/bf16 weights [E, 2I, H] and [E, H, I] to INT8 on the GPU."""
+    from . import int8_quantize
+    return INT8ExpertWeights(int8_quantize(w_gu.contiguous()), int8_quantize(w_dn.contiguous()))
+
+
+class INT8MoELayer:
+    """Preallocated INT8 MoE layer for T tokens, reusing the routing, permutation
+    and combine of the NVFP4 layer: route + permute, per-token quantisation of
+    x, gate_up grouped GEMM (A gathered through the permutation) with SwiGLU to
+    bf16 h rows, per-row quantisation of h, down grouped GEMM (bf16 rows),
+    weighted gather combine.  The scale of an h row spans all its I values,
+    which the column tiles of gate_up share out, so h goes through memory in
+    bf16 between the two."""
+
+    def __init__(self, T: int, H: int, I: int, E: int, k: int, device):
+        from . import INT8Tensor
+        self.T, self.H, self.I, self.E, self.k = T, H, I, E, k
+        dev = torch.device(device)
+        i32 = dict(dtype=torch.int32, device=dev)
+        f32 = dict(dtype=torch.float32, device=dev)
+        i8 = dict(dtype=torch.int8, device=dev)
+        bf = dict(dtype=torch.bfloat16, device=dev)
+        M = T * k
+        self.routing = Routing(torch.empty((T, k), **i32), torch.empty((T, k), **f32), torch.empty(E, **i32),
+                               torch.empty(E + 1, **i32), torch.empty(M, **i32), torch.empty(M, **i32),
+                               torch.empty(M, **f32))
+        self.route_ws = torch.empty(max(16, lib().moe_route_permute_workspace_size(T, E, k)), dtype=torch.uint8,
+                                    device=dev)
+        self.xq = INT8Tensor(torch.empty((T, H), **i8), torch.empty(T, **f32))
+        self.h = torch.empty((M, I), **bf)
+        self.hq = INT8Tensor(torch.empty((M, I), **i8), torch.empty(M, **f32))
+        self.y2 = torch.empty((M, H), **bf)
+        self.out = torch.empty((T, H), **bf)
+
+    def forward(self, logits: torch.Tensor, x: torch.Tensor, w: INT8ExpertWeights, stream=None,
+                marks=None) -> torch.Tensor:
+        """One layer step; ``marks``: optional 7 events recorded before routing
+        and after each stage (route, quantise x, gate_up + SwiGLU, quantise h,
+        down, combine)."""
+        from . import EPI_SWIGLU_BF16, int8_grouped_gemm, int8_quantize
+        T, k, M = self.T, self.k, self.T * self.k
+
+        def mark(i):
+            if marks is not None and marks[i] is not None:
+                marks[i].record(stream)
+
+        mark(0)
+        r = moe_route_permute(logits, k, out=self.routing, workspace=self.route_ws, stream=stream)
+        mark(1)
+        int8_quantize(x, out=self.xq, stream=stream)
+        mark(2)
+        int8_grouped_gemm(self.xq, w.gu, r.offsets, m_total=M, a_rows=r.perm_src_token, epilogue=EPI_SWIGLU_BF16,
+                          out=self.h, stream=stream)
+        mark(3)
+        int8_quantize(self.h, out=self.hq, stream=stream)
+        mark(4)
+        int8_grouped_gemm(self.hq, w.dn, r.offsets, m_total=M, epilogue=EPI_BF16, out=self.y2, stream=stream)
+        mark(5)
+        moe_unpermute_combine(self.y2, r.perm_of_assignment, r.topk_w, T, k, out=self.out, stream=stream)
+        mark(6)
+        return self.out
+
+
+# ------------------------------------------------------------------ 16-bit experts
+class MoELayer16:
+    """Preallocated MoE layer for T tokens on bfloat16 (or float16) expert
+    weights, row-major [E, 2I, H] and [E, H, I]: the form they are trained in
+    before quantize_expert_weights*.  forward: route + permute, gated block
+    (rows gathered through the permutation), down product, weighted gather
+    combine (bf16 weights; with float16 ones use expert_rows).  expert_rows and
+    expert_rows_backward are the experts alone, on rows in expert order, with
+    the gradients of x (per token) and of both weights; the weighting of the
+    rows by topk_w and its gradient stay with the caller's loss."""
+
+    def __init__(self, T: int, H: int, I: int, E: int, k: int, device, dtype=torch.bfloat16, activation: int = 0):
+        self.T, self.H, self.I, self.E, self.k = T, H, I, E, k
+        self.dtype, self.activation = dtype, activation
+        dev = torch.device(device)
+        i32 = dict(dtype=torch.int32, device=dev)
+        f32 = dict(dtype=torch.float32, device=dev)
+        M = T * k
+        self.routing = Routing(torch.empty((T, k), **i32), torch.empty((T, k), **f32), torch.empty(E, **i32),
+                               torch.empty(E + 1, **i32), torch.empty(M, **i32), torch.empty(M, **i32),
+                               torch.empty(M, **f32))
+        self.route_ws = torch.empty(max(16, lib().moe_route_permute_workspace_size(T, E, k)), dtype=torch.uint8,
+                                    device=dev)
+        self.h = torch.empty((M, I), dtype=dtype, device=dev)
+        self.y2 = torch.empty((M, H), dtype=dtype, device=dev)
+        self.out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+
+    def route(self, logits: torch.Tensor, stream=None) -> Routing:
+        return moe_route_permute(logits, self.k, out=self.routing, workspace=self.route_ws, stream=stream)
+
+    def forward(self, logits: torch.Tensor, x: torch.Tensor, w_gu: torch.Tensor, w_dn: torch.Tensor,
+                stream=None) -> torch.Tensor:
+        """One layer step, bf16 [T, H]."""
+        r = self.route(logits, stream)
+        self.expert_rows(x, w_gu, w_dn, stream=stream)
+        return moe_unpermute_combine(self.y2, r.perm_of_assignment, r.topk_w, self.T, self.k, out=self.out,
+                                     stream=stream)
+
+    def expert_rows(self, x: torch.Tensor, w_gu: torch.Tensor, w_dn: torch.Tensor, gu: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+        """y [T*k, H] of the routing made last (unweighted, in expert order); gu: float32
+        [T*k, 2I] for the pre-activations that expert_rows_backward needs."""
+        from . import moe_gated_ffn, moe_grouped_gemm
+        r, M = self.routing, self.T * self.k
+        moe_gated_ffn(x, w_gu, r.offsets, m_total=M, a_rows=r.perm_src_token, activation=self.activation, out=self.h,
+                      gu=gu, stream=stream)
+        return moe_grouped_gemm(self.h, w_dn, r.offsets, m_total=M, out=self.y2, stream=stream)
+
+    def expert_rows_backward(self, dy: torch.Tensor, gu: torch.Tensor, x: torch.Tensor, w_gu: torch.Tensor,
+                             w_dn: torch.Tensor, stream=None):
+        """Gradients from dy [T*k, H] of the last expert_rows call: (dx, dw_gu,
+        dw_dn).  dx [T, H] sums each token's rows in bf16; with float16 weights
+        dx is the rows [T*k, H] themselves."""
+        from . import moe_gated_ffn_backward, moe_grouped_gemm_backward
+        r = self.routing
+        dh, dw_dn = moe_grouped_gemm_backward(dy, self.h, w_dn, r.offsets, stream=stream)
+        dx, dw_gu = moe_gated_ffn_backward(dh, gu, x, w_gu, r.offsets, a_rows=r.perm_src_token,
+                                           activation=self.activation, stream=stream)
+        if self.dtype == torch.bfloat16:
+            dx = moe_unpermute_combine(dx, r.perm_of_assignment, None, self.T, self.k, stream=stream)
+        return dx, dw_gu, dw_dn
