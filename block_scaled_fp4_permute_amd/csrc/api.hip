@@ -726,10 +726,11 @@ hipError_t launch16(int32_t dtype, const nvfp4::TileParams& p, int layout, int e
 }
 
 // layouts and epilogues of tile_gemm.h
-enum : int { L_NT = 0, L_NN = 1, L_TN = 2, O_16 = 0, O_F32 = 1, O_GATED = 2 };
+enum : int { L_NT = 0, L_NN = 1, L_TN = 2, L_TC = 3, O_16 = 0, O_F32 = 1, O_GATED = 2 };
 
-// da = dy b and db = dy^T a of one grouped product: dy [m_total, n], b [E, n, k]
-int product_grad(const char* fn, int32_t dtype, const void* dy, const void* a, const int32_t* a_rows, int64_t rows_total,
+// da = dy b and db = dy^T a of one grouped product: dy [m_total, n], b [E, n, k];
+// dy_t (nullable): dy transposed, [n, ld], for db
+int product_grad(const char* fn, int32_t dtype, const void* dy, const void* dy_t, int64_t ld, const void* a, const int32_t* a_rows, int64_t rows_total,
                  const void* b, const int32_t* offsets, int32_t E, int32_t n, int32_t k, int64_t m_total, int32_t hint,
                  void* da, void* db, hipStream_t s) {
   nvfp4::TileParams p{};
@@ -747,13 +748,14 @@ int product_grad(const char* fn, int32_t dtype, const void* dy, const void* a, c
     if (err != hipSuccess) return hip_status(err, fn);
   }
   if (db) {
+    p.a = dy_t ? dy_t : dy;
     p.b = a;
-    p.K = 0;
+    p.K = static_cast<int>(ld);
     p.R = n;
     p.a_rows = a_rows;
     p.src_rows = static_cast<int>(rows_total);
     p.out = db;
-    const hipError_t err = launch16(dtype, p, L_TN, O_16, s);
+    const hipError_t err = launch16(dtype, p, dy_t ? L_TC : L_TN, O_16, s);
     if (err != hipSuccess) return hip_status(err, fn);
   }
   return ok();
@@ -799,7 +801,8 @@ size_t moe_gated_ffn_backward_workspace_size(int32_t E, int32_t H, int32_t I, in
   if (E <= 0 || E > 4096 || H <= 0 || I <= 0 || m_total < 0 || H % 8 != 0 || I % 8 != 0 || m_total >= (int64_t(1) << 31) ||
       I > (1 << 25))
     return 0;
-  return static_cast<size_t>(m_total > 0 ? m_total : 1) * 2 * static_cast<size_t>(I) * 2;   // dg and du in 16 bits
+  // dg and du in 16 bits, by rows and transposed
+  return (static_cast<size_t>(m_total) + nvfp4::gated_grad_ld(m_total, E)) * 2 * static_cast<size_t>(I) * 2;
 }
 
 int moe_gated_ffn_backward(const nvfp4moe_gated_grad_args* a, void* workspace, size_t workspace_bytes, void* stream) {
@@ -822,14 +825,18 @@ int moe_gated_ffn_backward(const nvfp4moe_gated_grad_args* a, void* workspace, s
     return fail(NVFP4MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes, need);
   if (!aligned(workspace, 256)) return fail(NVFP4MOE_ERR_INVALID, "%s: workspace not 256-byte aligned", fn);
   const hipStream_t s = static_cast<hipStream_t>(stream);
+  uint16_t* dgu = static_cast<uint16_t*>(workspace);
+  uint16_t* dgu_t = dgu + a->m_total * 2 * a->I;            // 16-byte aligned: I is a multiple of 8
+  const int64_t ld = nvfp4::gated_grad_ld(a->m_total, a->E);
+  if (ld >= (int64_t(1) << 31)) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: m_total + 64 E reaches 2^31", fn);
   if (a->m_total > 0) {
     const int st = debug_plain(fn, a->offsets, a->E, a->m_total, a->dw ? a->a_rows : nullptr, a->x_rows, s);
     if (st != NVFP4MOE_OK) return st;
     const hipError_t err = nvfp4::launch_gated_grad(a->gu, a->dh, a->dtype == NVFP4MOE_F16, a->I, a->m_total, a->offsets,
-                                                    a->E, a->activation, workspace, s);
+                                                    a->E, a->activation, a->dx ? dgu : nullptr, a->dw ? dgu_t : nullptr, s);
     if (err != hipSuccess) return hip_status(err, fn);
   }
-  return product_grad(fn, a->dtype, workspace, a->x, a->a_rows, a->x_rows, a->w, a->offsets, a->E, 2 * a->I, a->H,
+  return product_grad(fn, a->dtype, dgu, dgu_t, ld, a->x, a->a_rows, a->x_rows, a->w, a->offsets, a->E, 2 * a->I, a->H,
                       a->m_total, a->max_rows_per_expert_hint, a->dx, a->dw, s);
 }
 
@@ -883,7 +890,7 @@ int moe_grouped_gemm_backward(const nvfp4moe_product_grad_args* a, void* workspa
     const int st = debug_plain(fn, a->offsets, a->E, a->m_total, a->db ? a->a_rows : nullptr, a->a_rows_total, s);
     if (st != NVFP4MOE_OK) return st;
   }
-  return product_grad(fn, a->dtype, a->dy, a->a, a->a_rows, a->a_rows_total, a->b, a->offsets, a->E, a->N, a->K,
+  return product_grad(fn, a->dtype, a->dy, nullptr, 0, a->a, a->a_rows, a->a_rows_total, a->b, a->offsets, a->E, a->N, a->K,
                       a->m_total, a->max_rows_per_expert_hint, a->da, a->db, s);
 }
 

@@ -103,12 +103,12 @@ enum : int { TG_ACT_SILU = 0, TG_ACT_GELU = 1 };
 struct TileParams {
   const void* a;           // rows operand
   const void* b;           // columns operand
-  const int32_t* a_rows;   // gathered rows (NT: of a, TN: of b) or nullptr
+  const int32_t* a_rows;   // gathered rows (NT: of a, TN and TC: of b) or nullptr
   const float* sa;         // int8: scale per row of a
   const float* sb;         // int8: scale per expert and row of b
   const int32_t* offsets;
-  int E, N, K;             // N columns of the output (gated: 2I), K values of the reduction (NT, NN)
-  int R;                   // TN: rows of the output per expert
+  int E, N, K;             // N columns of the output (gated: 2I), K values of the reduction (NT, NN) or columns of a (TC)
+  int R;                   // TN, TC: rows of the output per expert
   int m_total;
   int src_rows;            // bound of the entries of a_rows
   int act;
@@ -121,7 +121,8 @@ hipError_t launch_tile_gemm_bf16(const TileParams& p, int layout, int epilogue, 
 hipError_t launch_tile_gemm_f16(const TileParams& p, int layout, int epilogue, hipStream_t stream);
 hipError_t launch_tile_gemm_i8(const TileParams& p, int epilogue, hipStream_t stream);
 hipError_t launch_gated_grad(const float* gu, const void* dh, int dtype_f16, int I, int64_t m_total,
-                             const int32_t* offsets, int E, int act, void* dgu, hipStream_t stream);
+                             const int32_t* offsets, int E, int act, void* dgu, void* dgu_t, hipStream_t stream);
+int64_t gated_grad_ld(int64_t m_total, int E);   // columns of dgu_t
 hipError_t launch_int8_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int8_t* codes, float* scales,
                                 hipStream_t stream);
 

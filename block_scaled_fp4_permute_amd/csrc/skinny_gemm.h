@@ -152,7 +152,7 @@ static hipError_t tg_launch(const TileParams& p, hipStream_t stream) {
     const int64_t experts = p.E < p.m_total ? p.E : p.m_total;
     if (p.rows_hint <= 16 && experts * ((width + bn - 1) / bn) < 256) return sk_launch<T, EPI>(p, stream);
   }
-  const int64_t r = L == TG_TN ? p.R : p.rows_hint;
+  const int64_t r = L == TG_TN || L == TG_TC ? p.R : p.rows_hint;
   if (r >= 192) return tg_start<T, L, EPI, 256, 256, 2, 4>(p, 1, stream);
   return tg_start<T, L, EPI, 128, 128, 2, 2>(p, 2, stream);
 }
@@ -164,6 +164,7 @@ static hipError_t tg_launch16(const TileParams& p, int layout, int epilogue, hip
            : epilogue == TG_OUT_F32 ? tg_launch<T, TG_NT, TG_OUT_F32>(p, stream)
                                     : tg_launch<T, TG_NT, TG_OUT_16>(p, stream);
   if (layout == TG_NN) return tg_launch<T, TG_NN, TG_OUT_16>(p, stream);
+  if (layout == TG_TC) return tg_launch<T, TG_TC, TG_OUT_16>(p, stream);
   return tg_launch<T, TG_TN, TG_OUT_16>(p, stream);
 }
 

@@ -7,6 +7,7 @@
 //   NT  y     rows of expert   N                K               [r][k]     [c][k]   y  = a B^T
 //   NN  da    rows of expert   K                N               [r][k]     [k][c]   da = dy B
 //   TN  dB    N                K                rows of expert  [k][r]     [k][c]   dB = dy^T a
+//   TC  dB    N                K                rows of expert  [r][k]     [k][c]   the same from dy^T
 // An operand stored [x][k] is K-contiguous, one stored [k][x] is K-major.
 //
 // The matrix instruction gets C as its first operand and R as its second, so a
@@ -26,7 +27,7 @@ typedef _Float16 half4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 enum : int { TG_BF16 = 0, TG_F16 = 1, TG_I8 = 2 };            // operand type
-enum : int { TG_NT = 0, TG_NN = 1, TG_TN = 2 };               // operand layouts
+enum : int { TG_NT = 0, TG_NN = 1, TG_TN = 2, TG_TC = 3 };    // operand layouts
 enum : int { TG_OUT_16 = 0, TG_OUT_F32 = 1, TG_OUT_GATED = 2 };  // epilogue
 
 template <int T>
@@ -278,11 +279,22 @@ __device__ __forceinline__ int tg_prefix(const TileParams& p, int* pre) {
 
 // task (c, nt): row chunk c of all experts' chunks (TN: row tile c), column tile
 // nt.  Inside an expert, groups of 4 chunks run column tile by column tile.
+// TC: the rows operand is stored transposed, [R][ld].  The columns of expert e
+// start at a multiple of `align` (64: a step's 128 bytes of a row are one line;
+// 8, 16 bytes, where experts have so few rows that the gaps would dominate), at
+// least one element behind those of the expert before; up to the next multiple
+// of 8 behind its last column they hold zeros.
+__host__ __device__ __forceinline__ int64_t tg_start_col(int64_t row0, int e, int align) {
+  return ((row0 + align - 1) & ~static_cast<int64_t>(align - 1)) + static_cast<int64_t>(align) * e;
+}
+__host__ __device__ __forceinline__ int tg_col_align(int64_t m_total, int E) { return m_total / E >= 64 ? 64 : 8; }
+
 template <int L, int BM, int SK>
 __device__ __forceinline__ void tg_decode(const TileParams& p, const int* pre, int c, int nt, TgTask& t) {
   const tg_const_ints off = (tg_const_ints)(p.offsets);
   int q, nc;                               // chunk of its expert, chunks of the expert
-  if constexpr (L == TG_TN) {
+  constexpr bool WEIGHT = L == TG_TN || L == TG_TC;
+  if constexpr (WEIGHT) {
     t.e = c / p.r_tiles;
     q = c - t.e * p.r_tiles;
     nc = p.r_tiles;
@@ -300,7 +312,7 @@ __device__ __forceinline__ void tg_decode(const TileParams& p, const int* pre, i
   }
   t.row0 = min(max(off[t.e], 0), p.m_total);
   const int Me = max(min(max(off[t.e + 1], 0), p.m_total) - t.row0, 0);
-  if constexpr (L != TG_TN) nc = (Me + BM - 1) / BM;
+  if constexpr (!WEIGHT) nc = (Me + BM - 1) / BM;
   const int w = (q & 3) * p.n_tiles + nt, left = nc - (q & ~3);
   int m = w >> 2, r = w & 3;               // w by the chunks of the group
   if (left == 1) { m = w; r = 0; }
@@ -308,8 +320,8 @@ __device__ __forceinline__ void tg_decode(const TileParams& p, const int* pre, i
   if (left == 3) { m = w / 3; r = w - 3 * m; }
   t.m0 = ((q & ~3) + r) * BM;
   t.nt = m;
-  t.rows = min(BM, (L == TG_TN ? p.R : Me) - t.m0);
-  t.kt = L == TG_TN ? Me : p.K;
+  t.rows = min(BM, (WEIGHT ? p.R : Me) - t.m0);
+  t.kt = WEIGHT ? Me : p.K;
   t.nsteps = max(2, (t.kt + SK - 1) / SK);
 }
 
@@ -344,6 +356,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   constexpr int SK = kTgStep / EB;          // values of k per step
   constexpr bool RKM = L == TG_TN, CKM = L != TG_NT;
   constexpr bool GATED = EPI == TG_OUT_GATED;
+  constexpr bool WEIGHT = L == TG_TN || L == TG_TC;         // a weight gradient: reduction over an expert's rows
   constexpr int RT = BM / WR / 16, CT = BN / WC / 16;     // 16-row and 16-column tiles of a wave
   constexpr int RH = RT / 2;
   constexpr int kStage = (BM + BN) * kTgStep;
@@ -357,13 +370,13 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   static_assert(CT == 4 && RT % 4 == 0, "the store's exchange takes 4 column tiles; row tiles are stored in quarters");
   static_assert(RowsK::N == NR && ColsK::N == NC && NR % 2 == 0 && NC % 2 == 0, "halves of the loads");
   static_assert(RKM || Rows::STEP * WR * 2 <= BM, "a load holds rows of one half");
-  constexpr int kMap = L == TG_TN ? 1 : kTgMaxExperts;
+  constexpr int kMap = WEIGHT ? 1 : kTgMaxExperts;
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
   __shared__ int pre[kMap];
   static_assert(fits_lds(sizeof(lds) + sizeof(pre), 1), "tile stages exceed the LDS of a CU");
 
   int n;
-  if constexpr (L == TG_TN) n = p.E * p.r_tiles * p.n_tiles;
+  if constexpr (WEIGHT) n = p.E * p.r_tiles * p.n_tiles;
   else n = tg_prefix<BM>(p, pre) * p.n_tiles;
   const int share = (n + 7) >> 3;
   const int lo = (blockIdx.x & 7) * share, hi = min(lo + share, n);
@@ -395,9 +408,14 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   auto begin = [&]() __attribute__((always_inline)) {
     const int c0 = pt.nt * (GATED ? BN / 2 : BN);
     const uint8_t* Be = B;
-    if constexpr (L != TG_TN) Be += static_cast<size_t>(pt.e) * p.N * p.K * EB;
+    if constexpr (!WEIGHT) Be += static_cast<size_t>(pt.e) * p.N * p.K * EB;
     if constexpr (L == TG_TN) {
       rk.setup(A + static_cast<int64_t>(pt.row0) * p.R * 2, static_cast<int64_t>(p.R) * 2, pt.m0, p.R);
+    } else if constexpr (L == TG_TC) {
+      const uint8_t* first = A + 2 * tg_start_col(pt.row0, pt.e, tg_col_align(p.m_total, p.E));
+      ra.setup([&](int r) __attribute__((always_inline)) {
+        return first + static_cast<int64_t>(pt.m0 + (r < pt.rows ? r : 0)) * p.K * 2;
+      });
     } else {
       ra.setup([&](int r) __attribute__((always_inline)) {
         int q = pt.row0 + pt.m0 + (r < pt.rows ? r : 0);
@@ -419,14 +437,14 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   };
   const uint32_t lds0 = tg_lds_addr(lds) + wave * 1024;
   int left = 0, left_k = 0;                 // of the reduction from the loads' step on: bytes (K-contiguous) and rows
-  // TN: source rows of the wave's loads.  They are the same for half a wave, so
+  // Weight gradients: source rows of the wave's loads.  They are the same for half a wave, so
   // scalar loads fetch them (a vector load would wait for all loads in flight),
   // half a step before they are needed.
-  constexpr int W = L == TG_TN ? ColsK::ROWS : 1;
+  constexpr int W = WEIGHT ? ColsK::ROWS : 1;
   int raw[NC][W];
   uint64_t src[NC][W];
   auto fetch = [&]() __attribute__((always_inline)) {
-    if constexpr (L == TG_TN) {
+    if constexpr (WEIGHT) {
 #pragma unroll
       for (int j = 0; j < NC; ++j)
 #pragma unroll
@@ -439,7 +457,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   auto open = [&]() __attribute__((always_inline)) {        // before a step's loads
     left_k = idle ? 0 : pt.kt - ps * 64;
     left = idle ? 0 : pt.kt * EB - ps * kTgStep;
-    if constexpr (L == TG_TN) {
+    if constexpr (WEIGHT) {
       const uint8_t* tile = B + static_cast<int64_t>(pt.nt) * BN * 2;
 #pragma unroll
       for (int j = 0; j < NC; ++j)
@@ -556,7 +574,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
     const int wave_cols = (GATED ? BN / 2 : BN) / WC;
     const int c0 = ct.nt * (GATED ? BN / 2 : BN) + wave_cols * wc;
     const int rows = ct.rows - (BM / WR) * wr;              // of the wave
-    const int64_t row0 = (L == TG_TN ? static_cast<int64_t>(ct.e) * p.R : static_cast<int64_t>(ct.row0)) + ct.m0 + (BM / WR) * wr;
+    const int64_t row0 = (WEIGHT ? static_cast<int64_t>(ct.e) * p.R : static_cast<int64_t>(ct.row0)) + ct.m0 + (BM / WR) * wr;
     full = rows >= BM / WR && c0 + wave_cols <= width;
     const int piece = 16 * (lg & 1) + 4 * (lg & 2);         // the lane's 8 columns of a pair of tiles after the exchange
     if constexpr (GATED) {
@@ -691,7 +709,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   // INT8 results need scales from memory, whose loads wait for all others: they
   // are stored at the end of the task in one go.  So are TN's, whose stores
   // among the products cost more registers than there are.
-  constexpr bool kSpread = T != TG_I8 && L != TG_TN;
+  constexpr bool kSpread = T != TG_I8 && !RKM;
   // One step.  FIRST of a task: the products start from zero, and the h = 1 half
   // of the task before is stored before unit 2 overwrites it.  LAST: the h = 0
   // half, complete after unit 1, is stored.
@@ -811,7 +829,7 @@ static hipError_t tg_start(TileParams p, int per_cu, hipStream_t stream) {
   p.n_tiles = (cols + bn - 1) / bn;
   p.r_tiles = (p.R + BM - 1) / BM;
   int64_t tasks;
-  if (L == TG_TN) {
+  if (L == TG_TN || L == TG_TC) {
     tasks = static_cast<int64_t>(p.E) * p.r_tiles * p.n_tiles;
   } else {
     // at most min(E, m_total) experts have rows, each with one partial chunk
