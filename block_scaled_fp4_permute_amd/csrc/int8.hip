@@ -4,13 +4,14 @@
 
 namespace nvfp4 {
 
-// s = absmax / 127 (float32 division, 1 where that is zero), code =
-// nearest-even integer of the correctly rounded float32 quotient x / s.
+// s = absmax * (1/127) (float32 product with the float32 nearest 1/127; 1 where
+// that is zero), code = nearest-even integer of the correctly rounded float32
+// quotient x / s.
 //
 // One read of x: LPR lanes hold a row in registers (NV pieces of 8 values a
 // lane), reduce its maximum and write codes and scale.  Bound by memory; the
 // quotient is x * (1 / s) except where that lands within 2^-14 of a tie between
-// two codes: |x / s| <= 127 (1 + 2^-23), so the product's two roundings and the
+// two codes: |x / s| <= 127 (1 + 2^-22), so the product's two roundings and the
 // quotient's own move it by less than 127 * 3 * 2^-24 < 2^-15, and only there
 // can they decide otherwise than the divided quotient.  Below 2^-100 the
 // reciprocal could leave float32's range, and the row is divided throughout.
@@ -95,7 +96,7 @@ __global__ __launch_bounds__(256) void k_int8_quantize(const void* __restrict__ 
     }
   }
   top = q8_row_max<LPR>(top);
-  float s = top / 127.0f;
+  float s = top * (1.0f / 127.0f);
   if (!(s > 0.0f)) s = 1.0f;
   const bool fast = s > 0x1p-100f;
   const float inv = 1.0f / s;

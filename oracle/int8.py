@@ -10,7 +10,7 @@ from .experts16 import HALF, TINY, U, act, groups
 def quantize(x):
     """float32 x [..., cols] -> codes int8, scales float32."""
     x = np.asarray(x, np.float32)
-    s = (np.abs(x).max(-1) / np.float32(127)).astype(np.float32)
+    s = (np.abs(x).max(-1) * np.float32(1 / 127)).astype(np.float32)
     s = np.where(s > 0, s, np.float32(1))
     q = np.rint((x / s[..., None]).astype(np.float32))
     return np.clip(q, -127, 127).astype(np.int8), s

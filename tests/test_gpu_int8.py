@@ -21,7 +21,7 @@ def test_quantize_bits(rows, cols, dtype):
     if rows > 1:
         x[1] = 0                                    # scale 1, codes 0
     if rows > 2:
-        x[2, :] = np.where(np.arange(cols) % 2, 1e-45, 0)   # absmax / 127 underflows to 0: scale 1
+        x[2, :] = np.where(np.arange(cols) % 2, 1e-45, 0)   # absmax / 127 rounds to 0: scale 1
     if rows > 3:
         k = np.arange(cols) % 255 - 127             # every code and every tie between two
         x[3] = k + 0.5 * (np.arange(cols) % 2) * (np.abs(k) < 127)
@@ -42,7 +42,7 @@ def test_quantize_dense_quotients():
     r = np.random.default_rng(6)
     rows, cols = 512, 1024
     top = (2.0 ** r.uniform(-20, 20, rows)).astype(np.float32)
-    s = (top / np.float32(127)).astype(np.float32)
+    s = (top * np.float32(1 / 127)).astype(np.float32)
     k = r.integers(-126, 126, (rows, cols)) + 0.5
     x = (k * s[:, None].astype(np.float64)).astype(np.float32)
     x = (x.view(np.int32) + r.integers(-2, 3, x.shape).astype(np.int32)).view(np.float32)
