@@ -726,13 +726,35 @@ hipError_t launch16(int32_t dtype, const nvfp4::TileParams& p, int layout, int e
 }
 
 // layouts and epilogues of tile_gemm.h
-enum : int { L_NT = 0, L_NN = 1, L_TN = 2, L_TC = 3, O_16 = 0, O_F32 = 1, O_GATED = 2 };
+enum : int { L_NT = 0, L_NN = 1, L_TN = 2, L_TC = 3, O_16 = 0, O_F32 = 1, O_GATED = 2, O_PART = 3 };
+
+// Parts of the reduction (n values) of da [m_total, k] whose 128 x 128 tiles
+// would fill less than half of the chip's 512 workgroup slots: as many as fill
+// it, of at least 4 steps of 64, at most 16; 1 = none.  From the sizes of the
+// call alone, so that the workspace query knows them.
+int grad_parts(int32_t E, int32_t n, int32_t k, int64_t m_total) {
+  if (m_total <= 0) return 1;
+  const int64_t tiles = ((m_total + 127) / 128 + (E < m_total ? E : m_total) - 1) * ((int64_t(k) + 127) / 128);
+  if (tiles >= 256) return 1;
+  const int64_t steps = (int64_t(n) + 63) / 64;
+  int64_t parts = 512 / tiles;
+  if (parts > steps / 4) parts = steps / 4;
+  if (parts > 16) parts = 16;
+  return parts < 2 ? 1 : static_cast<int>(parts);
+}
+
+size_t grad_parts_bytes(int32_t E, int32_t n, int32_t k, int64_t m_total) {
+  const int parts = grad_parts(E, n, k, m_total);
+  return parts == 1 ? 0 : static_cast<size_t>(parts) * static_cast<size_t>(m_total) * static_cast<size_t>(k) * 4;
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 // da = dy b and db = dy^T a of one grouped product: dy [m_total, n], b [E, n, k];
 // dy_t (nullable): dy transposed, [n, ld], for db
 int product_grad(const char* fn, int32_t dtype, const void* dy, const void* dy_t, int64_t ld, const void* a, const int32_t* a_rows, int64_t rows_total,
                  const void* b, const int32_t* offsets, int32_t E, int32_t n, int32_t k, int64_t m_total, int32_t hint,
-                 void* da, void* db, hipStream_t s) {
+                 void* da, void* db, void* part_ws, hipStream_t s) {
   nvfp4::TileParams p{};
   p.a = dy;
   p.offsets = offsets;
@@ -743,8 +765,12 @@ int product_grad(const char* fn, int32_t dtype, const void* dy, const void* dy_t
   if (da && m_total > 0) {
     p.b = b;
     p.K = n;
-    p.out = da;
-    const hipError_t err = launch16(dtype, p, L_NN, O_16, s);
+    p.parts = grad_parts(E, n, k, m_total);
+    p.out = p.parts > 1 ? part_ws : da;
+    p.part_k = ((n + 63) / 64 + p.parts - 1) / p.parts * 64;
+    hipError_t err = launch16(dtype, p, L_NN, p.parts > 1 ? O_PART : O_16, s);
+    if (err == hipSuccess && p.parts > 1)
+      err = nvfp4::launch_join(static_cast<const float*>(part_ws), p.parts, m_total, k, offsets, E, dtype == NVFP4MOE_F16, da, s);
     if (err != hipSuccess) return hip_status(err, fn);
   }
   if (db) {
@@ -801,8 +827,9 @@ size_t moe_gated_ffn_backward_workspace_size(int32_t E, int32_t H, int32_t I, in
   if (E <= 0 || E > 4096 || H <= 0 || I <= 0 || m_total < 0 || H % 8 != 0 || I % 8 != 0 || m_total >= (int64_t(1) << 31) ||
       I > (1 << 25))
     return 0;
-  // dg and du in 16 bits, by rows and transposed
-  return (static_cast<size_t>(m_total) + nvfp4::gated_grad_ld(m_total, E)) * 2 * static_cast<size_t>(I) * 2;
+  // dg and du in 16 bits, by rows and transposed, and the parts of dx
+  return round256((static_cast<size_t>(m_total) + nvfp4::gated_grad_ld(m_total, E)) * 2 * static_cast<size_t>(I) * 2) +
+         grad_parts_bytes(E, 2 * I, H, m_total);
 }
 
 int moe_gated_ffn_backward(const nvfp4moe_gated_grad_args* a, void* workspace, size_t workspace_bytes, void* stream) {
@@ -828,6 +855,7 @@ int moe_gated_ffn_backward(const nvfp4moe_gated_grad_args* a, void* workspace, s
   uint16_t* dgu = static_cast<uint16_t*>(workspace);
   uint16_t* dgu_t = dgu + a->m_total * 2 * a->I;            // 16-byte aligned: I is a multiple of 8
   const int64_t ld = nvfp4::gated_grad_ld(a->m_total, a->E);
+  uint8_t* part_ws = static_cast<uint8_t*>(workspace) + round256((static_cast<size_t>(a->m_total) + ld) * 2 * a->I * 2);
   if (ld >= (int64_t(1) << 31)) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: m_total + 64 E reaches 2^31", fn);
   if (a->m_total > 0) {
     const int st = debug_plain(fn, a->offsets, a->E, a->m_total, a->dw ? a->a_rows : nullptr, a->x_rows, s);
@@ -837,7 +865,7 @@ int moe_gated_ffn_backward(const nvfp4moe_gated_grad_args* a, void* workspace, s
     if (err != hipSuccess) return hip_status(err, fn);
   }
   return product_grad(fn, a->dtype, dgu, dgu_t, ld, a->x, a->a_rows, a->x_rows, a->w, a->offsets, a->E, 2 * a->I, a->H,
-                      a->m_total, a->max_rows_per_expert_hint, a->dx, a->dw, s);
+                      a->m_total, a->max_rows_per_expert_hint, a->dx, a->dw, part_ws, s);
 }
 
 int moe_grouped_gemm(const nvfp4moe_product_args* a, void* stream) {
@@ -870,7 +898,12 @@ int moe_grouped_gemm(const nvfp4moe_product_args* a, void* stream) {
   return hip_status(launch16(a->dtype, p, L_NT, a->out_dtype == NVFP4MOE_F32 ? O_F32 : O_16, s), fn);
 }
 
-size_t moe_grouped_gemm_backward_workspace_size(int32_t E, int32_t N, int32_t K, int64_t m_total) { return 0; }
+size_t moe_grouped_gemm_backward_workspace_size(int32_t E, int32_t N, int32_t K, int64_t m_total) {
+  if (E <= 0 || E > 4096 || N <= 0 || K <= 0 || N % 8 != 0 || K % 8 != 0 || m_total < 0 || m_total >= (int64_t(1) << 31) ||
+      N > (1 << 26) || K > (1 << 26))
+    return 0;
+  return grad_parts_bytes(E, N, K, m_total);
+}
 
 int moe_grouped_gemm_backward(const nvfp4moe_product_grad_args* a, void* workspace, size_t workspace_bytes, void* stream) {
   const char* fn = "moe_grouped_gemm_backward";
@@ -885,13 +918,14 @@ int moe_grouped_gemm_backward(const nvfp4moe_product_grad_args* a, void* workspa
   const size_t need = moe_grouped_gemm_backward_workspace_size(a->E, a->N, a->K, a->m_total);
   if (need && (!workspace || workspace_bytes < need))
     return fail(NVFP4MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes, need);
+  if (need && !aligned(workspace, 256)) return fail(NVFP4MOE_ERR_INVALID, "%s: workspace not 256-byte aligned", fn);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (a->m_total > 0) {
     const int st = debug_plain(fn, a->offsets, a->E, a->m_total, a->db ? a->a_rows : nullptr, a->a_rows_total, s);
     if (st != NVFP4MOE_OK) return st;
   }
   return product_grad(fn, a->dtype, a->dy, nullptr, 0, a->a, a->a_rows, a->a_rows_total, a->b, a->offsets, a->E, a->N, a->K,
-                      a->m_total, a->max_rows_per_expert_hint, a->da, a->db, s);
+                      a->m_total, a->max_rows_per_expert_hint, a->da, a->db, workspace, s);
 }
 
 // ------------------------------------------------------------------ INT8

@@ -28,7 +28,7 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 enum : int { TG_BF16 = 0, TG_F16 = 1, TG_I8 = 2 };            // operand type
 enum : int { TG_NT = 0, TG_NN = 1, TG_TN = 2, TG_TC = 3 };    // operand layouts
-enum : int { TG_OUT_16 = 0, TG_OUT_F32 = 1, TG_OUT_GATED = 2 };  // epilogue
+enum : int { TG_OUT_16 = 0, TG_OUT_F32 = 1, TG_OUT_GATED = 2, TG_OUT_PART = 3 };  // epilogue (PART: float32 sums of one part of the reduction)
 
 template <int T>
 struct TgType;
@@ -248,6 +248,7 @@ struct TgTask {
   int row0;       // first row of the expert
   int rows;       // live rows of the tile
   int kt;         // length of the reduction
+  int part, k0;   // part of the reduction and its first k
   int nsteps;     // at least 2: the loads run two steps ahead, short reductions get steps of zeros
 };
 
@@ -289,7 +290,7 @@ __host__ __device__ __forceinline__ int64_t tg_start_col(int64_t row0, int e, in
 }
 __host__ __device__ __forceinline__ int tg_col_align(int64_t m_total, int E) { return m_total / E >= 64 ? 64 : 8; }
 
-template <int L, int BM, int SK>
+template <int L, int BM, int SK, bool PART>
 __device__ __forceinline__ void tg_decode(const TileParams& p, const int* pre, int c, int nt, TgTask& t) {
   const tg_const_ints off = (tg_const_ints)(p.offsets);
   int q, nc;                               // chunk of its expert, chunks of the expert
@@ -322,6 +323,15 @@ __device__ __forceinline__ void tg_decode(const TileParams& p, const int* pre, i
   t.nt = m;
   t.rows = min(BM, (WEIGHT ? p.R : Me) - t.m0);
   t.kt = WEIGHT ? Me : p.K;
+  t.part = 0;
+  t.k0 = 0;
+  if constexpr (PART) {                    // the column tiles of part 0, then of part 1, ..
+    const int per = p.n_tiles / p.parts;
+    t.part = t.nt / per;
+    t.nt -= t.part * per;
+    t.k0 = t.part * p.part_k;
+    t.kt = max(min(p.part_k, p.K - t.k0), 0);
+  }
   t.nsteps = max(2, (t.kt + SK - 1) / SK);
 }
 
@@ -420,7 +430,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
       ra.setup([&](int r) __attribute__((always_inline)) {
         int q = pt.row0 + pt.m0 + (r < pt.rows ? r : 0);
         if (L == TG_NT && p.a_rows) q = valid_row(p.a_rows[q]);
-        return A + static_cast<int64_t>(q) * p.K * EB;
+        return A + (static_cast<int64_t>(q) * p.K + pt.k0) * EB;
       });
     }
     if constexpr (L == TG_NT)
@@ -433,7 +443,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
         return Be + static_cast<int64_t>(col) * p.K * EB;
       });
     else
-      ck.setup(Be, static_cast<int64_t>(p.N) * 2, c0, p.N);
+      ck.setup(Be + static_cast<int64_t>(pt.k0) * p.N * 2, static_cast<int64_t>(p.N) * 2, c0, p.N);
   };
   const uint32_t lds0 = tg_lds_addr(lds) + wave * 1024;
   int left = 0, left_k = 0;                 // of the reduction from the loads' step on: bytes (K-contiguous) and rows
@@ -514,7 +524,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
       }
       ps = 0;
       if (u < hi) {
-        tg_decode<L, BM, SK>(p, pre, uc, un, pt);
+        tg_decode<L, BM, SK, EPI == TG_OUT_PART>(p, pre, uc, un, pt);
         begin();
       } else {
         idle = true;
@@ -559,7 +569,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   // a store instruction writes whole 128-byte lines: 8 rows of 8 pieces.
   // The stores are non-temporal: no product of the call reads them, and the
   // operands keep the caches (weight gradients of 64 rows an expert: 543 -> 452 us).
-  constexpr int OB = EPI == TG_OUT_F32 ? 4 : 2;             // bytes of a result
+  constexpr int OB = EPI == TG_OUT_F32 || EPI == TG_OUT_PART ? 4 : 2;             // bytes of a result
   constexpr int PAIRB = OB == 2 ? 32 : 16;                  // columns from a lane's piece a to its piece b
   uint8_t* obase = static_cast<uint8_t*>(p.out);            // the wave's first result (gated: of h)
   float* gbase = p.gu;                      // gated: of the gate pre-activations
@@ -574,7 +584,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
     const int wave_cols = (GATED ? BN / 2 : BN) / WC;
     const int c0 = ct.nt * (GATED ? BN / 2 : BN) + wave_cols * wc;
     const int rows = ct.rows - (BM / WR) * wr;              // of the wave
-    const int64_t row0 = (WEIGHT ? static_cast<int64_t>(ct.e) * p.R : static_cast<int64_t>(ct.row0)) + ct.m0 + (BM / WR) * wr;
+    const int64_t row0 = (WEIGHT ? static_cast<int64_t>(ct.e) * p.R : static_cast<int64_t>(ct.row0) + static_cast<int64_t>(ct.part) * p.m_total) + ct.m0 + (BM / WR) * wr;
     full = rows >= BM / WR && c0 + wave_cols <= width;
     const int piece = 16 * (lg & 1) + 4 * (lg & 2);         // the lane's 8 columns of a pair of tiles after the exchange
     if constexpr (GATED) {
@@ -674,7 +684,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   };
 
   // ---- the stream
-  tg_decode<L, BM, SK>(p, pre, uc, un, pt);
+  tg_decode<L, BM, SK, EPI == TG_OUT_PART>(p, pre, uc, un, pt);
   begin();
   fetch();
 #pragma unroll
@@ -827,6 +837,7 @@ static hipError_t tg_start(TileParams p, int per_cu, hipStream_t stream) {
   const int cols = EPI == TG_OUT_GATED ? p.N / 2 : p.N;
   const int bn = EPI == TG_OUT_GATED ? BN / 2 : BN;
   p.n_tiles = (cols + bn - 1) / bn;
+  if (EPI == TG_OUT_PART) p.n_tiles *= p.parts;
   p.r_tiles = (p.R + BM - 1) / BM;
   int64_t tasks;
   if (L == TG_TN || L == TG_TC) {

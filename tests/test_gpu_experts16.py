@@ -66,6 +66,14 @@ def test_gated_block_and_gradients(counts, H, I, dtype, act):
     _close(gu, rgu, tgu, "gu")
     _close(dx, rdx, tdx, "dx")
     _close(dw, rdw, tdw, "dw")
+    # the tile kernels, which the sizes alone would not choose here
+    for hint in (5000, 200000):
+        hh, gg = m.moe_gated_ffn(x, w, off_d, m_total=M, save_gu=True, max_rows_per_expert_hint=hint, **kw)
+        _close(hh, rh, th, f"h, hint {hint}")
+        _close(gg, rgu, tgu, f"gu, hint {hint}")
+        ddx, ddw = m.moe_gated_ffn_backward(dh, gg, x, w, off_d, max_rows_per_expert_hint=hint, **kw)
+        _close(ddx, rdx, tdx, f"dx, hint {hint}")
+        _close(ddw, rdw, tdw, f"dw, hint {hint}")
     only_dx, none = m.moe_gated_ffn_backward(dh, gu, x, w, off_d, need_dw=False, **kw)
     assert none is None and torch.equal(only_dx, dx)
     none, only_dw = m.moe_gated_ffn_backward(dh, gu, x, w, off_d, need_dx=False, **kw)
@@ -84,6 +92,13 @@ def test_product_and_gradients(counts, N, K, dtype):
     dy, dy64 = _make((M, N), dtype, r)
     y = m.moe_grouped_gemm(a, b, off_d, m_total=M)
     y32 = m.moe_grouped_gemm(a, b, off_d, m_total=M, out_dtype=torch.float32)
+    for hint in (5000, 200000):
+        _close(m.moe_grouped_gemm(a, b, off_d, m_total=M, max_rows_per_expert_hint=hint), *X.product(a64, b64, off, None, dtype), "y")
+        _close(m.moe_grouped_gemm(a, b, off_d, m_total=M, out_dtype=torch.float32, max_rows_per_expert_hint=hint),
+               *X.product(a64, b64, off, None, "f32"), "y32")
+        for got, (want, tol) in zip(m.moe_grouped_gemm_backward(dy, a, b, off_d, max_rows_per_expert_hint=hint),
+                                    X.product_grad(dy64, a64, b64, off, None, dtype)):
+            _close(got, want, tol, f"gradient, hint {hint}")
     da, db = m.moe_grouped_gemm_backward(dy, a, b, off_d)
     _close(y, *X.product(a64, b64, off, None, dtype), "y")
     _close(y32, *X.product(a64, b64, off, None, "f32"), "y32")
@@ -98,7 +113,7 @@ def test_product_and_gradients(counts, N, K, dtype):
     _close(db, *X.product_grad(dy64, a64, b64, off, rows, dtype)[1], "gathered db")
 
 
-@pytest.mark.parametrize("hint", [1, 100, 5000])
+@pytest.mark.parametrize("hint", [1, 100, 5000, 100000])
 def test_every_hint_gives_a_right_result(hint):
     r = np.random.default_rng(hint)
     counts, H, I = [40, 0, 300, 9], 328, 104
@@ -115,7 +130,7 @@ def test_every_hint_gives_a_right_result(hint):
     _close(dw, *g2, "dw")
 
 
-@pytest.mark.parametrize("hint", [4, 400])
+@pytest.mark.parametrize("hint", [4, 5000, 200000])
 def test_garbage_outside_the_groups_is_neither_read_nor_written(hint):
     """NaN in unreferenced source rows, in rows behind the last expert and in the
     weights of empty experts stays there; result rows behind the last expert
@@ -157,6 +172,56 @@ def test_garbage_outside_the_groups_is_neither_read_nor_written(hint):
     for e in (0, 1, 3):
         _close(dw[e], g2[0][e], g2[1][e], f"dw[{e}]")
     assert not torch.isfinite(dw[2]).all()
+
+
+# sizes that choose each kernel by themselves: many tiles of 128 x 128, many of
+# 256 x 256 (with a last chunk of a few rows), and dense products whose row
+# gradient is summed in parts
+@pytest.mark.parametrize("counts,H,I", [([5] * 40, 1096, 520), ([300, 259, 256, 270, 512, 1, 330, 200], 2056, 1032),
+                                        ([37], 136, 1160), ([130], 72, 2056)], ids=["tile128", "tile256", "parts", "parts2"])
+def test_kernels_by_size(counts, H, I):
+    r = np.random.default_rng([H, I])
+    off, off_d = _off(counts)
+    M, E = int(off[-1]), len(counts)
+    x, x64 = _make((M, H), "bf16", r)
+    w, w64 = _make((E, 2 * I, H), "bf16", r, 1 / np.sqrt(H))
+    dh, dh64 = _make((M, I), "bf16", r)
+    h, gu = m.moe_gated_ffn(x, w, off_d, m_total=M, save_gu=True)
+    dx, dw = m.moe_gated_ffn_backward(dh, gu, x, w, off_d)
+    _close(h, *X.gated(x64, w64, off)[0], "h")
+    g1, g2 = X.gated_grad(dh64, x64, w64, off)
+    _close(dx, *g1, "dx")
+    _close(dw, *g2, "dw")
+    # two calls in one go on one workspace size, and again: the same bytes
+    dx2, dw2 = m.moe_gated_ffn_backward(dh, gu, x, w, off_d)
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+    a, a64 = _make((M, I), "f16", r)
+    b, b64 = _make((E, H, I), "f16", r, 1 / np.sqrt(I))
+    dy, dy64 = _make((M, H), "f16", r)
+    _close(m.moe_grouped_gemm(a, b, off_d, m_total=M), *X.product(a64, b64, off, None, "f16"), "y")
+    da, db = m.moe_grouped_gemm_backward(dy, a, b, off_d)
+    g1, g2 = X.product_grad(dy64, a64, b64, off, None, "f16")
+    _close(da, *g1, "da")
+    _close(db, *g2, "db")
+
+
+def test_row_gradient_in_parts_leaves_rows_behind_the_last_expert():
+    r = np.random.default_rng(31)
+    off, off_d = _off([20, 0, 13])
+    M, N, K = 40, 1024, 64
+    need = m.lib().moe_grouped_gemm_backward_workspace_size(3, N, K, M)
+    assert need > 0                       # the sizes do sum in parts
+    a, a64 = _make((M, K), "bf16", r)
+    b, b64 = _make((3, N, K), "bf16", r, 0.1)
+    dy, dy64 = _make((M, N), "bf16", r)
+    dy[33:] = float("nan")
+    da = torch.full((M, K), 7.0, dtype=torch.bfloat16, device=DEV)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)       # NaN patterns
+    m.moe_grouped_gemm_backward(dy, a, b, off_d, da=da, need_db=False, workspace=ws)
+    _close(da[:33], *X.product_grad(dy64, a64, b64, off)[0], "da")
+    assert (da[33:] == 7).all()
+    with pytest.raises(m.NVFP4MoEError):
+        m.moe_grouped_gemm_backward(dy, a, b, off_d, workspace=ws[:need - 256])
 
 
 def test_activation_at_the_ends():

@@ -76,7 +76,7 @@ def test_grouped_product(counts, N, K):
         err = np.abs(got.double().cpu().numpy() - want)
         assert (err <= t).all(), f"{what}: worst {np.max(err / np.maximum(t, 1e-300)):.3f} of the bound"
 
-    for hint in (0, 4, 400):
+    for hint in (0, 5000, 200000):
         close(m.int8_grouped_gemm(A, B, off_d, epilogue=m.EPI_F32, max_rows_per_expert_hint=hint, **kw), y, tol, "f32")
         close(m.int8_grouped_gemm(A, B, off_d, max_rows_per_expert_hint=hint, **kw), y, Q.rounded(y, tol, "bf16"), "bf16")
         h, th = Q.swiglu(y, tol)
@@ -108,7 +108,7 @@ def test_rows_behind_the_last_expert_keep_their_bytes():
     sa = np.full(40, np.nan, np.float32)          # scales behind the last expert are not used
     sa[:33] = 0.5
     A, B = m.INT8Tensor(up(a), up(sa)), m.INT8Tensor(up(b), up(np.ones((2, 32), np.float32)))
-    for hint in (4, 400):
+    for hint in (4, 5000, 200000):
         out = torch.full((40, 32), 7.0, dtype=torch.bfloat16, device=DEV)
         m.int8_grouped_gemm(A, B, up(np.array([0, 12, 33], np.int32)), m_total=40, out=out, max_rows_per_expert_hint=hint)
         assert (out[33:] == 7).all() and torch.isfinite(out.float()).all()
