@@ -24,7 +24,7 @@ __global__ __launch_bounds__(64 * WK * WC) __attribute__((amdgpu_waves_per_eu(2)
   constexpr int EB = TT::bytes;
   constexpr bool GATED = EPI == TG_OUT_GATED;
   constexpr int COLS = GATED ? 8 : 16;                      // output columns of a tile
-  constexpr int TURNS = RT == 1 ? 6 : RT == 2 ? 3 : 2;      // pieces loaded ahead: what the registers hold
+  constexpr int TURNS = RT == 1 ? 6 : 3;                    // pieces loaded ahead: what the registers hold
   __shared__ acc_t red[WK][WC][RT * CT][64];
   static_assert(fits_lds(sizeof(red), 1), "partial sums exceed the LDS of a CU");
   int e, m0, nt;
@@ -161,23 +161,28 @@ static hipError_t sk_start(TileParams p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// `rows` of one expert.  8 waves on one set of columns; rows of 1 KB and less (8
-// pieces) with 16 rows: pairs of waves
+// `rows` of one expert.  8 waves on one set of columns; 16 rows of 1 KB and less
+// (8 pieces): pairs of waves
 template <int T, int EPI>
 static hipError_t sk_launch(const TileParams& p, int64_t rows, hipStream_t stream) {
   const bool deep = static_cast<int64_t>(p.K) * TgType<T>::bytes > 8 * kSkPiece;
   if (rows <= 16) return deep ? sk_start<T, EPI, 1, 1, 8, 1>(p, stream) : sk_start<T, EPI, 1, 1, 2, 4>(p, stream);
   if (rows <= 32) return sk_start<T, EPI, 2, 2, 8, 1>(p, stream);
-  return sk_start<T, EPI, 4, 4, 8, 1>(p, stream);
+  return sk_start<T, EPI, 4, 2, 8, 1>(p, stream);
 }
 
 // ------------------------------------------------------------------ choice of the kernel
 // From the sizes alone: rows of one expert (the hint, or what m_total gives each
 // expert that can have any) and the tiles they make.
-//   forward, fewer than 256 tiles of 128 x 128 (half the slots of the chip): the
-//     kernel above (256 rows, 5632 -> 2048 columns: 108 us on 32 tiles)
-//   192 rows of output and at least 128 tiles of 256 x 256: those (16384 rows an
-//     expert: half the operand bytes a product of the 128 x 128 ones)
+//   forward, up to 32 rows and fewer than 256 tiles of 128 x 128 (half the chip's
+//     slots), or so few rows and columns that 64 x 32 tiles are one round of
+//     workgroups: the kernel above (17 rows, 5632 -> 2048: 19 us against 48 on
+//     tiles; 256 rows, 256 tasks: 35 against 48; 100 rows of 2048 -> 5632, 352
+//     tasks: 29 against 20, so tiles)
+//   192 rows of output and at least 128 tiles of 256 x 256: those, with half the
+//     operand traffic a product (512 rows an expert, 512 -> 6144 row gradient:
+//     1155 us against 1450 on 128 x 128 tiles; 512 rows of 2048 -> 2 x 5632, 88
+//     tiles: 50 us against 33, so 128 x 128)
 //   else 128 x 128, two workgroups a CU
 template <int T, int L, int EPI>
 static hipError_t tg_launch(const TileParams& p, hipStream_t stream) {
@@ -190,7 +195,8 @@ static hipError_t tg_launch(const TileParams& p, hipStream_t stream) {
   const int64_t width = GATED ? p.N / 2 : p.N;
   auto tiles = [&](int64_t bm, int64_t bn) { return experts * ((rows + bm - 1) / bm) * ((width + bn - 1) / bn); };
   if constexpr (L == TG_NT) {
-    if (tiles(128, GATED ? 64 : 128) < 256) return sk_launch<T, EPI>(p, rows, stream);
+    if ((rows <= 32 && tiles(128, GATED ? 64 : 128) < 256) || tiles(64, GATED ? 16 : 32) <= 256)
+      return sk_launch<T, EPI>(p, rows, stream);
   }
   if (EPI != TG_OUT_PART && rows >= 192 && tiles(256, GATED ? 128 : 256) >= 128)
     return tg_start<T, L, EPI, 256, 256, 2, 4>(p, 1, stream);
