@@ -805,10 +805,13 @@ def _result(out, shape, dtype, like, name):
     return out
 
 
-def _scratch(workspace, need, dev):
+def _scratch(workspace, need, dev, stream):
     import torch
     if workspace is None:
-        return torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        if stream is not None:
+            ws.record_stream(stream)       # its memory goes to nobody else before that stream's work is done
+        return ws
     _need(workspace, torch.uint8, "workspace", dev)
     return workspace
 
@@ -868,7 +871,7 @@ def moe_gated_ffn_backward(dh, gu, x, w, offsets, *, a_rows=None, activation: in
     dw = _result(dw, w.shape, w.dtype, w, "dw") if need_dw else None
     if m_total == 0 and not need_dw:
         return dx, dw
-    ws = _scratch(workspace, lib().moe_gated_ffn_backward_workspace_size(E, H, I, m_total), dev)
+    ws = _scratch(workspace, lib().moe_gated_ffn_backward_workspace_size(E, H, I, m_total), dev, stream)
     args = GatedGradArgs(x=x.data_ptr(), dtype=code, a_rows=_ptr(a_rows), x_rows=x.shape[0], w=w.data_ptr(),
                          offsets=offsets.data_ptr(), E=E, H=H, I=I, m_total=m_total, activation=activation,
                          max_rows_per_expert_hint=max_rows_per_expert_hint, gu=gu.data_ptr(), dh=dh.data_ptr(),
@@ -928,7 +931,7 @@ def moe_grouped_gemm_backward(dy, a, b, offsets, *, a_rows=None, need_da: bool =
     if m_total == 0 and not need_db:
         return da, db
     need = lib().moe_grouped_gemm_backward_workspace_size(E, N, K, m_total)
-    ws = _scratch(workspace, need, dev) if need else None
+    ws = _scratch(workspace, need, dev, stream) if need else None
     args = ProductGradArgs(a=a.data_ptr(), dtype=code, a_rows=_ptr(a_rows), a_rows_total=a.shape[0], b=b.data_ptr(),
                            offsets=offsets.data_ptr(), E=E, N=N, K=K, m_total=m_total,
                            max_rows_per_expert_hint=max_rows_per_expert_hint, dy=dy.data_ptr(), da=_ptr(da),
@@ -949,8 +952,8 @@ def int8_quantize(x, out: INT8Tensor | None = None, stream=None) -> INT8Tensor:
     (tokens of activations, output channels of weights)."""
     import torch
     code = _dtype_code(x)
-    if x.dim() < 1:
-        raise ValueError("x must have at least one dimension")
+    if x.dim() < 1 or x.shape[-1] == 0:
+        raise ValueError("x must have at least one dimension and one column")
     dev = x.device
     _need(x, x.dtype, "x", dev)
     cols = x.shape[-1]

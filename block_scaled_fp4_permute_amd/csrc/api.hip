@@ -696,8 +696,9 @@ int check_plain(const char* fn, int32_t dtype, const int32_t* offsets, int32_t E
     return fail(NVFP4MOE_ERR_INVALID, "%s: sizes must be > 0 and row counts >= 0", fn);
   if (N % 8 != 0 || K % 8 != 0) return fail(NVFP4MOE_ERR_INVALID, "%s: sizes %d and %d must be multiples of 8", fn, N, K);
   if (E > 4096) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: E=%d > 4096", fn, E);
-  if (m_total >= (int64_t(1) << 31) || rows_total >= (int64_t(1) << 31))
-    return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: 2^31 rows or more", fn);
+  // the kernels count bytes of a reduction over rows in 32 bits
+  if (m_total >= (int64_t(1) << 30) || rows_total >= (int64_t(1) << 31))
+    return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: 2^30 GEMM rows or 2^31 source rows, or more", fn);
   if (N > (1 << 26) || K > (1 << 26)) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: a dimension above 2^26", fn);
   if (!aligned(offsets, 4) || !aligned(a_rows, 4)) return fail(NVFP4MOE_ERR_INVALID, "%s: misaligned index array", fn);
   if (m_total > 0) {
@@ -824,7 +825,7 @@ int moe_gated_ffn(const nvfp4moe_gated_args* a, void* stream) {
 }
 
 size_t moe_gated_ffn_backward_workspace_size(int32_t E, int32_t H, int32_t I, int64_t m_total) {
-  if (E <= 0 || E > 4096 || H <= 0 || I <= 0 || m_total < 0 || H % 8 != 0 || I % 8 != 0 || m_total >= (int64_t(1) << 31) ||
+  if (E <= 0 || E > 4096 || H <= 0 || I <= 0 || m_total < 0 || H % 8 != 0 || I % 8 != 0 || m_total >= (int64_t(1) << 30) ||
       I > (1 << 25))
     return 0;
   // dg and du in 16 bits, by rows and transposed, and the parts of dx
@@ -856,7 +857,6 @@ int moe_gated_ffn_backward(const nvfp4moe_gated_grad_args* a, void* workspace, s
   uint16_t* dgu_t = dgu + a->m_total * 2 * a->I;            // 16-byte aligned: I is a multiple of 8
   const int64_t ld = nvfp4::gated_grad_ld(a->m_total, a->E);
   uint8_t* part_ws = static_cast<uint8_t*>(workspace) + round256((static_cast<size_t>(a->m_total) + ld) * 2 * a->I * 2);
-  if (ld >= (int64_t(1) << 31)) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: m_total + 64 E reaches 2^31", fn);
   if (a->m_total > 0) {
     const int st = debug_plain(fn, a->offsets, a->E, a->m_total, a->dw ? a->a_rows : nullptr, a->x_rows, s);
     if (st != NVFP4MOE_OK) return st;
@@ -899,7 +899,7 @@ int moe_grouped_gemm(const nvfp4moe_product_args* a, void* stream) {
 }
 
 size_t moe_grouped_gemm_backward_workspace_size(int32_t E, int32_t N, int32_t K, int64_t m_total) {
-  if (E <= 0 || E > 4096 || N <= 0 || K <= 0 || N % 8 != 0 || K % 8 != 0 || m_total < 0 || m_total >= (int64_t(1) << 31) ||
+  if (E <= 0 || E > 4096 || N <= 0 || K <= 0 || N % 8 != 0 || K % 8 != 0 || m_total < 0 || m_total >= (int64_t(1) << 30) ||
       N > (1 << 26) || K > (1 << 26))
     return 0;
   return grad_parts_bytes(E, N, K, m_total);

@@ -108,7 +108,7 @@ hipError_t launch_gated_grad(const float* gu, const void* dh, int dtype_f16, int
                              int E, int act, void* dgu, void* dgu_t, hipStream_t stream) {
   const int64_t chunks = m_total / kGgRows + (E < m_total ? E : m_total);
   const int64_t blocks = (chunks * ((I + kGgCols - 1) / kGgCols) + 7) / 8 * 8;
-  if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
+  if (blocks >= (int64_t(1) << 24)) return hipErrorInvalidConfiguration;   // 2^32 threads (more values than the memory holds)
   const dim3 grid(static_cast<unsigned>(blocks));
   const int64_t ld = gated_grad_ld(m_total, E);
   if (dtype_f16)
@@ -137,7 +137,7 @@ hipError_t launch_join(const float* part, int parts, int64_t m_total, int N, con
                        void* out, hipStream_t stream) {
   const int64_t values = m_total * N;
   const int64_t blocks = (values / 4 + 255) / 256;
-  if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
+  if (blocks >= (int64_t(1) << 24)) return hipErrorInvalidConfiguration;   // 2^32 threads (more values than the memory holds)
   const dim3 grid(static_cast<unsigned>(blocks));
   if (dtype_f16) hipLaunchKernelGGL((k_join<TG_F16>), grid, dim3(256), 0, stream, part, parts, values, N, offsets, E, static_cast<uint16_t*>(out));
   else hipLaunchKernelGGL((k_join<TG_BF16>), grid, dim3(256), 0, stream, part, parts, values, N, offsets, E, static_cast<uint16_t*>(out));

@@ -117,10 +117,17 @@ __global__ __launch_bounds__(256) void k_int8_quantize(const void* __restrict__ 
 
 template <int DT, int LPR, int NV>
 static hipError_t q8_start(const void* x, int64_t rows, int cols, int8_t* codes, float* scales, hipStream_t stream) {
-  const int64_t blocks = (rows + 256 / LPR - 1) / (256 / LPR);
-  hipLaunchKernelGGL((k_int8_quantize<DT, LPR, NV>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, x, rows, cols,
-                     codes, scales);
-  return hipGetLastError();
+  // a grid has fewer than 2^32 threads
+  constexpr int64_t kMost = int64_t(1) << 23;
+  for (int64_t r0 = 0; r0 < rows; r0 += kMost) {
+    const int64_t n = rows - r0 < kMost ? rows - r0 : kMost;
+    const int64_t blocks = (n + 256 / LPR - 1) / (256 / LPR);
+    hipLaunchKernelGGL((k_int8_quantize<DT, LPR, NV>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream,
+                       static_cast<const uint8_t*>(x) + r0 * cols * (DT == 0 ? 4 : 2), n, cols, codes + r0 * cols, scales + r0);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 // a wave per row up to 1024 values (2 pieces a lane), a workgroup above, to 16384

@@ -268,9 +268,9 @@ __device__ __forceinline__ int tg_prefix(const TileParams& p, int* pre) {
         c = (max(b - a, 0) + BM - 1) / BM;
       }
       int total;
-      const int before = base + wave_excl_scan(c, total);
+      const int before = min(base + wave_excl_scan(c, total), 1 << 28);
       if (g + lane < p.E) pre[g + lane] = before;
-      base += total;
+      base = min(base + total, 1 << 28);    // offsets that overlap: the tasks of some rows fall away
     }
     if (lane == 0) pre[0] = base;           // the place of the first expert's zero holds the total
   }
@@ -387,7 +387,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
 
   int n;
   if constexpr (WEIGHT) n = p.E * p.r_tiles * p.n_tiles;
-  else n = tg_prefix<BM>(p, pre) * p.n_tiles;
+  else n = static_cast<int>(min(static_cast<int64_t>(tg_prefix<BM>(p, pre)) * p.n_tiles, int64_t(1) << 30));
   const int share = (n + 7) >> 3;
   const int lo = (blockIdx.x & 7) * share, hi = min(lo + share, n);
   const int stride = gridDim.x >> 3;

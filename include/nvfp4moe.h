@@ -420,10 +420,11 @@ int fp8_grouped_gemm(const nvfp4moe_fp8_gemm_args* args, void* stream);
  * [offsets[e], offsets[e+1]) belong to expert e, rows p >= offsets[E] of a
  * result are not written, E = 1 is a dense product.  m_total may be 0 (then
  * the row operands may be NULL; a weight gradient is still written, as zeros).
- * Pointers 16-byte aligned; H, I, N and K multiples of 8; E <= 4096; an
- * operand or result may exceed 4 GiB.  A hint is the rows per expert the
- * caller expects (0: m_total / E): it picks the tile, never the result's
- * definition. */
+ * Pointers 16-byte aligned; H, I, N and K multiples of 8 up to 2^26; E <= 4096;
+ * m_total < 2^30; an operand or result may exceed 4 GiB.  A hint is the rows
+ * per expert the caller expects (0: m_total over the experts that can have
+ * rows): it picks the kernel, never the result's definition.  Index arrays: see
+ * NVFP4MOE_DEBUG above (bad a_rows entries read row 0). */
 
 /* h[p, i] = act(g[p, i]) * u[p, i] with g = x[r] w[e, :I]^T, u = x[r] w[e, I:]^T
  * and r = a_rows ? a_rows[p] : p; gate and up projection, activation and
@@ -496,7 +497,7 @@ int moe_grouped_gemm(const nvfp4moe_product_args* args, void* stream);
  *   da[p, :] = dy[p] b[e]  (one row per row p, as dx above),  db[e] = sum_p dy[p]^T a[r_p]
  * in dtype.  Either may be NULL; db of an expert without rows is zero.
  * workspace as above (moe_grouped_gemm_backward_workspace_size; may be NULL
- * where that is 0). */
+ * where that is 0: it holds the parts of da where its tiles are few). */
 typedef struct nvfp4moe_product_grad_args {
   const void* a;              /* as in the forward call (not read when db is NULL) */
   int32_t dtype;

@@ -67,7 +67,7 @@ def _int8(**o):
     (dict(activation=2), INV), (dict(x=BAD), INV), (dict(w=BAD), INV), (dict(h=BAD), INV), (dict(gu=BAD), INV),
     (dict(a_rows=F + 2), INV), (dict(E=5000), UNS), (dict(m_total=2 ** 31, x_rows=2 ** 31), UNS),
     (dict(I=2 ** 26), UNS), (dict(H=2 ** 27), UNS), (dict(I=I32MAX - 7, H=I32MAX - 7), UNS),
-    (dict(m_total=I64MAX, x_rows=I64MAX), UNS), (dict(m_total=2 ** 30, x_rows=2 ** 30, I=2 ** 20), UNS),
+    (dict(m_total=I64MAX, x_rows=I64MAX), UNS), (dict(m_total=2 ** 29, x_rows=2 ** 29, I=2 ** 20), UNS), (dict(m_total=2 ** 30, x_rows=2 ** 30), UNS),
     (dict(m_total=0, x=None, h=None, x_rows=0), OK),
 ])
 def test_gated_refusals(o, want):

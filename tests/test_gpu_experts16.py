@@ -348,6 +348,75 @@ def test_side_stream_and_replayed_graph():
         assert torch.equal(f0["out"], f1["out"]) and torch.equal(b0["dx"], b1["dx"]) and torch.equal(b0["dw"], b1["dw"]), i
 
 
+@pytest.mark.parametrize("hint", [0, 5000, 200000])
+def test_bad_gather_entries_read_row_0(hint):
+    """The kernels' own bound on the index array, in every product that gathers."""
+    r = np.random.default_rng(41)
+    off, off_d = _off([30, 50])
+    x, _ = _make((20, 136), "bf16", r)
+    w, _ = _make((2, 208, 136), "bf16", r, 0.1)
+    dh, _ = _make((80, 104), "bf16", r)
+    rows = r.integers(0, 20, 80).astype(np.int32)
+    good = rows.copy()
+    rows[[3, 31, 79]], good[[3, 31, 79]] = [-1, 20, 2 ** 31 - 1], 0
+    res = []
+    for q in (rows, good):
+        kw = dict(a_rows=torch.from_numpy(q).to(DEV), max_rows_per_expert_hint=hint)
+        h, gu = m.moe_gated_ffn(x, w, off_d, m_total=80, save_gu=True, **kw)
+        dw = m.moe_gated_ffn_backward(dh, gu, x, w, off_d, need_dx=False, **kw)[1]
+        dy = torch.cat([dh, dh], 1).contiguous()
+        db = m.moe_grouped_gemm_backward(dy, x, w, off_d, need_da=False, **kw)[1]
+        res.append((h, gu, dw, m.moe_grouped_gemm(x, w, off_d, m_total=80, **kw), db))
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+
+
+def test_debug_checks_cover_the_new_calls(monkeypatch):
+    """With NVFP4MOE_DEBUG bad index arrays are refused on the host, before any launch."""
+    monkeypatch.setenv("NVFP4MOE_DEBUG", "1")
+    x = torch.zeros((20, 64), dtype=torch.bfloat16, device=DEV)
+    w = torch.zeros((2, 64, 64), dtype=torch.bfloat16, device=DEV)
+    gu, dh = torch.zeros((20, 64), device=DEV), torch.zeros((20, 32), dtype=torch.bfloat16, device=DEV)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)   # noqa: E731
+    rows = i32(*([0] * 19 + [20]))
+    q = m.int8_quantize(x)
+    wq = m.int8_quantize(w)
+    for off, kw, text in ((i32(0, 12, 5), {}, "offsets decrease"), (i32(0, 12, 21), {}, "m_total"),
+                          (i32(0, 12, 20), dict(a_rows=rows), "a_rows[19] = 20")):
+        for call in (lambda: m.moe_gated_ffn(x, w, off, m_total=20, **kw),
+                     lambda: m.moe_gated_ffn_backward(dh, gu, x, w, off, **kw),
+                     lambda: m.moe_grouped_gemm(x, w, off, m_total=20, **kw),
+                     lambda: m.moe_grouped_gemm_backward(x, x, w, off, **kw),
+                     lambda: m.int8_grouped_gemm(q, wq, off, m_total=20, **kw)):
+            with pytest.raises(m.NVFP4MoEError) as e:
+                call()
+            assert e.value.status == m.ERR_INVALID and text in e.value.detail
+
+
+def test_backward_on_another_stream_with_its_own_workspace():
+    """The call's temporary workspace is not handed out again while the stream
+    it works on has not finished."""
+    r = np.random.default_rng(43)
+    off, off_d = _off([400, 300])
+    x, _ = _make((700, 512), "bf16", r)
+    w, _ = _make((2, 1024, 512), "bf16", r, 0.05)
+    dh, _ = _make((700, 512), "bf16", r)
+    h, gu = m.moe_gated_ffn(x, w, off_d, m_total=700, save_gu=True)
+    want = m.moe_gated_ffn_backward(dh, gu, x, w, off_d)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    busy = torch.randn((2048, 2048), device=DEV)
+    n = m.lib().moe_gated_ffn_backward_workspace_size(2, 512, 512, 700)
+    for _ in range(4):
+        dx, dw = torch.empty_like(want[0]), torch.empty_like(want[1])
+        with torch.cuda.stream(side):
+            busy @ busy
+        m.moe_gated_ffn_backward(dh, gu, x, w, off_d, dx=dx, dw=dw, stream=side)
+        torch.full((n,), 255, dtype=torch.uint8, device=DEV)          # would take the freed block
+        torch.cuda.synchronize()
+        assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+
+
 def test_wrong_operands_are_refused():
     H, I = 64, 32
     x = torch.zeros((4, H), dtype=torch.bfloat16, device=DEV)
