@@ -795,10 +795,13 @@ def _group(b, offsets, dev):
     return E
 
 
-def _result(out, shape, dtype, like, name):
+def _result(out, shape, dtype, like, name, stream):
     """A given result checked, or a new one on ``like``'s device."""
     if out is None:
-        return like.new_empty(shape, dtype=dtype)
+        out = like.new_empty(shape, dtype=dtype)
+        if stream is not None:
+            out.record_stream(stream)      # dropped early, its memory goes to nobody else before that stream's work is done
+        return out
     _need(out, dtype, name, like.device)
     if tuple(out.shape) != tuple(shape):
         raise ValueError(f"{name}: expected {list(shape)}, got {list(out.shape)}")
@@ -834,9 +837,9 @@ def moe_gated_ffn(x, w, offsets, *, m_total: int, a_rows=None, activation: int =
     if x.shape[1] != H or w.shape[1] != 2 * I:
         raise ValueError("operand shapes disagree")
     _rows_of(a_rows, x, m_total, dev, "x")
-    h = _result(out, (m_total, I), w.dtype, w, "out")
+    h = _result(out, (m_total, I), w.dtype, w, "out", stream)
     if save_gu or gu is not None:
-        gu = _result(gu, (m_total, 2 * I), torch.float32, w, "gu")
+        gu = _result(gu, (m_total, 2 * I), torch.float32, w, "gu", stream)
     args = GatedArgs(x=x.data_ptr(), dtype=code, a_rows=_ptr(a_rows), x_rows=x.shape[0], w=w.data_ptr(),
                      offsets=offsets.data_ptr(), E=E, H=H, I=I, m_total=m_total, activation=activation,
                      max_rows_per_expert_hint=max_rows_per_expert_hint, h=h.data_ptr(), gu=_ptr(gu))
@@ -867,8 +870,8 @@ def moe_gated_ffn_backward(dh, gu, x, w, offsets, *, a_rows=None, activation: in
     if x.shape[1] != H or w.shape[1] != 2 * I or dh.shape[1] != I or tuple(gu.shape) != (m_total, 2 * I):
         raise ValueError("operand shapes disagree")
     _rows_of(a_rows, x, m_total, dev, "x")
-    dx = _result(dx, (m_total, H), w.dtype, w, "dx") if need_dx else None
-    dw = _result(dw, w.shape, w.dtype, w, "dw") if need_dw else None
+    dx = _result(dx, (m_total, H), w.dtype, w, "dx", stream) if need_dx else None
+    dw = _result(dw, w.shape, w.dtype, w, "dw", stream) if need_dw else None
     if m_total == 0 and not need_dw:
         return dx, dw
     ws = _scratch(workspace, lib().moe_gated_ffn_backward_workspace_size(E, H, I, m_total), dev, stream)
@@ -899,7 +902,7 @@ def moe_grouped_gemm(a, b, offsets, *, m_total: int, a_rows=None, out=None, out_
     want = out.dtype if out is not None and out_dtype is None else (out_dtype or b.dtype)
     if want not in (b.dtype, torch.float32):
         raise TypeError(f"out: {b.dtype} or float32, got {want}")
-    out = _result(out, (m_total, N), want, b, "out")
+    out = _result(out, (m_total, N), want, b, "out", stream)
     args = ProductArgs(a=a.data_ptr(), dtype=code, a_rows=_ptr(a_rows), a_rows_total=a.shape[0], b=b.data_ptr(),
                        offsets=offsets.data_ptr(), E=E, N=N, K=K, m_total=m_total,
                        out_dtype=F32 if want == torch.float32 else code,
@@ -926,8 +929,8 @@ def moe_grouped_gemm_backward(dy, a, b, offsets, *, a_rows=None, need_da: bool =
     if a.shape[1] != K or dy.shape[1] != N:
         raise ValueError("operand shapes disagree")
     _rows_of(a_rows, a, m_total, dev, "a")
-    da = _result(da, (m_total, K), b.dtype, b, "da") if need_da else None
-    db = _result(db, b.shape, b.dtype, b, "db") if need_db else None
+    da = _result(da, (m_total, K), b.dtype, b, "da", stream) if need_da else None
+    db = _result(db, b.shape, b.dtype, b, "db", stream) if need_db else None
     if m_total == 0 and not need_db:
         return da, db
     need = lib().moe_grouped_gemm_backward_workspace_size(E, N, K, m_total)
@@ -958,7 +961,8 @@ def int8_quantize(x, out: INT8Tensor | None = None, stream=None) -> INT8Tensor:
     _need(x, x.dtype, "x", dev)
     cols = x.shape[-1]
     if out is None:
-        out = INT8Tensor(torch.empty_like(x, dtype=torch.int8), x.new_empty(x.shape[:-1], dtype=torch.float32))
+        out = INT8Tensor(_result(None, x.shape, torch.int8, x, "out.codes", stream),
+                         _result(None, x.shape[:-1], torch.float32, x, "out.scales", stream))
     else:
         _need(out.codes, torch.int8, "out.codes", dev)
         _need(out.scales, torch.float32, "out.scales", dev)
@@ -992,7 +996,7 @@ def int8_grouped_gemm(a: INT8Tensor, b: INT8Tensor, offsets, *, m_total: int, a_
     if epilogue not in (EPI_F32, EPI_BF16, EPI_SWIGLU_BF16):
         raise ValueError("int8_grouped_gemm: epilogue F32, BF16 or SWIGLU_BF16")
     out = _result(out, (m_total, N // 2 if epilogue == EPI_SWIGLU_BF16 else N),
-                  torch.float32 if epilogue == EPI_F32 else torch.bfloat16, b.codes, "out")
+                  torch.float32 if epilogue == EPI_F32 else torch.bfloat16, b.codes, "out", stream)
     args = Int8GemmArgs(a_codes=a.codes.data_ptr(), a_scales=a.scales.data_ptr(), a_rows=_ptr(a_rows),
                         a_rows_total=a.codes.shape[0], b_codes=b.codes.data_ptr(), b_scales=b.scales.data_ptr(),
                         offsets=offsets.data_ptr(), E=E, N=N, K=K, m_total=m_total, epilogue=epilogue,

@@ -5,8 +5,9 @@
 // as matrix operands, dx row by row and dw column by column (reduction over the
 // rows).  So they are written twice, row-major [m_total, 2I] and transposed
 // [2I, ld]: with both operands of dw K-major, its LDS reads are all transposing
-// 8-byte ones and bound it (16384 tokens, 512 rows an expert: see tile_gemm.h).
-// One pass, bound by memory.
+// 8-byte ones and bound it (131072 rows of 256 experts, 2 x 256 columns, in a
+// training step: 3240 us with one copy, 3150 with both).  One pass, bound by
+// memory: those rows, 604 MB read and written, take 113 us, 5.3 TB/s.
 #include "tile_gemm.h"
 
 namespace nvfp4 {
@@ -33,6 +34,7 @@ __global__ __launch_bounds__(256) void k_gated_grad(const float* __restrict__ gu
   const int row0 = min(max(offsets[e], 0), m_total);
   const int Me = min(max(offsets[e + 1], 0), m_total) - row0;
   const int rows = min(kGgRows, Me - m0);
+  if (rows <= 0 || m0 < 0) return;          // offsets that overlap so far that the task count does not fit
   const int t = threadIdx.x;
   const int c = nt * kGgCols + 4 * (t & 15);
 #pragma unroll
@@ -122,7 +124,8 @@ hipError_t launch_gated_grad(const float* gu, const void* dh, int dtype_f16, int
 
 // ------------------------------------------------------------------ joining parts
 // The sums over parts of a long reduction (few output tiles), added in the order
-// of the parts and rounded once.
+// of the parts and rounded once.  Bound by memory (256 rows, 2048 x 5632 product's
+// row gradient, parts and this together: 44 us against 108 with one part).
 template <int T>
 __global__ __launch_bounds__(256) void k_join(const float* __restrict__ part, int parts, int64_t values, int N,
                                               const int32_t* __restrict__ offsets, int E, uint16_t* __restrict__ out) {

@@ -237,7 +237,7 @@ __device__ __forceinline__ void tg_frags(const uint8_t* tile, int t0, int s, u32
 // ------------------------------------------------------------------ tasks
 // A task is one output tile.  NT and NN: row chunk by row chunk, column tile by
 // column tile within one, experts in order; a prefix sum of the experts'
-// chunks lies in LDS.  TN: every expert has the same tiles.  Each XCD gets an
+// chunks lies in LDS.  TN and TC: every expert has the same tiles.  Each XCD gets an
 // equal contiguous range of the tasks (workgroups go to XCDs round-robin), so
 // that the tiles side by side in its L2 share rows and weights; a workgroup
 // takes every (workgroups per XCD)th task of its XCD's range.
@@ -278,8 +278,9 @@ __device__ __forceinline__ int tg_prefix(const TileParams& p, int* pre) {
   return __builtin_amdgcn_readfirstlane(pre[0]);
 }
 
-// task (c, nt): row chunk c of all experts' chunks (TN: row tile c), column tile
-// nt.  Inside an expert, groups of 4 chunks run column tile by column tile.
+// task (c, nt): row chunk c of all experts' chunks (TN, TC: row tile c), column tile
+// nt.  Inside an expert, groups of 4 chunks run column tile by column tile, so
+// that the workgroups side by side share both operands in L2.
 // TC: the rows operand is stored transposed, [R][ld].  The columns of expert e
 // start at a multiple of `align` (64: a step's 128 bytes of a row are one line;
 // 8, 16 bytes, where experts have so few rows that the gaps would dominate), at
@@ -357,6 +358,29 @@ __device__ __forceinline__ void tg_decode(const TileParams& p, const int* pre, i
 // than a step's loads are waited for at once.  Loads are spread over a unit's
 // products: in one burst they would hold up the products behind them.  A
 // finished tile is stored while the next one's loads are in flight.
+//
+// Tiles: 256 x 256 loads half the bytes a product that 128 x 128 does; its 128
+// accumulators a lane and 128 KB of stages leave one workgroup of 8 waves a CU.
+// 128 x 128 has two workgroups of 4 waves a CU, which cover each other's task
+// ends: the better one where tasks are short or few (both sides measured at the
+// choice in skinny_gemm.h).
+//
+// Measured (MI355X):                                                 us   rate
+//   bf16 8192^3, NT / NN / TN                          770 / 780 / 1075   1430 / 1410 / 1020 TFLOP/s
+//   int8 8192^3, NT                                                 402   2740 TOPS
+//   256 experts, 512 rows each, bf16 6144 -> 2 x 256: forward       950   868 TFLOP/s
+//     row gradient, weight gradient (TC)                    1040 / 1165   793 / 708 TFLOP/s
+//   256 experts, 8 rows each, bf16 6144 -> 2 x 256 / 256 -> 6144:
+//                                                           287 / 166   5.6 / 5.0 TB/s
+//   the same 256 -> 6144 in int8 (two steps a task)                 110   3.9 TB/s
+// Large products run at 1.9 - 2.1 GHz, the clock that the matrix cores' power
+// leaves, with those busy 53 % (forward), 49 % (rows) and 34 % (weights) of the
+// cycles at 512 rows an expert; LDS reads have no bank conflicts.  There the rest
+// is the last chunk of each expert (512 +- 22 rows take 2.5 chunks of 256 on
+// average), the task ends, and for weights the wait for gathered rows.  TN is
+// bound by its LDS reads, all of 8 bytes.  Few rows: bound by the weights'
+// stream from memory; int8 waits at each task's end for its scales, which come
+// behind the loads in flight.
 template <int T, int L, int EPI, int BM, int BN, int WR, int WC>
 __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_tile_gemm(const TileParams p) {
   using TT = TgType<T>;

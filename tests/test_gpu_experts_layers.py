@@ -122,6 +122,29 @@ def test_layer16_forward_and_expert_gradients(activation, kind):
     assert not dw_gu[5].any() and not dw_dn[5].any()
 
 
+def test_layer16_gradients_on_another_stream():
+    """The rows between the two backward calls belong to the call alone; their
+    memory is not handed out again before the side stream has read them."""
+    rng, logits, x, w_gu, w_dn = _inputs(5)
+    layer = MoELayer16(T, H, I, E, K, DEV)
+    layer.route(logits)
+    gu = torch.empty((T * K, 2 * I), device=DEV)
+    layer.expert_rows(x, w_gu, w_dn, gu=gu)
+    dy = torch.from_numpy(rng.standard_normal((T * K, H)).astype(np.float32)).to(torch.bfloat16).to(DEV)
+    want = layer.expert_rows_backward(dy, gu, x, w_gu, w_dn)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    busy = torch.randn((2048, 2048), device=DEV)
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            busy @ busy
+        got = layer.expert_rows_backward(dy, gu, x, w_gu, w_dn, stream=side)
+        for cols in (I, H):                        # would take the freed rows
+            torch.full((T * K, cols), float("nan"), dtype=torch.bfloat16, device=DEV)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_layer16_float16_rows():
     rng, logits, x, w_gu, w_dn = _inputs(4)
     x, w_gu, w_dn = x.half(), w_gu.half(), w_dn.half()
