@@ -124,6 +124,11 @@ __device__ __forceinline__ void tg_dma(const uint8_t* src, uint32_t lds_wave) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_wave), "v"(src) : "memory");
 }
 
+// the same of 4 bytes a lane
+__device__ __forceinline__ void tg_dma4(const float* src, uint32_t lds_wave) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds_wave), "v"(src) : "memory");
+}
+
 // all but the N youngest memory operations of this wave are done, its LDS
 // reads too, and so for every wave of the workgroup
 template <int N>
@@ -237,7 +242,7 @@ __device__ __forceinline__ void tg_frags(const uint8_t* tile, int t0, int s, u32
 // ------------------------------------------------------------------ tasks
 // A task is one output tile.  NT and NN: row chunk by row chunk, column tile by
 // column tile within one, experts in order; a prefix sum of the experts'
-// chunks lies in LDS.  TN and TC: every expert has the same tiles.  Each XCD gets an
+// chunks lies in LDS, one entry for two experts.  TN and TC: every expert has the same tiles.  Each XCD gets an
 // equal contiguous range of the tasks (workgroups go to XCDs round-robin), so
 // that the tiles side by side in its L2 share rows and weights; a workgroup
 // takes every (workgroups per XCD)th task of its XCD's range.
@@ -256,20 +261,20 @@ struct TgTask {
 typedef const int __attribute__((address_space(4)))* tg_const_ints;
 
 template <int BM>
+__device__ __forceinline__ int tg_chunks(const TileParams& p, int first, int end) {
+  return (max(min(max(end, 0), p.m_total) - min(max(first, 0), p.m_total), 0) + BM - 1) / BM;
+}
+
+template <int BM>
 __device__ __forceinline__ int tg_prefix(const TileParams& p, int* pre) {
   const int lane = threadIdx.x & 63;
   if (threadIdx.x < 64) {
     int base = 0;
     for (int g = 0; g < p.E; g += 64) {
-      int c = 0;
-      if (g + lane < p.E) {
-        const int a = min(max(p.offsets[g + lane], 0), p.m_total);
-        const int b = min(max(p.offsets[g + lane + 1], 0), p.m_total);
-        c = (max(b - a, 0) + BM - 1) / BM;
-      }
+      const int c = g + lane < p.E ? tg_chunks<BM>(p, p.offsets[g + lane], p.offsets[g + lane + 1]) : 0;
       int total;
       const int before = min(base + wave_excl_scan(c, total), 1 << 28);
-      if (g + lane < p.E) pre[g + lane] = before;
+      if (g + lane < p.E && !(lane & 1)) pre[(g + lane) >> 1] = before;
       base = min(base + total, 1 << 28);    // offsets that overlap: the tasks of some rows fall away
     }
     if (lane == 0) pre[0] = base;           // the place of the first expert's zero holds the total
@@ -301,16 +306,22 @@ __device__ __forceinline__ void tg_decode(const TileParams& p, const int* pre, i
     q = c - t.e * p.r_tiles;
     nc = p.r_tiles;
   } else {
-    const int lane = threadIdx.x & 63;
-    int e = t.e & ~63;                     // the experts whose chunks all lie before c, counted 64 at a time
+    const int lane = threadIdx.x & 63, pairs = (p.E + 1) >> 1;
+    int i = (t.e >> 1) & ~63;              // the pairs of experts whose chunks all lie before c, counted 64 at a time
     for (;;) {
-      const bool past = e + lane + 1 < p.E && pre[e + lane + 1] <= c;
+      const bool past = i + lane + 1 < pairs && pre[i + lane + 1] <= c;
       const int n = __popcll(__ballot(past));
-      e += n;
+      i += n;
       if (n < 64) break;
     }
-    t.e = __builtin_amdgcn_readfirstlane(e);
-    q = c - (t.e ? __builtin_amdgcn_readfirstlane(pre[t.e]) : 0);
+    i = __builtin_amdgcn_readfirstlane(i);
+    q = c - (i ? __builtin_amdgcn_readfirstlane(pre[i]) : 0);
+    t.e = 2 * i;                           // the first of the pair, or the second
+    const int of_first = tg_chunks<BM>(p, off[t.e], off[t.e + 1]);
+    if (q >= of_first && t.e + 1 < p.E) {
+      q -= of_first;
+      ++t.e;
+    }
   }
   t.row0 = min(max(off[t.e], 0), p.m_total);
   const int Me = max(min(max(off[t.e + 1], 0), p.m_total) - t.row0, 0);
@@ -372,15 +383,15 @@ __device__ __forceinline__ void tg_decode(const TileParams& p, const int* pre, i
 //     row gradient, weight gradient (TC)                    1040 / 1165   793 / 708 TFLOP/s
 //   256 experts, 8 rows each, bf16 6144 -> 2 x 256 / 256 -> 6144:
 //                                                           287 / 166   5.6 / 5.0 TB/s
-//   the same 256 -> 6144 in int8 (two steps a task)                 110   3.9 TB/s
+//   the same 256 -> 6144 in int8 (two steps a task)                 113   3.8 TB/s
+//     (118 with the scales read from memory at each task's end)
 // Large products run at 1.9 - 2.1 GHz, the clock that the matrix cores' power
 // leaves, with those busy 53 % (forward), 49 % (rows) and 34 % (weights) of the
 // cycles at 512 rows an expert; LDS reads have no bank conflicts.  There the rest
 // is the last chunk of each expert (512 +- 22 rows take 2.5 chunks of 256 on
 // average), the task ends, and for weights the wait for gathered rows.  TN is
 // bound by its LDS reads, all of 8 bytes.  Few rows: bound by the weights'
-// stream from memory; int8 waits at each task's end for its scales, which come
-// behind the loads in flight.
+// stream from memory.
 template <int T, int L, int EPI, int BM, int BN, int WR, int WC>
 __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_tile_gemm(const TileParams p) {
   using TT = TgType<T>;
@@ -404,10 +415,13 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   static_assert(CT == 4 && RT % 4 == 0, "the store's exchange takes 4 column tiles; row tiles are stored in quarters");
   static_assert(RowsK::N == NR && ColsK::N == NC && NR % 2 == 0 && NC % 2 == 0, "halves of the loads");
   static_assert(RKM || Rows::STEP * WR * 2 <= BM, "a load holds rows of one half");
-  constexpr int kMap = WEIGHT ? 1 : kTgMaxExperts;
+  constexpr int kMap = WEIGHT ? 1 : kTgMaxExperts / 2;
+  constexpr int kScales = T == TG_I8 ? BM + BN : 1;         // INT8: a tile's scales, one a thread
+  static_assert(T != TG_I8 || kScales == TH, "a thread fetches one scale");
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
   __shared__ int pre[kMap];
-  static_assert(fits_lds(sizeof(lds) + sizeof(pre), 1), "tile stages exceed the LDS of a CU");
+  __shared__ __attribute__((aligned(16))) float scl[2][kScales];
+  static_assert(fits_lds(sizeof(lds) + sizeof(pre) + sizeof(scl), BM == 128 ? 2 : 1), "tile stages exceed the LDS of a CU");
 
   int n;
   if constexpr (WEIGHT) n = p.E * p.r_tiles * p.n_tiles;
@@ -439,6 +453,11 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   Cols ca;
   RowsK rk;
   ColsK ck;
+  // INT8: the task's scales, rows then columns, come with its first step's loads.
+  // Two buffers in turn: a task's are read before the step in which those of the
+  // task two further on go out has met.
+  const float* scale = nullptr;             // the thread's
+  int pbuf = 0;                             // the buffer of the loads' task
   auto begin = [&]() __attribute__((always_inline)) {
     const int c0 = pt.nt * (GATED ? BN / 2 : BN);
     const uint8_t* Be = B;
@@ -468,6 +487,16 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
       });
     else
       ck.setup(Be + static_cast<int64_t>(pt.k0) * p.N * 2, static_cast<int64_t>(p.N) * 2, c0, p.N);
+    if constexpr (T == TG_I8) {
+      const int t = tg_thread(), c = t - BM;
+      if (c < 0) {
+        const int q = pt.row0 + pt.m0 + (t < pt.rows ? t : 0);
+        scale = p.sa + (p.a_rows ? valid_row(p.a_rows[q]) : q);
+      } else {
+        const int col = GATED ? min(c0 + (c & (BN / 2 - 1)), half - 1) + (c >= BN / 2 ? half : 0) : min(c0 + c, p.N - 1);
+        scale = p.sb + static_cast<size_t>(pt.e) * p.N + col;
+      }
+    }
   };
   const uint32_t lds0 = tg_lds_addr(lds) + wave * 1024;
   int left = 0, left_k = 0;                 // of the reduction from the loads' step on: bytes (K-contiguous) and rows
@@ -491,6 +520,12 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   auto open = [&]() __attribute__((always_inline)) {        // before a step's loads
     left_k = idle ? 0 : pt.kt - ps * 64;
     left = idle ? 0 : pt.kt * EB - ps * kTgStep;
+    if constexpr (T == TG_I8) {
+      if (ps == 0 && !idle) {
+        tg_dma4(scale, tg_lds_addr(scl) + (pbuf * kScales + wave * 64) * 4);
+        pbuf ^= 1;
+      }
+    }
     if constexpr (WEIGHT) {
       const uint8_t* tile = B + static_cast<int64_t>(pt.nt) * BN * 2;
 #pragma unroll
@@ -642,24 +677,18 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   constexpr int kStores = GATED ? 1 : 2 * CT / (OB == 2 ? 4 : 2);   // store instructions of a row tile, at least
   float row_scale[T == TG_I8 ? RT : 1];     // INT8: scales of the lane's rows and columns
   float4v col_scale[T == TG_I8 ? CT : 1];
+  int cbuf = 0;
   auto scales = [&]() __attribute__((always_inline)) {
     if constexpr (T == TG_I8) {
       const int t = tg_thread();
-      const int c0 = ct.nt * (GATED ? BN / 2 : BN) + (GATED ? BN / 2 : BN) / WC * wc + 4 * ((t >> 4) & 3);
-      const float* sb = p.sb + static_cast<size_t>(ct.e) * p.N;
-      const int width = GATED ? half : p.N;
+      const float* r = scl[cbuf] + (BM / WR) * wr + (t & 15);
+      const float* c = scl[cbuf] + BM + (GATED ? BN / 2 : BN) / WC * wc + 4 * ((t >> 4) & 3);
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const int r = ct.row0 + ct.m0 + min((BM / WR) * wr + 16 * i + (t & 15), ct.rows - 1);
-        row_scale[i] = p.sa[p.a_rows ? valid_row(p.a_rows[r]) : r];
-      }
+      for (int i = 0; i < RT; ++i) row_scale[i] = r[16 * i];
 #pragma unroll
-      for (int j = 0; j < CT; ++j) {
-        // scales behind the last column are not there; those results are not stored
-        const int q = GATED ? j % (CT / 2) : j;
-        const int c = min(c0 + 16 * q, width - 4) + (GATED && j >= CT / 2 ? half : 0);
-        col_scale[j] = *reinterpret_cast<const float4v*>(sb + c);
-      }
+      for (int j = 0; j < CT; ++j)
+        col_scale[j] = *reinterpret_cast<const float4v*>(c + 16 * (GATED ? j % (CT / 2) : j) + (GATED && j >= CT / 2 ? BN / 2 : 0));
+      cbuf ^= 1;
     }
   };
   auto store = [&](int i) __attribute__((always_inline)) {  // row tile i
@@ -740,9 +769,10 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
     }
     tg_wait<NX + NY>();
   };
-  // INT8 results need scales from memory, whose loads wait for all others: they
-  // are stored at the end of the task in one go.  So are TN's, whose stores
-  // among the products cost more registers than there are.
+  // INT8 results are stored at the end of the task in one go (their scales would
+  // take registers during the products; gate_up of 64 rows an expert 185 us
+  // among the products, 180 so).  So are TN's, whose stores among the products
+  // cost more registers than there are.
   constexpr bool kSpread = T != TG_I8 && !RKM;
   // One step.  FIRST of a task: the products start from zero, and the h = 1 half
   // of the task before is stored before unit 2 overwrites it.  LAST: the h = 0
