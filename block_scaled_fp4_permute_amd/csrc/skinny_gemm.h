@@ -182,6 +182,11 @@ static hipError_t sk_launch(const TileParams& p, int64_t rows, hipStream_t strea
 //     workgroups: the kernel above (17 rows, 5632 -> 2048: 19 us against 48 on
 //     tiles; 256 rows, 256 tasks: 35 against 48; 100 rows of 2048 -> 5632, 352
 //     tasks: 29 against 20, so tiles)
+//   forward, up to 32 rows and 1 KB of reduction (8 steps): 64 x 128 tiles, three
+//     workgroups a CU (256 experts, 8 rows, int8 256 -> 6144: 94 us against 112 on
+//     128 x 128; bf16 256 -> 6144 161 against 166; 32 rows, int8 512 -> 2048 50
+//     against 58; longer ones level off, bf16 1024 -> 2048 206 against 203, and
+//     64 rows lose, bf16 256 -> 6144 209 against 196)
 //   192 rows of output and at least 128 tiles of 256 x 256: those, with half the
 //     operand traffic a product (512 rows an expert, 512 -> 6144 row gradient:
 //     1155 us against 1450 on 128 x 128 tiles; 512 rows of 2048 -> 2 x 5632, 88
@@ -201,9 +206,13 @@ static hipError_t tg_launch(const TileParams& p, hipStream_t stream) {
     if ((rows <= 32 && tiles(128, GATED ? 64 : 128) < 256) || tiles(64, GATED ? 16 : 32) <= 256)
       return sk_launch<T, EPI>(p, rows, stream);
   }
+  if constexpr (L == TG_NT) {
+    if (rows <= 32 && p.E <= tg_most_experts(64) && static_cast<int64_t>(p.K) * TgType<T>::bytes <= 1024)
+      return tg_start<T, L, EPI, 64, 128, 1, 2>(p, stream);
+  }
   if (EPI != TG_OUT_PART && rows >= 192 && tiles(256, GATED ? 128 : 256) >= 128)
-    return tg_start<T, L, EPI, 256, 256, 2, 4>(p, 1, stream);
-  return tg_start<T, L, EPI, 128, 128, 2, 2>(p, 2, stream);
+    return tg_start<T, L, EPI, 256, 256, 2, 4>(p, stream);
+  return tg_start<T, L, EPI, 128, 128, 2, 2>(p, stream);
 }
 
 template <int T>

@@ -247,6 +247,9 @@ __device__ __forceinline__ void tg_frags(const uint8_t* tile, int t0, int s, u32
 // that the tiles side by side in its L2 share rows and weights; a workgroup
 // takes every (workgroups per XCD)th task of its XCD's range.
 constexpr int kTgMaxExperts = 4096;
+// Tiles of 64 rows take fewer, so that their workgroups lie three to a CU.
+constexpr int tg_most_experts(int bm) { return bm == 64 ? 1024 : kTgMaxExperts; }
+constexpr int tg_per_cu(int bm) { return bm == 256 ? 1 : bm == 128 ? 2 : 3; }
 
 struct TgTask {
   int e, m0, nt;
@@ -373,8 +376,9 @@ __device__ __forceinline__ void tg_decode(const TileParams& p, const int* pre, i
 // Tiles: 256 x 256 loads half the bytes a product that 128 x 128 does; its 128
 // accumulators a lane and 128 KB of stages leave one workgroup of 8 waves a CU.
 // 128 x 128 has two workgroups of 4 waves a CU, which cover each other's task
-// ends: the better one where tasks are short or few (both sides measured at the
-// choice in skinny_gemm.h).
+// ends: the better one where tasks are short or few.  64 x 128 has three of 2
+// waves, for tasks of a few rows and steps (both sides of each are measured at
+// the choice in skinny_gemm.h).
 //
 // Measured (MI355X):                                                 us   rate
 //   bf16 8192^3, NT / NN / TN                          770 / 780 / 1075   1430 / 1410 / 1020 TFLOP/s
@@ -382,9 +386,8 @@ __device__ __forceinline__ void tg_decode(const TileParams& p, const int* pre, i
 //   256 experts, 512 rows each, bf16 6144 -> 2 x 256: forward       950   868 TFLOP/s
 //     row gradient, weight gradient (TC)                    1040 / 1165   793 / 708 TFLOP/s
 //   256 experts, 8 rows each, bf16 6144 -> 2 x 256 / 256 -> 6144:
-//                                                           287 / 166   5.6 / 5.0 TB/s
-//   the same 256 -> 6144 in int8 (two steps a task)                 113   3.8 TB/s
-//     (118 with the scales read from memory at each task's end)
+//                                                           287 / 161   5.6 / 5.2 TB/s
+//   the same 256 -> 6144 in int8 (two steps a task)                  94   4.6 TB/s
 // Large products run at 1.9 - 2.1 GHz, the clock that the matrix cores' power
 // leaves, with those busy 53 % (forward), 49 % (rows) and 34 % (weights) of the
 // cycles at 512 rows an expert; LDS reads have no bank conflicts.  There the rest
@@ -407,21 +410,23 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   constexpr int kStage = (BM + BN) * kTgStep;
   using Rows = TgRows<BM, TH>;
   using Cols = TgRows<BN, TH>;
-  using RowsK = TgCols<BM, TH>;
-  using ColsK = TgCols<BN, TH>;
+  using RowsK = TgCols<RKM ? BM : 128, RKM ? TH : 256>;     // (the other layouts do not use it)
+  using ColsK = TgCols<CKM ? BN : 128, CKM ? TH : 256>;
   constexpr int NR = Rows::N, NC = Cols::N;               // loads of a thread per step and operand
   constexpr int NX = RKM ? NR / 2 + NC / 2 : NC + NR / 2, NY = NR + NC - NX;
   static_assert(T != TG_I8 || L == TG_NT, "int8 has the forward product only");
   static_assert(CT == 4 && RT % 4 == 0, "the store's exchange takes 4 column tiles; row tiles are stored in quarters");
-  static_assert(RowsK::N == NR && ColsK::N == NC && NR % 2 == 0 && NC % 2 == 0, "halves of the loads");
-  static_assert(RKM || Rows::STEP * WR * 2 <= BM, "a load holds rows of one half");
-  constexpr int kMap = WEIGHT ? 1 : kTgMaxExperts / 2;
-  constexpr int kScales = T == TG_I8 ? BM + BN : 1;         // INT8: a tile's scales, one a thread
-  static_assert(T != TG_I8 || kScales == TH, "a thread fetches one scale");
+  static_assert((!RKM || RowsK::N == NR) && (!CKM || ColsK::N == NC) && NR % 2 == 0 && NC % 2 == 0, "halves of the loads");
+  constexpr int RL = BM / WR / 2 / Rows::STEP;              // row loads of a half of a wave's rows
+  static_assert(RKM || RL * Rows::STEP * WR * 2 == BM, "a load holds rows of one half");
+  constexpr int kMap = WEIGHT ? 1 : tg_most_experts(BM) / 2;
+  constexpr int kScales = T == TG_I8 ? BM + BN : 1;         // INT8: a tile's scales
+  constexpr int SL = (kScales + TH - 1) / TH;               // a thread fetches so many
+  static_assert(T != TG_I8 || kScales % 64 == 0, "whole waves fetch scales");
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
   __shared__ int pre[kMap];
   __shared__ __attribute__((aligned(16))) float scl[2][kScales];
-  static_assert(fits_lds(sizeof(lds) + sizeof(pre) + sizeof(scl), BM == 128 ? 2 : 1), "tile stages exceed the LDS of a CU");
+  static_assert(fits_lds(sizeof(lds) + sizeof(pre) + sizeof(scl), tg_per_cu(BM)), "tile stages exceed the LDS of a CU");
 
   int n;
   if constexpr (WEIGHT) n = p.E * p.r_tiles * p.n_tiles;
@@ -456,7 +461,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   // INT8: the task's scales, rows then columns, come with its first step's loads.
   // Two buffers in turn: a task's are read before the step in which those of the
   // task two further on go out has met.
-  const float* scale = nullptr;             // the thread's
+  const float* scale[SL];                   // the thread's
   int pbuf = 0;                             // the buffer of the loads' task
   auto begin = [&]() __attribute__((always_inline)) {
     const int c0 = pt.nt * (GATED ? BN / 2 : BN);
@@ -488,13 +493,17 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
     else
       ck.setup(Be + static_cast<int64_t>(pt.k0) * p.N * 2, static_cast<int64_t>(p.N) * 2, c0, p.N);
     if constexpr (T == TG_I8) {
-      const int t = tg_thread(), c = t - BM;
-      if (c < 0) {
-        const int q = pt.row0 + pt.m0 + (t < pt.rows ? t : 0);
-        scale = p.sa + (p.a_rows ? valid_row(p.a_rows[q]) : q);
-      } else {
-        const int col = GATED ? min(c0 + (c & (BN / 2 - 1)), half - 1) + (c >= BN / 2 ? half : 0) : min(c0 + c, p.N - 1);
-        scale = p.sb + static_cast<size_t>(pt.e) * p.N + col;
+      const int t = tg_thread();
+#pragma unroll
+      for (int i = 0; i < SL; ++i) {
+        const int r = t + i * TH, c = r - BM;
+        if (c < 0) {
+          const int q = pt.row0 + pt.m0 + (r < pt.rows ? r : 0);
+          scale[i] = p.sa + (p.a_rows ? valid_row(p.a_rows[q]) : q);
+        } else {
+          const int col = GATED ? min(c0 + (c & (BN / 2 - 1)), half - 1) + (c >= BN / 2 ? half : 0) : min(c0 + c, p.N - 1);
+          scale[i] = p.sb + static_cast<size_t>(pt.e) * p.N + col;
+        }
       }
     }
   };
@@ -522,7 +531,9 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
     left = idle ? 0 : pt.kt * EB - ps * kTgStep;
     if constexpr (T == TG_I8) {
       if (ps == 0 && !idle) {
-        tg_dma4(scale, tg_lds_addr(scl) + (pbuf * kScales + wave * 64) * 4);
+#pragma unroll
+        for (int i = 0; i < SL; ++i)
+          if (wave * 64 + i * TH < kScales) tg_dma4(scale[i], tg_lds_addr(scl) + (pbuf * kScales + wave * 64 + i * TH) * 4);
         pbuf ^= 1;
       }
     }
@@ -559,7 +570,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
       else issue_row(q - NC / 2, l);
     } else {
       if (q < NC) issue_col(q, l);
-      else issue_row(2 * (q - NC), l);
+      else issue_row((q - NC) / RL * 2 * RL + (q - NC) % RL, l);
     }
   };
   auto issue_y = [&](int q) __attribute__((always_inline)) {
@@ -568,7 +579,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
       if (q < NC / 2) issue_col(NC / 2 + q, l);
       else issue_row(NR / 2 + q - NC / 2, l);
     } else {
-      issue_row(2 * q + 1, l);
+      issue_row(q / RL * 2 * RL + q % RL + RL, l);
     }
   };
   auto advance = [&]() __attribute__((always_inline)) {     // after a step's loads
@@ -887,7 +898,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
 
 // persistent workgroups: as many as are resident at once (256 CUs)
 template <int T, int L, int EPI, int BM, int BN, int WR, int WC>
-static hipError_t tg_start(TileParams p, int per_cu, hipStream_t stream) {
+static hipError_t tg_start(TileParams p, hipStream_t stream) {
   const int cols = EPI == TG_OUT_GATED ? p.N / 2 : p.N;
   const int bn = EPI == TG_OUT_GATED ? BN / 2 : BN;
   p.n_tiles = (cols + bn - 1) / bn;
@@ -903,7 +914,7 @@ static hipError_t tg_start(TileParams p, int per_cu, hipStream_t stream) {
   }
   if (tasks >= (int64_t(1) << 31) - 8) return hipErrorInvalidConfiguration;
   if (tasks == 0) return hipSuccess;
-  const int64_t blocks = min(int64_t(256) * per_cu, (tasks + 7) / 8 * 8);
+  const int64_t blocks = min(int64_t(256) * tg_per_cu(BM), (tasks + 7) / 8 * 8);
   hipLaunchKernelGGL((k_tile_gemm<T, L, EPI, BM, BN, WR, WC>), dim3(static_cast<unsigned>(blocks)), dim3(64 * WR * WC), 0, stream, p);
   return hipGetLastError();
 }

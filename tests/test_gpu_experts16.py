@@ -39,8 +39,10 @@ GROUPS = [
     ([1], 64, 32), ([0, 1, 0, 2], 136, 40), ([8] * 5, 256, 128), ([17, 0, 63, 65], 264, 72), ([129, 5], 8, 8),
     ([0, 0, 300], 200, 136), ([257, 31, 1, 0, 16], 512, 256), ([15, 16, 17], 1032, 24),
     ([520], 320, 264), ([3, 700, 0, 64], 192, 128),
+    # few rows an expert, short reductions, many tiles: the 64-row tiles (of both products)
+    ([5] * 30 + [0, 70, 0, 129, 64] + [9] * 6, 136, 520), ([5] * 30 + [0, 70, 0, 129, 64] + [9] * 6, 1096, 136),
 ]
-IDS = [f"{'-'.join(map(str, c))}x{h}x{i}" for c, h, i in GROUPS]
+IDS = [f"{'-'.join(map(str, c)) if len(c) < 9 else f'{len(c)}experts'}x{h}x{i}" for c, h, i in GROUPS]
 
 
 @pytest.mark.parametrize("dtype,act", [("bf16", "silu"), ("f16", "gelu")])
@@ -275,6 +277,21 @@ def test_more_experts_than_one_scan_group():
     g1, g2 = X.product_grad(dy64, a64, b64, off)
     _close(da, *g1, "da")
     _close(db, *g2, "db")
+
+
+@pytest.mark.parametrize("E", [1023, 1024, 1025, 4096])
+def test_many_experts(E):
+    """Up to the limit, rows for about half of them: the map of 64-row tiles ends at 1024."""
+    r = np.random.default_rng(E)
+    counts = r.integers(0, 3, E) * r.integers(0, 2, E)
+    counts[[0, E // 2, E - 1]] = [70, 130, 65]
+    off, off_d = _off(counts)
+    M = int(off[-1])
+    a, a64 = _make((M, 40), "f16", r)
+    b, b64 = _make((E, 24, 40), "f16", r, 0.2)
+    _close(m.moe_grouped_gemm(a, b, off_d, m_total=M), *X.product(a64, b64, off, None, "f16"), "y")
+    w, w64 = _make((E, 16, 40), "f16", r, 0.2)
+    _close(m.moe_gated_ffn(a, w, off_d, m_total=M), *X.gated(a64, w64, off, None, "silu", "f16")[0], "h")
 
 
 def test_gradients_against_differences_on_the_gpu():

@@ -54,10 +54,12 @@ def test_quantize_dense_quotients():
 
 
 GROUPS = [([1], 64, 32), ([0, 1, 0, 2], 48, 144), ([8] * 5, 256, 128), ([17, 0, 63, 65], 272, 80), ([129, 5], 16, 16),
-          ([257, 31, 1, 0, 16], 512, 256), ([520], 336, 272), ([3, 700, 0, 64], 192, 1040)]
+          ([257, 31, 1, 0, 16], 512, 256), ([520], 336, 272), ([3, 700, 0, 64], 192, 1040),
+          # few rows an expert, short reductions, many tiles: the 64-row tiles
+          ([5] * 30 + [0, 70, 0, 129, 64] + [9] * 6, 2080, 144), ([5] * 30 + [0, 70, 0, 129, 64] + [9] * 6, 1040, 16)]
 
 
-@pytest.mark.parametrize("counts,N,K", GROUPS, ids=[f"{'-'.join(map(str, c))}x{n}x{k}" for c, n, k in GROUPS])
+@pytest.mark.parametrize("counts,N,K", GROUPS, ids=[f"{'-'.join(map(str, c)) if len(c) < 9 else f'{len(c)}experts'}x{n}x{k}" for c, n, k in GROUPS])
 def test_grouped_product(counts, N, K):
     print(f"int8 product {counts} N={N} K={K}", flush=True)
     r = np.random.default_rng([N, K])
