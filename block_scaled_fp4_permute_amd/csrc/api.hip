@@ -729,15 +729,26 @@ hipError_t launch16(int32_t dtype, const nvfp4::TileParams& p, int layout, int e
 // layouts and epilogues of tile_gemm.h
 enum : int { L_NT = 0, L_NN = 1, L_TN = 2, L_TC = 3, O_16 = 0, O_F32 = 1, O_GATED = 2, O_PART = 3 };
 
-// Parts of the reduction (n values) of da [m_total, k] whose 128 x 128 tiles
-// would fill less than half of the chip's 512 workgroup slots: as many as fill
-// it, of at least 4 steps of 64, at most 16; 1 = none.  From the sizes of the
-// call alone, so that the workspace query knows them.
+// Parts of the reduction (n values) of da [m_total, k], 1 = none.  From the
+// sizes of the call alone, so that the workspace query knows them.
+//   128 x 128 tiles that would fill less than half of the chip's 512 workgroup
+//   slots: as many parts as fill it, of at least 4 steps of 64, at most 16
+//   256 x 256 tiles (tg_launch's choice) whose last round of 256 workgroups is
+//   badly filled: 3 parts, if the thirds of a round saved, 0.28 us a step (half a
+//   chip runs at a higher clock, so less than a third of a step's 1.5), are worth
+//   the parts' 24 bytes a value at 4.8 TB/s and a launch (136 tiles, 16384 ->
+//   2048: 270 us against 302 in one part; 144 tiles, 8192 -> 4096: 159 against 155)
 int grad_parts(int32_t E, int32_t n, int32_t k, int64_t m_total) {
   if (m_total <= 0) return 1;
-  const int64_t tiles = ((m_total + 127) / 128 + (E < m_total ? E : m_total) - 1) * ((int64_t(k) + 127) / 128);
-  if (tiles >= 256) return 1;
+  const int64_t experts = E < m_total ? E : m_total;
   const int64_t steps = (int64_t(n) + 63) / 64;
+  const int64_t large = ((m_total + 255) / 256 + experts - 1) * ((int64_t(k) + 255) / 256);
+  if (m_total / experts >= 192 && large >= 128) {
+    const int64_t saved = 3 * ((large + 255) / 256) - (3 * large + 255) / 256;   // thirds of a round
+    return saved * steps * 280 > 5000 + m_total * k / 200 ? 3 : 1;
+  }
+  const int64_t tiles = ((m_total + 127) / 128 + experts - 1) * ((int64_t(k) + 127) / 128);
+  if (tiles >= 256) return 1;
   int64_t parts = 512 / tiles;
   if (parts > steps / 4) parts = steps / 4;
   if (parts > 16) parts = 16;

@@ -210,7 +210,7 @@ static hipError_t tg_launch(const TileParams& p, hipStream_t stream) {
     if (rows <= 32 && p.E <= tg_most_experts(64) && static_cast<int64_t>(p.K) * TgType<T>::bytes <= 1024)
       return tg_start<T, L, EPI, 64, 128, 1, 2>(p, stream);
   }
-  if (EPI != TG_OUT_PART && rows >= 192 && tiles(256, GATED ? 128 : 256) >= 128)
+  if (rows >= 192 && tiles(256, GATED ? 128 : 256) >= 128)
     return tg_start<T, L, EPI, 256, 256, 2, 4>(p, stream);
   return tg_start<T, L, EPI, 128, 128, 2, 2>(p, stream);
 }

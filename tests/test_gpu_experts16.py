@@ -226,6 +226,25 @@ def test_row_gradient_in_parts_leaves_rows_behind_the_last_expert():
         m.moe_grouped_gemm_backward(dy, a, b, off_d, workspace=ws[:need - 256])
 
 
+def test_row_gradient_of_a_badly_filled_last_round():
+    """128 tiles of 256 x 256 on 256 CUs: summed in three parts of the reduction."""
+    r = np.random.default_rng(12)
+    M, N, K = 257, 6200, 16136
+    assert m.lib().moe_grouped_gemm_backward_workspace_size(1, N, K, M + 7) == 3 * (M + 7) * K * 4
+    _, off_d = _off([M])
+    dy, dy64 = _make((M + 7, N), "bf16", r)
+    b = torch.randn((1, N, K), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    da = torch.full((M + 7, K), 7.0, dtype=torch.bfloat16, device=DEV)
+    m.moe_grouped_gemm_backward(dy, torch.empty((M + 7, K), dtype=torch.bfloat16, device=DEV), b.to(DEV), off_d, need_db=False, da=da)
+    assert (da[M:] == 7).all()
+    for k in range(0, K, 4096):
+        b64 = b[0, :, k:k + 4096].double().numpy()
+        want = dy64[:M] @ b64
+        # at most N float32 additions in any order, then one rounding
+        tol = N * X.U * (np.abs(dy64[:M]) @ np.abs(b64)) * (1 + X.HALF["bf16"]) + X.HALF["bf16"] * np.abs(want) + X.TINY["bf16"]
+        _close(da[:M, k:k + 4096], want, tol, f"da from column {k}")
+
+
 def test_activation_at_the_ends():
     """g far out on both sides: act(g) u without NaN, and its gradient."""
     g = torch.tensor([-3e38, -1e4, -100, -20, -1, 0, 1, 20, 100, 1e4], dtype=torch.float32)
