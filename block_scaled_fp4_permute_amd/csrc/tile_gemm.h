@@ -389,7 +389,7 @@ __device__ __forceinline__ void tg_decode(const TileParams& p, const int* pre, i
 //                                                           287 / 161   5.6 / 5.2 TB/s
 //   the same 256 -> 6144 in int8 (two steps a task)                  94   4.6 TB/s
 // Large products run at 1.9 - 2.1 GHz, the clock that the matrix cores' power
-// leaves, with those busy 53 % (forward), 49 % (rows) and 34 % (weights) of the
+// leaves, with those busy 53 % (forward), 48 % (rows) and 34 % (weights) of the
 // cycles at 512 rows an expert; LDS reads have no bank conflicts.  There the rest
 // is the last chunk of each expert (512 +- 22 rows take 2.5 chunks of 256 on
 // average), the task ends, and for weights the wait for gathered rows.  TN is
