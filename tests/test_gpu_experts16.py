@@ -279,6 +279,12 @@ def test_no_rows_at_all(E):
     assert m.moe_grouped_gemm(x, w, off, m_total=0).shape == (0, 2 * I)
     da, db = m.moe_grouped_gemm_backward(torch.empty((0, 2 * I), dtype=torch.bfloat16, device=DEV), x, w, off)
     assert da.shape == (0, H) and not db.any()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    assert m.moe_gated_ffn(x, w, off, m_total=0, stream=side).shape == (0, I)
+    dx, dw = m.moe_gated_ffn_backward(h, gu, x, w, off, stream=side)
+    side.synchronize()
+    assert dx.shape == (0, H) and not dw.any()
 
 
 def test_more_experts_than_one_scan_group():
@@ -451,6 +457,31 @@ def test_backward_on_another_stream_with_its_own_workspace():
         torch.full((n,), 255, dtype=torch.uint8, device=DEV)          # would take the freed block
         torch.cuda.synchronize()
         assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+
+
+def test_two_streams_at_once():
+    """Calls of different sizes side by side on two streams give what they give one after another."""
+    r = np.random.default_rng(44)
+    sets = []
+    for counts, H, I in (([300, 20, 129], 512, 1032), ([7] * 60, 264, 520)):
+        off, off_d = _off(counts)
+        x, _ = _make((int(off[-1]), H), "bf16", r)
+        w, _ = _make((len(counts), 2 * I, H), "bf16", r, 0.05)
+        dh, _ = _make((int(off[-1]), I), "bf16", r)
+        sets.append((x, w, dh, off_d, int(off[-1])))
+
+    def both(x, w, dh, off_d, M, stream=None):
+        h, gu = m.moe_gated_ffn(x, w, off_d, m_total=M, save_gu=True, stream=stream)
+        return (h, gu) + m.moe_gated_ffn_backward(dh, gu, x, w, off_d, stream=stream)
+
+    want = [both(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = [both(*s, stream=q) for s, q in zip(sets, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(u, v) for u, v in zip(a, b))
 
 
 def test_wrong_operands_are_refused():
