@@ -183,36 +183,39 @@ struct TgCols {
   const uint8_t* p[N];                      // of the next step
   int64_t ld;                               // bytes of a row
   int k0;                                   // the thread's first row of a step
-  uint32_t col;                             // gathered: byte of the thread's chunk in the tile's row
+  const uint8_t* base;                      // gathered: the thread's chunk in row 0 of the operand
   __device__ __forceinline__ void setup(const uint8_t* mem, int64_t ld_bytes, int c0, int cols) {
     const int t = tg_thread();
     k0 = t / PER;
     const int f = (k0 & 3) + 4 * ((k0 >> 3) & 1);
     const int c = 8 * ((t % PER) ^ (2 * f));
     ld = ld_bytes;
-    col = 2 * min(c, cols - 8 - c0);
+    base = mem + 2 * static_cast<int64_t>(c0) + 2 * min(c, cols - 8 - c0);
 #pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = mem + 2 * static_cast<int64_t>(c0) + col + (k0 + i * STEP) * ld;
+    for (int i = 0; i < N; ++i) p[i] = base + (k0 + i * STEP) * ld;
   }
   // left: rows of the reduction from this step on
   __device__ __forceinline__ void issue(int i, int left, uint32_t lds_wave) {
     tg_dma(k0 < left - i * STEP ? p[i] : reinterpret_cast<const uint8_t*>(tg_zero), lds_wave + i * TH * 16);
     p[i] += 64 * ld;
   }
-  // gathered: rows of the wave's load, from the tile's first column on
-  __device__ __forceinline__ void issue_rows(int i, const uint64_t (&src)[ROWS], uint32_t lds_wave) {
+  // the thread's of the rows of the wave's load, which all its threads know
+  __device__ __forceinline__ int own_row(const int (&rows)[ROWS]) const {
     const int w = (threadIdx.x & 63) / PER;
-    uint32_t lo = static_cast<uint32_t>(src[0]), hi = static_cast<uint32_t>(src[0] >> 32);
+    int r = rows[0];
     tg_for<ROWS - 1>([&](auto ic) __attribute__((always_inline)) {
       constexpr int q = decltype(ic)::value + 1;
-      // moved to vector registers here: a plain choice among the array's entries becomes a table in memory
-      uint32_t a, b;
-      asm("v_mov_b32 %0, %1" : "=v"(a) : "s"(static_cast<uint32_t>(src[q])));
-      asm("v_mov_b32 %0, %1" : "=v"(b) : "s"(static_cast<uint32_t>(src[q] >> 32)));
-      lo = w == q ? a : lo;
-      hi = w == q ? b : hi;
+      // moved to a vector register here: a plain choice among the array's entries becomes a table in memory
+      int a;
+      asm("v_mov_b32 %0, %1" : "=v"(a) : "s"(rows[q]));
+      r = w == q ? a : r;
     });
-    tg_dma(reinterpret_cast<const uint8_t*>((static_cast<uint64_t>(hi) << 32 | lo) + col), lds_wave + i * TH * 16);
+    return r;
+  }
+  // gathered: the thread's chunk of `row`
+  __device__ __forceinline__ void issue_row(int i, int row, uint32_t ld_bytes, int left, uint32_t lds_wave) {
+    const uint8_t* a = base + static_cast<uint64_t>(static_cast<uint32_t>(row)) * ld_bytes;
+    tg_dma(k0 < left - i * STEP ? a : reinterpret_cast<const uint8_t*>(tg_zero), lds_wave + i * TH * 16);
   }
 };
 
@@ -514,7 +517,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   // half a step before they are needed.
   constexpr int W = WEIGHT ? ColsK::ROWS : 1;
   int raw[NC][W];
-  uint64_t src[NC][W];
+  int src[NC];                              // of the thread's loads
   auto fetch = [&]() __attribute__((always_inline)) {
     if constexpr (WEIGHT) {
 #pragma unroll
@@ -538,16 +541,11 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
       }
     }
     if constexpr (WEIGHT) {
-      const uint8_t* tile = B + static_cast<int64_t>(pt.nt) * BN * 2;
 #pragma unroll
-      for (int j = 0; j < NC; ++j)
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-          int r = __builtin_amdgcn_readfirstlane(raw[j][w]);
-          if (p.a_rows) r = valid_row(r);
-          const int k = wave * W + j * ColsK::STEP + w;
-          src[j][w] = reinterpret_cast<uint64_t>(k < left_k ? tile + static_cast<int64_t>(r) * p.N * 2 : reinterpret_cast<const uint8_t*>(tg_zero));
-        }
+      for (int j = 0; j < NC; ++j) {
+        src[j] = ck.own_row(raw[j]);
+        if (p.a_rows) src[j] = valid_row(src[j]);
+      }
     }
   };
   auto issue_row = [&](int i, uint32_t l) __attribute__((always_inline)) {
@@ -560,7 +558,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
     } else if constexpr (L == TG_NN) {
       ck.issue(j, left_k, l + BM * kTgStep);
     } else {
-      ck.issue_rows(j, src[j], l + BM * kTgStep);
+      ck.issue_row(j, src[j], p.N * 2, left_k, l + BM * kTgStep);
     }
   };
   auto issue_x = [&](int q) __attribute__((always_inline)) {   // load q of X
