@@ -133,6 +133,7 @@ __device__ __forceinline__ void tg_dma4(const float* src, uint32_t lds_wave) {
 // reads too, and so for every wave of the workgroup
 template <int N>
 __device__ __forceinline__ void tg_wait() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);       // lgkmcnt(0) for the compiler to know: it does not wait for those reads again
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
@@ -384,15 +385,15 @@ __device__ __forceinline__ void tg_decode(const TileParams& p, const int* pre, i
 // the choice in skinny_gemm.h).
 //
 // Measured (MI355X):                                                 us   rate
-//   bf16 8192^3, NT / NN / TN                          770 / 780 / 1075   1430 / 1410 / 1020 TFLOP/s
-//   int8 8192^3, NT                                                 402   2740 TOPS
+//   bf16 8192^3, NT / NN / TN                          780 / 785 / 945    1410 / 1400 / 1160 TFLOP/s
+//   int8 8192^3, NT                                                 401   2740 TOPS
 //   256 experts, 512 rows each, bf16 6144 -> 2 x 256: forward       950   868 TFLOP/s
-//     row gradient, weight gradient (TC)                    1040 / 1165   793 / 708 TFLOP/s
+//     row gradient, weight gradient (TC)                    1040 / 1080   793 / 764 TFLOP/s
 //   256 experts, 8 rows each, bf16 6144 -> 2 x 256 / 256 -> 6144:
 //                                                           287 / 161   5.6 / 5.2 TB/s
 //   the same 256 -> 6144 in int8 (two steps a task)                  94   4.6 TB/s
 // Large products run at 1.9 - 2.1 GHz, the clock that the matrix cores' power
-// leaves, with those busy 53 % (forward), 48 % (rows) and 34 % (weights) of the
+// leaves, with those busy 53 % (forward), 48 % (rows) and 38 % (weights) of the
 // cycles at 512 rows an expert; LDS reads have no bank conflicts.  There the rest
 // is the last chunk of each expert (512 +- 22 rows take 2.5 chunks of 256 on
 // average), the task ends, and for weights the wait for gathered rows.  TN is
@@ -520,11 +521,12 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   int src[NC];                              // of the thread's loads
   auto fetch = [&]() __attribute__((always_inline)) {
     if constexpr (WEIGHT) {
+      const int at = pt.row0 + ps * 64 + wave * W, last = pt.row0 + max(pt.kt - 1, 0);
 #pragma unroll
       for (int j = 0; j < NC; ++j)
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-          raw[j][w] = pt.row0 + max(min(ps * 64 + wave * W + j * ColsK::STEP + w, pt.kt - 1), 0);
+          raw[j][w] = min(at + j * ColsK::STEP + w, last);
           if (p.a_rows && pt.kt > 0) raw[j][w] = ((tg_const_ints)(p.a_rows))[raw[j][w]];
         }
     }
