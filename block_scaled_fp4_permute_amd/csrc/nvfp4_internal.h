@@ -113,7 +113,7 @@ struct TileParams {
   int src_rows;            // bound of the entries of a_rows
   int act;
   int rows_hint;           // expected rows per expert
-  int parts, part_k;       // float32 sums by parts: parts of the reduction and their length (a multiple of 64)
+  int parts, part_k;       // float32 sums by parts: parts of the reduction and (NN) their length, a multiple of 64
   int n_tiles, r_tiles;    // set by the launcher
   void* out;
   float* gu;               // gated: float32 pre-activations [m_total, N], or nullptr
@@ -124,8 +124,8 @@ hipError_t launch_tile_gemm_i8(const TileParams& p, int epilogue, hipStream_t st
 hipError_t launch_gated_grad(const float* gu, const void* dh, int dtype_f16, int I, int64_t m_total,
                              const int32_t* offsets, int E, int act, void* dgu, void* dgu_t, hipStream_t stream);
 int64_t gated_grad_ld(int64_t m_total, int E);   // columns of dgu_t
-// sum of `parts` float32 matrices [m_total, N] in their order, rounded to 16 bits; rows behind the last expert are left
-hipError_t launch_join(const float* part, int parts, int64_t m_total, int N, const int32_t* offsets, int E, int dtype_f16,
+// sum of `parts` float32 matrices [rows, N] in their order, rounded to 16 bits; with offsets, rows behind the last expert are left
+hipError_t launch_join(const float* part, int parts, int64_t rows, int N, const int32_t* offsets, int E, int dtype_f16,
                        void* out, hipStream_t stream);
 hipError_t launch_int8_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int8_t* codes, float* scales,
                                 hipStream_t stream);

@@ -210,8 +210,9 @@ static hipError_t tg_launch(const TileParams& p, hipStream_t stream) {
     if (rows <= 32 && p.E <= tg_most_experts(64) && static_cast<int64_t>(p.K) * TgType<T>::bytes <= 1024)
       return tg_start<T, L, EPI, 64, 128, 1, 2>(p, stream);
   }
-  if (rows >= 192 && tiles(256, GATED ? 128 : 256) >= 128)
-    return tg_start<T, L, EPI, 256, 256, 2, 4>(p, stream);
+  if constexpr (!(WEIGHT && EPI == TG_OUT_PART)) {
+    if (rows >= 192 && tiles(256, GATED ? 128 : 256) >= 128) return tg_start<T, L, EPI, 256, 256, 2, 4>(p, stream);
+  }
   return tg_start<T, L, EPI, 128, 128, 2, 2>(p, stream);
 }
 
@@ -223,8 +224,9 @@ static hipError_t tg_launch16(const TileParams& p, int layout, int epilogue, hip
                                     : tg_launch<T, TG_NT, TG_OUT_16>(p, stream);
   if (layout == TG_NN)
     return epilogue == TG_OUT_PART ? tg_launch<T, TG_NN, TG_OUT_PART>(p, stream) : tg_launch<T, TG_NN, TG_OUT_16>(p, stream);
-  if (layout == TG_TC) return tg_launch<T, TG_TC, TG_OUT_16>(p, stream);
-  return tg_launch<T, TG_TN, TG_OUT_16>(p, stream);
+  if (layout == TG_TC)
+    return epilogue == TG_OUT_PART ? tg_launch<T, TG_TC, TG_OUT_PART>(p, stream) : tg_launch<T, TG_TC, TG_OUT_16>(p, stream);
+  return epilogue == TG_OUT_PART ? tg_launch<T, TG_TN, TG_OUT_PART>(p, stream) : tg_launch<T, TG_TN, TG_OUT_16>(p, stream);
 }
 
 }  // namespace nvfp4

@@ -348,8 +348,9 @@ __device__ __forceinline__ void tg_decode(const TileParams& p, const int* pre, i
     const int per = p.n_tiles / p.parts;
     t.part = t.nt / per;
     t.nt -= t.part * per;
-    t.k0 = t.part * p.part_k;
-    t.kt = max(min(p.part_k, p.K - t.k0), 0);
+    const int len = WEIGHT ? ((Me + 63) / 64 + p.parts - 1) / p.parts * 64 : p.part_k;
+    t.k0 = t.part * len;
+    t.kt = max(min(len, t.kt - t.k0), 0);
   }
   t.nsteps = max(2, (t.kt + SK - 1) / SK);
 }
@@ -472,9 +473,9 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
     const uint8_t* Be = B;
     if constexpr (!WEIGHT) Be += static_cast<size_t>(pt.e) * p.N * p.K * EB;
     if constexpr (L == TG_TN) {
-      rk.setup(A + static_cast<int64_t>(pt.row0) * p.R * 2, static_cast<int64_t>(p.R) * 2, pt.m0, p.R);
+      rk.setup(A + (static_cast<int64_t>(pt.row0) + pt.k0) * p.R * 2, static_cast<int64_t>(p.R) * 2, pt.m0, p.R);
     } else if constexpr (L == TG_TC) {
-      const uint8_t* first = A + 2 * tg_start_col(pt.row0, pt.e, tg_col_align(p.m_total, p.E));
+      const uint8_t* first = A + 2 * (tg_start_col(pt.row0, pt.e, tg_col_align(p.m_total, p.E)) + pt.k0);
       ra.setup([&](int r) __attribute__((always_inline)) {
         return first + static_cast<int64_t>(pt.m0 + (r < pt.rows ? r : 0)) * p.K * 2;
       });
@@ -494,8 +495,8 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
           col = min(c0 + c, p.N - 1);
         return Be + static_cast<int64_t>(col) * p.K * EB;
       });
-    else
-      ck.setup(Be + static_cast<int64_t>(pt.k0) * p.N * 2, static_cast<int64_t>(p.N) * 2, c0, p.N);
+    else                                    // (weight gradients: every load adds its row)
+      ck.setup(Be + (WEIGHT ? 0 : static_cast<int64_t>(pt.k0) * p.N * 2), static_cast<int64_t>(p.N) * 2, c0, p.N);
     if constexpr (T == TG_I8) {
       const int t = tg_thread();
 #pragma unroll
@@ -521,7 +522,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   int src[NC];                              // of the thread's loads
   auto fetch = [&]() __attribute__((always_inline)) {
     if constexpr (WEIGHT) {
-      const int at = pt.row0 + ps * 64 + wave * W, last = pt.row0 + max(pt.kt - 1, 0);
+      const int first = pt.row0 + pt.k0, at = first + ps * 64 + wave * W, last = first + max(pt.kt - 1, 0);
 #pragma unroll
       for (int j = 0; j < NC; ++j)
 #pragma unroll
@@ -654,7 +655,7 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
     const int wave_cols = (GATED ? BN / 2 : BN) / WC;
     const int c0 = ct.nt * (GATED ? BN / 2 : BN) + wave_cols * wc;
     const int rows = ct.rows - (BM / WR) * wr;              // of the wave
-    const int64_t row0 = (WEIGHT ? static_cast<int64_t>(ct.e) * p.R : static_cast<int64_t>(ct.row0) + static_cast<int64_t>(ct.part) * p.m_total) + ct.m0 + (BM / WR) * wr;
+    const int64_t row0 = (WEIGHT ? (static_cast<int64_t>(ct.part) * p.E + ct.e) * p.R : static_cast<int64_t>(ct.row0) + static_cast<int64_t>(ct.part) * p.m_total) + ct.m0 + (BM / WR) * wr;
     full = rows >= BM / WR && c0 + wave_cols <= width;
     const int piece = 16 * (lg & 1) + 4 * (lg & 2);         // the lane's 8 columns of a pair of tiles after the exchange
     if constexpr (GATED) {

@@ -497,7 +497,7 @@ int moe_grouped_gemm(const nvfp4moe_product_args* args, void* stream);
  *   da[p, :] = dy[p] b[e]  (one row per row p, as dx above),  db[e] = sum_p dy[p]^T a[r_p]
  * in dtype.  Either may be NULL; db of an expert without rows is zero.
  * workspace as above (moe_grouped_gemm_backward_workspace_size; may be NULL
- * where that is 0: it holds the parts of da where its tiles are few). */
+ * where that is 0: it holds the parts of da or db where its tiles are few). */
 typedef struct nvfp4moe_product_grad_args {
   const void* a;              /* as in the forward call (not read when db is NULL) */
   int32_t dtype;

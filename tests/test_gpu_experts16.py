@@ -226,6 +226,40 @@ def test_row_gradient_in_parts_leaves_rows_behind_the_last_expert():
         m.moe_grouped_gemm_backward(dy, a, b, off_d, workspace=ws[:need - 256])
 
 
+@pytest.mark.parametrize("counts,H,I,parts", [([3000, 0, 5, 1501], 72, 40, 4), ([5003], 136, 200, 19),
+                                              ([2700, 1, 900, 0, 260], 264, 136, 3), ([700, 1, 900, 0, 260], 264, 136, 0)],
+                         ids=["small", "dense", "uneven", "one_part"])
+def test_weight_gradient_in_parts_of_the_rows(counts, H, I, parts):
+    """Few tiles and many rows: summed in parts, with the gathered and the direct rows, on a workspace of NaN."""
+    r = np.random.default_rng([H, I, 5])
+    off, off_d = _off(counts)
+    M, E, T = int(off[-1]), len(counts), 911
+    src = r.integers(0, T, M).astype(np.int32)
+    x, x64 = _make((T, H), "bf16", r)
+    w, w64 = _make((E, 2 * I, H), "bf16", r, 1 / np.sqrt(H))
+    dh, dh64 = _make((M, I), "bf16", r)
+    rows = torch.from_numpy(src).to(DEV)
+    h, gu = m.moe_gated_ffn(x, w, off_d, m_total=M, a_rows=rows, save_gu=True)
+    need = m.lib().moe_gated_ffn_backward_workspace_size(E, H, I, M)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+    dx, dw = m.moe_gated_ffn_backward(dh, gu, x, w, off_d, a_rows=rows, workspace=ws)
+    g1, g2 = X.gated_grad(dh64, x64, w64, off, src)
+    _close(dx, *g1, "dx")
+    _close(dw, *g2, "dw")
+    dy, dy64 = _make((M, 2 * I), "f16", r)
+    a, a64 = _make((T, H), "f16", r)
+    b, b64 = _make((E, 2 * I, H), "f16", r, 0.1)
+    need = m.lib().moe_grouped_gemm_backward_workspace_size(E, 2 * I, H, M)
+    assert need >= parts * E * 2 * I * H * 4
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+    da, db = m.moe_grouped_gemm_backward(dy, a, b, off_d, a_rows=rows, workspace=ws)
+    g1, g2 = X.product_grad(dy64, a64, b64, off, src, "f16")
+    _close(da, *g1, "da")
+    _close(db, *g2, "db")
+    db2 = m.moe_grouped_gemm_backward(dy, a[rows.long()], b, off_d, need_da=False)[1]
+    assert torch.equal(db, db2)
+
+
 def test_row_gradient_of_a_badly_filled_last_round():
     """128 tiles of 256 x 256 on 256 CUs: summed in three parts of the reduction."""
     r = np.random.default_rng(12)
