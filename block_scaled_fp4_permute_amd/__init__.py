@@ -746,6 +746,9 @@ def fp8_grouped_gemm(a: FP8Tensor, b_packed, b_scales, offsets, *, N: int, m_tot
 
 
 # ----------------------------------------------------------------- 16-bit expert FFN
+# With stream=, the operands (and given results and workspaces) have to be ready
+# on that stream, and the caller orders it before work that reads the results;
+# the memory that a call allocates needs no such order.
 def _call(dev, stream, fn, *args):
     """A C call on ``stream`` (None: the current stream of the operands' device)
     with that device current."""
@@ -795,12 +798,25 @@ def _group(b, offsets, dev):
     return E
 
 
+def _new(shape, dtype, dev, stream):
+    """Memory for a call on ``stream`` (None: the current one), from that
+    stream's pool.  A block of the current stream's pool may have been freed
+    with work still queued there that uses it, and nothing orders that work
+    before the call's."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _result(out, shape, dtype, like, name, stream):
     """A given result checked, or a new one on ``like``'s device."""
+    import torch
     if out is None:
-        out = like.new_empty(shape, dtype=dtype)
-        if stream is not None:
-            out.record_stream(stream)      # dropped early, its memory goes to nobody else before that stream's work is done
+        out = _new(shape, dtype, like.device, stream)
+        if stream is not None:             # the caller reads it on the current stream: dropped, it is held until that is done
+            out.record_stream(torch.cuda.current_stream(like.device))
         return out
     _need(out, dtype, name, like.device)
     if tuple(out.shape) != tuple(shape):
@@ -811,10 +827,7 @@ def _result(out, shape, dtype, like, name, stream):
 def _scratch(workspace, need, dev, stream):
     import torch
     if workspace is None:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-        if stream is not None:
-            ws.record_stream(stream)       # its memory goes to nobody else before that stream's work is done
-        return ws
+        return _new(max(need, 256), torch.uint8, dev, stream)
     _need(workspace, torch.uint8, "workspace", dev)
     return workspace
 

@@ -1,0 +1,58 @@
+"""Calls on an idle side stream while the current stream still has work queued
+that writes memory which it has already freed: the results are those of a call
+on the current stream, since the call's own memory is the side stream's."""
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_fp4_permute_amd as m
+from tests.gpu_common import DEV
+
+pytestmark = pytest.mark.gpu
+M, H, I, E = 700, 512, 256, 2
+
+
+def _operands():
+    r = np.random.default_rng(61)
+
+    def t(*shape, std=1.0):
+        return torch.from_numpy((r.standard_normal(shape) * std).astype(np.float32)).to(torch.bfloat16).to(DEV)
+
+    x, w = t(M, H), t(E, 2 * I, H, std=0.05)
+    off = torch.tensor([0, 300, M], dtype=torch.int32, device=DEV)
+    return dict(x=x, w=w, off=off, dh=t(M, I), dy=t(M, 2 * I), gu=t(M, 2 * I).float(), q=m.int8_quantize(x),
+                wq=m.int8_quantize(w))
+
+
+CALLS = {
+    "gated": lambda o, s: m.moe_gated_ffn(o["x"], o["w"], o["off"], m_total=M, save_gu=True, stream=s),
+    "gated_backward": lambda o, s: m.moe_gated_ffn_backward(o["dh"], o["gu"], o["x"], o["w"], o["off"], stream=s),
+    "product": lambda o, s: (m.moe_grouped_gemm(o["x"], o["w"], o["off"], m_total=M, stream=s),),
+    "product_backward": lambda o, s: m.moe_grouped_gemm_backward(o["dy"], o["x"], o["w"], o["off"], stream=s),
+    "int8_quantize": lambda o, s: (lambda q: (q.codes, q.scales))(m.int8_quantize(o["x"], stream=s)),
+    "int8_product": lambda o, s: (m.int8_grouped_gemm(o["q"], o["wq"], o["off"], m_total=M, stream=s),),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_call_beside_pending_work_on_freed_memory(name):
+    o = _operands()
+    want = CALLS[name](o, None)
+    ws = {"gated_backward": m.lib().moe_gated_ffn_backward_workspace_size(E, H, I, M),
+          "product_backward": m.lib().moe_grouped_gemm_backward_workspace_size(E, 2 * I, H, M)}.get(name, 0)
+    sizes = [t.numel() * t.element_size() for t in want] + [max(ws, 256)]
+    side = torch.cuda.Stream()
+    busy = torch.randn((4096, 4096), device=DEV)
+    for _ in range(3):
+        blocks = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in sizes]
+        torch.cuda.synchronize()
+        for _ in range(4):
+            busy @ busy                       # milliseconds
+        for b in blocks:
+            b.fill_(255)                      # behind them, into blocks that are free by then
+        del b, blocks
+        got = CALLS[name](o, side)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        del a, b, got

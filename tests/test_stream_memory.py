@@ -1,0 +1,97 @@
+"""Memory that a call allocates for itself, on the host side (no GPU needed): it
+comes from the pool of the stream that the call works on.  A block of another
+stream's pool may have been freed with work still queued there that reads or
+writes it, and nothing orders that work before the call's.  Results are held
+for the caller's stream as well.  The library calls are replaced by a recorder;
+the tensors lie on the CPU."""
+import contextlib
+
+import pytest
+import torch
+
+import block_scaled_fp4_permute_amd as m
+
+E, H, I, T = 2, 64, 32, 16
+MAIN, SIDE = "main", "side"
+
+
+class Stream:
+    def __init__(self, name):
+        self.name, self.device, self.cuda_stream = name, torch.device("cpu"), 0
+
+    def __eq__(self, other):
+        return self.name == other.name
+
+
+@pytest.fixture
+def pools(monkeypatch):
+    """Allocations as (stream that was current, bytes); streams that blocks are held for; launches."""
+    seen = {"alloc": [], "held": [], "calls": 0}
+    current = [Stream(MAIN)]
+
+    @contextlib.contextmanager
+    def stream(s):
+        before, current[0] = current[0], s
+        yield
+        current[0] = before
+
+    def recording(make):
+        def f(*a, **k):
+            t = make(*a, **k)
+            seen["alloc"].append((current[0].name, t))
+            return t
+        return f
+
+    def launched(*a):
+        seen["calls"] += 1
+        return m.OK
+
+    def held(t, s):
+        seen["held"].append((s.name, t))
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current[0])
+    monkeypatch.setattr(torch, "empty", recording(torch.empty))
+    monkeypatch.setattr(torch.Tensor, "new_empty", recording(torch.Tensor.new_empty))
+    monkeypatch.setattr(torch.Tensor, "record_stream", held)
+    monkeypatch.setattr(m, "_need", lambda t, dtype, name, device=None: None)
+    monkeypatch.setattr(m, "_call", launched)
+    return seen
+
+
+def _operands():
+    bf = torch.bfloat16
+    off = torch.tensor([0, 8, T], dtype=torch.int32)
+    return dict(x=torch.zeros((T, H), dtype=bf), w=torch.zeros((E, 2 * I, H), dtype=bf), off=off,
+                dh=torch.zeros((T, I), dtype=bf), gu=torch.zeros((T, 2 * I)), dy=torch.zeros((T, 2 * I), dtype=bf),
+                q=m.INT8Tensor(torch.zeros((T, H), dtype=torch.int8), torch.ones(T)),
+                wq=m.INT8Tensor(torch.zeros((E, 2 * I, H), dtype=torch.int8), torch.ones((E, 2 * I))))
+
+
+CALLS = {
+    "gated": lambda o, s: m.moe_gated_ffn(o["x"], o["w"], o["off"], m_total=T, save_gu=True, stream=s),
+    "gated_backward": lambda o, s: m.moe_gated_ffn_backward(o["dh"], o["gu"], o["x"], o["w"], o["off"], stream=s),
+    "product": lambda o, s: (m.moe_grouped_gemm(o["x"], o["w"], o["off"], m_total=T, stream=s),),
+    "product_backward": lambda o, s: m.moe_grouped_gemm_backward(o["dy"], o["x"], o["w"], o["off"], stream=s),
+    "int8_quantize": lambda o, s: (lambda q: (q.codes, q.scales))(m.int8_quantize(o["x"], stream=s)),
+    "int8_product": lambda o, s: (m.int8_grouped_gemm(o["q"], o["wq"], o["off"], m_total=T, stream=s),),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_calls_memory_comes_from_the_pool_of_its_stream(pools, name):
+    o = _operands()
+    pools["alloc"].clear()
+    results = CALLS[name](o, Stream(SIDE))
+    assert pools["calls"] == 1 and len(pools["alloc"]) >= len(results)
+    assert {s for s, _ in pools["alloc"]} == {SIDE}
+    for r in results:                       # the caller reads them on its own stream
+        assert any(s == MAIN and t is r for s, t in pools["held"])
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_without_a_stream_the_current_one_is_used(pools, name):
+    o = _operands()
+    pools["alloc"].clear()
+    CALLS[name](o, None)
+    assert pools["calls"] == 1 and {s for s, _ in pools["alloc"]} == {MAIN} and not pools["held"]
