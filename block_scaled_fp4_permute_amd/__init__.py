@@ -1045,7 +1045,7 @@ def moe_unpermute_combine(y, perm_of_assignment, topk_w, T: int, k: int, out=Non
     _need(y, y.dtype, "y")
     H = y.shape[1]
     if out is None:
-        out = torch.empty((T, H), dtype=out_dtype or torch.bfloat16, device=y.device)
+        out = _result(None, (T, H), out_dtype or torch.bfloat16, y, "out", stream)
     if tuple(out.shape) != (T, H):
         raise ValueError(f"out: expected [{T}, {H}], got {list(out.shape)}")
     _need(out, out.dtype, "out")

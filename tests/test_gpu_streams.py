@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import block_scaled_fp4_permute_amd as m
+from block_scaled_fp4_permute_amd.layer import MoELayer16
 from tests.gpu_common import DEV
 
 pytestmark = pytest.mark.gpu
@@ -31,6 +32,7 @@ CALLS = {
     "product_backward": lambda o, s: m.moe_grouped_gemm_backward(o["dy"], o["x"], o["w"], o["off"], stream=s),
     "int8_quantize": lambda o, s: (lambda q: (q.codes, q.scales))(m.int8_quantize(o["x"], stream=s)),
     "int8_product": lambda o, s: (m.int8_grouped_gemm(o["q"], o["wq"], o["off"], m_total=M, stream=s),),
+    "combine": lambda o, s: (m.moe_unpermute_combine(o["x"], None, None, M // 2, 2, stream=s),),
 }
 
 
@@ -56,3 +58,46 @@ def test_call_beside_pending_work_on_freed_memory(name):
         for a, b in zip(got, want):
             assert torch.equal(a, b)
         del a, b, got
+
+
+def test_layer_gradients_beside_pending_work():
+    """dh, the rows' gradients, both workspaces and the token gradient of
+    expert_rows_backward are the side stream's, and the last is held for the
+    caller's stream."""
+    T = 128
+    o = _operands()
+    x, w_gu = o["x"][:T].contiguous(), o["w"]
+    w_dn = o["w"].transpose(1, 2).contiguous()[:, :, :I].contiguous()
+    layer = MoELayer16(T, H, I, E, 2, DEV)
+    layer.route(o["gu"][:T, :E].contiguous())
+    gu = torch.empty((2 * T, 2 * I), device=DEV)
+    layer.expert_rows(x, w_gu, w_dn, gu=gu)
+    dy = o["x"][T:3 * T].contiguous()
+    want = layer.expert_rows_backward(dy, gu, x, w_gu, w_dn)
+    side = torch.cuda.Stream()
+    busy = torch.randn((4096, 4096), device=DEV)
+    rows = 2 * T
+    sizes = [rows * I * 2, rows * H * 2, T * H * 2, E * 2 * I * H * 2, E * H * I * 2,
+             m.lib().moe_gated_ffn_backward_workspace_size(E, H, I, rows),
+             max(256, m.lib().moe_grouped_gemm_backward_workspace_size(E, H, I, rows))]
+    for _ in range(3):
+        blocks = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in sizes]
+        torch.cuda.synchronize()
+        for _ in range(4):
+            busy @ busy
+        for b in blocks:
+            b.fill_(255)
+        del b, blocks
+        got = layer.expert_rows_backward(dy, gu, x, w_gu, w_dn, stream=side)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        # read on the current stream behind pending work, dropped before that has run, and its memory asked for again
+        torch.cuda.current_stream().wait_stream(side)
+        busy @ busy
+        copy = got[0].clone()
+        del a, b, got
+        with torch.cuda.stream(side):
+            torch.full((T, H), float("nan"), dtype=torch.bfloat16, device=DEV)
+        torch.cuda.synchronize()
+        assert torch.equal(copy, want[0])

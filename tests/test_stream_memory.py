@@ -23,6 +23,15 @@ class Stream:
         return self.name == other.name
 
 
+class _Recorder:
+    """The library with its calls recorded; sizes are the real ones."""
+    def __init__(self, real, launched):
+        self.real, self.launched = real, launched
+
+    def __getattr__(self, name):
+        return getattr(self.real, name) if name.endswith("_size") else self.launched
+
+
 @pytest.fixture
 def pools(monkeypatch):
     """Allocations as (stream that was current, bytes); streams that blocks are held for; launches."""
@@ -56,6 +65,7 @@ def pools(monkeypatch):
     monkeypatch.setattr(torch.Tensor, "record_stream", held)
     monkeypatch.setattr(m, "_need", lambda t, dtype, name, device=None: None)
     monkeypatch.setattr(m, "_call", launched)
+    monkeypatch.setattr(m, "lib", lambda real=m.lib(): _Recorder(real, launched))
     return seen
 
 
@@ -75,6 +85,7 @@ CALLS = {
     "product_backward": lambda o, s: m.moe_grouped_gemm_backward(o["dy"], o["x"], o["w"], o["off"], stream=s),
     "int8_quantize": lambda o, s: (lambda q: (q.codes, q.scales))(m.int8_quantize(o["x"], stream=s)),
     "int8_product": lambda o, s: (m.int8_grouped_gemm(o["q"], o["wq"], o["off"], m_total=T, stream=s),),
+    "combine": lambda o, s: (m.moe_unpermute_combine(o["dy"], None, None, T // 2, 2, stream=s),),
 }
 
 
