@@ -13,6 +13,10 @@ nvfp4_grouped_gemm, moe_swiglu, moe_unpermute_combine, moe_route_quantize
 (gate_up + SwiGLU requant + down for all experts, one persistent launch at
 decode sizes); mxfp4_* and fp8_* variants; moe_gated_ffn and moe_grouped_gemm
 with their gradients (16-bit experts); int8_quantize and int8_grouped_gemm.
+
+With stream=, operands, given results and given workspaces have to be ready on
+that stream, and the caller orders it before work that reads the results; the
+memory that a call allocates for itself is that stream's and needs no such order.
 """
 from __future__ import annotations
 
@@ -198,7 +202,6 @@ def _stream(stream) -> int:
 
 
 def _need(t, dtype, name, device=None):
-    import torch
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if not t.is_cuda:
@@ -207,6 +210,28 @@ def _need(t, dtype, name, device=None):
         raise ValueError(f"{name}: must be contiguous")
     if device is not None and t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
+
+
+def _new(shape, dtype, dev, stream):
+    """Working memory of a call on ``stream`` (None: the current one), from that
+    stream's pool.  A block of the current stream's pool may have been freed
+    with work still queued there that uses it, and nothing orders that work
+    before the call's."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _new_result(shape, dtype, dev, stream):
+    """Memory for a call's result; the caller reads it on the current stream, for
+    which it is held when it is dropped."""
+    import torch
+    out = _new(shape, dtype, dev, stream)
+    if stream is not None:
+        out.record_stream(torch.cuda.current_stream(dev))
+    return out
 
 
 def _dtype_code(t):
@@ -230,6 +255,13 @@ class Routing:
     perm_weight: "object"
 
 
+def _new_routing(T, E, k, dev, stream):
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    shapes = ((T, k), i32), ((T, k), f32), (E, i32), (E + 1, i32), (T * k, i32), (T * k, i32), (T * k, f32)
+    return Routing(*(_new_result(s, t, dev, stream) for s, t in shapes))
+
+
 def moe_route_permute(logits, k: int, out: Routing | None = None, workspace=None, stream=None) -> Routing:
     """logits float32 [T, E] -> Routing (see include/nvfp4moe.h)."""
     import torch
@@ -237,13 +269,10 @@ def moe_route_permute(logits, k: int, out: Routing | None = None, workspace=None
     T, E = logits.shape
     dev = logits.device
     if out is None:
-        i32 = dict(dtype=torch.int32, device=dev)
-        out = Routing(torch.empty((T, k), **i32), torch.empty((T, k), dtype=torch.float32, device=dev),
-                      torch.empty(E, **i32), torch.empty(E + 1, **i32), torch.empty(T * k, **i32),
-                      torch.empty(T * k, **i32), torch.empty(T * k, dtype=torch.float32, device=dev))
+        out = _new_routing(T, E, k, dev, stream)
     nbytes = lib().moe_route_permute_workspace_size(T, E, k)
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        workspace = _new(max(nbytes, 16), torch.uint8, dev, stream)
     _check(lib().moe_route_permute(
         logits.data_ptr(), T, E, k, out.topk_ids.data_ptr(), out.topk_w.data_ptr(), out.counts.data_ptr(),
         out.offsets.data_ptr(), out.perm_src_token.data_ptr(), out.perm_of_assignment.data_ptr(),
@@ -269,11 +298,11 @@ def nvfp4_quantize(x, g=None, out: NVFP4Tensor | None = None, workspace=None, st
     rows, cols = x.shape
     dev = x.device
     if out is None:
-        out = NVFP4Tensor(torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev),
-                          torch.empty((rows, cols // 16), dtype=torch.uint8, device=dev),
-                          torch.empty(1, dtype=torch.float32, device=dev))
+        out = NVFP4Tensor(_new_result((rows, cols // 2), torch.uint8, dev, stream),
+                          _new_result((rows, cols // 16), torch.uint8, dev, stream),
+                          _new_result(1, torch.float32, dev, stream))
     if workspace is None:
-        workspace = torch.empty(lib().nvfp4_quantize_workspace_size(), dtype=torch.uint8, device=dev)
+        workspace = _new(lib().nvfp4_quantize_workspace_size(), torch.uint8, dev, stream)
     _check(lib().nvfp4_quantize(x.data_ptr(), _dtype_code(x), rows, cols, _ptr(g), _ptr(out.g),
                                 out.codes.data_ptr(), out.scales.data_ptr(), workspace.data_ptr(),
                                 workspace.numel(), _stream(stream)))
@@ -290,7 +319,7 @@ def nvfp4_weight_repack(codes, scales, out=None, stream=None):
     E, N, K2 = codes.shape
     nbytes = lib().nvfp4_weight_packed_size(E, N, 2 * K2)
     if out is None:
-        out = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+        out = _new_result(nbytes, torch.uint8, codes.device, stream)
     _check(lib().nvfp4_weight_repack(codes.data_ptr(), scales.data_ptr(), E, N, 2 * K2, out.data_ptr(),
                                      out.numel(), _stream(stream)))
     return out
@@ -310,17 +339,14 @@ def moe_route_quantize(logits, k: int, x, g=None, out: Routing | None = None, xq
     cols = x.shape[1]
     dev = logits.device
     if out is None:
-        i32 = dict(dtype=torch.int32, device=dev)
-        out = Routing(torch.empty((T, k), **i32), torch.empty((T, k), dtype=torch.float32, device=dev),
-                      torch.empty(E, **i32), torch.empty(E + 1, **i32), torch.empty(T * k, **i32),
-                      torch.empty(T * k, **i32), torch.empty(T * k, dtype=torch.float32, device=dev))
+        out = _new_routing(T, E, k, dev, stream)
     if xq is None:
-        xq = NVFP4Tensor(torch.empty((T, cols // 2), dtype=torch.uint8, device=dev),
-                         torch.empty((T, cols // 16), dtype=torch.uint8, device=dev),
-                         torch.empty(1, dtype=torch.float32, device=dev))
+        xq = NVFP4Tensor(_new_result((T, cols // 2), torch.uint8, dev, stream),
+                         _new_result((T, cols // 16), torch.uint8, dev, stream),
+                         _new_result(1, torch.float32, dev, stream))
     nbytes = lib().moe_route_quantize_workspace_size(T, E, k)
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        workspace = _new(max(nbytes, 16), torch.uint8, dev, stream)
     _check(lib().moe_route_quantize(
         logits.data_ptr(), T, E, k, out.topk_ids.data_ptr(), out.topk_w.data_ptr(), out.counts.data_ptr(),
         out.offsets.data_ptr(), out.perm_src_token.data_ptr(), out.perm_of_assignment.data_ptr(),
@@ -392,7 +418,7 @@ def nvfp4_grouped_gemm(a: NVFP4Tensor, b_codes, b_scales, b_g, offsets, *, m_tot
     if epilogue in (EPI_F32, EPI_BF16):
         want = torch.float32 if epilogue == EPI_F32 else torch.bfloat16
         if out is None:
-            out = torch.empty((m_total, N), dtype=want, device=dev)
+            out = _new_result((m_total, N), want, dev, stream)
         else:
             _need(out, want, "out")
             if tuple(out.shape) != (m_total, N):
@@ -402,8 +428,8 @@ def nvfp4_grouped_gemm(a: NVFP4Tensor, b_codes, b_scales, b_g, offsets, *, m_tot
             raise ValueError("EPI_SWIGLU_NVFP4 needs out_g (the per-tensor scale of h)")
         _need(out_g, torch.float32, "out_g")
         if out_codes is None:
-            out_codes = torch.empty((m_total, I // 2), dtype=torch.uint8, device=dev)
-            out_scales = torch.empty((m_total, I // 16), dtype=torch.uint8, device=dev)
+            out_codes = _new_result((m_total, I // 2), torch.uint8, dev, stream)
+            out_scales = _new_result((m_total, I // 16), torch.uint8, dev, stream)
         _need(out_codes, torch.uint8, "out_codes")
         _need(out_scales, torch.uint8, "out_scales")
         if tuple(out_codes.shape) != (m_total, I // 2) or tuple(out_scales.shape) != (m_total, I // 16):
@@ -469,12 +495,12 @@ def moe_expert_ffn(xq: NVFP4Tensor, perm_src_token, offsets, w_gu_packed, g_gu, 
         if t.numel() < n:
             raise ValueError(f"{name}: needs {n} values")
     if h is None:
-        h = NVFP4Tensor(torch.empty((m_total, I // 2), dtype=torch.uint8, device=dev),
-                        torch.empty((m_total, I // 16), dtype=torch.uint8, device=dev), g_h)
+        h = NVFP4Tensor(_new_result((m_total, I // 2), torch.uint8, dev, stream),
+                        _new_result((m_total, I // 16), torch.uint8, dev, stream), g_h)
     if tuple(h.codes.shape) != (m_total, I // 2) or tuple(h.scales.shape) != (m_total, I // 16):
         raise ValueError("h codes/scales must be [m_total, I/2] and [m_total, I/16]")
     if y is None:
-        y = torch.empty((m_total, H), dtype=torch.bfloat16, device=dev)
+        y = _new_result((m_total, H), torch.bfloat16, dev, stream)
     _need(y, torch.bfloat16, "y")
     if tuple(y.shape) != (m_total, H):
         raise ValueError("y must be bf16 [m_total, H]")
@@ -488,12 +514,12 @@ def moe_expert_ffn(xq: NVFP4Tensor, perm_src_token, offsets, w_gu_packed, g_gu, 
         if perm_of_assignment.numel() < m_total or topk_w.numel() < m_total:
             raise ValueError("perm_of_assignment and topk_w need T * k values")
         if out is None:
-            out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+            out = _new_result((T, H), torch.bfloat16, dev, stream)
         _need(out, torch.bfloat16, "out")
         if tuple(out.shape) != (T, H):
             raise ValueError("out must be bf16 [T, H]")
     if workspace is None:
-        workspace = moe_expert_ffn_workspace(E, m_total, H, I, dev)
+        workspace = _new(max(lib().moe_expert_ffn_workspace_size(E, m_total, H, I), 256), torch.uint8, dev, stream)
     args = FfnArgs(x_codes=xq.codes.data_ptr(), x_scales=xq.scales.data_ptr(), x_g=xq.g.data_ptr(),
                    x_rows=xq.codes.shape[0], perm_src_token=perm_src_token.data_ptr(), offsets=offsets.data_ptr(),
                    E=E, H=H, I=I, m_total=m_total, w_gu_packed=w_gu_packed.data_ptr(), g_gu=g_gu.data_ptr(),
@@ -524,8 +550,8 @@ def mxfp4_quantize(x, out: MXFP4Tensor | None = None, stream=None) -> MXFP4Tenso
     rows = x.numel() // cols
     dev = x.device
     if out is None:
-        out = MXFP4Tensor(torch.empty(x.shape[:-1] + (cols // 2,), dtype=torch.uint8, device=dev),
-                          torch.empty(x.shape[:-1] + (cols // 32,), dtype=torch.uint8, device=dev))
+        out = MXFP4Tensor(_new_result(x.shape[:-1] + (cols // 2,), torch.uint8, dev, stream),
+                          _new_result(x.shape[:-1] + (cols // 32,), torch.uint8, dev, stream))
     if out.codes.numel() != rows * (cols // 2) or out.scales.numel() != rows * (cols // 32):
         raise ValueError("out codes/scales do not match x")
     _need(out.codes, torch.uint8, "out.codes")
@@ -544,10 +570,17 @@ def mxfp4_weight_repack(b: MXFP4Tensor, out=None, stream=None):
     E, N, K2 = b.codes.shape
     nbytes = lib().mxfp4_weight_packed_size(E, N, 2 * K2)
     if out is None:
-        out = torch.empty(nbytes, dtype=torch.uint8, device=b.codes.device)
+        out = _new_result(nbytes, torch.uint8, b.codes.device, stream)
     _check(lib().mxfp4_weight_repack(b.codes.data_ptr(), b.scales.data_ptr(), E, N, 2 * K2, out.data_ptr(),
                                      out.numel(), _stream(stream)))
     return out
+
+
+def _new_ones(n, dev, stream):
+    """n float32 ones, filled on the call's own stream."""
+    import torch
+    with torch.cuda.stream(stream):        # None: no change
+        return torch.ones(n, dtype=torch.float32, device=dev)
 
 
 def mxfp4_grouped_gemm(a: MXFP4Tensor, b: MXFP4Tensor, offsets, *, m_total: int, a_rows=None, epilogue: int = EPI_F32,
@@ -582,23 +615,23 @@ def mxfp4_grouped_gemm(a: MXFP4Tensor, b: MXFP4Tensor, offsets, *, m_total: int,
         if a_rows.numel() < m_total:
             raise ValueError("a_rows shorter than m_total")
     if a_g is None:
-        a_g = torch.ones(1, dtype=torch.float32, device=dev)
+        a_g = _new_ones(1, dev, stream)
     if b_g is None:
-        b_g = torch.ones(E, dtype=torch.float32, device=dev)
+        b_g = _new_ones(E, dev, stream)
     _need(a_g, torch.float32, "a_g")
     _need(b_g, torch.float32, "b_g")
     I = N // 2
     if epilogue in (EPI_F32, EPI_BF16):
         want = torch.float32 if epilogue == EPI_F32 else torch.bfloat16
         if out is None:
-            out = torch.empty((m_total, N), dtype=want, device=dev)
+            out = _new_result((m_total, N), want, dev, stream)
         _need(out, want, "out")
         if tuple(out.shape) != (m_total, N):
             raise ValueError("out must be [m_total, N]")
     elif epilogue == EPI_SWIGLU_NVFP4:
         if out_codes is None:
-            out_codes = torch.empty((m_total, I // 2), dtype=torch.uint8, device=dev)
-            out_scales = torch.empty((m_total, I // 32), dtype=torch.uint8, device=dev)
+            out_codes = _new_result((m_total, I // 2), torch.uint8, dev, stream)
+            out_scales = _new_result((m_total, I // 32), torch.uint8, dev, stream)
         if tuple(out_codes.shape) != (m_total, I // 2) or tuple(out_scales.shape) != (m_total, I // 32):
             raise ValueError("out_codes/out_scales must be [m_total, I/2] and [m_total, I/32]")
     args = GemmArgs(a_codes=a.codes.data_ptr(), a_scales=a.scales.data_ptr(), a_g=a_g.data_ptr(), a_rows=_ptr(a_rows),
@@ -640,8 +673,8 @@ def fp8_quantize(x, block_rows: int = 1, out: FP8Tensor | None = None, stream=No
         sshape = x.shape[:-2] + ((rows + FP8_BLOCK - 1) // FP8_BLOCK, cols // FP8_BLOCK)
     dev = x.device
     if out is None:
-        out = FP8Tensor(torch.empty(x.shape, dtype=torch.uint8, device=dev),
-                        torch.empty(sshape, dtype=torch.float32, device=dev), block_rows)
+        out = FP8Tensor(_new_result(x.shape, torch.uint8, dev, stream),
+                        _new_result(sshape, torch.float32, dev, stream), block_rows)
     if out.codes.numel() != x.numel() or tuple(out.scales.shape) != tuple(sshape):
         raise ValueError("out codes/scales do not match x")
     _need(out.codes, torch.uint8, "out.codes")
@@ -659,8 +692,8 @@ def fp8_swiglu_quantize(gate_up, out: FP8Tensor | None = None, stream=None) -> F
     I = N2 // 2
     dev = gate_up.device
     if out is None:
-        out = FP8Tensor(torch.empty((M, I), dtype=torch.uint8, device=dev),
-                        torch.empty((M, I // FP8_BLOCK), dtype=torch.float32, device=dev), 1)
+        out = FP8Tensor(_new_result((M, I), torch.uint8, dev, stream),
+                        _new_result((M, I // FP8_BLOCK), torch.float32, dev, stream), 1)
     if tuple(out.codes.shape) != (M, I) or tuple(out.scales.shape) != (M, I // FP8_BLOCK):
         raise ValueError("out codes/scales must be [M, I] and [M, I/128]")
     _need(out.codes, torch.uint8, "out.codes")
@@ -677,7 +710,7 @@ def fp8_weight_repack(codes, out=None, stream=None):
     E, N, K = codes.shape
     nbytes = lib().fp8_weight_packed_size(E, N, K)
     if out is None:
-        out = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+        out = _new_result(nbytes, torch.uint8, codes.device, stream)
     _check(lib().fp8_weight_repack(codes.data_ptr(), E, N, K, out.data_ptr(), out.numel(), _stream(stream)))
     return out
 
@@ -716,8 +749,8 @@ def fp8_grouped_gemm(a: FP8Tensor, b_packed, b_scales, offsets, *, N: int, m_tot
             raise ValueError("fp8_grouped_gemm: SwiGLU needs N = 2I with I % 128 == 0")
         I = N // 2
         if out is None:
-            out = FP8Tensor(torch.empty((m_total, I), dtype=torch.uint8, device=dev),
-                            torch.empty((m_total, I // FP8_BLOCK), dtype=torch.float32, device=dev), 1)
+            out = FP8Tensor(_new_result((m_total, I), torch.uint8, dev, stream),
+                            _new_result((m_total, I // FP8_BLOCK), torch.float32, dev, stream), 1)
         _need(out.codes, torch.uint8, "out.codes")
         _need(out.scales, torch.float32, "out.scales")
         if tuple(out.codes.shape) != (m_total, I) or tuple(out.scales.shape) != (m_total, I // FP8_BLOCK):
@@ -733,7 +766,7 @@ def fp8_grouped_gemm(a: FP8Tensor, b_packed, b_scales, offsets, *, N: int, m_tot
         raise ValueError("fp8_grouped_gemm: epilogue F32, BF16 or SwiGLU")
     want = torch.float32 if epilogue == EPI_F32 else torch.bfloat16
     if out is None:
-        out = torch.empty((m_total, N), dtype=want, device=dev)
+        out = _new_result((m_total, N), want, dev, stream)
     _need(out, want, "out")
     if tuple(out.shape) != (m_total, N):
         raise ValueError("out must be [m_total, N]")
@@ -746,9 +779,6 @@ def fp8_grouped_gemm(a: FP8Tensor, b_packed, b_scales, offsets, *, N: int, m_tot
 
 
 # ----------------------------------------------------------------- 16-bit expert FFN
-# With stream=, the operands (and given results and workspaces) have to be ready
-# on that stream, and the caller orders it before work that reads the results;
-# the memory that a call allocates needs no such order.
 def _call(dev, stream, fn, *args):
     """A C call on ``stream`` (None: the current stream of the operands' device)
     with that device current."""
@@ -798,26 +828,10 @@ def _group(b, offsets, dev):
     return E
 
 
-def _new(shape, dtype, dev, stream):
-    """Memory for a call on ``stream`` (None: the current one), from that
-    stream's pool.  A block of the current stream's pool may have been freed
-    with work still queued there that uses it, and nothing orders that work
-    before the call's."""
-    import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
-
-
 def _result(out, shape, dtype, like, name, stream):
     """A given result checked, or a new one on ``like``'s device."""
-    import torch
     if out is None:
-        out = _new(shape, dtype, like.device, stream)
-        if stream is not None:             # the caller reads it on the current stream: dropped, it is held until that is done
-            out.record_stream(torch.cuda.current_stream(like.device))
-        return out
+        return _new_result(shape, dtype, like.device, stream)
     _need(out, dtype, name, like.device)
     if tuple(out.shape) != tuple(shape):
         raise ValueError(f"{name}: expected {list(shape)}, got {list(out.shape)}")
@@ -1027,11 +1041,11 @@ def moe_swiglu(gate_up, g=None, out: NVFP4Tensor | None = None, workspace=None, 
     I = N2 // 2
     dev = gate_up.device
     if out is None:
-        out = NVFP4Tensor(torch.empty((M, I // 2), dtype=torch.uint8, device=dev),
-                          torch.empty((M, I // 16), dtype=torch.uint8, device=dev),
-                          torch.empty(1, dtype=torch.float32, device=dev))
+        out = NVFP4Tensor(_new_result((M, I // 2), torch.uint8, dev, stream),
+                          _new_result((M, I // 16), torch.uint8, dev, stream),
+                          _new_result(1, torch.float32, dev, stream))
     if workspace is None:
-        workspace = torch.empty(lib().moe_swiglu_workspace_size(), dtype=torch.uint8, device=dev)
+        workspace = _new(lib().moe_swiglu_workspace_size(), torch.uint8, dev, stream)
     _check(lib().moe_swiglu(gate_up.data_ptr(), _dtype_code(gate_up), M, I, _ptr(g), _ptr(out.g),
                             out.codes.data_ptr(), out.scales.data_ptr(), workspace.data_ptr(), workspace.numel(),
                             _stream(stream)))

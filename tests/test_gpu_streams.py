@@ -101,3 +101,45 @@ def test_layer_gradients_beside_pending_work():
             torch.full((T, H), float("nan"), dtype=torch.bfloat16, device=DEV)
         torch.cuda.synchronize()
         assert torch.equal(copy, want[0])
+
+
+def test_block_scaled_calls_beside_pending_work():
+    """The same of the calls on block-scaled operands: operands quantised, and
+    multiplied, on the side stream."""
+    o = _operands()
+
+    def calls(s):
+        a, b = m.nvfp4_quantize(o["x"], stream=s), m.mxfp4_quantize(o["x"], stream=s)
+        w = m.nvfp4_quantize(o["w"].view(-1, H), stream=s)
+        codes, scales = w.codes.view(E, 2 * I, H // 2), w.scales.view(E, 2 * I, H // 16)
+        g = _two(w.g, s)
+        y = m.nvfp4_grouped_gemm(a, codes, scales, g, o["off"], m_total=M, stream=s)
+        q = m.moe_swiglu(y, stream=s)
+        mw = m.mxfp4_quantize(o["w"], stream=s)
+        z = m.mxfp4_grouped_gemm(b, mw, o["off"], m_total=M, stream=s)
+        f = m.fp8_quantize(o["x"], stream=s)
+        r = m.moe_route_permute(logits, 8, stream=s)
+        return (a.codes, a.scales, b.codes, y, q.codes, q.scales, z, f.codes, f.scales, r.topk_ids, r.perm_src_token)
+
+    def _two(t, s):
+        with torch.cuda.stream(s):
+            return t.expand(E).contiguous()
+
+    logits = o["gu"][:, :64].contiguous()
+    want = calls(None)
+    sizes = [t.numel() * t.element_size() for t in want] * 2
+    side = torch.cuda.Stream()
+    busy = torch.randn((4096, 4096), device=DEV)
+    for _ in range(3):
+        blocks = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in sizes]
+        torch.cuda.synchronize()
+        for _ in range(4):
+            busy @ busy
+        for b in blocks:
+            b.fill_(255)
+        del b, blocks
+        got = calls(side)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        del a, b, got

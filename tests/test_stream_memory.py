@@ -40,7 +40,7 @@ def pools(monkeypatch):
 
     @contextlib.contextmanager
     def stream(s):
-        before, current[0] = current[0], s
+        before, current[0] = current[0], s or current[0]
         yield
         current[0] = before
 
@@ -61,6 +61,7 @@ def pools(monkeypatch):
     monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current[0])
     monkeypatch.setattr(torch, "empty", recording(torch.empty))
+    monkeypatch.setattr(torch, "ones", recording(torch.ones))
     monkeypatch.setattr(torch.Tensor, "new_empty", recording(torch.Tensor.new_empty))
     monkeypatch.setattr(torch.Tensor, "record_stream", held)
     monkeypatch.setattr(m, "_need", lambda t, dtype, name, device=None: None)
@@ -69,13 +70,27 @@ def pools(monkeypatch):
     return seen
 
 
+def _u8(*shape):
+    return torch.zeros(shape, dtype=torch.uint8)
+
+
 def _operands():
     bf = torch.bfloat16
     off = torch.tensor([0, 8, T], dtype=torch.int32)
     return dict(x=torch.zeros((T, H), dtype=bf), w=torch.zeros((E, 2 * I, H), dtype=bf), off=off,
                 dh=torch.zeros((T, I), dtype=bf), gu=torch.zeros((T, 2 * I)), dy=torch.zeros((T, 2 * I), dtype=bf),
+                logits=torch.zeros((T, E)), g=torch.ones(E), perm=torch.zeros(T, dtype=torch.int32),
+                x4=m.NVFP4Tensor(_u8(T, H // 2), _u8(T, H // 16), torch.ones(1)),
+                w4=m.NVFP4Tensor(_u8(E, 2 * I, H // 2), _u8(E, 2 * I, H // 16), torch.ones(E)), packed=_u8(1 << 18),
+                xm=m.MXFP4Tensor(_u8(T, H // 2), _u8(T, H // 32)), wm=m.MXFP4Tensor(_u8(E, 2 * I, H // 2), _u8(E, 2 * I, H // 32)),
+                x8=torch.zeros((T, 128), dtype=bf), gu8=torch.zeros((T, 256), dtype=bf), w8=_u8(E, 256, 128),
+                a8=m.FP8Tensor(_u8(T, 128), torch.ones((T, 1)), 1), s8=torch.ones((E, 2, 1)),
                 q=m.INT8Tensor(torch.zeros((T, H), dtype=torch.int8), torch.ones(T)),
                 wq=m.INT8Tensor(torch.zeros((E, 2 * I, H), dtype=torch.int8), torch.ones((E, 2 * I))))
+
+
+def _fields(t):
+    return tuple(vars(t).values())
 
 
 CALLS = {
@@ -85,6 +100,30 @@ CALLS = {
     "product_backward": lambda o, s: m.moe_grouped_gemm_backward(o["dy"], o["x"], o["w"], o["off"], stream=s),
     "int8_quantize": lambda o, s: (lambda q: (q.codes, q.scales))(m.int8_quantize(o["x"], stream=s)),
     "int8_product": lambda o, s: (m.int8_grouped_gemm(o["q"], o["wq"], o["off"], m_total=T, stream=s),),
+    "route": lambda o, s: _fields(m.moe_route_permute(o["logits"], 2, stream=s)),
+    "quantize": lambda o, s: _fields(m.nvfp4_quantize(o["x"], stream=s)),
+    "route_quantize": lambda o, s: sum(map(_fields, m.moe_route_quantize(o["logits"], 2, o["x"], stream=s)), ()),
+    "repack": lambda o, s: (m.nvfp4_weight_repack(o["w4"].codes, o["w4"].scales, stream=s),),
+    "nvfp4": lambda o, s: (m.nvfp4_grouped_gemm(o["x4"], o["w4"].codes, o["w4"].scales, o["g"], o["off"], m_total=T,
+                                                stream=s),),
+    "nvfp4_swiglu": lambda o, s: _fields(m.nvfp4_grouped_gemm(
+        o["x4"], o["w4"].codes, o["w4"].scales, o["g"], o["off"], m_total=T, epilogue=m.EPI_SWIGLU_NVFP4,
+        out_g=o["g"], stream=s))[:2],
+    "ffn": lambda o, s: (lambda r: _fields(r[0])[:2] + r[1:])(m.moe_expert_ffn(
+        o["x4"], o["perm"], o["off"], o["packed"], o["g"], o["packed"], o["g"], o["g"], H=H, I=I, m_total=T,
+        perm_of_assignment=o["perm"], topk_w=o["gu"], k=2, stream=s)),
+    "mx_quantize": lambda o, s: _fields(m.mxfp4_quantize(o["x"], stream=s)),
+    "mx_repack": lambda o, s: (m.mxfp4_weight_repack(o["wm"], stream=s),),
+    "mx": lambda o, s: (m.mxfp4_grouped_gemm(o["xm"], o["wm"], o["off"], m_total=T, stream=s),),
+    "mx_swiglu": lambda o, s: _fields(m.mxfp4_grouped_gemm(o["xm"], o["wm"], o["off"], m_total=T,
+                                                           epilogue=m.EPI_SWIGLU_NVFP4, stream=s)),
+    "fp8_quantize": lambda o, s: _fields(m.fp8_quantize(o["x8"], stream=s))[:2],
+    "fp8_swiglu": lambda o, s: _fields(m.fp8_swiglu_quantize(o["gu8"], stream=s))[:2],
+    "fp8_repack": lambda o, s: (m.fp8_weight_repack(o["w8"], stream=s),),
+    "fp8": lambda o, s: (m.fp8_grouped_gemm(o["a8"], o["packed"], o["s8"], o["off"], N=256, m_total=T, stream=s),),
+    "fp8_gated": lambda o, s: _fields(m.fp8_grouped_gemm(o["a8"], o["packed"], o["s8"], o["off"], N=256, m_total=T,
+                                                         epilogue=m.EPI_SWIGLU_NVFP4, stream=s))[:2],
+    "swiglu": lambda o, s: _fields(m.moe_swiglu(o["gu"], stream=s)),
     "combine": lambda o, s: (m.moe_unpermute_combine(o["dy"], None, None, T // 2, 2, stream=s),),
 }
 
