@@ -201,6 +201,25 @@ def _stream(stream) -> int:
     return stream.cuda_stream
 
 
+def _call(dev, stream, fn, *args):
+    """A C call on ``stream`` (None: the current stream of the operands' device)
+    with that device current, whichever one is."""
+    import torch
+    if stream is not None:
+        if getattr(stream, "device", dev) != dev:
+            raise ValueError(f"stream: of {stream.device}, the operands are on {dev}")
+        raw = stream.cuda_stream
+    else:
+        raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    if torch._C._cuda_getDevice() == dev.index:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status:
+        _check(status)
+
+
 def _need(t, dtype, name, device=None):
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
@@ -273,10 +292,10 @@ def moe_route_permute(logits, k: int, out: Routing | None = None, workspace=None
     nbytes = lib().moe_route_permute_workspace_size(T, E, k)
     if workspace is None:
         workspace = _new(max(nbytes, 16), torch.uint8, dev, stream)
-    _check(lib().moe_route_permute(
-        logits.data_ptr(), T, E, k, out.topk_ids.data_ptr(), out.topk_w.data_ptr(), out.counts.data_ptr(),
-        out.offsets.data_ptr(), out.perm_src_token.data_ptr(), out.perm_of_assignment.data_ptr(),
-        _ptr(out.perm_weight), workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    _call(dev, stream, lib().moe_route_permute,
+          logits.data_ptr(), T, E, k, out.topk_ids.data_ptr(), out.topk_w.data_ptr(), out.counts.data_ptr(),
+          out.offsets.data_ptr(), out.perm_src_token.data_ptr(), out.perm_of_assignment.data_ptr(),
+          _ptr(out.perm_weight), workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -779,23 +798,6 @@ def fp8_grouped_gemm(a: FP8Tensor, b_packed, b_scales, offsets, *, N: int, m_tot
 
 
 # ----------------------------------------------------------------- 16-bit expert FFN
-def _call(dev, stream, fn, *args):
-    """A C call on ``stream`` (None: the current stream of the operands' device)
-    with that device current."""
-    import torch
-    if stream is not None:
-        raw = stream.cuda_stream
-    else:
-        raw = torch._C._cuda_getCurrentRawStream(dev.index)
-    if torch._C._cuda_getDevice() == dev.index:
-        status = fn(*args, raw)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, raw)
-    if status:
-        _check(status)
-
-
 def _dtype16(t, name):
     import torch
     if t.dtype == torch.bfloat16:
@@ -1073,8 +1075,8 @@ def moe_unpermute_combine(y, perm_of_assignment, topk_w, T: int, k: int, out=Non
         _need(topk_w, torch.float32, "topk_w")
         if topk_w.numel() < T * k:
             raise ValueError(f"topk_w: {topk_w.numel()} values, expected T*k = {T * k}")
-    _check(lib().moe_unpermute_combine(y.data_ptr(), _dtype_code(y), _ptr(perm_of_assignment), _ptr(topk_w),
-                                       T, k, H, out.data_ptr(), _dtype_code(out), _stream(stream)))
+    _call(y.device, stream, lib().moe_unpermute_combine, y.data_ptr(), _dtype_code(y), _ptr(perm_of_assignment),
+          _ptr(topk_w), T, k, H, out.data_ptr(), _dtype_code(out))
     return out
 
 
