@@ -497,8 +497,11 @@ class MoELayer16:
         self.h = torch.empty((M, I), dtype=dtype, device=dev)
         self.y2 = torch.empty((M, H), dtype=dtype, device=dev)
         self.out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        # address of the gu that belongs to self.h and self.routing; only to refuse other gradients with
+        self._gu_of_h = None
 
     def route(self, logits: torch.Tensor, stream=None) -> Routing:
+        self._gu_of_h = None
         return moe_route_permute(logits, self.k, out=self.routing, workspace=self.route_ws, stream=stream)
 
     def forward(self, logits: torch.Tensor, x: torch.Tensor, w_gu: torch.Tensor, w_dn: torch.Tensor,
@@ -512,20 +515,29 @@ class MoELayer16:
     def expert_rows(self, x: torch.Tensor, w_gu: torch.Tensor, w_dn: torch.Tensor, gu: torch.Tensor | None = None,
                     stream=None) -> torch.Tensor:
         """y [T*k, H] of the routing made last (unweighted, in expert order); gu: float32
-        [T*k, 2I] for the pre-activations that expert_rows_backward needs."""
+        [T*k, 2I] for the pre-activations that expert_rows_backward needs.  y is
+        the layer's buffer: the next expert_rows or forward writes it again."""
         from . import moe_gated_ffn, moe_grouped_gemm
         r, M = self.routing, self.T * self.k
+        self._gu_of_h = None
         moe_gated_ffn(x, w_gu, r.offsets, m_total=M, a_rows=r.perm_src_token, activation=self.activation, out=self.h,
                       gu=gu, stream=stream)
-        return moe_grouped_gemm(self.h, w_dn, r.offsets, m_total=M, out=self.y2, stream=stream)
+        moe_grouped_gemm(self.h, w_dn, r.offsets, m_total=M, out=self.y2, stream=stream)
+        self._gu_of_h = None if gu is None else gu.data_ptr()
+        return self.y2
 
     def expert_rows_backward(self, dy: torch.Tensor, gu: torch.Tensor, x: torch.Tensor, w_gu: torch.Tensor,
                              w_dn: torch.Tensor, stream=None):
-        """Gradients from dy [T*k, H] of the last expert_rows call: (dx, dw_gu,
-        dw_dn).  dx [T, H] sums each token's rows in bf16; with float16 weights
-        dx is the rows [T*k, H] themselves."""
+        """Gradients from dy [T*k, H] of the last expert_rows call, whose gu and x
+        these are: (dx, dw_gu, dw_dn).  h and the routing are the layer's own, so
+        the gradients of an earlier call (any route, forward or expert_rows since)
+        are refused: batches in flight side by side take a layer each.  dx [T, H]
+        sums each token's rows in bf16; with float16 weights dx is the rows
+        [T*k, H] themselves."""
         from . import moe_gated_ffn_backward, moe_grouped_gemm_backward
         r = self.routing
+        if self._gu_of_h is None or gu.data_ptr() != self._gu_of_h:
+            raise ValueError("gu is not that of the last expert_rows call: h and the routing are another call's")
         dh, dw_dn = moe_grouped_gemm_backward(dy, self.h, w_dn, r.offsets, stream=stream)
         dx, dw_gu = moe_gated_ffn_backward(dh, gu, x, w_gu, r.offsets, a_rows=r.perm_src_token,
                                            activation=self.activation, stream=stream)
