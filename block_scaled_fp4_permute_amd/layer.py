@@ -507,6 +507,8 @@ class MoELayer16:
     def forward(self, logits: torch.Tensor, x: torch.Tensor, w_gu: torch.Tensor, w_dn: torch.Tensor,
                 stream=None) -> torch.Tensor:
         """One layer step, bf16 [T, H]."""
+        if self.dtype == torch.float16:
+            raise TypeError("forward: the combine takes bfloat16 rows, not float16 ones (use route and expert_rows)")
         r = self.route(logits, stream)
         self.expert_rows(x, w_gu, w_dn, stream=stream)
         return moe_unpermute_combine(self.y2, r.perm_of_assignment, r.topk_w, self.T, self.k, out=self.out,

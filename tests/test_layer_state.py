@@ -58,3 +58,17 @@ def test_gradients_of_another_call_are_refused(layer, between):
         layer.expert_rows_backward(dy, gu, *ops)
     if between == "another_batch":
         assert len(layer.expert_rows_backward(dy, other, *ops)) == 3
+
+
+def test_float16_forward_is_refused_before_anything_runs(monkeypatch):
+    """The combine takes no float16 rows; expert_rows is for those."""
+    ran = []
+    monkeypatch.setattr(m, "_need", lambda t, dtype, name, device=None: None)
+    monkeypatch.setattr(m, "_call", lambda *a: ran.append(a))
+    layer = MoELayer16(T, H, I, E, K, "cpu", dtype=torch.float16)
+    x, w_gu, w_dn = (t.half() for t in _operands())
+    with pytest.raises(TypeError, match="float16"):
+        layer.forward(torch.zeros((T, E)), x, w_gu, w_dn)
+    assert not ran
+    layer.route(torch.zeros((T, E)))
+    assert layer.expert_rows(x, w_gu, w_dn).dtype == torch.float16
