@@ -781,6 +781,12 @@ size_t grad_parts_bytes(int32_t E, int32_t n, int32_t k, int64_t m_total) {
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
+// whether the activation's gradient fits a grid (below 2^32 threads of 256 a block);
+// with I = 8 rows beyond it would still fit the memory
+bool gated_grad_fits(int32_t E, int32_t I, int64_t m_total) {
+  return nvfp4::gated_grad_blocks(I, m_total, E) < (int64_t(1) << 24);
+}
+
 // da = dy b and db = dy^T a of one grouped product: dy [m_total, n], b [E, n, k];
 // dy_t (nullable): dy transposed, [n, ld], for db
 int product_grad(const char* fn, int32_t dtype, const void* dy, const void* dy_t, int64_t ld, const void* a, const int32_t* a_rows, int64_t rows_total,
@@ -859,7 +865,7 @@ int moe_gated_ffn(const nvfp4moe_gated_args* a, void* stream) {
 
 size_t moe_gated_ffn_backward_workspace_size(int32_t E, int32_t H, int32_t I, int64_t m_total) {
   if (E <= 0 || E > 4096 || H <= 0 || I <= 0 || m_total < 0 || H % 8 != 0 || I % 8 != 0 || m_total >= (int64_t(1) << 30) ||
-      I > (1 << 25))
+      I > (1 << 25) || !gated_grad_fits(E, I, m_total))
     return 0;
   // dg and du in 16 bits, by rows and transposed, and the parts of dx
   return round256((static_cast<size_t>(m_total) + nvfp4::gated_grad_ld(m_total, E)) * 2 * static_cast<size_t>(I) * 2) +
@@ -881,6 +887,8 @@ int moe_gated_ffn_backward(const nvfp4moe_gated_grad_args* a, void* workspace, s
   if (!aligned(a->x, 16) || !aligned(a->w, 16) || !aligned(a->gu, 16) || !aligned(a->dh, 16) || !aligned(a->dx, 16) ||
       !aligned(a->dw, 16))
     return fail(NVFP4MOE_ERR_INVALID, "%s: pointers must be 16-byte aligned", fn);
+  if (!gated_grad_fits(a->E, a->I, a->m_total))
+    return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: 2^24 blocks of 64 rows and 64 columns, or more", fn);
   const size_t need = moe_gated_ffn_backward_workspace_size(a->E, a->H, a->I, a->m_total);
   if (!workspace || workspace_bytes < need)
     return fail(NVFP4MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes, need);

@@ -106,11 +106,15 @@ int64_t gated_grad_ld(int64_t m_total, int E) {
   return tg_start_col(m_total, E, align) + align;
 }
 
+int64_t gated_grad_blocks(int I, int64_t m_total, int E) {
+  const int64_t chunks = m_total / kGgRows + (E < m_total ? E : m_total);
+  return (chunks * ((I + kGgCols - 1) / kGgCols) + 7) / 8 * 8;
+}
+
 hipError_t launch_gated_grad(const float* gu, const void* dh, int dtype_f16, int I, int64_t m_total, const int32_t* offsets,
                              int E, int act, void* dgu, void* dgu_t, hipStream_t stream) {
-  const int64_t chunks = m_total / kGgRows + (E < m_total ? E : m_total);
-  const int64_t blocks = (chunks * ((I + kGgCols - 1) / kGgCols) + 7) / 8 * 8;
-  if (blocks >= (int64_t(1) << 24)) return hipErrorInvalidConfiguration;   // 2^32 threads (more values than the memory holds)
+  const int64_t blocks = gated_grad_blocks(I, m_total, E);
+  if (blocks >= (int64_t(1) << 24)) return hipErrorInvalidConfiguration;   // 2^32 threads (the entry point refuses them)
   const dim3 grid(static_cast<unsigned>(blocks));
   const int64_t ld = gated_grad_ld(m_total, E);
   if (dtype_f16)

@@ -124,6 +124,7 @@ hipError_t launch_tile_gemm_i8(const TileParams& p, int epilogue, hipStream_t st
 hipError_t launch_gated_grad(const float* gu, const void* dh, int dtype_f16, int I, int64_t m_total,
                              const int32_t* offsets, int E, int act, void* dgu, void* dgu_t, hipStream_t stream);
 int64_t gated_grad_ld(int64_t m_total, int E);   // columns of dgu_t
+int64_t gated_grad_blocks(int I, int64_t m_total, int E);   // workgroups, fewer than 2^24
 // sum of `parts` float32 matrices [rows, N] in their order, rounded to 16 bits; with offsets, rows behind the last expert are left
 hipError_t launch_join(const float* part, int parts, int64_t rows, int N, const int32_t* offsets, int E, int dtype_f16,
                        void* out, hipStream_t stream);

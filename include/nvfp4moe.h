@@ -454,8 +454,10 @@ int moe_gated_ffn(const nvfp4moe_gated_args* args, void* stream);
  * dx rows are per GEMM row: for gathered x, the gradient of a token is the sum
  * of its rows, moe_unpermute_combine(dx, perm_of_assignment, NULL, ...).
  * Either of dx and dw may be NULL (not wanted).  dw of an expert without rows
- * is zero.  workspace: moe_gated_ffn_backward_workspace_size bytes, 256-byte
- * aligned, caller-owned; calls sharing one must not overlap. */
+ * is zero.  (m_total / 64 + min(E, m_total)) * ceil(I / 64) <= 2^24 - 8: for
+ * I <= 64 about 2^30 - 64 E rows.  workspace:
+ * moe_gated_ffn_backward_workspace_size bytes, 256-byte aligned, caller-owned;
+ * calls sharing one must not overlap. */
 typedef struct nvfp4moe_gated_grad_args {
   const void* x;              /* as in the forward call (not read when dw is NULL) */
   int32_t dtype;
