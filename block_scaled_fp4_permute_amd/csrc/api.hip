@@ -685,6 +685,19 @@ int fp8_grouped_gemm(const nvfp4moe_fp8_gemm_args* a, void* stream) {
 // ------------------------------------------------------------------ 16-bit expert FFN
 namespace {
 
+// 2^31 tiles or more: one grid dimension holds every tile of the smallest tile shape
+bool too_many_tiles(int32_t E, int32_t N, int32_t K, int64_t m_total) {
+  const int64_t chunks = m_total / 16 + (E < m_total ? E : m_total);
+  return prod_ge(chunks, N / 64 + 1, int64_t(1) << 31) || prod_ge(chunks, K / 64 + 1, int64_t(1) << 31) ||
+         prod_ge(E, N / 64 + 1, K / 64 + 1, int64_t(1) << 31);
+}
+
+// the sizes that check_plain lets through, for the workspace queries
+bool plain_sizes(int32_t E, int32_t N, int32_t K, int64_t m_total) {
+  return E > 0 && E <= 4096 && N > 0 && N <= (1 << 26) && N % 8 == 0 && K > 0 && K <= (1 << 26) && K % 8 == 0 && m_total >= 0 &&
+         m_total < (int64_t(1) << 30) && !too_many_tiles(E, N, K, m_total);
+}
+
 // the checks that the calls on plain operands share; `row_ptrs` is whether
 // every row operand is there (needed once there are rows)
 int check_plain(const char* fn, int32_t dtype, const int32_t* offsets, int32_t E, int32_t N, int32_t K, int64_t m_total,
@@ -707,10 +720,7 @@ int check_plain(const char* fn, int32_t dtype, const int32_t* offsets, int32_t E
       return fail(NVFP4MOE_ERR_INVALID, "%s: %lld source rows for %lld GEMM rows", fn, static_cast<long long>(rows_total),
                   static_cast<long long>(m_total));
   }
-  // one grid dimension holds every tile of the smallest tile shape
-  const int64_t chunks = m_total / 16 + (E < m_total ? E : m_total);
-  if (prod_ge(chunks, N / 64 + 1, int64_t(1) << 31) || prod_ge(chunks, K / 64 + 1, int64_t(1) << 31) ||
-      prod_ge(E, N / 64 + 1, K / 64 + 1, int64_t(1) << 31))
+  if (too_many_tiles(E, N, K, m_total))
     return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: 2^31 tiles or more", fn);
   return NVFP4MOE_OK;
 }
@@ -864,9 +874,7 @@ int moe_gated_ffn(const nvfp4moe_gated_args* a, void* stream) {
 }
 
 size_t moe_gated_ffn_backward_workspace_size(int32_t E, int32_t H, int32_t I, int64_t m_total) {
-  if (E <= 0 || E > 4096 || H <= 0 || I <= 0 || m_total < 0 || H % 8 != 0 || I % 8 != 0 || m_total >= (int64_t(1) << 30) ||
-      I > (1 << 25) || !gated_grad_fits(E, I, m_total))
-    return 0;
+  if (I <= 0 || I > (1 << 25) || I % 8 != 0 || !plain_sizes(E, 2 * I, H, m_total) || !gated_grad_fits(E, I, m_total)) return 0;
   // dg and du in 16 bits, by rows and transposed, and the parts of dx
   return round256((static_cast<size_t>(m_total) + nvfp4::gated_grad_ld(m_total, E)) * 2 * static_cast<size_t>(I) * 2) +
          grad_parts_bytes(E, 2 * I, H, m_total);
@@ -940,9 +948,7 @@ int moe_grouped_gemm(const nvfp4moe_product_args* a, void* stream) {
 }
 
 size_t moe_grouped_gemm_backward_workspace_size(int32_t E, int32_t N, int32_t K, int64_t m_total) {
-  if (E <= 0 || E > 4096 || N <= 0 || K <= 0 || N % 8 != 0 || K % 8 != 0 || m_total < 0 || m_total >= (int64_t(1) << 30) ||
-      N > (1 << 26) || K > (1 << 26))
-    return 0;
+  if (!plain_sizes(E, N, K, m_total)) return 0;
   return grad_parts_bytes(E, N, K, m_total);
 }
 
