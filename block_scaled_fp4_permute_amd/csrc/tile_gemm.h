@@ -119,15 +119,21 @@ __device__ const u32x4 tg_zero[32] = {};
 
 // The load is written as assembly because the compiler, which cannot tell
 // which stage a read touches, would wait for every load in flight before each
-// transposing read.  It has no register result; tg_wait waits for it.
+// transposing read.  It has no register result; tg_wait waits for it.  m0 is
+// named as written, so that no m0 of the compiler's own (which it sets in front
+// of an instruction that reads it, none in these kernels today) lies across it;
+// the warning, that the compiler keeps no value in m0, does not matter then.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void tg_dma(const uint8_t* src, uint32_t lds_wave) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_wave), "v"(src) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_wave), "v"(src) : "memory", "m0");
 }
 
 // the same of 4 bytes a lane
 __device__ __forceinline__ void tg_dma4(const float* src, uint32_t lds_wave) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds_wave), "v"(src) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds_wave), "v"(src) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // all but the N youngest memory operations of this wave are done, its LDS
 // reads too, and so for every wave of the workgroup
