@@ -16,6 +16,9 @@ namespace nvfp4 {
 // quotient's own move it by less than 127 * 3 * 2^-24 < 2^-15, and only there
 // can they decide otherwise than the divided quotient.  Below 2^-100 the
 // reciprocal could leave float32's range, and the row is divided throughout.
+//
+// The maximum keeps a NaN (as many instructions as one that drops it): a row that
+// holds one, or an infinity, gets scale NaN and codes 0.
 template <int DT>
 struct Q8Piece {
   u32x4 w[DT == 0 ? 2 : 1];
@@ -42,14 +45,14 @@ __device__ __forceinline__ int q8_code(float x, float s, float inv, bool fast) {
 }
 
 template <int DT>
-__device__ __forceinline__ void q8_store(const Q8Piece<DT>& v, float s, float inv, bool fast, int8_t* __restrict__ dst) {
+__device__ __forceinline__ void q8_store(const Q8Piece<DT>& v, float s, float inv, bool fast, uint32_t keep, int8_t* __restrict__ dst) {
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t r = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) r |= (static_cast<uint32_t>(q8_code(v.at(4 * h + i), s, inv, fast)) & 0xFFu) << (8 * i);
-    w[h] = r;
+    w[h] = r & keep;
   }
   *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
 }
@@ -58,12 +61,12 @@ __device__ __forceinline__ void q8_store(const Q8Piece<DT>& v, float s, float in
 template <int LPR>
 __device__ __forceinline__ float q8_row_max(float m) {
 #pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+  for (int d = 32; d >= 1; d >>= 1) m = __builtin_elementwise_maximum(m, __shfl_xor(m, d));
   if constexpr (LPR == 256) {
     __shared__ float part[4];
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
     __syncthreads();
-    m = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+    m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(part[0], part[1]), __builtin_elementwise_maximum(part[2], part[3]));
   }
   return m;
 }
@@ -88,17 +91,19 @@ __global__ __launch_bounds__(256) void k_int8_quantize(const void* __restrict__ 
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int q = 0; q < 8; ++q) top = fmaxf(top, fabsf(v[i].at(q)));
+      for (int q = 0; q < 8; ++q) top = __builtin_elementwise_maximum(top, fabsf(v[i].at(q)));
   } else {
     for (int c = l; c < pieces; c += LPR) {
       const Q8Piece<DT> w = q8_load<DT>(x, base + 8 * static_cast<int64_t>(c));
 #pragma unroll
-      for (int q = 0; q < 8; ++q) top = fmaxf(top, fabsf(w.at(q)));
+      for (int q = 0; q < 8; ++q) top = __builtin_elementwise_maximum(top, fabsf(w.at(q)));
     }
   }
   top = q8_row_max<LPR>(top);
-  float s = top * (1.0f / 127.0f);
-  if (!(s > 0.0f)) s = 1.0f;
+  const bool finite = top < __builtin_inff();
+  const uint32_t keep = finite ? ~0u : 0u;  // of the codes
+  float s = finite ? top * (1.0f / 127.0f) : __builtin_nanf("");
+  if (s == 0.0f) s = 1.0f;
   const bool fast = s > 0x1p-100f;
   const float inv = 1.0f / s;
   if (l == 0) scales[row] = s;
@@ -106,12 +111,12 @@ __global__ __launch_bounds__(256) void k_int8_quantize(const void* __restrict__ 
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = l + i * LPR;
-      if (c < pieces) q8_store<DT>(v[i], s, inv, fast, codes + base + 8 * c);
+      if (c < pieces) q8_store<DT>(v[i], s, inv, fast, keep, codes + base + 8 * c);
     }
   } else {
     for (int c = l; c < pieces; c += LPR) {
       const int64_t o = base + 8 * static_cast<int64_t>(c);
-      q8_store<DT>(q8_load<DT>(x, o), s, inv, fast, codes + o);
+      q8_store<DT>(q8_load<DT>(x, o), s, inv, fast, keep, codes + o);
     }
   }
 }

@@ -521,10 +521,12 @@ int moe_grouped_gemm_backward(const nvfp4moe_product_grad_args* args, void* work
 /* ---------------------------------------------------------------- INT8 variant
  * Symmetric 8-bit integers with one float32 scale per row: per token for
  * activations, per output channel for weights (value = code * scale).
- * int8_quantize: x [rows, cols] (bf16 or float32, finite) -> codes int8 in
- * [-127, 127] and scales [rows]: s = absmax * (1/127) (float32 product with the
- * float32 nearest 1/127; 1 where that is zero), code = nearest-even integer of the correctly rounded float32
- * quotient x / s.  Reproducible bit for bit.  cols % 8 == 0; x 16-byte, codes
+ * int8_quantize: x [rows, cols] (bf16 or float32) -> codes int8 in [-127, 127]
+ * and scales [rows]: s = absmax * (1/127) (float32 product with the float32
+ * nearest 1/127; 1 where that is zero), code = nearest-even integer of the
+ * correctly rounded float32 quotient x / s.  A row that holds a NaN or an
+ * infinity gets scale NaN and codes 0, so that products of it are NaN.
+ * Reproducible bit for bit.  cols % 8 == 0; x 16-byte, codes
  * 8-byte, scales 4-byte aligned; rows < 2^31. */
 int int8_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int8_t* codes, float* scales,
                   void* stream);
