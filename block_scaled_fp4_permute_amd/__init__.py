@@ -231,25 +231,37 @@ def _need(t, dtype, name, device=None):
         raise ValueError(f"{name}: on {t.device}, expected {device}")
 
 
+_torch = None       # imported with the first allocation: the library itself needs none
+
+
+def _empty(shape, dtype, dev):
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _new(shape, dtype, dev, stream):
     """Working memory of a call on ``stream`` (None: the current one), from that
     stream's pool.  A block of the current stream's pool may have been freed
     with work still queued there that uses it, and nothing orders that work
     before the call's."""
-    import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return _empty(shape, dtype, dev)
+    import torch
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return _empty(shape, dtype, dev)
 
 
 def _new_result(shape, dtype, dev, stream):
     """Memory for a call's result; the caller reads it on the current stream, for
     which it is held when it is dropped."""
+    if stream is None:
+        return _empty(shape, dtype, dev)
     import torch
     out = _new(shape, dtype, dev, stream)
-    if stream is not None:
-        out.record_stream(torch.cuda.current_stream(dev))
+    out.record_stream(torch.cuda.current_stream(dev))
     return out
 
 
@@ -277,8 +289,10 @@ class Routing:
 def _new_routing(T, E, k, dev, stream):
     import torch
     i32, f32 = torch.int32, torch.float32
-    shapes = ((T, k), i32), ((T, k), f32), (E, i32), (E + 1, i32), (T * k, i32), (T * k, i32), (T * k, f32)
-    return Routing(*(_new_result(s, t, dev, stream) for s, t in shapes))
+    new = _new_result
+    return Routing(new((T, k), i32, dev, stream), new((T, k), f32, dev, stream), new(E, i32, dev, stream),
+                   new(E + 1, i32, dev, stream), new(T * k, i32, dev, stream), new(T * k, i32, dev, stream),
+                   new(T * k, f32, dev, stream))
 
 
 def moe_route_permute(logits, k: int, out: Routing | None = None, workspace=None, stream=None) -> Routing:
@@ -833,6 +847,8 @@ def _group(b, offsets, dev):
 def _result(out, shape, dtype, like, name, stream):
     """A given result checked, or a new one on ``like``'s device."""
     if out is None:
+        if stream is None:
+            return like.new_empty(shape, dtype=dtype)
         return _new_result(shape, dtype, like.device, stream)
     _need(out, dtype, name, like.device)
     if tuple(out.shape) != tuple(shape):

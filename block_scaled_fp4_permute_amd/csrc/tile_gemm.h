@@ -113,9 +113,8 @@ constexpr int kTgStep = 128;                // a K step: 128 bytes of each K-con
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 #define TG_LDS __attribute__((address_space(3)))
 
-// zeros for the parts of a step behind the end of the reduction (as wide as a
-// row of the widest K-major tile)
-__device__ const u32x4 tg_zero[32] = {};
+// zeros for the loads of a step behind the end of the reduction (16 bytes a lane, the same for all)
+__device__ const u32x4 tg_zero = {};
 
 // The load is written as assembly because the compiler, which cannot tell
 // which stage a read touches, would wait for every load in flight before each
@@ -172,7 +171,7 @@ struct TgRows {
   }
   // left: bytes of the reduction from this step on
   __device__ __forceinline__ void issue(int i, int left, uint32_t lds_wave) {
-    tg_dma(ch16 < left ? p[i] : reinterpret_cast<const uint8_t*>(tg_zero), lds_wave + i * TH * 16);
+    tg_dma(ch16 < left ? p[i] : reinterpret_cast<const uint8_t*>(&tg_zero), lds_wave + i * TH * 16);
     p[i] += kTgStep;
   }
 };
@@ -203,7 +202,7 @@ struct TgCols {
   }
   // left: rows of the reduction from this step on
   __device__ __forceinline__ void issue(int i, int left, uint32_t lds_wave) {
-    tg_dma(k0 < left - i * STEP ? p[i] : reinterpret_cast<const uint8_t*>(tg_zero), lds_wave + i * TH * 16);
+    tg_dma(k0 < left - i * STEP ? p[i] : reinterpret_cast<const uint8_t*>(&tg_zero), lds_wave + i * TH * 16);
     p[i] += 64 * ld;
   }
   // the thread's of the rows of the wave's load, which all its threads know
@@ -222,7 +221,7 @@ struct TgCols {
   // gathered: the thread's chunk of `row`
   __device__ __forceinline__ void issue_row(int i, int row, uint32_t ld_bytes, int left, uint32_t lds_wave) {
     const uint8_t* a = base + static_cast<uint64_t>(static_cast<uint32_t>(row)) * ld_bytes;
-    tg_dma(k0 < left - i * STEP ? a : reinterpret_cast<const uint8_t*>(tg_zero), lds_wave + i * TH * 16);
+    tg_dma(k0 < left - i * STEP ? a : reinterpret_cast<const uint8_t*>(&tg_zero), lds_wave + i * TH * 16);
   }
 };
 
@@ -296,9 +295,6 @@ __device__ __forceinline__ int tg_prefix(const TileParams& p, int* pre) {
   return __builtin_amdgcn_readfirstlane(pre[0]);
 }
 
-// task (c, nt): row chunk c of all experts' chunks (TN, TC: row tile c), column tile
-// nt.  Inside an expert, groups of 4 chunks run column tile by column tile, so
-// that the workgroups side by side share both operands in L2.
 // TC: the rows operand is stored transposed, [R][ld].  The columns of expert e
 // start at a multiple of `align` (64: a step's 128 bytes of a row are one line;
 // 8, 16 bytes, where experts have so few rows that the gaps would dominate), at
@@ -309,6 +305,9 @@ __host__ __device__ __forceinline__ int64_t tg_start_col(int64_t row0, int e, in
 }
 __host__ __device__ __forceinline__ int tg_col_align(int64_t m_total, int E) { return m_total / E >= 64 ? 64 : 8; }
 
+// task (c, nt): row chunk c of all experts' chunks (TN, TC: row tile c), column tile
+// nt.  Inside an expert, groups of 4 chunks run column tile by column tile, so
+// that the workgroups side by side share both operands in L2.
 template <int L, int BM, int SK, bool PART>
 __device__ __forceinline__ void tg_decode(const TileParams& p, const int* pre, int c, int nt, TgTask& t) {
   const tg_const_ints off = (tg_const_ints)(p.offsets);
