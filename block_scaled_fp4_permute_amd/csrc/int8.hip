@@ -10,7 +10,7 @@ namespace nvfp4 {
 //
 // One read of x: LPR lanes hold a row in registers (NV pieces of 8 values a
 // lane), reduce its maximum and write codes and scale.  Bound by memory: bf16
-// 16384 x 6144 takes 54 us, 5.6 TB/s (164 with two reads and divisions).  The
+// 16384 x 6144 takes 50 - 55 us, 5.5 - 6.0 TB/s (164 with two reads and divisions).  The
 // quotient is x * (1 / s) except where that lands within 2^-14 of a tie between
 // two codes: |x / s| <= 127 (1 + 2^-22), so the product's two roundings and the
 // quotient's own move it by less than 127 * 3 * 2^-24 < 2^-15, and only there

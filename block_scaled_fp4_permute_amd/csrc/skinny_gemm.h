@@ -183,13 +183,13 @@ static hipError_t sk_launch(const TileParams& p, int64_t rows, hipStream_t strea
 //     tiles; 256 rows, 256 tasks: 35 against 48; 100 rows of 2048 -> 5632, 352
 //     tasks: 29 against 20, so tiles)
 //   forward, up to 32 rows and 1 KB of reduction (8 steps): 64 x 128 tiles, three
-//     workgroups a CU (256 experts, 8 rows, int8 256 -> 6144: 94 us against 112 on
+//     workgroups a CU (256 experts, 8 rows, int8 256 -> 6144: 90 us against 112 on
 //     128 x 128; bf16 256 -> 6144 161 against 166; 32 rows, int8 512 -> 2048 50
 //     against 58; longer ones level off, bf16 1024 -> 2048 206 against 203, and
 //     64 rows lose, bf16 256 -> 6144 209 against 196)
 //   192 rows of output and at least 128 tiles of 256 x 256: those, with half the
 //     operand traffic a product (512 rows an expert, 512 -> 6144 row gradient:
-//     1155 us against 1450 on 128 x 128 tiles; 512 rows of 2048 -> 2 x 5632, 88
+//     995 us against 1270 on 128 x 128 tiles; 512 rows of 2048 -> 2 x 5632, 88
 //     tiles: 50 us against 33, so 128 x 128)
 //   else 128 x 128, two workgroups a CU
 template <int T, int L, int EPI>

@@ -390,14 +390,16 @@ __device__ __forceinline__ void tg_decode(const TileParams& p, const int* pre, i
 // waves, for tasks of a few rows and steps (both sides of each are measured at
 // the choice in skinny_gemm.h).
 //
-// Measured (MI355X):                                                 us   rate
-//   bf16 8192^3, NT / NN / TN                          780 / 785 / 945    1410 / 1400 / 1160 TFLOP/s
-//   int8 8192^3, NT                                                 401   2740 TOPS
-//   256 experts, 512 rows each, bf16 6144 -> 2 x 256: forward       950   868 TFLOP/s
-//     row gradient, weight gradient (TC)                    1040 / 1080   793 / 764 TFLOP/s
+// Measured (MI355X, several boxes: a product's clock differs):       us   rate
+//   bf16 8192^3, NT        734 - 780    1410 - 1500 TFLOP/s
+//     NN, TN               750 - 785, 913 - 945    1400 - 1465, 1160 - 1200 TFLOP/s
+//   int8 8192^3, NT        391 - 425    2590 - 2810 TOPS
+//   256 experts, 512 rows each, bf16 6144 -> 2 x 256: forward       943 - 950   868 - 874 TFLOP/s
+//     row gradient, weight gradient (TC), each in a loop of its own 995, 957    829, 862 TFLOP/s
+//     the same one behind the other                                 1037, 1081  795, 763 TFLOP/s
 //   256 experts, 8 rows each, bf16 6144 -> 2 x 256 / 256 -> 6144:
-//                                                           287 / 161   5.6 / 5.2 TB/s
-//   the same 256 -> 6144 in int8 (two steps a task)                  94   4.6 TB/s
+//                                                    284 - 291 / 160   5.5 - 5.7 / 5.2 TB/s
+//   the same 256 -> 6144 in int8 (two steps a task)            89 - 90   4.9 TB/s
 // Large products run at 1.9 - 2.1 GHz, the clock that the matrix cores' power
 // leaves, with those busy 53 % (forward), 48 % (rows) and 38 % (weights) of the
 // cycles at 512 rows an expert; LDS reads have no bank conflicts.  There the rest
@@ -643,8 +645,10 @@ __global__ __launch_bounds__(64 * WR * WC) __attribute__((amdgpu_waves_per_eu(2,
   // tile.  Lane groups exchange 16-bit results of two tiles, so that each lane
   // has 8 neighbouring columns, and lanes lr and lr ^ 8 exchange 16 bytes, so that
   // a store instruction writes whole 128-byte lines: 8 rows of 8 pieces.
-  // The stores are non-temporal: no product of the call reads them, and the
-  // operands keep the caches (weight gradients of 64 rows an expert: 543 -> 452 us).
+  // These stores are non-temporal: no product of the call reads them, and the
+  // operands keep the caches (256 experts' weight gradients of 64 rows each 543 ->
+  // 368 us, of 512 rows 1068 -> 957; other products up to 3 %).  h, which the next
+  // product of a layer reads, leaves through the caches.
   constexpr int OB = EPI == TG_OUT_F32 || EPI == TG_OUT_PART ? 4 : 2;             // bytes of a result
   constexpr int PAIRB = OB == 2 ? 32 : 16;                  // columns from a lane's piece a to its piece b
   uint8_t* obase = static_cast<uint8_t*>(p.out);            // the wave's first result (gated: of h)

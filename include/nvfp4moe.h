@@ -423,8 +423,9 @@ int fp8_grouped_gemm(const nvfp4moe_fp8_gemm_args* args, void* stream);
  * Pointers 16-byte aligned; H, I, N and K multiples of 8 up to 2^26; E <= 4096;
  * m_total < 2^30; an operand or result may exceed 4 GiB.  A hint is the rows
  * per expert the caller expects (0: m_total over the experts that can have
- * rows): it picks the kernel, never the result's definition.  Index arrays: see
- * NVFP4MOE_DEBUG above (bad a_rows entries read row 0). */
+ * rows): it picks the kernel, never the result's definition.  Results must not
+ * overlap operands.  Index arrays: see NVFP4MOE_DEBUG above (bad a_rows entries
+ * read row 0). */
 
 /* h[p, i] = act(g[p, i]) * u[p, i] with g = x[r] w[e, :I]^T, u = x[r] w[e, I:]^T
  * and r = a_rows ? a_rows[p] : p; gate and up projection, activation and
@@ -448,7 +449,8 @@ int moe_gated_ffn(const nvfp4moe_gated_args* args, void* stream);
 
 /* Gradients of moe_gated_ffn from dh, the gradient of h, and the gu it saved:
  *   dg = dh * u * act'(g), du = dh * act(g)   (float32, rounded to dtype: the
- *                                              operand of both products)
+ *                                              operand of both products; in
+ *                                              float16 above 65504 infinite)
  *   dx[p, :] = dg[p] w[e, :I] + du[p] w[e, I:]         one row per row p
  *   dw[e, :I] = sum_p dg[p]^T x[r_p], dw[e, I:] = sum_p du[p]^T x[r_p]
  * dx rows are per GEMM row: for gathered x, the gradient of a token is the sum
