@@ -81,3 +81,27 @@ def test_gradients_in_parts_and_int8():
             t.copy_(_normal(r, t.shape))
 
     _replay(step, refresh)
+
+
+def test_a_captured_fork_whose_calls_allocate():
+    """Calls on a second stream of the capture, with memory of their own, beside one on the first."""
+    r = np.random.default_rng(73)
+    M, H, I, E = 500, 136, 264, 3
+    x, w, dh = _normal(r, (M, H)), _normal(r, (E, 2 * I, H), 0.1), _normal(r, (M, I))
+    off = torch.tensor([0, 200, 201, M], dtype=torch.int32, device=DEV)
+    side = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        h, gu = m.moe_gated_ffn(x, w, off, m_total=M, save_gu=True, stream=side)
+        dx, dw = m.moe_gated_ffn_backward(dh, gu, x, w, off, stream=side)
+        q = m.int8_quantize(x)
+        here.wait_stream(side)
+        return h, dx, dw, q.codes, q.scales
+
+    def refresh():
+        for t in (x, dh):
+            t.copy_(_normal(r, t.shape))
+
+    _replay(step, refresh)
