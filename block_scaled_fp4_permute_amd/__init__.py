@@ -12,7 +12,10 @@ nvfp4_grouped_gemm, moe_swiglu, moe_unpermute_combine, moe_route_quantize
 (routing and activation quantisation in shared launches) and moe_expert_ffn
 (gate_up + SwiGLU requant + down for all experts, one persistent launch at
 decode sizes); mxfp4_* and fp8_* variants; moe_gated_ffn and moe_grouped_gemm
-with their gradients (16-bit experts); int8_quantize and int8_grouped_gemm.
+with their gradients (16-bit experts); int8_quantize and int8_grouped_gemm;
+moe_route_scored (softmax or sigmoid scores, balance bias, expert groups) and
+moe_unpermute_combine_backward with their gradients; int4_quantize,
+int4_dequantize and int4_grouped_gemv (4-bit weights on 16-bit rows).
 
 With stream=, operands, given results and given workspaces have to be ready on
 that stream, and the caller orders it before work that reads the results; the
@@ -31,6 +34,7 @@ OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_HIP = range(5)
 F32, BF16, F16 = 0, 1, 2
 EPI_F32, EPI_BF16, EPI_SWIGLU_NVFP4, EPI_COMBINE_F32, EPI_SWIGLU_BF16 = range(5)
 ACT_SILU, ACT_GELU = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
 
 class NVFP4MoEError(RuntimeError):
@@ -84,7 +88,7 @@ class Fp8GemmArgs(ctypes.Structure):
 
 
 def _struct(name, doc, fields):
-    kinds = {"p": ctypes.c_void_p, "i": ctypes.c_int32, "l": ctypes.c_int64}
+    kinds = {"p": ctypes.c_void_p, "i": ctypes.c_int32, "l": ctypes.c_int64, "f": ctypes.c_float}
     return type(name, (ctypes.Structure,), {"__doc__": doc, "_fields_": [(n, kinds[k]) for n, k in fields]})
 
 
@@ -105,6 +109,19 @@ Int8GemmArgs = _struct("Int8GemmArgs", "Mirror of nvfp4moe_int8_gemm_args.", [
     ("a_codes", "p"), ("a_scales", "p"), ("a_rows", "p"), ("a_rows_total", "l"), ("b_codes", "p"), ("b_scales", "p"),
     ("offsets", "p"), ("E", "i"), ("N", "i"), ("K", "i"), ("m_total", "l"), ("epilogue", "i"),
     ("max_rows_per_expert_hint", "i"), ("out", "p")])
+RouteArgs = _struct("RouteArgs", "Mirror of nvfp4moe_route_args.", [
+    ("logits", "p"), ("dtype", "i"), ("T", "i"), ("E", "i"), ("k", "i"), ("score", "i"), ("renormalize", "i"),
+    ("scale", "f"), ("bias", "p"), ("n_group", "i"), ("topk_group", "i"), ("group_top", "i"), ("topk_ids", "p"),
+    ("topk_w", "p"), ("counts", "p"), ("offsets", "p"), ("perm_src_token", "p"), ("perm_of_assignment", "p"),
+    ("perm_weight", "p"), ("scores", "p")])
+RouteGradArgs = _struct("RouteGradArgs", "Mirror of nvfp4moe_route_grad_args.", [
+    ("logits", "p"), ("dtype", "i"), ("T", "i"), ("E", "i"), ("k", "i"), ("score", "i"), ("renormalize", "i"),
+    ("scale", "f"), ("bias", "p"), ("topk_ids", "p"), ("d_topk_w", "p"), ("d_scores", "p"), ("d_scores_ld", "l"),
+    ("dlogits", "p")])
+Int4GemvArgs = _struct("Int4GemvArgs", "Mirror of nvfp4moe_int4_gemv_args.", [
+    ("a", "p"), ("dtype", "i"), ("a_rows", "p"), ("a_rows_total", "l"), ("b_codes", "p"), ("b_scales", "p"),
+    ("b_zeros", "p"), ("group", "i"), ("offsets", "p"), ("E", "i"), ("N", "i"), ("K", "i"), ("m_total", "l"),
+    ("gated", "i"), ("activation", "i"), ("out_dtype", "i"), ("max_rows_per_expert_hint", "i"), ("out", "p")])
 
 
 _lib = None
@@ -162,6 +179,16 @@ _SIGNATURES = {
     "int8_quantize": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
                                      ctypes.c_void_p, ctypes.c_void_p]),
     "int8_grouped_gemm": (ctypes.c_int, [ctypes.POINTER(Int8GemmArgs), ctypes.c_void_p]),
+    "moe_route_scored": (ctypes.c_int, [ctypes.POINTER(RouteArgs), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "moe_route_scored_backward": (ctypes.c_int, [ctypes.POINTER(RouteGradArgs), ctypes.c_void_p]),
+    "moe_unpermute_combine_backward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
+                                                      ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p]
+                                       + [ctypes.c_int32] * 3 + [ctypes.c_void_p] * 3),
+    "int4_quantize": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
+                                     ctypes.c_int32] + [ctypes.c_void_p] * 4),
+    "int4_dequantize": (ctypes.c_int, [ctypes.c_void_p] * 3 + [ctypes.c_int64] * 2 + [ctypes.c_int32] * 3
+                        + [ctypes.c_void_p] * 2),
+    "int4_grouped_gemv": (ctypes.c_int, [ctypes.POINTER(Int4GemvArgs), ctypes.c_void_p]),
     "nvfp4moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "nvfp4moe_last_error_detail": (ctypes.c_char_p, []),
     "nvfp4moe_version": (ctypes.c_int, []),
@@ -274,6 +301,20 @@ def _dtype_code(t):
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
+def _dtype_any(t, name):
+    import torch
+    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: expected float32, bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def _need_shape(t, shape, dtype, name, device):
+    _need(t, dtype, name, device)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected {list(shape)}, got {list(t.shape)}")
+
+
 # --------------------------------------------------------------------------- route
 @dataclass
 class Routing:
@@ -311,6 +352,78 @@ def moe_route_permute(logits, k: int, out: Routing | None = None, workspace=None
           out.offsets.data_ptr(), out.perm_src_token.data_ptr(), out.perm_of_assignment.data_ptr(),
           _ptr(out.perm_weight), workspace.data_ptr(), workspace.numel())
     return out
+
+
+# --------------------------------------------------------------- router with scores
+def moe_route_scored(logits, k: int, *, score: int = SCORE_SOFTMAX, bias=None, n_group: int = 1, topk_group: int = 1,
+                     group_top: int = 1, renormalize: bool = True, scale: float = 1.0, save_scores: bool = False,
+                     scores=None, out: Routing | None = None, workspace=None, stream=None):
+    """logits float32/bf16/f16 [T, E] -> Routing by softmax or sigmoid scores, with
+    a balance bias float32 [E] on the choice, the topk_group best of n_group expert
+    groups, weights renormalised over the k chosen or not, times scale (see
+    include/nvfp4moe.h).  save_scores (or a float32 scores [T, E]): returns
+    (Routing, scores)."""
+    import torch
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    code = _dtype_any(logits, "logits")
+    dev = logits.device
+    _need(logits, logits.dtype, "logits", dev)
+    T, E = logits.shape
+    if bias is not None:
+        _need_shape(bias, (E,), torch.float32, "bias", dev)
+    f32, i32 = torch.float32, torch.int32
+    if out is None:
+        out = _new_routing(T, E, k, dev, stream)
+    else:
+        for t, shape, dtype, name in ((out.topk_ids, (T, k), i32, "topk_ids"), (out.topk_w, (T, k), f32, "topk_w"),
+                                      (out.counts, (E,), i32, "counts"), (out.offsets, (E + 1,), i32, "offsets"),
+                                      (out.perm_src_token, (T * k,), i32, "perm_src_token"),
+                                      (out.perm_of_assignment, (T * k,), i32, "perm_of_assignment")):
+            _need_shape(t, shape, dtype, "out." + name, dev)
+        if out.perm_weight is not None:
+            _need_shape(out.perm_weight, (T * k,), f32, "out.perm_weight", dev)
+    if save_scores or scores is not None:
+        scores = _result(scores, (T, E), f32, logits, "scores", stream)
+    ws = _scratch(workspace, lib().moe_route_permute_workspace_size(T, E, k), dev, stream)
+    args = RouteArgs(logits=logits.data_ptr(), dtype=code, T=T, E=E, k=k, score=score, renormalize=int(renormalize),
+                     scale=scale, bias=_ptr(bias), n_group=n_group, topk_group=topk_group, group_top=group_top,
+                     topk_ids=out.topk_ids.data_ptr(), topk_w=out.topk_w.data_ptr(), counts=out.counts.data_ptr(),
+                     offsets=out.offsets.data_ptr(), perm_src_token=out.perm_src_token.data_ptr(),
+                     perm_of_assignment=out.perm_of_assignment.data_ptr(), perm_weight=_ptr(out.perm_weight),
+                     scores=_ptr(scores))
+    _call(dev, stream, lib().moe_route_scored, ctypes.byref(args), ws.data_ptr(), ws.numel())
+    return out if scores is None else (out, scores)
+
+
+def moe_route_scored_backward(d_topk_w, logits, topk_ids, *, score: int = SCORE_SOFTMAX, bias=None,
+                              renormalize: bool = True, scale: float = 1.0, d_scores=None, dlogits=None, stream=None):
+    """Gradient of the logits [T, E], in their type, from d_topk_w float32 [T, k];
+    logits, topk_ids and options of the forward call (bias only if it holds -inf or
+    NaN).  d_scores: float32 gradient of the scores, [T, E] or one row [E] for all
+    tokens."""
+    import torch
+    if logits.dim() != 2 or topk_ids.dim() != 2:
+        raise ValueError("logits must be [T, E] and topk_ids [T, k]")
+    code = _dtype_any(logits, "logits")
+    dev = logits.device
+    _need(logits, logits.dtype, "logits", dev)
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    _need_shape(topk_ids, (T, k), torch.int32, "topk_ids", dev)
+    _need_shape(d_topk_w, (T, k), torch.float32, "d_topk_w", dev)
+    if bias is not None:
+        _need_shape(bias, (E,), torch.float32, "bias", dev)
+    ld = 0
+    if d_scores is not None:
+        ld = E if d_scores.dim() == 2 else 0
+        _need_shape(d_scores, (T, E) if ld else (E,), torch.float32, "d_scores", dev)
+    dlogits = _result(dlogits, (T, E), logits.dtype, logits, "dlogits", stream)
+    args = RouteGradArgs(logits=logits.data_ptr(), dtype=code, T=T, E=E, k=k, score=score, renormalize=int(renormalize),
+                         scale=scale, bias=_ptr(bias), topk_ids=topk_ids.data_ptr(), d_topk_w=d_topk_w.data_ptr(),
+                         d_scores=_ptr(d_scores), d_scores_ld=ld, dlogits=dlogits.data_ptr())
+    _call(dev, stream, lib().moe_route_scored_backward, ctypes.byref(args))
+    return dlogits
 
 
 # ------------------------------------------------------------------------ quantise
@@ -1050,6 +1163,111 @@ def int8_grouped_gemm(a: INT8Tensor, b: INT8Tensor, offsets, *, m_total: int, a_
     return out
 
 
+# --------------------------------------------------------------------------- INT4
+@dataclass
+class INT4Tensor:
+    codes: "object"     # uint8 [..., rows, cols/2]
+    scales: "object"    # bf16/f16 [..., rows, cols/group]
+    zeros: "object"     # uint8 [..., rows, cols/group] or None (8 everywhere)
+    group: int          # 32, 64 or 128
+
+
+def _need_int4(q, name, dev):
+    """Checks of an INT4Tensor on ``dev``: the code of its scales' type."""
+    import torch
+    code = _dtype16(q.scales, name + ".scales")
+    if q.group not in (32, 64, 128):
+        raise ValueError(f"{name}: group {q.group} (32, 64 or 128)")
+    _need(q.codes, torch.uint8, name + ".codes", dev)
+    shape = tuple(q.codes.shape[:-1]) + (2 * q.codes.shape[-1] // q.group,)
+    if 2 * q.codes.shape[-1] % q.group:
+        raise ValueError(f"{name}: {2 * q.codes.shape[-1]} columns, not a multiple of the group of {q.group}")
+    _need_shape(q.scales, shape, q.scales.dtype, name + ".scales", dev)
+    if q.zeros is not None:
+        _need_shape(q.zeros, shape, torch.uint8, name + ".zeros", dev)
+    return code
+
+
+def int4_quantize(x, group: int = 128, zeros: bool = False, scale_dtype=None, out: INT4Tensor | None = None,
+                  stream=None) -> INT4Tensor:
+    """x float32/bf16/f16 [..., rows, cols] -> INT4Tensor, groups along the last
+    axis; scales in x's 16-bit type, or scale_dtype (bf16 for float32 x)."""
+    import torch
+    code = _dtype_any(x, "x")
+    dev = x.device
+    _need(x, x.dtype, "x", dev)
+    if group not in (32, 64, 128):
+        raise ValueError(f"group {group} (32, 64 or 128)")
+    if x.dim() < 1 or x.shape[-1] == 0 or x.shape[-1] % group:
+        raise ValueError(f"x: the last dimension must be a positive multiple of the group of {group}")
+    cols = x.shape[-1]
+    if out is None:
+        dtype = scale_dtype or (torch.bfloat16 if code == F32 else x.dtype)
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"scale_dtype: expected bfloat16 or float16, got {dtype}")
+        lead, gs = tuple(x.shape[:-1]), cols // group
+        out = INT4Tensor(_result(None, lead + (cols // 2,), torch.uint8, x, "out.codes", stream),
+                         _result(None, lead + (gs,), dtype, x, "out.scales", stream),
+                         _result(None, lead + (gs,), torch.uint8, x, "out.zeros", stream) if zeros else None, group)
+    elif out.group != group or tuple(out.codes.shape) != tuple(x.shape[:-1]) + (cols // 2,) or \
+            (out.zeros is not None) != zeros or (scale_dtype is not None and out.scales.dtype != scale_dtype):
+        raise ValueError("out does not match x, group, zeros and scale_dtype")
+    scode = _need_int4(out, "out", dev)
+    if x.numel() == 0:
+        return out
+    _call(dev, stream, lib().int4_quantize, x.data_ptr(), code, x.numel() // cols, cols, group, scode,
+          out.codes.data_ptr(), out.scales.data_ptr(), _ptr(out.zeros))
+    return out
+
+
+def int4_dequantize(q: INT4Tensor, out_dtype=None, out=None, stream=None):
+    """The values of q [..., rows, cols] in its scales' type, or float32."""
+    import torch
+    dev = q.codes.device
+    code = _need_int4(q, "q", dev)
+    cols = 2 * q.codes.shape[-1]
+    want = out.dtype if out is not None and out_dtype is None else (out_dtype or q.scales.dtype)
+    if want not in (q.scales.dtype, torch.float32):
+        raise TypeError(f"out: {q.scales.dtype} or float32, got {want}")
+    out = _result(out, tuple(q.codes.shape[:-1]) + (cols,), want, q.codes, "out", stream)
+    if out.numel() == 0:
+        return out
+    _call(dev, stream, lib().int4_dequantize, q.codes.data_ptr(), q.scales.data_ptr(), _ptr(q.zeros),
+          out.numel() // cols, cols, q.group, code, F32 if want == torch.float32 else code, out.data_ptr())
+    return out
+
+
+def int4_grouped_gemv(a, b: INT4Tensor, offsets, *, m_total: int, a_rows=None, gated: bool = False,
+                      activation: int = ACT_SILU, out=None, out_dtype=None, max_rows_per_expert_hint: int = 0,
+                      stream=None):
+    """Products of few rows with INT4 weights (see include/nvfp4moe.h): a bf16/f16
+    [rows, K], b [E, N, K] with scales in a's type, offsets int32 [E+1] -> y
+    [m_total, N] in a's type or float32; gated (N = 2I, gate rows first): h =
+    act(gate) * up [m_total, I]."""
+    import torch
+    if a.dim() != 2 or b.codes.dim() != 3:
+        raise ValueError("a must be [rows, K] and b [E, N, K]")
+    dev = b.codes.device
+    code = _need_int4(b, "b", dev)
+    _need(a, b.scales.dtype, "a", dev)
+    E = _group(b.codes, offsets, dev)
+    N, K = b.codes.shape[1], 2 * b.codes.shape[2]
+    if a.shape[1] != K or (gated and N % 2):
+        raise ValueError("operand shapes disagree")
+    _rows_of(a_rows, a, m_total, dev, "a")
+    want = out.dtype if out is not None and out_dtype is None else (out_dtype or a.dtype)
+    if want != a.dtype and (gated or want != torch.float32):
+        raise TypeError(f"out: {a.dtype}{'' if gated else ' or float32'}, got {want}")
+    out = _result(out, (m_total, N // 2 if gated else N), want, a, "out", stream)
+    args = Int4GemvArgs(a=a.data_ptr(), dtype=code, a_rows=_ptr(a_rows), a_rows_total=a.shape[0],
+                        b_codes=b.codes.data_ptr(), b_scales=b.scales.data_ptr(), b_zeros=_ptr(b.zeros), group=b.group,
+                        offsets=offsets.data_ptr(), E=E, N=N, K=K, m_total=m_total, gated=int(gated),
+                        activation=activation, out_dtype=F32 if want == torch.float32 else code,
+                        max_rows_per_expert_hint=max_rows_per_expert_hint, out=out.data_ptr())
+    _call(dev, stream, lib().int4_grouped_gemv, ctypes.byref(args))
+    return out
+
+
 # -------------------------------------------------------------------------- swiglu
 def moe_swiglu(gate_up, g=None, out: NVFP4Tensor | None = None, workspace=None, stream=None) -> NVFP4Tensor:
     """gate_up float32/bf16 [M, 2I] -> NVFP4 h = silu(gate) * up."""
@@ -1096,10 +1314,49 @@ def moe_unpermute_combine(y, perm_of_assignment, topk_w, T: int, k: int, out=Non
     return out
 
 
+def moe_unpermute_combine_backward(dout, y, perm_of_assignment, topk_w, *, need_dy: bool = True, need_dw: bool = True,
+                                   dy=None, d_topk_w=None, stream=None):
+    """Gradients of moe_unpermute_combine from dout [T, H]: (dy [rows, H] in y's
+    type, d_topk_w float32 [T, k]); None where not needed.  topk_w float32 [T, k];
+    perm_of_assignment as in the forward call (None: row t*k + j), its entries all
+    different.  Rows of a new dy that no entry names are zero."""
+    import torch
+    if dout.dim() != 2 or y.dim() != 2 or topk_w.dim() != 2:
+        raise ValueError("dout must be [T, H], y [rows, H] and topk_w [T, k]")
+    if not (need_dy or need_dw):
+        raise ValueError("neither dy nor d_topk_w is needed")
+    dev = y.device
+    y_code, d_code = _dtype_code(y), _dtype_code(dout)
+    _need(y, y.dtype, "y", dev)
+    _need(dout, dout.dtype, "dout", dev)
+    (T, H), k, rows = dout.shape, topk_w.shape[1], y.shape[0]
+    _need_shape(topk_w, (T, k), torch.float32, "topk_w", dev)
+    if y.shape[1] != H:
+        raise ValueError("operand shapes disagree")
+    if perm_of_assignment is not None:
+        _need_shape(perm_of_assignment, (T * k,), torch.int32, "perm_of_assignment", dev)
+    elif rows < T * k:
+        raise ValueError(f"y has {rows} rows, fewer than T*k = {T * k} (and no perm_of_assignment)")
+    if need_dy:
+        fresh = dy is None
+        dy = _result(dy, (rows, H), y.dtype, y, "dy", stream)
+        if fresh and rows > T * k:
+            with torch.cuda.stream(stream):
+                dy.zero_()
+    else:
+        dy = None
+    d_topk_w = _result(d_topk_w, (T, k), torch.float32, y, "d_topk_w", stream) if need_dw else None
+    _call(dev, stream, lib().moe_unpermute_combine_backward, dout.data_ptr(), d_code, y.data_ptr(), y_code, rows,
+          _ptr(perm_of_assignment), topk_w.data_ptr(), T, k, H, _ptr(dy), _ptr(d_topk_w))
+    return dy, d_topk_w
+
+
 __all__ = ["lib", "moe_route_permute", "moe_route_quantize", "moe_route_quantize_noalloc", "nvfp4_quantize", "nvfp4_grouped_gemm", "moe_swiglu", "nvfp4_weight_repack",
            "moe_unpermute_combine", "moe_expert_ffn", "moe_expert_ffn_workspace", "mxfp4_quantize",
            "mxfp4_grouped_gemm", "mxfp4_weight_repack", "MXFP4Tensor", "fp8_quantize", "fp8_swiglu_quantize", "fp8_weight_repack",
            "fp8_grouped_gemm", "FP8Tensor", "Fp8GemmArgs", "NVFP4Tensor", "Routing", "GemmArgs", "NVFP4MoEError",
            "moe_gated_ffn", "moe_gated_ffn_backward", "moe_grouped_gemm", "moe_grouped_gemm_backward", "int8_quantize",
-           "int8_grouped_gemm", "INT8Tensor", "ACT_SILU", "ACT_GELU", "F16", "EPI_SWIGLU_BF16",
+           "int8_grouped_gemm", "INT8Tensor", "moe_route_scored", "moe_route_scored_backward",
+           "moe_unpermute_combine_backward", "int4_quantize", "int4_dequantize", "int4_grouped_gemv", "INT4Tensor",
+           "SCORE_SOFTMAX", "SCORE_SIGMOID", "ACT_SILU", "ACT_GELU", "F16", "EPI_SWIGLU_BF16",
            "F32", "BF16", "EPI_F32", "EPI_BF16", "EPI_SWIGLU_NVFP4", "EPI_COMBINE_F32"]

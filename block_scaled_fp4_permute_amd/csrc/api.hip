@@ -133,6 +133,28 @@ int check_route_quantize(const char* fn, const float* logits, int32_t T, int32_t
   return NVFP4MOE_OK;
 }
 
+// the checks that the router and its gradient share
+int check_router(const char* fn, const void* logits, int32_t dtype, int32_t T, int32_t E, int32_t k, int32_t score,
+                 int32_t renormalize, float scale, const float* bias) {
+  if (!logits) return fail(NVFP4MOE_ERR_INVALID, "%s: null logits", fn);
+  if (dtype != NVFP4MOE_F32 && dtype != NVFP4MOE_BF16 && dtype != NVFP4MOE_F16)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: dtype %d", fn, dtype);
+  if (T <= 0 || E <= 0 || k <= 0) return fail(NVFP4MOE_ERR_INVALID, "%s: T, E, k must be > 0", fn);
+  if (k > E) return fail(NVFP4MOE_ERR_INVALID, "%s: k=%d > E=%d", fn, k, E);
+  if (score != NVFP4MOE_SCORE_SOFTMAX && score != NVFP4MOE_SCORE_SIGMOID)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: score %d", fn, score);
+  if (renormalize != 0 && renormalize != 1) return fail(NVFP4MOE_ERR_INVALID, "%s: renormalize %d", fn, renormalize);
+  if (!(scale - scale == 0.0f)) return fail(NVFP4MOE_ERR_INVALID, "%s: scale is not finite", fn);
+  if (k > 32) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: k=%d > 32", fn, k);
+  if (E > 4096) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: E=%d > 4096", fn, E);
+  // four tokens a workgroup of 256 threads, of fewer than 2^32 in a grid
+  if (static_cast<int64_t>(T) * k >= (int64_t(1) << 30) || T >= (1 << 25))
+    return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: T*k >= 2^30 or T >= 2^25", fn);
+  if (!aligned(logits, dtype == NVFP4MOE_F32 ? 4 : 2) || !aligned(bias, 4))
+    return fail(NVFP4MOE_ERR_INVALID, "%s: misaligned logits or bias", fn);
+  return NVFP4MOE_OK;
+}
+
 // ------------------------------------------------------------------ scratch of the no-allocation entry point
 // One fixed block of device memory per GPU, held until the process ends,
 // shared by every call of moe_route_quantize_noalloc on that GPU.  In host
@@ -207,6 +229,82 @@ int moe_route_permute(const float* logits, int32_t T, int32_t E, int32_t k, int3
                                                 perm_of_assignment, perm_weight, workspace,
                                                 static_cast<hipStream_t>(stream)),
                     "moe_route_permute");
+}
+
+// ------------------------------------------------------------------ router with scores
+int moe_route_scored(const nvfp4moe_route_args* a, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_route_scored";
+  if (!a) return fail(NVFP4MOE_ERR_INVALID, "%s: args is NULL", fn);
+  const int bad = check_router(fn, a->logits, a->dtype, a->T, a->E, a->k, a->score, a->renormalize, a->scale, a->bias);
+  if (bad != NVFP4MOE_OK) return bad;
+  if (!a->topk_ids || !a->topk_w || !a->counts || !a->offsets || !a->perm_src_token || !a->perm_of_assignment)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: null routing pointer argument", fn);
+  if (a->n_group <= 0 || a->E % a->n_group != 0)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: n_group=%d does not divide E=%d", fn, a->n_group, a->E);
+  const int size = a->E / a->n_group;
+  if (a->topk_group <= 0 || a->topk_group > a->n_group)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: topk_group=%d of %d groups", fn, a->topk_group, a->n_group);
+  if (a->group_top < 1 || a->group_top > 2 || a->group_top > size)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: group_top=%d (1 or 2, at most the group's %d experts)", fn, a->group_top, size);
+  if (static_cast<int64_t>(a->topk_group) * size < a->k)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: k=%d > %d experts of the groups that stay", fn, a->k, a->topk_group * size);
+  if (a->n_group > 64) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: n_group=%d > 64", fn, a->n_group);
+  for (const void* p : {static_cast<const void*>(a->topk_ids), static_cast<const void*>(a->topk_w),
+                        static_cast<const void*>(a->counts), static_cast<const void*>(a->offsets),
+                        static_cast<const void*>(a->perm_src_token), static_cast<const void*>(a->perm_of_assignment),
+                        static_cast<const void*>(a->perm_weight), static_cast<const void*>(a->scores)})
+    if (!aligned(p, 4)) return fail(NVFP4MOE_ERR_INVALID, "%s: misaligned output", fn);
+  const size_t need = nvfp4::route_permute_ws_bytes(a->T, a->E, a->k);
+  if (!workspace || workspace_bytes < need)
+    return fail(NVFP4MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes, need);
+  if (!aligned(workspace, 16)) return fail(NVFP4MOE_ERR_INVALID, "%s: workspace not 16-byte aligned", fn);
+  nvfp4::ScoredParams p{};
+  p.logits = a->logits;
+  p.bias = a->bias;
+  p.T = a->T;
+  p.E = a->E;
+  p.k = a->k;
+  p.softmax = a->score == NVFP4MOE_SCORE_SOFTMAX;
+  p.renormalize = a->renormalize;
+  p.n_group = a->topk_group == a->n_group ? 1 : a->n_group;   // all groups stay: no choice among them
+  p.topk_group = a->topk_group;
+  p.group_top = a->group_top;
+  p.scale = a->scale;
+  p.topk_ids = a->topk_ids;
+  p.topk_w = a->topk_w;
+  p.scores = a->scores;
+  return hip_status(nvfp4::launch_route_scored(p, a->dtype, a->counts, a->offsets, a->perm_src_token,
+                                               a->perm_of_assignment, a->perm_weight, workspace,
+                                               static_cast<hipStream_t>(stream)), fn);
+}
+
+int moe_route_scored_backward(const nvfp4moe_route_grad_args* a, void* stream) {
+  const char* fn = "moe_route_scored_backward";
+  if (!a) return fail(NVFP4MOE_ERR_INVALID, "%s: args is NULL", fn);
+  const int bad = check_router(fn, a->logits, a->dtype, a->T, a->E, a->k, a->score, a->renormalize, a->scale, a->bias);
+  if (bad != NVFP4MOE_OK) return bad;
+  if (!a->topk_ids || !a->d_topk_w || !a->dlogits)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: null topk_ids, d_topk_w or dlogits", fn);
+  if (a->d_scores && a->d_scores_ld != 0 && a->d_scores_ld != a->E)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: d_scores_ld=%lld (E or 0)", fn, static_cast<long long>(a->d_scores_ld));
+  if (!aligned(a->topk_ids, 4) || !aligned(a->d_topk_w, 4) || !aligned(a->d_scores, 4) ||
+      !aligned(a->dlogits, a->dtype == NVFP4MOE_F32 ? 4 : 2))
+    return fail(NVFP4MOE_ERR_INVALID, "%s: misaligned pointer", fn);
+  nvfp4::ScoredGradParams p{};
+  p.logits = a->logits;
+  p.bias = a->bias;
+  p.T = a->T;
+  p.E = a->E;
+  p.k = a->k;
+  p.softmax = a->score == NVFP4MOE_SCORE_SOFTMAX;
+  p.renormalize = a->renormalize;
+  p.scale = a->scale;
+  p.topk_ids = a->topk_ids;
+  p.d_topk_w = a->d_topk_w;
+  p.d_scores = a->d_scores;
+  p.d_scores_ld = a->d_scores_ld;
+  p.dlogits = a->dlogits;
+  return hip_status(nvfp4::launch_route_scored_grad(p, a->dtype, static_cast<hipStream_t>(stream)), fn);
 }
 
 // ------------------------------------------------------------------ quantise
@@ -725,6 +823,22 @@ int check_plain(const char* fn, int32_t dtype, const int32_t* offsets, int32_t E
   return NVFP4MOE_OK;
 }
 
+// a tensor in INT4 groups
+int check_int4(const char* fn, const uint8_t* codes, const void* scales, int64_t rows, int64_t cols, int32_t group,
+               int32_t scale_dtype) {
+  if (!codes || !scales) return fail(NVFP4MOE_ERR_INVALID, "%s: null codes or scales", fn);
+  if (group != 32 && group != 64 && group != 128)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: group=%d (32, 64 or 128)", fn, group);
+  if (rows <= 0 || cols <= 0 || cols % group != 0)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: rows > 0 and cols a positive multiple of group=%d needed", fn, group);
+  if (scale_dtype != NVFP4MOE_BF16 && scale_dtype != NVFP4MOE_F16)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: scale_dtype %d (bf16 or f16)", fn, scale_dtype);
+  if (prod_ge(rows, cols, int64_t(1) << 40)) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: 2^40 values or more", fn);
+  if (!aligned(codes, 16) || !aligned(scales, 2))
+    return fail(NVFP4MOE_ERR_INVALID, "%s: codes must be 16-byte, scales 2-byte aligned", fn);
+  return NVFP4MOE_OK;
+}
+
 int debug_plain(const char* fn, const int32_t* offsets, int32_t E, int64_t m_total, const int32_t* a_rows,
                 int64_t rows_total, hipStream_t s) {
   if (!debug_checks()) return NVFP4MOE_OK;
@@ -1034,6 +1148,79 @@ int int8_grouped_gemm(const nvfp4moe_int8_gemm_args* a, void* stream) {
   return hip_status(nvfp4::launch_tile_gemm_i8(p, epi, s), fn);
 }
 
+// ------------------------------------------------------------------ INT4
+int int4_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int32_t group, int32_t scale_dtype,
+                  uint8_t* codes, void* scales, uint8_t* zeros, void* stream) {
+  const char* fn = "int4_quantize";
+  if (!x) return fail(NVFP4MOE_ERR_INVALID, "%s: null x", fn);
+  if (x_dtype != NVFP4MOE_F32 && x_dtype != NVFP4MOE_BF16 && x_dtype != NVFP4MOE_F16)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: x_dtype %d", fn, x_dtype);
+  const int bad = check_int4(fn, codes, scales, rows, cols, group, scale_dtype);
+  if (bad != NVFP4MOE_OK) return bad;
+  if (!aligned(x, 16)) return fail(NVFP4MOE_ERR_INVALID, "%s: x must be 16-byte aligned", fn);
+  return hip_status(nvfp4::launch_int4_quantize(x, x_dtype, rows, cols, group, scale_dtype == NVFP4MOE_F16, codes, scales,
+                                                zeros, static_cast<hipStream_t>(stream)), fn);
+}
+
+int int4_dequantize(const uint8_t* codes, const void* scales, const uint8_t* zeros, int64_t rows, int64_t cols,
+                    int32_t group, int32_t scale_dtype, int32_t out_dtype, void* out, void* stream) {
+  const char* fn = "int4_dequantize";
+  const int bad = check_int4(fn, codes, scales, rows, cols, group, scale_dtype);
+  if (bad != NVFP4MOE_OK) return bad;
+  if (!out) return fail(NVFP4MOE_ERR_INVALID, "%s: null out", fn);
+  if (out_dtype != NVFP4MOE_F32 && out_dtype != scale_dtype)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: out_dtype %d (scale_dtype or float32)", fn, out_dtype);
+  if (!aligned(out, 16)) return fail(NVFP4MOE_ERR_INVALID, "%s: out must be 16-byte aligned", fn);
+  return hip_status(nvfp4::launch_int4_dequantize(codes, scales, zeros, rows, cols, group, scale_dtype == NVFP4MOE_F16,
+                                                  out_dtype, out, static_cast<hipStream_t>(stream)), fn);
+}
+
+int int4_grouped_gemv(const nvfp4moe_int4_gemv_args* a, void* stream) {
+  const char* fn = "int4_grouped_gemv";
+  if (!a) return fail(NVFP4MOE_ERR_INVALID, "%s: args is NULL", fn);
+  if (a->group != 32 && a->group != 64 && a->group != 128)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: group=%d (32, 64 or 128)", fn, a->group);
+  if (a->N <= 0 || a->K <= 0 || a->K % a->group != 0)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: N=%d must be > 0 and K=%d a positive multiple of group=%d", fn, a->N, a->K, a->group);
+  if (a->N > (1 << 26)) return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: N above 2^26", fn);
+  // N of any value here: the shared checks want multiples of 8
+  const int bad = check_plain(fn, a->dtype, a->offsets, a->E, (a->N + 7) / 8 * 8, a->K, a->m_total, a->a_rows,
+                              a->a_rows_total, a->a && a->out, true);
+  if (bad != NVFP4MOE_OK) return bad;
+  if (!a->b_codes || !a->b_scales) return fail(NVFP4MOE_ERR_INVALID, "%s: null b_codes or b_scales", fn);
+  if (a->gated != 0 && a->gated != 1) return fail(NVFP4MOE_ERR_INVALID, "%s: gated=%d", fn, a->gated);
+  if (a->gated && a->N % 2 != 0) return fail(NVFP4MOE_ERR_INVALID, "%s: gated needs N = 2I", fn);
+  if (a->gated && a->activation != NVFP4MOE_ACT_SILU && a->activation != NVFP4MOE_ACT_GELU)
+    return fail(NVFP4MOE_ERR_INVALID, "%s: activation %d", fn, a->activation);
+  if (a->out_dtype != a->dtype && (a->gated || a->out_dtype != NVFP4MOE_F32))
+    return fail(NVFP4MOE_ERR_INVALID, "%s: out_dtype %d (dtype, or float32 if not gated)", fn, a->out_dtype);
+  if (!aligned(a->a, 16) || !aligned(a->b_codes, 16) || !aligned(a->b_scales, 2) || !aligned(a->out, 16))
+    return fail(NVFP4MOE_ERR_INVALID, "%s: a, b_codes and out must be 16-byte, b_scales 2-byte aligned", fn);
+  const int64_t hint = a->max_rows_per_expert_hint > 0 ? a->max_rows_per_expert_hint : 0;
+  if (nvfp4::int4_gemv_threads(a->E, a->N, a->K, a->m_total, hint, a->gated) >= (int64_t(1) << 32))
+    return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: 2^32 threads or more", fn);
+  if (a->m_total == 0) return ok();
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const int st = debug_plain(fn, a->offsets, a->E, a->m_total, a->a_rows, a->a_rows_total, s);
+  if (st != NVFP4MOE_OK) return st;
+  nvfp4::Int4Params p{};
+  p.a = a->a;
+  p.a_rows = a->a_rows;
+  p.codes = a->b_codes;
+  p.scales = a->b_scales;
+  p.zeros = a->b_zeros;
+  p.offsets = a->offsets;
+  p.E = a->E;
+  p.N = a->N;
+  p.K = a->K;
+  p.m_total = static_cast<int>(a->m_total);
+  p.src_rows = static_cast<int>(a->a_rows_total);
+  p.act = a->activation == NVFP4MOE_ACT_GELU ? nvfp4::TG_ACT_GELU : nvfp4::TG_ACT_SILU;
+  p.rows_hint = static_cast<int>(hint);
+  p.out = a->out;
+  return hip_status(nvfp4::launch_int4_gemv(p, a->dtype == NVFP4MOE_F16, a->group, a->gated, a->out_dtype == NVFP4MOE_F32, s), fn);
+}
+
 // ------------------------------------------------------------------ packed weights
 size_t nvfp4_weight_packed_size(int32_t E, int32_t N, int32_t K) {
   if (E <= 0 || N <= 0 || K <= 0 || K % 32 != 0 || prod_ge(E, N, int64_t(1) << 31)) return 0;
@@ -1093,6 +1280,44 @@ int moe_unpermute_combine(const void* y, int32_t y_dtype, const int32_t* perm_of
   return hip_status(nvfp4::launch_combine(y, y_dtype, perm_of_assignment, topk_w, T, k, H, out, out_dtype,
                                           static_cast<hipStream_t>(stream)),
                     "moe_unpermute_combine");
+}
+
+int moe_unpermute_combine_backward(const void* dout, int32_t dout_dtype, const void* y, int32_t y_dtype, int64_t y_rows,
+                                   const int32_t* perm_of_assignment, const float* topk_w, int32_t T, int32_t k,
+                                   int32_t H, void* dy, float* d_topk_w, void* stream) {
+  const char* fn = "moe_unpermute_combine_backward";
+  if (!dout) return fail(NVFP4MOE_ERR_INVALID, "%s: null dout", fn);
+  if (!dy && !d_topk_w) return fail(NVFP4MOE_ERR_INVALID, "%s: neither dy nor d_topk_w", fn);
+  if (d_topk_w && !y) return fail(NVFP4MOE_ERR_INVALID, "%s: d_topk_w needs y", fn);
+  if ((dout_dtype != NVFP4MOE_F32 && dout_dtype != NVFP4MOE_BF16) || (y_dtype != NVFP4MOE_F32 && y_dtype != NVFP4MOE_BF16))
+    return fail(NVFP4MOE_ERR_INVALID, "%s: dtype", fn);
+  if (T <= 0 || k <= 0 || H <= 0) return fail(NVFP4MOE_ERR_INVALID, "%s: T, k, H must be > 0", fn);
+  if (H % 8 != 0) return fail(NVFP4MOE_ERR_INVALID, "%s: H=%d not a multiple of 8", fn, H);
+  if (y_rows <= 0 || (!perm_of_assignment && y_rows < static_cast<int64_t>(T) * k))
+    return fail(NVFP4MOE_ERR_INVALID, "%s: %lld rows of y for T*k = %lld assignments", fn, static_cast<long long>(y_rows),
+                static_cast<long long>(T) * k);
+  if (k > 1024 || y_rows >= (int64_t(1) << 31) || static_cast<int64_t>(T) * ((k + 3) / 4) >= (int64_t(1) << 24))
+    return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: k > 1024, 2^31 rows of y, or T * ceil(k / 4) >= 2^24", fn);
+  if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(dy, 16) || !aligned(d_topk_w, 4) || !aligned(topk_w, 4) ||
+      !aligned(perm_of_assignment, 4))
+    return fail(NVFP4MOE_ERR_INVALID, "%s: misaligned", fn);
+  if (debug_checks()) {
+    const int st = debug_check_range(fn, "perm_of_assignment", perm_of_assignment, static_cast<int64_t>(T) * k, y_rows,
+                                     static_cast<hipStream_t>(stream));
+    if (st != NVFP4MOE_OK) return st;
+  }
+  nvfp4::CombineGradParams p{};
+  p.dout = dout;
+  p.y = y;
+  p.perm = perm_of_assignment;
+  p.w = topk_w;
+  p.T = T;
+  p.k = k;
+  p.H = H;
+  p.rows = y_rows;
+  p.dy = dy;
+  p.dw = d_topk_w;
+  return hip_status(nvfp4::launch_combine_grad(p, dout_dtype, y_dtype, static_cast<hipStream_t>(stream)), fn);
 }
 
 }  // extern "C"

@@ -40,6 +40,9 @@ size_t route_permute_ws_bytes(int T, int E, int k);
 hipError_t launch_route_permute(const float* logits, int T, int E, int k, int* topk_ids, float* topk_w,
                                 int* counts, int* offsets, int* perm_src_token, int* perm_of_assignment,
                                 float* perm_weight, void* ws, hipStream_t stream);
+// the permutation of given choices (the steps of launch_route_permute behind the routing itself)
+hipError_t launch_permute(const int* topk_ids, const float* topk_w, int T, int E, int k, int* counts, int* offsets,
+                          int* perm_src_token, int* perm_of_assignment, float* perm_weight, void* ws, hipStream_t stream);
 size_t route_quantize_ws_bytes(int T, int E, int k);
 hipError_t launch_route_quantize(const float* logits, int T, int E, int k, int* topk_ids, float* topk_w,
                                  int* counts, int* offsets, int* perm_src_token, int* perm_of_assignment,
@@ -128,6 +131,75 @@ int64_t gated_grad_blocks(int I, int64_t m_total, int E);   // workgroups, fewer
 // sum of `parts` float32 matrices [rows, N] in their order, rounded to 16 bits; with offsets, rows behind the last expert are left
 hipError_t launch_join(const float* part, int parts, int64_t rows, int N, const int32_t* offsets, int E, int dtype_f16,
                        void* out, hipStream_t stream);
+// Kernel-side arguments of the router with scores (validated on the host first).
+struct ScoredParams {
+  const void* logits;
+  const float* bias;       // [E] or nullptr
+  int T, E, k;
+  int softmax, renormalize;
+  int n_group, topk_group, group_top;
+  float scale;
+  int* topk_ids;
+  float* topk_w;
+  float* scores;           // [T, E] or nullptr
+  // set by the launcher
+  int need_all;            // every expert's score is needed
+  int vec;                 // rows can be read 4 values at a time
+  int lanes_per_group;     // a power of two, or 0: groups by way of LDS
+  int lds_token;           // doubles of LDS a token
+};
+struct ScoredGradParams {
+  const void* logits;
+  const float* bias;
+  int T, E, k;
+  int softmax, renormalize;
+  float scale;
+  const int* topk_ids;
+  const float* d_topk_w;
+  const float* d_scores;   // or nullptr
+  int64_t d_scores_ld;     // E, or 0: one row for all tokens
+  void* dlogits;
+  int vec;                 // set by the launcher
+};
+hipError_t launch_route_scored(const ScoredParams& p, int dtype, int* counts, int* offsets, int* perm_src_token,
+                               int* perm_of_assignment, float* perm_weight, void* ws, hipStream_t stream);
+hipError_t launch_route_scored_grad(const ScoredGradParams& p, int dtype, hipStream_t stream);
+
+// Gradients of the weighted combine.
+struct CombineGradParams {
+  const void* dout;        // [T, H]
+  const void* y;           // [rows, H]; not read without dw
+  const int* perm;         // [T * k] or nullptr
+  const float* w;          // [T * k] or nullptr: 1
+  int T, k, H;
+  int64_t rows;
+  void* dy;                // [rows, H] or nullptr
+  float* dw;               // [T * k] or nullptr
+};
+hipError_t launch_combine_grad(const CombineGradParams& p, int dout_dtype, int y_dtype, hipStream_t stream);
+
+// INT4 groups along the last axis.
+hipError_t launch_int4_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int group, int scale_f16, uint8_t* codes,
+                                void* scales, uint8_t* zeros, hipStream_t stream);
+hipError_t launch_int4_dequantize(const uint8_t* codes, const void* scales, const uint8_t* zeros, int64_t rows, int64_t cols,
+                                  int group, int scale_f16, int out_dtype, void* out, hipStream_t stream);
+struct Int4Params {
+  const void* a;           // rows, 16 bit
+  const int32_t* a_rows;
+  const uint8_t* codes;    // [E, N, K/2]
+  const void* scales;      // [E, N, K/group], 16 bit
+  const uint8_t* zeros;    // [E, N, K/group] or nullptr: 8
+  const int32_t* offsets;
+  int E, N, K;             // N: rows of the weights (gated: 2I)
+  int m_total;
+  int src_rows;
+  int act;
+  int rows_hint;
+  int n_tiles;             // set by the launcher
+  void* out;
+};
+int64_t int4_gemv_threads(int E, int N, int K, int64_t m_total, int64_t hint, int gated);   // of the launch
+hipError_t launch_int4_gemv(const Int4Params& p, int f16, int group, int gated, int out_f32, hipStream_t stream);
 hipError_t launch_int8_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int8_t* codes, float* scales,
                                 hipStream_t stream);
 

@@ -353,9 +353,8 @@ size_t route_permute_ws_bytes(int T, int E, int k) {
   return rank + hist;
 }
 
-hipError_t launch_route_permute(const float* logits, int T, int E, int k, int* topk_ids, float* topk_w,
-                                int* counts, int* offsets, int* perm_src_token, int* perm_of_assignment,
-                                float* perm_weight, void* ws, hipStream_t stream) {
+hipError_t launch_permute(const int* topk_ids, const float* topk_w, int T, int E, int k, int* counts, int* offsets,
+                          int* perm_src_token, int* perm_of_assignment, float* perm_weight, void* ws, hipStream_t stream) {
   const int n = T * k;
   const int nchunks = (n + kChunk - 1) / kChunk;
   int* local_rank = static_cast<int*>(ws);
@@ -363,18 +362,9 @@ hipError_t launch_route_permute(const float* logits, int T, int E, int k, int* t
                                            ((static_cast<size_t>(n) * sizeof(int) + 255) & ~size_t(255)));
   int nbits = 0;
   while ((1 << nbits) <= E) ++nbits;   // bits needed for ids 0..E (E is the padding sentinel)
-
-  if (E <= 256)
-    hipLaunchKernelGGL(k_route<4>, dim3((T + 3) / 4), dim3(256), 0, stream, logits, T, E, k, topk_ids, topk_w);
-  else if (E <= 1024)
-    hipLaunchKernelGGL(k_route<16>, dim3((T + 3) / 4), dim3(256), 0, stream, logits, T, E, k, topk_ids, topk_w);
-  else
-    hipLaunchKernelGGL(k_route<0>, dim3((T + 3) / 4), dim3(256), 0, stream, logits, T, E, k, topk_ids, topk_w);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
   hipLaunchKernelGGL(k_chunk_rank, dim3(nchunks), dim3(kRankThreads), 4 * E * sizeof(int), stream, topk_ids,
                      n, E, nbits, local_rank, chunk_hist);
-  err = hipGetLastError();
+  hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   hipLaunchKernelGGL(k_scan, dim3(1), dim3(1024), 0, stream, chunk_hist, nchunks, E, counts, offsets);
   err = hipGetLastError();
@@ -382,6 +372,21 @@ hipError_t launch_route_permute(const float* logits, int T, int E, int k, int* t
   hipLaunchKernelGGL(k_scatter, dim3((n + 255) / 256), dim3(256), 0, stream, topk_ids, topk_w, local_rank,
                      chunk_hist, n, E, k, perm_src_token, perm_of_assignment, perm_weight);
   return hipGetLastError();
+}
+
+hipError_t launch_route_permute(const float* logits, int T, int E, int k, int* topk_ids, float* topk_w,
+                                int* counts, int* offsets, int* perm_src_token, int* perm_of_assignment,
+                                float* perm_weight, void* ws, hipStream_t stream) {
+  if (E <= 256)
+    hipLaunchKernelGGL(k_route<4>, dim3((T + 3) / 4), dim3(256), 0, stream, logits, T, E, k, topk_ids, topk_w);
+  else if (E <= 1024)
+    hipLaunchKernelGGL(k_route<16>, dim3((T + 3) / 4), dim3(256), 0, stream, logits, T, E, k, topk_ids, topk_w);
+  else
+    hipLaunchKernelGGL(k_route<0>, dim3((T + 3) / 4), dim3(256), 0, stream, logits, T, E, k, topk_ids, topk_w);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  return launch_permute(topk_ids, topk_w, T, E, k, counts, offsets, perm_src_token, perm_of_assignment, perm_weight, ws,
+                        stream);
 }
 
 size_t route_quantize_ws_bytes(int T, int E, int k) {

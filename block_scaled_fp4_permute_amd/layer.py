@@ -26,8 +26,9 @@ Choices:
 
 Buffers are allocated once per layer object (torch device memory); a forward
 allocates nothing.  Beside MoELayer: MXMoELayer, FP8MoELayer and INT8MoELayer
-on the other number formats, MoELayer16 on 16-bit weights with the experts'
-gradients.
+on the other number formats, INT4MoELayer on 4-bit weights and 16-bit rows,
+MoELayer16 on 16-bit weights with the layer's gradients.  Every layer takes a
+Router in place of the plain softmax one.
 """
 from __future__ import annotations
 
@@ -36,8 +37,38 @@ from dataclasses import dataclass
 import torch
 
 from . import (BF16, EPI_BF16, EPI_COMBINE_F32, EPI_F32, EPI_SWIGLU_NVFP4, F32, NVFP4Tensor, Routing, lib,
-               moe_expert_ffn, moe_expert_ffn_workspace, moe_route_permute, moe_route_quantize, moe_swiglu,
-               moe_unpermute_combine, nvfp4_grouped_gemm, nvfp4_quantize, nvfp4_weight_repack)
+               SCORE_SOFTMAX, moe_expert_ffn, moe_expert_ffn_workspace, moe_route_permute, moe_route_quantize,
+               moe_route_scored, moe_swiglu, moe_unpermute_combine, nvfp4_grouped_gemm, nvfp4_quantize,
+               nvfp4_weight_repack)
+
+
+@dataclass
+class Router:
+    """Options of moe_route_scored for a layer's routing: scores, balance bias
+    (float32 [E] or None), expert groups, weights.  The default is the softmax
+    router of moe_route_permute."""
+    score: int = SCORE_SOFTMAX
+    bias: torch.Tensor | None = None
+    n_group: int = 1
+    topk_group: int = 1
+    group_top: int = 1
+    renormalize: bool = True
+    scale: float = 1.0
+
+    def weights(self) -> dict:
+        """The options that the gradient takes too."""
+        return dict(score=self.score, bias=self.bias, renormalize=self.renormalize, scale=self.scale)
+
+    def route(self, logits, k, out=None, workspace=None, stream=None):
+        return moe_route_scored(logits, k, n_group=self.n_group, topk_group=self.topk_group, group_top=self.group_top,
+                                out=out, workspace=workspace, stream=stream, **self.weights())
+
+
+def _route(layer, logits: torch.Tensor, stream) -> Routing:
+    """A layer's routing, by its Router if it has one."""
+    if layer.router is not None:
+        return layer.router.route(logits, layer.k, out=layer.routing, workspace=layer.route_ws, stream=stream)
+    return moe_route_permute(logits, layer.k, out=layer.routing, workspace=layer.route_ws, stream=stream)
 
 
 @dataclass
@@ -98,7 +129,7 @@ class MoELayer:
     """Preallocated NVFP4 MoE layer for T tokens."""
 
     def __init__(self, T: int, H: int, I: int, E: int, k: int, device, swiglu: str = "fused",
-                 combine: str = "gather", ffn: str = "one_launch"):
+                 combine: str = "gather", ffn: str = "one_launch", router: Router | None = None):
         assert swiglu in ("fused", "separate") and combine in ("gather", "atomic", "fused")
         assert ffn in ("one_launch", "two_launch")
         if ffn == "one_launch" and (swiglu, combine) not in (("fused", "gather"), ("fused", "fused")):
@@ -106,7 +137,7 @@ class MoELayer:
         if ffn == "two_launch" and combine == "fused":
             combine = "gather"
         self.T, self.H, self.I, self.E, self.k = T, H, I, E, k
-        self.swiglu, self.combine, self.ffn = swiglu, combine, ffn
+        self.swiglu, self.combine, self.ffn, self.router = swiglu, combine, ffn, router
         dev = torch.device(device)
         i32 = dict(dtype=torch.int32, device=dev)
         f32 = dict(dtype=torch.float32, device=dev)
@@ -146,7 +177,11 @@ class MoELayer:
                 marks[i].record(stream)
 
         mark(0)
-        r, _ = moe_route_quantize(logits, k, x, out=self.routing, xq=self.xq, workspace=self.route_ws, stream=stream)
+        if self.router is None:
+            r, _ = moe_route_quantize(logits, k, x, out=self.routing, xq=self.xq, workspace=self.route_ws, stream=stream)
+        else:
+            r = _route(self, logits, stream)
+            nvfp4_quantize(x, out=self.xq, workspace=self.small_ws, stream=stream)
         mark(1)
         mark(2)
         if self.ffn == "one_launch" and w.gu_packed is not None and w.dn_packed is not None:
@@ -246,8 +281,9 @@ class MXMoELayer:
     quantisation of x, gate_up grouped GEMM with the fused SwiGLU + MXFP4
     requantisation, down grouped GEMM (bf16 rows), weighted gather combine."""
 
-    def __init__(self, T: int, H: int, I: int, E: int, k: int, device):
+    def __init__(self, T: int, H: int, I: int, E: int, k: int, device, router: Router | None = None):
         from . import MXFP4Tensor
+        self.router = router
         self.T, self.H, self.I, self.E, self.k = T, H, I, E, k
         dev = torch.device(device)
         i32 = dict(dtype=torch.int32, device=dev)
@@ -276,7 +312,7 @@ class MXMoELayer:
                 marks[i].record(stream)
 
         mark(0)
-        r = moe_route_permute(logits, k, out=self.routing, workspace=self.route_ws, stream=stream)
+        r = _route(self, logits, stream)
         mark(1)
         mxfp4_quantize(x, out=self.xq, stream=stream)
         mark(2)
@@ -329,8 +365,10 @@ class FP8MoELayer:
     which writes float32 rows for the separate kernel); "separate" always
     writes the float32 rows.  Both give the same h, bit for bit."""
 
-    def __init__(self, T: int, H: int, I: int, E: int, k: int, device, swiglu: str = "fused"):
+    def __init__(self, T: int, H: int, I: int, E: int, k: int, device, swiglu: str = "fused",
+                 router: Router | None = None):
         from . import FP8_BLOCK, FP8Tensor
+        self.router = router
         if swiglu not in ("fused", "separate"):
             raise ValueError("swiglu: 'fused' or 'separate'")
         self.T, self.H, self.I, self.E, self.k = T, H, I, E, k
@@ -365,7 +403,7 @@ class FP8MoELayer:
                 marks[i].record(stream)
 
         mark(0)
-        r = moe_route_permute(logits, k, out=self.routing, workspace=self.route_ws, stream=stream)
+        r = _route(self, logits, stream)
         mark(1)
         fp8_quantize(x, 1, out=self.xq, stream=stream)
         mark(2)
@@ -422,8 +460,9 @@ class INT8MoELayer:
     which the column tiles of gate_up share out, so h goes through memory in
     bf16 between the two."""
 
-    def __init__(self, T: int, H: int, I: int, E: int, k: int, device):
+    def __init__(self, T: int, H: int, I: int, E: int, k: int, device, router: Router | None = None):
         from . import INT8Tensor
+        self.router = router
         self.T, self.H, self.I, self.E, self.k = T, H, I, E, k
         dev = torch.device(device)
         i32 = dict(dtype=torch.int32, device=dev)
@@ -455,7 +494,7 @@ class INT8MoELayer:
                 marks[i].record(stream)
 
         mark(0)
-        r = moe_route_permute(logits, k, out=self.routing, workspace=self.route_ws, stream=stream)
+        r = _route(self, logits, stream)
         mark(1)
         int8_quantize(x, out=self.xq, stream=stream)
         mark(2)
@@ -471,18 +510,107 @@ class INT8MoELayer:
         return self.out
 
 
+# ------------------------------------------------------------------ INT4 variant
+@dataclass
+class INT4ExpertWeights:
+    """Per-expert INT4 weights in groups along the reduction: gate_up [E, 2I, H] and
+    down [E, H, I], row-major (no packed form)."""
+    gu: "object"
+    dn: "object"
+
+    @property
+    def E(self):
+        return self.gu.codes.shape[0]
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for q in (self.gu, self.dn) for t in (q.codes, q.scales, q.zeros)
+                   if t is not None)
+
+
+def quantize_expert_weights_int4(w_gu: torch.Tensor, w_dn: torch.Tensor, group: int = 128,
+                                 zeros: bool = False) -> INT4ExpertWeights:
+    """Quantise float32/bf16 weights [E, 2I, H] and [E, H, I] to INT4 on the GPU,
+    with bf16 scales."""
+    from . import int4_quantize
+    return INT4ExpertWeights(*(int4_quantize(w.contiguous(), group, zeros, torch.bfloat16) for w in (w_gu, w_dn)))
+
+
+class INT4MoELayer:
+    """Preallocated MoE layer for T tokens on INT4 weights and bf16 rows, reusing the
+    routing, permutation and combine of the NVFP4 layer: route + permute, gate_up
+    with SiLU and the product (rows gathered through the permutation), down product
+    (bf16 rows), weighted gather combine.  Above `most_rows` rows per expert the
+    weights are dequantised into bf16 buffers of the layer's own each step and the
+    16-bit products run on those: the 4-bit kernels read weights once for up to 64
+    rows and are bound by the decoding beyond."""
+
+    most_rows = 64
+
+    def __init__(self, T: int, H: int, I: int, E: int, k: int, device, router: Router | None = None):
+        self.T, self.H, self.I, self.E, self.k, self.router = T, H, I, E, k, router
+        dev = torch.device(device)
+        i32 = dict(dtype=torch.int32, device=dev)
+        f32 = dict(dtype=torch.float32, device=dev)
+        bf = dict(dtype=torch.bfloat16, device=dev)
+        M = T * k
+        self.routing = Routing(torch.empty((T, k), **i32), torch.empty((T, k), **f32), torch.empty(E, **i32),
+                               torch.empty(E + 1, **i32), torch.empty(M, **i32), torch.empty(M, **i32),
+                               torch.empty(M, **f32))
+        self.route_ws = torch.empty(max(16, lib().moe_route_permute_workspace_size(T, E, k)), dtype=torch.uint8,
+                                    device=dev)
+        self.h = torch.empty((M, I), **bf)
+        self.y2 = torch.empty((M, H), **bf)
+        self.out = torch.empty((T, H), **bf)
+        self.wide = M > self.most_rows * E
+        if self.wide:
+            self.w_gu, self.w_dn = torch.empty((E, 2 * I, H), **bf), torch.empty((E, H, I), **bf)
+
+    def forward(self, logits: torch.Tensor, x: torch.Tensor, w: INT4ExpertWeights, stream=None,
+                marks=None) -> torch.Tensor:
+        """One layer step; ``marks``: optional 5 events recorded before routing and
+        after each stage (route, gate_up, down, combine)."""
+        from . import int4_dequantize, int4_grouped_gemv, moe_gated_ffn, moe_grouped_gemm
+        T, k, M = self.T, self.k, self.T * self.k
+
+        def mark(i):
+            if marks is not None and marks[i] is not None:
+                marks[i].record(stream)
+
+        mark(0)
+        r = _route(self, logits, stream)
+        mark(1)
+        if self.wide:
+            int4_dequantize(w.gu, out=self.w_gu, stream=stream)
+            moe_gated_ffn(x, self.w_gu, r.offsets, m_total=M, a_rows=r.perm_src_token, out=self.h, stream=stream)
+            mark(2)
+            int4_dequantize(w.dn, out=self.w_dn, stream=stream)
+            moe_grouped_gemm(self.h, self.w_dn, r.offsets, m_total=M, out=self.y2, stream=stream)
+        else:
+            int4_grouped_gemv(x, w.gu, r.offsets, m_total=M, a_rows=r.perm_src_token, gated=True, out=self.h,
+                              stream=stream)
+            mark(2)
+            int4_grouped_gemv(self.h, w.dn, r.offsets, m_total=M, out=self.y2, stream=stream)
+        mark(3)
+        moe_unpermute_combine(self.y2, r.perm_of_assignment, r.topk_w, T, k, out=self.out, stream=stream)
+        mark(4)
+        return self.out
+
+
 # ------------------------------------------------------------------ 16-bit experts
 class MoELayer16:
     """Preallocated MoE layer for T tokens on bfloat16 (or float16) expert
     weights, row-major [E, 2I, H] and [E, H, I]: the form they are trained in
     before quantize_expert_weights*.  forward: route + permute, gated block
     (rows gathered through the permutation), down product, weighted gather
-    combine (bf16 weights; with float16 ones use expert_rows).  expert_rows and
+    combine (bf16 weights; with float16 ones use expert_rows); backward: the
+    layer's gradients, those of the logits among them.  expert_rows and
     expert_rows_backward are the experts alone, on rows in expert order, with
     the gradients of x (per token) and of both weights; the weighting of the
-    rows by topk_w and its gradient stay with the caller's loss."""
+    rows by topk_w and its gradient stay with the caller's loss there."""
 
-    def __init__(self, T: int, H: int, I: int, E: int, k: int, device, dtype=torch.bfloat16, activation: int = 0):
+    def __init__(self, T: int, H: int, I: int, E: int, k: int, device, dtype=torch.bfloat16, activation: int = 0,
+                 router: Router | None = None):
+        self.router = router
         self.T, self.H, self.I, self.E, self.k = T, H, I, E, k
         self.dtype, self.activation = dtype, activation
         dev = torch.device(device)
@@ -502,15 +630,15 @@ class MoELayer16:
 
     def route(self, logits: torch.Tensor, stream=None) -> Routing:
         self._gu_of_h = None
-        return moe_route_permute(logits, self.k, out=self.routing, workspace=self.route_ws, stream=stream)
+        return _route(self, logits, stream)
 
     def forward(self, logits: torch.Tensor, x: torch.Tensor, w_gu: torch.Tensor, w_dn: torch.Tensor,
-                stream=None) -> torch.Tensor:
-        """One layer step, bf16 [T, H]."""
+                stream=None, gu: torch.Tensor | None = None) -> torch.Tensor:
+        """One layer step, bf16 [T, H]; gu: as for expert_rows, for backward."""
         if self.dtype == torch.float16:
             raise TypeError("forward: the combine takes bfloat16 rows, not float16 ones (use route and expert_rows)")
         r = self.route(logits, stream)
-        self.expert_rows(x, w_gu, w_dn, stream=stream)
+        self.expert_rows(x, w_gu, w_dn, gu=gu, stream=stream)
         return moe_unpermute_combine(self.y2, r.perm_of_assignment, r.topk_w, self.T, self.k, out=self.out,
                                      stream=stream)
 
@@ -546,3 +674,21 @@ class MoELayer16:
         if self.dtype == torch.bfloat16:
             dx = moe_unpermute_combine(dx, r.perm_of_assignment, None, self.T, self.k, stream=stream)
         return dx, dw_gu, dw_dn
+
+    def backward(self, dout: torch.Tensor, gu: torch.Tensor, logits: torch.Tensor, x: torch.Tensor, w_gu: torch.Tensor,
+                 w_dn: torch.Tensor, d_scores: torch.Tensor | None = None, stream=None):
+        """Gradients from dout [T, H] (bf16 or float32) of the last forward call,
+        whose gu and inputs these are: (dlogits, dx, dw_gu, dw_dn).  d_scores: the
+        gradient of the router's scores (a balance loss), as for
+        moe_route_scored_backward.  Refused as in expert_rows_backward; bf16
+        weights only."""
+        from . import moe_route_scored_backward, moe_unpermute_combine_backward
+        if self.dtype == torch.float16:
+            raise TypeError("backward: the combine takes bfloat16 rows, not float16 ones (use expert_rows_backward)")
+        if self._gu_of_h is None or gu.data_ptr() != self._gu_of_h:
+            raise ValueError("gu is not that of the last forward call: h, y and the routing are another call's")
+        r = self.routing
+        dy, dw = moe_unpermute_combine_backward(dout, self.y2, r.perm_of_assignment, r.topk_w, stream=stream)
+        how = (self.router or Router()).weights()
+        dlogits = moe_route_scored_backward(dw, logits, r.topk_ids, d_scores=d_scores, stream=stream, **how)
+        return (dlogits,) + self.expert_rows_backward(dy, gu, x, w_gu, w_dn, stream=stream)

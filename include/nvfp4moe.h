@@ -67,7 +67,7 @@ typedef enum nvfp4moe_status {
 typedef enum nvfp4moe_dtype {
   NVFP4MOE_F32 = 0,
   NVFP4MOE_BF16 = 1,
-  NVFP4MOE_F16 = 2               /* moe_gated_ffn, moe_grouped_gemm and their gradients only */
+  NVFP4MOE_F16 = 2               /* the 16-bit expert FFN, the router with scores and INT4 only */
 } nvfp4moe_dtype;
 
 /* activation of the gated feed-forward block */
@@ -75,6 +75,12 @@ typedef enum nvfp4moe_activation {
   NVFP4MOE_ACT_SILU = 0,         /* g / (1 + exp(-g)) */
   NVFP4MOE_ACT_GELU = 1          /* g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
 } nvfp4moe_activation;
+
+/* scores of moe_route_scored */
+typedef enum nvfp4moe_score {
+  NVFP4MOE_SCORE_SOFTMAX = 0,    /* softmax over the token's open experts */
+  NVFP4MOE_SCORE_SIGMOID = 1     /* 1 / (1 + exp(-l)) */
+} nvfp4moe_score;
 
 typedef enum nvfp4moe_epilogue {
   /* y[p, n] = acc * (g_a * g_b[e]) written as float32 to out[p*N + n], p < m_total */
@@ -159,6 +165,76 @@ int moe_route_permute(const float* logits, int32_t T, int32_t E, int32_t k,
                       int32_t* topk_ids, float* topk_w, int32_t* counts, int32_t* offsets,
                       int32_t* perm_src_token, int32_t* perm_of_assignment, float* perm_weight,
                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- router with scores
+ * moe_route_permute with the choices of a trained router (the router of
+ * "Discovering SM120-Specific CUTLASS MoE Kernels", section "Input Knowledge
+ * Required", whose form the pages leave open):
+ *   scores   s [T, E] of the logits l (float32, bf16 or f16), by `score`
+ *   keys     s + bias[e] (the balance bias enters the choice, not the weights)
+ *   groups   the E experts are n_group groups of neighbours; a group's value is the
+ *            sum of its group_top (1 or 2) largest keys; the topk_group best stay
+ *            (ties: the lower group)
+ *   choice   the k largest keys of the groups that stay, descending, ties to the
+ *            lower id; without a bias by the logits themselves (the scores' order
+ *            without their saturation)
+ *   weights  the chosen scores u_j, as they are or (renormalize) u_j / sum(u), times
+ *            `scale`, rounded to float32 once
+ * Scores, keys and weights are float64 up to there, so near-equal keys are ordered
+ * as defined.  An expert is closed if its logit is -inf or NaN, or its key -inf or
+ * NaN (a bias of -inf takes it out).  Closed experts have score 0 in a softmax,
+ * count nothing in their group (a group without an open expert comes last), and
+ * are chosen, by ascending id and with weight 0, only where the groups that stay
+ * have fewer than k open ones; a row without any open expert has weights 0.  +inf
+ * counts as the largest float32.
+ * Outputs, permutation and workspace as for moe_route_permute; `scores` (nullable)
+ * receives s as float32, 0 where the logit is -inf or NaN.  Limits as there, and
+ * n_group divides E, n_group <= 64, k <= topk_group * E / n_group,
+ * group_top <= E / n_group. */
+typedef struct nvfp4moe_route_args {
+  const void* logits;         /* [T, E] */
+  int32_t dtype;              /* nvfp4moe_dtype of the logits */
+  int32_t T, E, k;
+  int32_t score;              /* nvfp4moe_score */
+  int32_t renormalize;        /* 0 or 1 */
+  float scale;
+  const float* bias;          /* [E] or NULL */
+  int32_t n_group;            /* 1: no groups (then topk_group and group_top are 1) */
+  int32_t topk_group;
+  int32_t group_top;
+  int32_t* topk_ids;          /* out [T, k] */
+  float* topk_w;              /* out [T, k] */
+  int32_t* counts;            /* out [E] */
+  int32_t* offsets;           /* out [E+1] */
+  int32_t* perm_src_token;    /* out [T*k] */
+  int32_t* perm_of_assignment;/* out [T*k] */
+  float* perm_weight;         /* out [T*k] or NULL */
+  float* scores;              /* out [T, E] or NULL */
+} nvfp4moe_route_args;
+int moe_route_scored(const nvfp4moe_route_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of the logits from d_topk_w [T, k], that of the weights, and (nullable)
+ * d_scores, that of the scores (a balance loss): [T, E] with d_scores_ld = E, or one
+ * row for all tokens with d_scores_ld = 0.  logits, topk_ids and the options are
+ * those of the forward call (bias: only its -inf and NaN matter).  The choice and
+ * the bias have no gradient; closed logits get 0.  Ids outside [0, E) are left out;
+ * an id that stands twice in a row counts twice.  dlogits has the logits' type;
+ * float32 arithmetic, rounded once. */
+typedef struct nvfp4moe_route_grad_args {
+  const void* logits;
+  int32_t dtype;
+  int32_t T, E, k;
+  int32_t score;
+  int32_t renormalize;
+  float scale;
+  const float* bias;
+  const int32_t* topk_ids;
+  const float* d_topk_w;
+  const float* d_scores;      /* or NULL */
+  int64_t d_scores_ld;        /* E or 0 */
+  void* dlogits;              /* out [T, E] */
+} nvfp4moe_route_grad_args;
+int moe_route_scored_backward(const nvfp4moe_route_grad_args* args, void* stream);
 
 /* ---------------------------------------------------------------- quantise
  * The NVFP4 encoding of an operand (e2m1 values with one ue4m3 scale per 16
@@ -554,6 +630,60 @@ typedef struct nvfp4moe_int8_gemm_args {
 } nvfp4moe_int8_gemm_args;
 int int8_grouped_gemm(const nvfp4moe_int8_gemm_args* args, void* stream);
 
+/* ---------------------------------------------------------------- INT4 variant
+ * Weights in 4 bits on 16-bit activations, for few rows an expert (decode), where
+ * the weights' stream is the cost.  Groups of 32, 64 or 128 values along the
+ * reduction share a scale and, optionally, a zero point:
+ *   codes   uint8 [rows, cols/2]      element 2i in the low nibble of byte i
+ *   scales  bf16 or f16 [rows, cols/group]
+ *   zeros   uint8 [rows, cols/group], 0 .. 15, or NULL (8 everywhere)
+ *   value = (code - zero) * scale
+ * int4_quantize: x [rows, cols] (float32, bf16 or f16).  Without zeros: scale =
+ * absmax * (1/7), code = clamp(rint(x / scale), -8, 7) + 8; with: lo = min(x, 0), hi
+ * = max(x, 0), scale = (hi - lo) * (1/15), zero = clamp(rint(-lo / scale), 0, 15),
+ * code = clamp(rint(x / scale) + zero, 0, 15).  The scale is a float32 product (with
+ * the float32 nearest 1/7 or 1/15) rounded to its type (1 where that is zero),
+ * quotients are correctly rounded float32 ones, rint goes to the nearest even:
+ * reproducible bit for bit.  A group that holds a NaN or an
+ * infinity, or whose scale overflows its type, gets scale NaN and codes 8 (with
+ * zeros: codes and zero 0).  cols % group == 0; x and codes 16-byte aligned;
+ * rows * cols < 2^40. */
+int int4_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int32_t group, int32_t scale_dtype,
+                  uint8_t* codes, void* scales, uint8_t* zeros, void* stream);
+/* The values: out [rows, cols] in scale_dtype (rounded once) or float32 (exact).
+ * 16-byte aligned codes and out. */
+int int4_dequantize(const uint8_t* codes, const void* scales, const uint8_t* zeros, int64_t rows, int64_t cols,
+                    int32_t group, int32_t scale_dtype, int32_t out_dtype, void* out, void* stream);
+/* Grouped product, rows and experts as in the 16-bit expert FFN:
+ *   y[p, n] = sum_k a[r, k] value(b)[e, n, k]       (r = a_rows ? a_rows[p] : p)
+ * in dtype or float32; gated (N = 2I, rows [0, I) gate): h[p, i] = act(y[p, i]) *
+ * y[p, I + i] [m_total, I] in dtype.  Exact products, float32 sums in a fixed
+ * order.  Any N (gated: even); K % group == 0; E <= 4096; zeros entries above 15
+ * count as they are.  Activations finite (a row with an infinity or a NaN gives
+ * NaNs in its own results only).  Any number of rows gives the product; from some
+ * 64 rows an expert int4_dequantize and the 16-bit products are faster.  Size limits
+ * (NVFP4MOE_ERR_UNSUPPORTED beyond them) as there, and fewer than 2^32 threads in
+ * all. */
+typedef struct nvfp4moe_int4_gemv_args {
+  const void* a;              /* [a_rows_total, K], 16-byte aligned */
+  int32_t dtype;              /* NVFP4MOE_BF16 or NVFP4MOE_F16: of a, b_scales and 16-bit results */
+  const int32_t* a_rows;      /* device [m_total] or NULL; entries in [0, a_rows_total) */
+  int64_t a_rows_total;       /* without a_rows: at least m_total */
+  const uint8_t* b_codes;     /* [E, N, K/2], 16-byte aligned */
+  const void* b_scales;       /* [E, N, K/group] */
+  const uint8_t* b_zeros;     /* [E, N, K/group] or NULL */
+  int32_t group;              /* 32, 64 or 128 */
+  const int32_t* offsets;     /* device [E+1] */
+  int32_t E, N, K;
+  int64_t m_total;
+  int32_t gated;              /* 0 or 1 */
+  int32_t activation;         /* nvfp4moe_activation, gated only */
+  int32_t out_dtype;          /* dtype, or NVFP4MOE_F32 (not gated) */
+  int32_t max_rows_per_expert_hint;
+  void* out;                  /* 16-byte aligned */
+} nvfp4moe_int4_gemv_args;
+int int4_grouped_gemv(const nvfp4moe_int4_gemv_args* args, void* stream);
+
 /* ---------------------------------------------------------------- packed weights
  * Weights are static, so they can be repacked once into a tile layout that the
  * grouped GEMM streams with fully contiguous, non-temporal loads: tile
@@ -600,6 +730,18 @@ int moe_swiglu(const void* gate_up, int32_t dtype, int64_t M, int32_t I,
 int moe_unpermute_combine(const void* y, int32_t y_dtype, const int32_t* perm_of_assignment,
                           const float* topk_w, int32_t T, int32_t k, int32_t H,
                           void* out, int32_t out_dtype, void* stream);
+
+/* Gradients of moe_unpermute_combine from dout [T, H]: dy[row(t, j), :] = topk_w[t, j]
+ * * dout[t, :] in y's type, and d_topk_w[t, j] = <dout[t], y[row(t, j)]> in float32
+ * (fixed order).  y [y_rows, H]; perm_of_assignment and topk_w as in the forward
+ * call (either NULL), entries of perm_of_assignment all different: rows of dy that
+ * none names are left as they are, and an entry outside [0, y_rows) is left out
+ * (d_topk_w 0).  Either of dy and d_topk_w may be NULL; y is not read without
+ * d_topk_w.  float32 and bf16, each of dout and y.  H % 8 == 0; T >= 1; k <= 1024;
+ * T * ceil(k / 4) < 2^24. */
+int moe_unpermute_combine_backward(const void* dout, int32_t dout_dtype, const void* y, int32_t y_dtype, int64_t y_rows,
+                                   const int32_t* perm_of_assignment, const float* topk_w, int32_t T, int32_t k,
+                                   int32_t H, void* dy, float* d_topk_w, void* stream);
 
 /* ---------------------------------------------------------------- status */
 const char* nvfp4moe_status_string(int status);
