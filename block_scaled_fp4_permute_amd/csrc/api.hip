@@ -1194,6 +1194,9 @@ int int4_grouped_gemv(const nvfp4moe_int4_gemv_args* a, void* stream) {
     return fail(NVFP4MOE_ERR_INVALID, "%s: activation %d", fn, a->activation);
   if (a->out_dtype != a->dtype && (a->gated || a->out_dtype != NVFP4MOE_F32))
     return fail(NVFP4MOE_ERR_INVALID, "%s: out_dtype %d (dtype, or float32 if not gated)", fn, a->out_dtype);
+  // the kernels' offsets from a gate row to its up row, in bytes of codes
+  if (a->gated && prod_ge(a->N / 2 + 64, a->K / 2, (int64_t(1) << 32) - 64))
+    return fail(NVFP4MOE_ERR_UNSUPPORTED, "%s: gated with I * K about 2^33 or more", fn);
   if (!aligned(a->a, 16) || !aligned(a->b_codes, 16) || !aligned(a->b_scales, 2) || !aligned(a->out, 16))
     return fail(NVFP4MOE_ERR_INVALID, "%s: a, b_codes and out must be 16-byte, b_scales 2-byte aligned", fn);
   const int64_t hint = a->max_rows_per_expert_hint > 0 ? a->max_rows_per_expert_hint : 0;

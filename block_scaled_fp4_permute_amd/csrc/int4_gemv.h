@@ -13,12 +13,16 @@
 // float32, sums and scales are float32; the offset of 16 costs about two bits of
 // the sum's 24.
 //
-// A wave's step is 128 codes of 16 weight rows: one 16-byte load a lane.  With
-// groups of 32 or 64 the four dwords are transposed over the lane groups (two
+// A wave takes 256 codes (128 bytes) of 16 weight rows at a time where registers
+// allow: loads of 64 bytes a row reach 3.6 TB/s from memory (non-temporal, 4 loads in
+// flight), of 128 bytes 6.6, as contiguous ones do.  A step is 128 codes.  With
+// groups of 32 or 64 a lane's four dwords are transposed over the lane groups (two
 // swaps each of 32 and 16 lanes), so that one matrix instruction takes 32
 // neighbouring codes, of one group.  Within 8 codes the pairs are (i, i + 4), as
-// the shifts give them; x is permuted alike in registers.
+// the shifts give them; x is permuted alike.
 #pragma once
+
+#include <type_traits>
 
 #include "tile_gemm.h"
 
@@ -32,10 +36,7 @@ struct I4Type<false> {
   static constexpr uint32_t mask = 0x00780078u, base = 0x41804180u;     // bits of q, 16.0
   static constexpr uint32_t one = 0x3F803F80u, minus24 = 0xC1C0C1C0u;
   template <int P>
-  static __device__ __forceinline__ uint32_t pair(uint32_t w) {          // codes P and P + 4
-    const uint32_t s = P == 0 ? w << 3 : w >> (4 * P - 3);
-    return (s & mask) | base;
-  }
+  static __device__ __forceinline__ uint32_t shift(uint32_t w) { return P == 0 ? w << 3 : w >> (4 * P - 3); }   // codes P and P + 4
   static __device__ __forceinline__ float value(uint16_t b) { return bf16_to_f32(b); }
 };
 template <>
@@ -44,12 +45,17 @@ struct I4Type<true> {
   static constexpr uint32_t mask = 0x03C003C0u, base = 0x4C004C00u;
   static constexpr uint32_t one = 0x3C003C00u, minus24 = 0xCE00CE00u;
   template <int P>
-  static __device__ __forceinline__ uint32_t pair(uint32_t w) {
-    const uint32_t s = P < 2 ? w << (6 - 4 * P) : w >> (4 * P - 6);
-    return (s & mask) | base;
-  }
+  static __device__ __forceinline__ uint32_t shift(uint32_t w) { return P < 2 ? w << (6 - 4 * P) : w >> (4 * P - 6); }
   static __device__ __forceinline__ float value(uint16_t b) { return static_cast<float>(__builtin_bit_cast(_Float16, b)); }
 };
+
+// 8 codes -> 16 + q in pairs (i, i + 4).  mask and base are in registers that the
+// compiler takes for variables: as constants they would not fit one and-or.
+template <class I4>
+__device__ __forceinline__ u32x4 i4_decode(uint32_t w, uint32_t mask, uint32_t base) {
+  return u32x4{(I4::template shift<0>(w) & mask) | base, (I4::template shift<1>(w) & mask) | base,
+               (I4::template shift<2>(w) & mask) | base, (I4::template shift<3>(w) & mask) | base};
+}
 
 // 8 values of x in memory order -> pairs (i, i + 4)
 __device__ __forceinline__ u32x4 i4_pairs(u32x4 d) {
@@ -75,187 +81,342 @@ constexpr int kI4Step = 128;               // codes of a weight row per wave and
 
 // Shapes of a workgroup: RT x 16 rows of an expert times WC x CT tiles of 16 weight
 // rows (gated: 8 of gate and the 8 of up for the same columns), WK waves sharing
-// the reduction.
+// the reduction, in blocks of `bs` steps.  xlds: all of the rows' x in LDS.
 struct Int4Shape {
-  int rt, ct, wk, wc;
+  int rt, ct, wk, wc, bs, xlds;
 };
-constexpr Int4Shape kI4Shapes[] = {{1, 1, 8, 1}, {1, 4, 1, 4}, {4, 2, 4, 1}};
-#define I4_SHAPE(i) kI4Shapes[i].rt, kI4Shapes[i].ct, kI4Shapes[i].wk, kI4Shapes[i].wc
+constexpr Int4Shape kI4Shapes[] = {{1, 1, 8, 1, 2, 1}, {1, 2, 8, 1, 2, 0}, {1, 2, 4, 1, 2, 0}, {1, 2, 1, 4, 2, 0}, {4, 2, 4, 1, 1, 0}};
+constexpr int kI4XBytes = 64 * 1024;       // of LDS for x, at most
 
-// which of them, by rows of one expert (the hint, or what m_total gives each expert
-// that can have any) and the length of the reduction
-static inline int i4_choice(int E, int N, int K, int64_t m_total, int64_t hint, int gated) {
-  const int64_t experts = E < m_total ? E : m_total;
-  const int64_t share = experts ? (m_total + experts - 1) / experts : 0;
-  const int64_t rows = hint > share ? hint : share;
-  if (rows > 16) return 2;
-  return K <= 512 ? 1 : 0;
-}
+static inline int64_t i4_xbytes(int64_t rows, int K) { return rows * ((K + kI4Step - 1) / kI4Step) * (2 * kI4Step); }
 static inline int i4_tiles(const Int4Shape& s, int N, int gated) {
   const int width = gated ? N / 2 : N, per = (gated ? 8 : 16) * s.ct * s.wc;
   return (width + per - 1) / per;
 }
-// workgroups: at least one for each task (find_task)
+static inline int64_t i4_rows(int E, int64_t m_total, int64_t hint) {
+  const int64_t experts = E < m_total ? E : m_total;
+  const int64_t share = experts ? (m_total + experts - 1) / experts : 0;
+  return hint > share ? hint : share;
+}
+// which of them, by rows of one expert (the hint, or what m_total gives each expert
+// that can have any), the length of the reduction, and tasks
+static inline int i4_choice(int E, int N, int K, int64_t m_total, int64_t hint, int gated) {
+  const int64_t experts = E < m_total ? E : m_total;
+  const int64_t rows = i4_rows(E, m_total, hint);
+  if (rows > 16) return 4;
+  if (K <= 512) return 3;
+  const int64_t tasks = experts * i4_tiles(kI4Shapes[1], N, gated);
+  if (tasks >= 1024) return 2;
+  return i4_xbytes(rows, K) <= kI4XBytes && tasks <= 512 ? 0 : 1;
+}
+// iterations of a wave over column groups (the short reductions): about 16 waves a CU
+static inline int i4_rounds(const Int4Shape& s, int E, int N, int64_t m_total, int gated) {
+  if (s.wk > 1) return 1;
+  const int64_t chunks = m_total / (16 * s.rt) + (E < m_total ? E : m_total);
+  const int64_t n = chunks * i4_tiles(s, N, gated) / 1024;
+  return n < 1 ? 1 : n > 16 ? 16 : static_cast<int>(n);
+}
+// workgroups: at least one for each task (i4_find)
 static inline int64_t i4_blocks(const Int4Shape& s, int E, int N, int64_t m_total, int gated) {
   const int64_t chunks = m_total / (16 * s.rt) + (E < m_total ? E : m_total);
-  return (chunks * i4_tiles(s, N, gated) + 7) / 8 * 8;
+  const int rounds = i4_rounds(s, E, N, m_total, gated);
+  return (chunks * ((i4_tiles(s, N, gated) + rounds - 1) / rounds) + 7) / 8 * 8;
 }
 
-template <bool F16, int GROUP, bool ZEROS, int RT, int CT, int WK, int WC>
-__global__ __launch_bounds__(64 * WK * WC) __attribute__((amdgpu_waves_per_eu(2))) void k_int4_gemv(const Int4Params p, int gated, int out32) {
+// inclusive prefix sum over the 64 lanes
+__device__ __forceinline__ int i4_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);      // row_shr:1, zeros shifted in
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+  const int r0 = __builtin_amdgcn_readlane(v, 15), r1 = __builtin_amdgcn_readlane(v, 31), r2 = __builtin_amdgcn_readlane(v, 47);
+  const int row = (threadIdx.x & 63) >> 4;
+  return v + (row > 0 ? r0 : 0) + (row > 1 ? r1 : 0) + (row > 2 ? r2 : 0);
+}
+
+// The task of workgroup blockIdx.x: a chunk of MC rows of an expert and a column
+// tile.  Tasks are numbered by chunk, then column tile, and each XCD (workgroups go
+// round them in turn) gets a contiguous eighth, so that the tiles of a chunk share
+// its rows in one L2.  Every wave finds its task on its own from the offsets, 4
+// experts a lane.  row0: the chunk's first row, rows: how many.  False where the
+// workgroup has none.  Offsets are clamped, so that inconsistent ones give wrong
+// rows, never an access out of bounds.
+template <int MC>
+__device__ __forceinline__ bool i4_find(const Int4Params& p, int& e_out, int& row0, int& rows, int& nt) {
+  const int lane = threadIdx.x & 63;
+  int at[5], c[4], incl = 0, sum = 0;
+  auto group = [&](int g0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) at[i] = min(max(p.offsets[min(g0 + 4 * lane + i, p.E)], 0), p.m_total);
+    sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = (max(at[i + 1] - at[i], 0) + MC - 1) / MC;
+      sum += c[i];
+    }
+    incl = i4_scan(sum);
+  };
+  int64_t total = 0;
+  for (int g0 = 0; g0 < p.E; g0 += 256) {
+    group(g0);
+    total += __builtin_amdgcn_readlane(incl, 63);
+  }
+  total = total * p.n_tiles;
+  const int64_t per = (total + 7) >> 3;
+  const int64_t id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((blockIdx.x >> 3) >= per || id >= total) return false;
+  int chunk = static_cast<int>(static_cast<uint32_t>(id) / static_cast<uint32_t>(p.n_tiles));
+  nt = static_cast<int>(id) - chunk * p.n_tiles;
+  int g0 = 0;
+  if (p.E > 256) {
+    for (;; g0 += 256) {
+      group(g0);
+      const int n = __builtin_amdgcn_readlane(incl, 63);
+      if (chunk < n || g0 + 256 >= p.E) break;
+      chunk -= n;
+    }
+  }
+  const uint64_t have = __ballot(incl > chunk);
+  const int who = have ? __builtin_ctzll(have) : 63;
+  int m = chunk - (incl - sum), e = g0 + 4 * lane, r = at[0], end = at[1];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const bool on = e == g0 + 4 * lane + i && m >= c[i];
+    m -= on ? c[i] : 0;
+    e += on ? 1 : 0;
+    r = on ? at[i + 1] : r;
+    end = on ? at[i + 2] : end;
+  }
+  m = __builtin_amdgcn_readlane(m, who);
+  e_out = __builtin_amdgcn_readlane(e, who);
+  row0 = __builtin_amdgcn_readlane(r, who) + m * MC;
+  rows = min(MC, __builtin_amdgcn_readlane(end, who) - row0);
+  return e_out < p.E && m >= 0 && rows > 0;
+}
+
+// rows of 16 lanes r0 .. r3 -> four values that hold row i in every row
+__device__ __forceinline__ void i4_spread(uint32_t v, uint32_t (&out)[4]) {
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);         // r0 r0 r2 r2, r1 r1 r3 r3
+  const auto b = __builtin_amdgcn_permlane32_swap(a[0], a[0], false, false);
+  const auto c = __builtin_amdgcn_permlane32_swap(a[1], a[1], false, false);
+  out[0] = b[0];
+  out[1] = c[0];
+  out[2] = b[1];
+  out[3] = c[1];
+}
+
+template <bool F16, int GROUP, bool ZEROS, int SHAPE>
+__global__ __launch_bounds__(64 * kI4Shapes[SHAPE].wk * kI4Shapes[SHAPE].wc) __attribute__((amdgpu_waves_per_eu(kI4Shapes[SHAPE].rt == 1 && !kI4Shapes[SHAPE].xlds ? 3 : 2)))
+void k_int4_gemv(const Int4Params p, int gated, int out32) {
   using I4 = I4Type<F16>;
   using TT = typename I4::TT;
+  constexpr int RT = kI4Shapes[SHAPE].rt, CT = kI4Shapes[SHAPE].ct, WK = kI4Shapes[SHAPE].wk, WC = kI4Shapes[SHAPE].wc;
+  constexpr int BS = kI4Shapes[SHAPE].bs;
+  constexpr bool XLDS = kI4Shapes[SHAPE].xlds, LOOP = WK == 1;
+  constexpr int DEPTH = XLDS ? 3 : 1;                       // blocks of codes on their way
   constexpr bool TR = GROUP < kI4Step;
   constexpr int GS = kI4Step / GROUP;                       // groups of a step
   constexpr int MS = 4 / GS;                                // matrix instructions of a group
-  constexpr int TURNS = RT * CT <= 2 ? 4 : RT * CT <= 4 ? 2 : 1;   // steps loaded ahead
+  constexpr int PAIRS = CT * BS;                            // (step, tile) pairs of a block
+  constexpr int LPR = 4 * BS, RPL = 64 / LPR;               // lanes of a row's load, rows of a load
   constexpr int LD = 16 * CT + 4;                           // floats of a row of partial sums
+  static_assert(PAIRS <= 4, "a lane group holds the scales of one pair");
+  static_assert(!XLDS || RT == 1, "one chunk of rows in LDS");
   __shared__ float red[WK][WC][16 * RT][LD];
-  static_assert(fits_lds(sizeof(red), 1), "partial sums exceed the LDS of a CU");
-  int e, m0, nt;
-  bool narrow;
-  {
-    GemmParams map{};
-    map.offsets = p.offsets;
-    map.E = p.E;
-    map.m_total = p.m_total;
-    map.n_tiles = p.n_tiles;
-    map.slots = 1 << 30;
-    if (!find_task<RT, false, 0>(map, e, m0, nt, narrow)) return;
-  }
-  const int row0 = min(max(p.offsets[e], 0), p.m_total);
-  const int rows = min(16 * RT, min(max(p.offsets[e + 1], 0), p.m_total) - row0 - m0);
-  if (rows <= 0 || m0 < 0) return;          // offsets that overlap so far that the task count does not fit
+  __shared__ u32x4 stage[WK * WC][CT][64 * BS];
+  extern __shared__ u32x4 xall[];
+  static_assert(fits_lds(sizeof(red) + sizeof(stage) + (XLDS ? kI4XBytes : 0), 1), "partial sums and stages exceed the LDS of a CU");
+  int e, row0, rows, nt;
+  if (!i4_find<16 * RT>(p, e, row0, rows, nt)) return;
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wk = wave % WK, wc = wave / WK;
   const int cols = gated ? 8 : 16;                          // output columns of a tile
   const int width = gated ? p.N / 2 : p.N;
-  const int c0 = nt * (WC * CT * cols);                     // of the task
   const int K = p.K;
   const int groups = K / GROUP;
-  const uint8_t* x[RT];
+  const int steps = (K + kI4Step - 1) / kI4Step;
+  const int per = (steps + WK - 1) / WK;
+  const int first = wk * per, last = min(first + per, steps);
+
+  // Codes are read as memory has them, neighbouring lanes 64 BS bytes of a row (lanes
+  // as the matrix instruction wants them would touch a line each), and change lanes
+  // by way of LDS: chunk c of row r at place c ^ f(r), so that neither side meets a
+  // bank twice.
+  auto swizzle = [](int r) __attribute__((always_inline)) { return BS == 2 ? (r >> 1) & 7 : (r >> 2) & 3; };
+  u32x4* const put = &stage[wave][0][lane];
+  const u32x4* const get = &stage[wave][0][LPR * lr];
+  // Weights: the wave's first row as a base, 32-bit offsets of the lane's from there
+  // (gated: the caller keeps the up half's below 2^32; scales have a quarter of the
+  // codes' bytes at most).  Scales: lane group g those of pair g (step g / CT, tile
+  // g % CT), spread over the groups in registers.
+  const int pair = lg & (PAIRS - 1);
+  const uint8_t *qb, *sb, *zb;
+  uint32_t qo[CT][BS], so;
+  auto columns = [&](int c0) __attribute__((always_inline)) {             // the wave's first column
+    const int cw = min(c0, width - 1);
+    const int64_t n0 = static_cast<int64_t>(e) * p.N + cw;
+    qb = p.codes + n0 * (K / 2);
+    sb = static_cast<const uint8_t*>(p.scales) + n0 * groups * 2;
+    zb = ZEROS ? p.zeros + n0 * groups : nullptr;
+    auto row_of = [&](int j, int r) __attribute__((always_inline)) {
+      return static_cast<uint32_t>(min(c0 + j * cols + (gated ? r & 7 : r), width - 1) - cw + (gated ? (r >> 3) * width : 0));
+    };
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    int r = row0 + m0 + (16 * i + lr < rows ? 16 * i + lr : 0);
+    for (int j = 0; j < CT; ++j)
+#pragma unroll
+      for (int h = 0; h < BS; ++h) {
+        const int r = h * RPL + lane / LPR;
+        qo[j][h] = row_of(j, r) * static_cast<uint32_t>(K / 2) + 16 * ((lane % LPR) ^ swizzle(r));
+      }
+    so = row_of(pair % CT, lr) * static_cast<uint32_t>(groups) + (pair / CT) * GS;
+  };
+
+  // rows of x; places past the chunk's hold zeros or the first row again: nothing of theirs is written
+  auto source = [&](int place) __attribute__((always_inline)) {
+    int r = row0 + (place < rows ? place : 0);
     if (p.a_rows) {
       r = p.a_rows[r];
       r = (r >= 0 && r < p.src_rows) ? r : 0;
     }
-    x[i] = static_cast<const uint8_t*>(p.a) + static_cast<int64_t>(r) * K * 2;
+    return static_cast<const uint8_t*>(p.a) + static_cast<int64_t>(r) * K * 2;
+  };
+  const uint8_t* x[RT];
+  if constexpr (!XLDS) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) x[i] = source(16 * i + lr) + (TR ? 16 : 64) * lg;
   }
-  const uint8_t* q[CT];
-  const uint16_t* s[CT];
-  const uint8_t* z[CT];
+  uint32_t mask = I4::mask, base = I4::base;
+  asm("" : "+v"(mask));
+  asm("" : "+s"(base));
+  const uint32_t c24 = ZEROS ? I4::one : I4::minus24;
+  const u32x4 fixed = {c24, c24, c24, c24};
+
+  struct Block {
+    u32x4 w[CT][BS];
+    uint32_t s[(GS + 1) / 2], z;
+  };
+  // codes and scales of steps [t, t + BS); beyond the wave's last or the end of the reduction scales are 0
+  auto load_codes = [&](Block& f, int t) __attribute__((always_inline)) {
+    const int k0 = t * kI4Step, g0 = t * GS;
+    f.z = 0;
+    if (t + BS <= last && k0 + BS * kI4Step <= K) {
 #pragma unroll
-  for (int j = 0; j < CT; ++j) {
-    const int at = (wc * CT + j) * cols + c0;
-    const int wrow = gated ? min(at + (lr & 7), width - 1) + (lr >> 3) * width : min(at + lr, width - 1);
-    const int64_t n = static_cast<int64_t>(e) * p.N + wrow;
-    q[j] = p.codes + n * (K / 2) + 16 * lg;
-    s[j] = static_cast<const uint16_t*>(p.scales) + n * groups;
-    if constexpr (ZEROS) z[j] = p.zeros + n * groups;
-  }
-  float4v acc[RT][CT];
+      for (int j = 0; j < CT; ++j)
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int j = 0; j < CT; ++j) acc[i][j] = float4v{0, 0, 0, 0};
-  const int steps = (K + kI4Step - 1) / kI4Step;
-  const int per = (steps + WK - 1) / WK;
-  const int first = wk * per, last = min(first + per, steps);
-  const u32x4 fixed = {ZEROS ? I4::one : I4::minus24, ZEROS ? I4::one : I4::minus24, ZEROS ? I4::one : I4::minus24,
-                       ZEROS ? I4::one : I4::minus24};
-  for (int t0 = first; t0 < last; t0 += TURNS) {
-    u32x4 w[TURNS][CT];
-    uint16_t sc[TURNS][CT][GS];
-    uint8_t zp[TURNS][CT][GS];
-    u32x4 xv[TURNS][RT][4];
-#pragma unroll
-    for (int t = 0; t < TURNS; ++t) {
-      const int k0 = (t0 + t) * kI4Step;
-      const bool in = t0 + t < last;
-#pragma unroll
-      for (int j = 0; j < CT; ++j) {
-        w[t][j] = u32x4{0, 0, 0, 0};
-        if (in && k0 + 32 * lg < K) {
-          const u32x4* src = reinterpret_cast<const u32x4*>(q[j] + k0 / 2);
-          w[t][j] = RT == 1 ? __builtin_nontemporal_load(src) : *src;
+        for (int h = 0; h < BS; ++h) {
+          const u32x4* src = reinterpret_cast<const u32x4*>(qb + k0 / 2 + qo[j][h]);
+          f.w[j][h] = RT == 1 ? __builtin_nontemporal_load(src) : *src;
         }
-#pragma unroll
-        for (int g = 0; g < GS; ++g) {
-          const int gi = k0 / GROUP + g;
-          sc[t][j][g] = 0;
-          zp[t][j][g] = 0;
-          if (in && gi < groups) {
-            sc[t][j][g] = s[j][gi];
-            if constexpr (ZEROS) zp[t][j][g] = z[j][gi];
-          }
-        }
+      if constexpr (GS == 1) f.s[0] = *reinterpret_cast<const uint16_t*>(sb + 2 * g0 + 2 * so);
+      else __builtin_memcpy(f.s, sb + 2 * g0 + 2 * so, 2 * GS);
+      if constexpr (ZEROS) {
+        if constexpr (GS == 1) f.z = zb[g0 + so];
+        else __builtin_memcpy(&f.z, zb + g0 + so, GS);
       }
+    } else {
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
+      for (int j = 0; j < CT; ++j)
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const int k = k0 + (TR ? 32 * m + 8 * lg : 32 * lg + 8 * m);
-          xv[t][i][m] = u32x4{0, 0, 0, 0};
-          if (in && k < K && 16 * i + lr < rows) xv[t][i][m] = *reinterpret_cast<const u32x4*>(x[i] + 2 * k);
+        for (int h = 0; h < BS; ++h) {
+          const uint32_t chunk = (lane % LPR) ^ swizzle(h * RPL + lane / LPR);
+          const bool in = k0 + 32 * static_cast<int>(chunk) < K;
+          f.w[j][h] = *reinterpret_cast<const u32x4*>(qb + (in ? k0 / 2 + qo[j][h] : qo[j][h] - 16 * chunk));   // behind the end any code
         }
+#pragma unroll
+      for (int g = 0; g < GS; ++g) {
+        const bool in = t + pair / CT < last && g0 + pair / CT * GS + g < groups;
+        const uint32_t at = in ? g0 + g + so : so - pair / CT * GS;
+        const uint32_t v = *reinterpret_cast<const uint16_t*>(sb + 2 * at);
+        f.s[g / 2] = (g % 2 ? f.s[g / 2] : 0) | (in ? v << (16 * (g % 2)) : 0);
+        if constexpr (ZEROS) f.z |= static_cast<uint32_t>(zb[at]) << (8 * g);
+      }
     }
+  };
+  u32x4 xv[XLDS ? 1 : BS][RT][4];
+  auto load_x = [&](int t) __attribute__((always_inline)) {
+    if constexpr (!XLDS) {
+      const int k0 = t * kI4Step;
+      if (k0 + BS * kI4Step <= K) {
 #pragma unroll
-    for (int t = 0; t < TURNS; ++t) {
-      float4v off[RT][GS];
+        for (int b = 0; b < BS; ++b)
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
+          for (int i = 0; i < RT; ++i)
+            if (16 * i + lr < rows)
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          xv[t][i][m] = i4_pairs(xv[t][i][m]);
-          off[i][m / MS] = TT::mfma(xv[t][i][m], fixed, m % MS ? off[i][m / MS] : float4v{0, 0, 0, 0});
-        }
+              for (int m = 0; m < 4; ++m)
+                xv[b][i][m] = *reinterpret_cast<const u32x4*>(x[i] + 2 * (k0 + b * kI4Step) + (TR ? 64 : 16) * m);
+      } else {
 #pragma unroll
-      for (int j = 0; j < CT; ++j) {
-        const u32x4 c = TR ? i4_transpose(w[t][j]) : w[t][j];
-#pragma unroll
-        for (int g = 0; g < GS; ++g) {
-          float4v d[RT];
-#pragma unroll
-          for (int i = 0; i < RT; ++i) d[i] = ZEROS ? float4v{0, 0, 0, 0} : off[i][g];
-#pragma unroll
-          for (int m = 0; m < MS; ++m) {
-            const uint32_t v = c[g * MS + m];
-            const u32x4 b = {I4::template pair<0>(v), I4::template pair<1>(v), I4::template pair<2>(v), I4::template pair<3>(v)};
-#pragma unroll
-            for (int i = 0; i < RT; ++i) d[i] = TT::mfma(xv[t][i][g * MS + m], b, d[i]);
-          }
-          const float sg = I4::value(sc[t][j][g]);
-          const float zg = -16.0f - static_cast<float>(zp[t][j][g]);
+        for (int b = 0; b < BS; ++b)
 #pragma unroll
           for (int i = 0; i < RT; ++i)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              float v = d[i][u];
-              if constexpr (ZEROS) v = fmaf(zg, off[i][g][u], v);
-              acc[i][j][u] = fmaf(sg, v, acc[i][j][u]);
+            for (int m = 0; m < 4; ++m) {
+              const int k = k0 + b * kI4Step + (TR ? 32 * m + 8 * lg : 32 * lg + 8 * m);
+              xv[b][i][m] = u32x4{0, 0, 0, 0};
+              if (k < K && 16 * i + lr < rows)
+                xv[b][i][m] = *reinterpret_cast<const u32x4*>(x[i] + 2 * (k0 + b * kI4Step) + (TR ? 64 : 16) * m);
             }
-        }
       }
     }
-  }
+  };
+  float4v acc[RT][CT];
+  auto products = [&](const u32x4 (&xp)[RT][4], int b, const uint32_t (&sq)[(GS + 1) / 2][4], const uint32_t (&zq)[4])
+      __attribute__((always_inline)) {
+    float4v off[RT][GS];
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        off[i][m / MS] = TT::mfma(xp[i][m], fixed, m % MS ? off[i][m / MS] : float4v{0, 0, 0, 0});
+    u32x4 c[CT];
+#pragma unroll
+    for (int j = 0; j < CT; ++j) {
+      c[j] = get[64 * BS * j + ((4 * b + lg) ^ swizzle(lr))];
+      if constexpr (TR) c[j] = i4_transpose(c[j]);
+    }
+    // the tiles' products in turn: neighbouring ones do not wait for each other
+#pragma unroll
+    for (int g = 0; g < GS; ++g) {
+      float4v d[RT][CT];
+#pragma unroll
+      for (int m = 0; m < MS; ++m)
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+          const u32x4 v = i4_decode<I4>(c[j][g * MS + m], mask, base);
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+            d[i][j] = TT::mfma(xp[i][g * MS + m], v, m ? d[i][j] : ZEROS ? float4v{0, 0, 0, 0} : off[i][g]);
+        }
+#pragma unroll
+      for (int j = 0; j < CT; ++j) {
+        const float sg = I4::value(static_cast<uint16_t>(sq[g / 2][b * CT + j] >> (16 * (g % 2))));
+        const float zg = ZEROS ? -16.0f - static_cast<float>((zq[b * CT + j] >> (8 * g)) & 255u) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            float v = d[i][j][u];
+            if constexpr (ZEROS) v = fmaf(zg, off[i][g][u], v);
+            acc[i][j][u] = fmaf(sg, v, acc[i][j][u]);
+          }
+      }
+    }
+  };
+  auto unpack = [&](const Block& f, uint32_t (&sq)[(GS + 1) / 2][4], uint32_t (&zq)[4]) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < CT; ++j)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) red[wk][wc][16 * i + 4 * lg + u][16 * j + lr] = acc[i][j][u];
-  __syncthreads();
-
+      for (int h = 0; h < BS; ++h) put[64 * (BS * j + h)] = f.w[j][h];
+#pragma unroll
+    for (int h = 0; h < (GS + 1) / 2; ++h) i4_spread(f.s[h], sq[h]);
+    if constexpr (ZEROS) i4_spread(f.z, zq);
+  };
   // a thread: 8 neighbouring columns of a row, the waves' sums added in their order
-  const int pieces = gated ? CT : 2 * CT;
-  for (int o = threadIdx.x; o < WC * pieces * 16 * RT; o += 64 * WK * WC) {
-    const int piece = o % pieces, w = o / pieces % WC, r = o / (pieces * WC);
-    if (r >= rows) continue;
-    const int c = c0 + (w * pieces + piece) * 8;
-    if (c >= width) continue;
+  auto result = [&](int r, int w, int piece, int c0) __attribute__((always_inline)) {
+    const int c = c0 + piece * 8;
+    if (c >= width) return;
     const int at = gated ? 16 * piece : 8 * piece;
     float v[8];
 #pragma unroll
@@ -273,7 +434,7 @@ __global__ __launch_bounds__(64 * WK * WC) __attribute__((amdgpu_waves_per_eu(2)
 #pragma unroll
       for (int u = 0; u < 4; ++u) v[4 * h + u] = a[u];
     }
-    const int64_t to = (static_cast<int64_t>(row0) + m0 + r) * width + c;
+    const int64_t to = (static_cast<int64_t>(row0) + r) * width + c;
     const uint2 lo = TT::pack(float4v{v[0], v[1], v[2], v[3]}), hi = TT::pack(float4v{v[4], v[5], v[6], v[7]});
     if (width % 8 == 0) {
       if (out32) {
@@ -283,7 +444,7 @@ __global__ __launch_bounds__(64 * WK * WC) __attribute__((amdgpu_waves_per_eu(2)
       } else {
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + to) = make_uint4(lo.x, lo.y, hi.x, hi.y);
       }
-      continue;
+      return;
     }
     const uint32_t packed[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
@@ -292,16 +453,157 @@ __global__ __launch_bounds__(64 * WK * WC) __attribute__((amdgpu_waves_per_eu(2)
       if (out32) static_cast<float*>(p.out)[to + u] = v[u];
       else static_cast<uint16_t*>(p.out)[to + u] = static_cast<uint16_t>(packed[u / 2] >> (16 * (u % 2)));
     }
+  };
+  auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < CT; ++j) acc[i][j] = float4v{0, 0, 0, 0};
+  };
+  auto leave = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < CT; ++j)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) red[wk][wc][16 * i + 4 * lg + u][16 * j + lr] = acc[i][j][u];
+  };
+  const int pieces = gated ? CT : 2 * CT;                   // of 8 columns, of a wave's columns
+  clear();
+
+  if constexpr (XLDS) {
+    // x in LDS, permuted, row after row; a few blocks of codes are asked for before it.  Rows past what fits are
+    // taken in further rounds over the weights (only where the caller's hint was too low).
+    const int c0 = nt * (CT * cols);
+    columns(c0);
+    const int fit = p.xrows;
+    for (int r0 = 0; r0 < rows; r0 += fit) {
+      const int n = min(fit, rows - r0);
+      Block f[DEPTH];
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d)
+        if (first + d * BS < last) load_codes(f[d], first + d * BS);
+      for (int u = threadIdx.x; u < n * 16 * steps; u += 64 * WK) {
+        const int r = u / (16 * steps), k = u - r * 16 * steps;        // unit k of the row: values 8 k ..
+        u32x4 v = {0, 0, 0, 0};
+        if (8 * k < K) v = i4_pairs(*reinterpret_cast<const u32x4*>(source(r0 + r) + 16 * k));
+        xall[u] = v;
+      }
+      __syncthreads();
+      const u32x4* xr = &xall[(lr < n ? lr : 0) * 16 * steps + (TR ? lg : 4 * lg)];
+      for (int t0 = first; t0 < last; t0 += DEPTH * BS) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+          const int t = t0 + d * BS;
+          if (t < last) {
+            uint32_t sq[(GS + 1) / 2][4], zq[4];
+            unpack(f[d], sq, zq);
+            if (t + DEPTH * BS < last) load_codes(f[d], t + DEPTH * BS);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int b = 0; b < BS; ++b) {
+              u32x4 xp[RT][4];
+#pragma unroll
+              for (int m = 0; m < 4; ++m) xp[0][m] = xr[16 * min(t + b, steps - 1) + (TR ? 4 : 1) * m];
+              products(xp, b, sq, zq);
+            }
+          }
+        }
+      }
+      leave();
+      __syncthreads();
+      for (int o = threadIdx.x; o < pieces * n; o += 64 * WK) {
+        const int r = o / pieces;
+        // the round's rows lie at 0 .. n of the sums
+        row0 += r0;
+        result(r, 0, o % pieces, c0);
+        row0 -= r0;
+      }
+      if (r0 + fit < rows) {
+        __syncthreads();
+        clear();
+      }
+    }
+    return;
+  }
+
+  // column groups of the wave: one, or (short reductions) `rounds` of them
+  const int tiles = (width + WC * CT * cols - 1) / (WC * CT * cols);
+  const int it0 = LOOP ? nt * p.rounds : nt, it1 = LOOP ? min(it0 + p.rounds, tiles) : nt + 1;
+  const bool one = LOOP && last - first <= BS;              // x of the whole reduction stays
+  Block f;
+#pragma unroll
+  for (int b = 0; b < BS; ++b)
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) xv[b][i][m] = u32x4{0, 0, 0, 0};
+  columns((it0 * WC + wc) * CT * cols);
+  if (first < last) {
+    load_codes(f, first);
+    load_x(first);
+  }
+  u32x4 xp[BS][RT][4];
+  for (int it = it0; it < it1; ++it) {
+    const int c0 = (it * WC + wc) * CT * cols;
+    for (int t = first; t < last; t += BS) {
+      // the block leaves the registers that the next one's loads come into
+      uint32_t sq[(GS + 1) / 2][4], zq[4];
+      unpack(f, sq, zq);
+      if (!one || it == it0) {
+#pragma unroll
+        for (int b = 0; b < BS; ++b)
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) xp[b][i][m] = i4_pairs(xv[b][i][m]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (t + BS < last) {
+        load_codes(f, t + BS);
+        load_x(t + BS);
+      } else if (LOOP && it + 1 < it1) {
+        columns(((it + 1) * WC + wc) * CT * cols);
+        load_codes(f, first);
+        if (!one) load_x(first);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int b = 0; b < BS; ++b) products(xp[b], b, sq, zq);
+    }
+    leave();
+    if constexpr (LOOP) {
+      // the sums are the wave's own
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      for (int o = lane; o < pieces * rows; o += 64) result(o / pieces, wc, o % pieces, c0);
+      clear();
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    } else {
+      __syncthreads();
+      for (int o = threadIdx.x; o < WC * pieces * rows; o += 64 * WK * WC) {
+        const int w = o / pieces % WC;
+        result(o / (pieces * WC), w, o % pieces, (it * WC + w) * CT * cols);
+      }
+    }
   }
 }
 
-template <bool F16, int GROUP, bool ZEROS, int RT, int CT, int WK, int WC>
+template <bool F16, int GROUP, bool ZEROS, int SHAPE>
 static hipError_t i4_start(Int4Params p, int gated, int out32, hipStream_t stream) {
-  constexpr Int4Shape shape = {RT, CT, WK, WC};
-  p.n_tiles = i4_tiles(shape, p.N, gated);
+  constexpr Int4Shape shape = kI4Shapes[SHAPE];
+  p.rounds = i4_rounds(shape, p.E, p.N, p.m_total, gated);
+  p.n_tiles = (i4_tiles(shape, p.N, gated) + p.rounds - 1) / p.rounds;
   const int64_t blocks = i4_blocks(shape, p.E, p.N, p.m_total, gated);
   if (blocks == 0) return hipSuccess;
-  hipLaunchKernelGGL((k_int4_gemv<F16, GROUP, ZEROS, RT, CT, WK, WC>), dim3(static_cast<unsigned>(blocks)), dim3(64 * WK * WC), 0,
+  size_t lds = 0;
+  if (shape.xlds) {                          // rows of x that a workgroup holds
+    p.xrows = static_cast<int>(i4_rows(p.E, p.m_total, p.rows_hint));
+    lds = static_cast<size_t>(i4_xbytes(p.xrows, p.K));
+  }
+  hipLaunchKernelGGL((k_int4_gemv<F16, GROUP, ZEROS, SHAPE>), dim3(static_cast<unsigned>(blocks)), dim3(64 * shape.wk * shape.wc), lds,
                      stream, p, gated, out32);
   return hipGetLastError();
 }
@@ -309,9 +611,11 @@ static hipError_t i4_start(Int4Params p, int gated, int out32, hipStream_t strea
 template <bool F16, int GROUP, bool ZEROS>
 static hipError_t i4_launch(const Int4Params& p, int gated, int out32, hipStream_t stream) {
   switch (i4_choice(p.E, p.N, p.K, p.m_total, p.rows_hint, gated)) {
-    case 0: return i4_start<F16, GROUP, ZEROS, I4_SHAPE(0)>(p, gated, out32, stream);
-    case 1: return i4_start<F16, GROUP, ZEROS, I4_SHAPE(1)>(p, gated, out32, stream);
-    default: return i4_start<F16, GROUP, ZEROS, I4_SHAPE(2)>(p, gated, out32, stream);
+    case 0: return i4_start<F16, GROUP, ZEROS, 0>(p, gated, out32, stream);
+    case 1: return i4_start<F16, GROUP, ZEROS, 1>(p, gated, out32, stream);
+    case 2: return i4_start<F16, GROUP, ZEROS, 2>(p, gated, out32, stream);
+    case 3: return i4_start<F16, GROUP, ZEROS, 3>(p, gated, out32, stream);
+    default: return i4_start<F16, GROUP, ZEROS, 4>(p, gated, out32, stream);
   }
 }
 
