@@ -85,7 +85,7 @@ constexpr int kI4Step = 128;               // codes of a weight row per wave and
 struct Int4Shape {
   int rt, ct, wk, wc, bs, xlds;
 };
-constexpr Int4Shape kI4Shapes[] = {{1, 1, 8, 1, 2, 1}, {1, 2, 8, 1, 2, 0}, {1, 2, 4, 1, 2, 0}, {1, 2, 1, 4, 2, 0}, {4, 2, 4, 1, 1, 0}};
+constexpr Int4Shape kI4Shapes[] = {{1, 1, 8, 1, 2, 1}, {1, 2, 8, 1, 2, 0}, {1, 4, 4, 1, 2, 0}, {1, 2, 1, 4, 2, 0}, {4, 2, 4, 1, 1, 0}};
 constexpr int kI4XBytes = 64 * 1024;       // of LDS for x, at most
 
 static inline int64_t i4_xbytes(int64_t rows, int K) { return rows * ((K + kI4Step - 1) / kI4Step) * (2 * kI4Step); }
@@ -206,7 +206,7 @@ __device__ __forceinline__ void i4_spread(uint32_t v, uint32_t (&out)[4]) {
 }
 
 template <bool F16, int GROUP, bool ZEROS, int SHAPE>
-__global__ __launch_bounds__(64 * kI4Shapes[SHAPE].wk * kI4Shapes[SHAPE].wc) __attribute__((amdgpu_waves_per_eu(kI4Shapes[SHAPE].rt == 1 && !kI4Shapes[SHAPE].xlds ? 3 : 2)))
+__global__ __launch_bounds__(64 * kI4Shapes[SHAPE].wk * kI4Shapes[SHAPE].wc) __attribute__((amdgpu_waves_per_eu(kI4Shapes[SHAPE].rt * kI4Shapes[SHAPE].ct <= 2 && !kI4Shapes[SHAPE].xlds ? 3 : 2)))
 void k_int4_gemv(const Int4Params p, int gated, int out32) {
   using I4 = I4Type<F16>;
   using TT = typename I4::TT;
@@ -217,10 +217,13 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
   constexpr bool TR = GROUP < kI4Step;
   constexpr int GS = kI4Step / GROUP;                       // groups of a step
   constexpr int MS = 4 / GS;                                // matrix instructions of a group
-  constexpr int PAIRS = CT * BS;                            // (step, tile) pairs of a block
+  // A lane group holds scales of one tile and step, or of one tile and all steps of a
+  // block; they are spread over the groups in registers.
+  constexpr bool ALL = CT == 4;
+  constexpr int PAIRS = ALL ? 4 : CT * BS, SN = ALL ? BS * GS : GS, SW = (SN + 1) / 2, ZW = (SN + 3) / 4;
   constexpr int LPR = 4 * BS, RPL = 64 / LPR;               // lanes of a row's load, rows of a load
   constexpr int LD = 16 * CT + 4;                           // floats of a row of partial sums
-  static_assert(PAIRS <= 4, "a lane group holds the scales of one pair");
+  static_assert(PAIRS <= 4, "four lane groups");
   static_assert(!XLDS || RT == 1, "one chunk of rows in LDS");
   __shared__ float red[WK][WC][16 * RT][LD];
   __shared__ u32x4 stage[WK * WC][CT][64 * BS];
@@ -248,8 +251,7 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
   const u32x4* const get = &stage[wave][0][LPR * lr];
   // Weights: the wave's first row as a base, 32-bit offsets of the lane's from there
   // (gated: the caller keeps the up half's below 2^32; scales have a quarter of the
-  // codes' bytes at most).  Scales: lane group g those of pair g (step g / CT, tile
-  // g % CT), spread over the groups in registers.
+  // codes' bytes at most).
   const int pair = lg & (PAIRS - 1);
   const uint8_t *qb, *sb, *zb;
   uint32_t qo[CT][BS], so;
@@ -294,12 +296,13 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
 
   struct Block {
     u32x4 w[CT][BS];
-    uint32_t s[(GS + 1) / 2], z;
+    uint32_t s[SW], z[ZW];
   };
   // codes and scales of steps [t, t + BS); beyond the wave's last or the end of the reduction scales are 0
   auto load_codes = [&](Block& f, int t) __attribute__((always_inline)) {
     const int k0 = t * kI4Step, g0 = t * GS;
-    f.z = 0;
+#pragma unroll
+    for (int i = 0; i < ZW; ++i) f.z[i] = 0;
     if (t + BS <= last && k0 + BS * kI4Step <= K) {
 #pragma unroll
       for (int j = 0; j < CT; ++j)
@@ -308,11 +311,11 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
           const u32x4* src = reinterpret_cast<const u32x4*>(qb + k0 / 2 + qo[j][h]);
           f.w[j][h] = RT == 1 ? __builtin_nontemporal_load(src) : *src;
         }
-      if constexpr (GS == 1) f.s[0] = *reinterpret_cast<const uint16_t*>(sb + 2 * g0 + 2 * so);
-      else __builtin_memcpy(f.s, sb + 2 * g0 + 2 * so, 2 * GS);
+      if constexpr (SN == 1) f.s[0] = *reinterpret_cast<const uint16_t*>(sb + 2 * g0 + 2 * so);
+      else __builtin_memcpy(f.s, sb + 2 * g0 + 2 * so, 2 * SN);
       if constexpr (ZEROS) {
-        if constexpr (GS == 1) f.z = zb[g0 + so];
-        else __builtin_memcpy(&f.z, zb + g0 + so, GS);
+        if constexpr (SN == 1) f.z[0] = zb[g0 + so];
+        else __builtin_memcpy(f.z, zb + g0 + so, SN);
       }
     } else {
 #pragma unroll
@@ -323,13 +326,14 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
           const bool in = k0 + 32 * static_cast<int>(chunk) < K;
           f.w[j][h] = *reinterpret_cast<const u32x4*>(qb + (in ? k0 / 2 + qo[j][h] : qo[j][h] - 16 * chunk));   // behind the end any code
         }
+      const int s0 = pair / CT * GS;                        // the lane's first group of the block
 #pragma unroll
-      for (int g = 0; g < GS; ++g) {
-        const bool in = t + pair / CT < last && g0 + pair / CT * GS + g < groups;
-        const uint32_t at = in ? g0 + g + so : so - pair / CT * GS;
+      for (int g = 0; g < SN; ++g) {
+        const bool in = t + (s0 + g) / GS < last && g0 + s0 + g < groups;
+        const uint32_t at = in ? g0 + g + so : so - s0;
         const uint32_t v = *reinterpret_cast<const uint16_t*>(sb + 2 * at);
         f.s[g / 2] = (g % 2 ? f.s[g / 2] : 0) | (in ? v << (16 * (g % 2)) : 0);
-        if constexpr (ZEROS) f.z |= static_cast<uint32_t>(zb[at]) << (8 * g);
+        if constexpr (ZEROS) f.z[g / 4] |= static_cast<uint32_t>(zb[at]) << (8 * (g % 4));
       }
     }
   };
@@ -362,7 +366,7 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
     }
   };
   float4v acc[RT][CT];
-  auto products = [&](const u32x4 (&xp)[RT][4], int b, const uint32_t (&sq)[(GS + 1) / 2][4], const uint32_t (&zq)[4])
+  auto products = [&](const u32x4 (&xp)[RT][4], int b, const uint32_t (&sq)[SW][4], const uint32_t (&zq)[ZW][4])
       __attribute__((always_inline)) {
     float4v off[RT][GS];
 #pragma unroll
@@ -391,8 +395,9 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
         }
 #pragma unroll
       for (int j = 0; j < CT; ++j) {
-        const float sg = I4::value(static_cast<uint16_t>(sq[g / 2][b * CT + j] >> (16 * (g % 2))));
-        const float zg = ZEROS ? -16.0f - static_cast<float>((zq[b * CT + j] >> (8 * g)) & 255u) : 0.0f;
+        const int n = ALL ? b * GS + g : g, from = ALL ? j : b * CT + j;
+        const float sg = I4::value(static_cast<uint16_t>(sq[n / 2][from] >> (16 * (n % 2))));
+        const float zg = ZEROS ? -16.0f - static_cast<float>((zq[n / 4][from] >> (8 * (n % 4))) & 255u) : 0.0f;
 #pragma unroll
         for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -404,14 +409,16 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
       }
     }
   };
-  auto unpack = [&](const Block& f, uint32_t (&sq)[(GS + 1) / 2][4], uint32_t (&zq)[4]) __attribute__((always_inline)) {
+  auto unpack = [&](const Block& f, uint32_t (&sq)[SW][4], uint32_t (&zq)[ZW][4]) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < CT; ++j)
 #pragma unroll
       for (int h = 0; h < BS; ++h) put[64 * (BS * j + h)] = f.w[j][h];
 #pragma unroll
-    for (int h = 0; h < (GS + 1) / 2; ++h) i4_spread(f.s[h], sq[h]);
-    if constexpr (ZEROS) i4_spread(f.z, zq);
+    for (int h = 0; h < SW; ++h) i4_spread(f.s[h], sq[h]);
+    if constexpr (ZEROS)
+#pragma unroll
+      for (int h = 0; h < ZW; ++h) i4_spread(f.z[h], zq[h]);
   };
   // a thread: 8 neighbouring columns of a row, the waves' sums added in their order
   auto result = [&](int r, int w, int piece, int c0) __attribute__((always_inline)) {
@@ -496,7 +503,7 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
         for (int d = 0; d < DEPTH; ++d) {
           const int t = t0 + d * BS;
           if (t < last) {
-            uint32_t sq[(GS + 1) / 2][4], zq[4];
+            uint32_t sq[SW][4], zq[ZW][4];
             unpack(f[d], sq, zq);
             if (t + DEPTH * BS < last) load_codes(f[d], t + DEPTH * BS);
             __builtin_amdgcn_sched_barrier(0);
@@ -548,7 +555,7 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
     const int c0 = (it * WC + wc) * CT * cols;
     for (int t = first; t < last; t += BS) {
       // the block leaves the registers that the next one's loads come into
-      uint32_t sq[(GS + 1) / 2][4], zq[4];
+      uint32_t sq[SW][4], zq[ZW][4];
       unpack(f, sq, zq);
       if (!one || it == it0) {
 #pragma unroll
