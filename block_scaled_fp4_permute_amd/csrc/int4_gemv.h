@@ -81,39 +81,39 @@ constexpr int kI4Step = 128;               // codes of a weight row per wave and
 
 // Shapes of a workgroup: RT x 16 rows of an expert times WC x CT tiles of 16 weight
 // rows (gated: 8 of gate and the 8 of up for the same columns), WK waves sharing
-// the reduction, in blocks of `bs` steps.  xlds: all of the rows' x in LDS.
+// the reduction, in blocks of `bs` steps, `ahead` blocks of codes on their way.
 struct Int4Shape {
-  int rt, ct, wk, wc, bs, xlds;
+  int rt, ct, wk, wc, bs, ahead;
 };
-constexpr Int4Shape kI4Shapes[] = {{1, 1, 8, 1, 2, 1}, {1, 2, 8, 1, 2, 0}, {1, 4, 4, 1, 2, 0}, {1, 2, 1, 4, 2, 0}, {4, 2, 4, 1, 1, 0}};
-constexpr int kI4XBytes = 64 * 1024;       // of LDS for x, at most
+constexpr Int4Shape kI4Shapes[] = {{1, 2, 8, 1, 2, 3}, {1, 4, 4, 1, 2, 1}, {1, 4, 1, 4, 2, 1}, {4, 2, 4, 1, 1, 1}, {1, 1, 8, 1, 2, 3}};
 
-static inline int64_t i4_xbytes(int64_t rows, int K) { return rows * ((K + kI4Step - 1) / kI4Step) * (2 * kI4Step); }
 static inline int i4_tiles(const Int4Shape& s, int N, int gated) {
   const int width = gated ? N / 2 : N, per = (gated ? 8 : 16) * s.ct * s.wc;
   return (width + per - 1) / per;
 }
-static inline int64_t i4_rows(int E, int64_t m_total, int64_t hint) {
-  const int64_t experts = E < m_total ? E : m_total;
-  const int64_t share = experts ? (m_total + experts - 1) / experts : 0;
-  return hint > share ? hint : share;
-}
-// which of them, by rows of one expert (the hint, or what m_total gives each expert
-// that can have any), the length of the reduction, and tasks
+// Which of them, by rows of one expert (the hint, or what m_total gives each expert
+// that can have any), the length of the reduction, and tasks:
+//   3  more than 16 rows
+//   2  reductions of up to 512: a wave's own, over several column groups
+//   1  four tiles a wave from a workgroup a CU on (64 tokens, 6144 -> 2 x 256: 80 us
+//      against 120 in shape 0; 8 tokens 27 against 37)
+//   0  else, twice the waves for the same columns (2 tokens: 17 us against 19; dense
+//      8192 x 8192, 3 rows: 20 against 27)
+//   4  and one tile a wave where even those leave CUs without a workgroup
 static inline int i4_choice(int E, int N, int K, int64_t m_total, int64_t hint, int gated) {
   const int64_t experts = E < m_total ? E : m_total;
-  const int64_t rows = i4_rows(E, m_total, hint);
-  if (rows > 16) return 4;
-  if (K <= 512) return 3;
-  const int64_t tasks = experts * i4_tiles(kI4Shapes[1], N, gated);
-  if (tasks >= 1024) return 2;
-  return i4_xbytes(rows, K) <= kI4XBytes && tasks <= 512 ? 0 : 1;
+  const int64_t share = experts ? (m_total + experts - 1) / experts : 0;
+  if ((hint > share ? hint : share) > 16) return 3;
+  if (K <= 512) return 2;
+  if (experts * i4_tiles(kI4Shapes[1], N, gated) >= 256) return 1;
+  return experts * i4_tiles(kI4Shapes[0], N, gated) >= 256 ? 0 : 4;
 }
-// iterations of a wave over column groups (the short reductions): about 16 waves a CU
+// Column groups of a wave, one after the other (short reductions): some 2048
+// workgroups (256 experts, 8 rows, 256 -> 6144: 63 us; 70 with 1024 of them, 80 with 8192)
 static inline int i4_rounds(const Int4Shape& s, int E, int N, int64_t m_total, int gated) {
   if (s.wk > 1) return 1;
   const int64_t chunks = m_total / (16 * s.rt) + (E < m_total ? E : m_total);
-  const int64_t n = chunks * i4_tiles(s, N, gated) / 1024;
+  const int64_t n = chunks * i4_tiles(s, N, gated) / 2048;
   return n < 1 ? 1 : n > 16 ? 16 : static_cast<int>(n);
 }
 // workgroups: at least one for each task (i4_find)
@@ -206,14 +206,14 @@ __device__ __forceinline__ void i4_spread(uint32_t v, uint32_t (&out)[4]) {
 }
 
 template <bool F16, int GROUP, bool ZEROS, int SHAPE>
-__global__ __launch_bounds__(64 * kI4Shapes[SHAPE].wk * kI4Shapes[SHAPE].wc) __attribute__((amdgpu_waves_per_eu(kI4Shapes[SHAPE].rt * kI4Shapes[SHAPE].ct <= 2 && !kI4Shapes[SHAPE].xlds ? 3 : 2)))
+__global__ __launch_bounds__(64 * kI4Shapes[SHAPE].wk * kI4Shapes[SHAPE].wc) __attribute__((amdgpu_waves_per_eu(2)))
 void k_int4_gemv(const Int4Params p, int gated, int out32) {
   using I4 = I4Type<F16>;
   using TT = typename I4::TT;
   constexpr int RT = kI4Shapes[SHAPE].rt, CT = kI4Shapes[SHAPE].ct, WK = kI4Shapes[SHAPE].wk, WC = kI4Shapes[SHAPE].wc;
   constexpr int BS = kI4Shapes[SHAPE].bs;
-  constexpr bool XLDS = kI4Shapes[SHAPE].xlds, LOOP = WK == 1;
-  constexpr int DEPTH = XLDS ? 3 : 1;                       // blocks of codes on their way
+  constexpr int AHEAD = kI4Shapes[SHAPE].ahead;
+  constexpr bool LOOP = WK == 1;
   constexpr bool TR = GROUP < kI4Step;
   constexpr int GS = kI4Step / GROUP;                       // groups of a step
   constexpr int MS = 4 / GS;                                // matrix instructions of a group
@@ -224,11 +224,10 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
   constexpr int LPR = 4 * BS, RPL = 64 / LPR;               // lanes of a row's load, rows of a load
   constexpr int LD = 16 * CT + 4;                           // floats of a row of partial sums
   static_assert(PAIRS <= 4, "four lane groups");
-  static_assert(!XLDS || RT == 1, "one chunk of rows in LDS");
+  static_assert(!LOOP || AHEAD == 1, "a block of the next columns");
   __shared__ float red[WK][WC][16 * RT][LD];
   __shared__ u32x4 stage[WK * WC][CT][64 * BS];
-  extern __shared__ u32x4 xall[];
-  static_assert(fits_lds(sizeof(red) + sizeof(stage) + (XLDS ? kI4XBytes : 0), 1), "partial sums and stages exceed the LDS of a CU");
+  static_assert(fits_lds(sizeof(red) + sizeof(stage), 1), "partial sums and stages exceed the LDS of a CU");
   int e, row0, rows, nt;
   if (!i4_find<16 * RT>(p, e, row0, rows, nt)) return;
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
@@ -274,20 +273,6 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
     so = row_of(pair % CT, lr) * static_cast<uint32_t>(groups) + (pair / CT) * GS;
   };
 
-  // rows of x; places past the chunk's hold zeros or the first row again: nothing of theirs is written
-  auto source = [&](int place) __attribute__((always_inline)) {
-    int r = row0 + (place < rows ? place : 0);
-    if (p.a_rows) {
-      r = p.a_rows[r];
-      r = (r >= 0 && r < p.src_rows) ? r : 0;
-    }
-    return static_cast<const uint8_t*>(p.a) + static_cast<int64_t>(r) * K * 2;
-  };
-  const uint8_t* x[RT];
-  if constexpr (!XLDS) {
-#pragma unroll
-    for (int i = 0; i < RT; ++i) x[i] = source(16 * i + lr) + (TR ? 16 : 64) * lg;
-  }
   uint32_t mask = I4::mask, base = I4::base;
   asm("" : "+v"(mask));
   asm("" : "+s"(base));
@@ -337,32 +322,31 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
       }
     }
   };
-  u32x4 xv[XLDS ? 1 : BS][RT][4];
+  const uint8_t* x[RT];
+  u32x4 xv[BS][RT][4];
   auto load_x = [&](int t) __attribute__((always_inline)) {
-    if constexpr (!XLDS) {
-      const int k0 = t * kI4Step;
-      if (k0 + BS * kI4Step <= K) {
+    const int k0 = t * kI4Step;
+    if (k0 + BS * kI4Step <= K) {
 #pragma unroll
-        for (int b = 0; b < BS; ++b)
+      for (int b = 0; b < BS; ++b)
 #pragma unroll
-          for (int i = 0; i < RT; ++i)
-            if (16 * i + lr < rows)
+        for (int i = 0; i < RT; ++i)
+          if (16 * i + lr < rows)
 #pragma unroll
-              for (int m = 0; m < 4; ++m)
-                xv[b][i][m] = *reinterpret_cast<const u32x4*>(x[i] + 2 * (k0 + b * kI4Step) + (TR ? 64 : 16) * m);
-      } else {
+            for (int m = 0; m < 4; ++m)
+              xv[b][i][m] = *reinterpret_cast<const u32x4*>(x[i] + 2 * (k0 + b * kI4Step) + (TR ? 64 : 16) * m);
+    } else {
 #pragma unroll
-        for (int b = 0; b < BS; ++b)
+      for (int b = 0; b < BS; ++b)
 #pragma unroll
-          for (int i = 0; i < RT; ++i)
+        for (int i = 0; i < RT; ++i)
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const int k = k0 + b * kI4Step + (TR ? 32 * m + 8 * lg : 32 * lg + 8 * m);
-              xv[b][i][m] = u32x4{0, 0, 0, 0};
-              if (k < K && 16 * i + lr < rows)
-                xv[b][i][m] = *reinterpret_cast<const u32x4*>(x[i] + 2 * (k0 + b * kI4Step) + (TR ? 64 : 16) * m);
-            }
-      }
+          for (int m = 0; m < 4; ++m) {
+            const int k = k0 + b * kI4Step + (TR ? 32 * m + 8 * lg : 32 * lg + 8 * m);
+            xv[b][i][m] = u32x4{0, 0, 0, 0};
+            if (k < K && 16 * i + lr < rows)
+              xv[b][i][m] = *reinterpret_cast<const u32x4*>(x[i] + 2 * (k0 + b * kI4Step) + (TR ? 64 : 16) * m);
+          }
     }
   };
   float4v acc[RT][CT];
@@ -478,67 +462,11 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
   const int pieces = gated ? CT : 2 * CT;                   // of 8 columns, of a wave's columns
   clear();
 
-  if constexpr (XLDS) {
-    // x in LDS, permuted, row after row; a few blocks of codes are asked for before it.  Rows past what fits are
-    // taken in further rounds over the weights (only where the caller's hint was too low).
-    const int c0 = nt * (CT * cols);
-    columns(c0);
-    const int fit = p.xrows;
-    for (int r0 = 0; r0 < rows; r0 += fit) {
-      const int n = min(fit, rows - r0);
-      Block f[DEPTH];
-#pragma unroll
-      for (int d = 0; d < DEPTH; ++d)
-        if (first + d * BS < last) load_codes(f[d], first + d * BS);
-      for (int u = threadIdx.x; u < n * 16 * steps; u += 64 * WK) {
-        const int r = u / (16 * steps), k = u - r * 16 * steps;        // unit k of the row: values 8 k ..
-        u32x4 v = {0, 0, 0, 0};
-        if (8 * k < K) v = i4_pairs(*reinterpret_cast<const u32x4*>(source(r0 + r) + 16 * k));
-        xall[u] = v;
-      }
-      __syncthreads();
-      const u32x4* xr = &xall[(lr < n ? lr : 0) * 16 * steps + (TR ? lg : 4 * lg)];
-      for (int t0 = first; t0 < last; t0 += DEPTH * BS) {
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-          const int t = t0 + d * BS;
-          if (t < last) {
-            uint32_t sq[SW][4], zq[ZW][4];
-            unpack(f[d], sq, zq);
-            if (t + DEPTH * BS < last) load_codes(f[d], t + DEPTH * BS);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int b = 0; b < BS; ++b) {
-              u32x4 xp[RT][4];
-#pragma unroll
-              for (int m = 0; m < 4; ++m) xp[0][m] = xr[16 * min(t + b, steps - 1) + (TR ? 4 : 1) * m];
-              products(xp, b, sq, zq);
-            }
-          }
-        }
-      }
-      leave();
-      __syncthreads();
-      for (int o = threadIdx.x; o < pieces * n; o += 64 * WK) {
-        const int r = o / pieces;
-        // the round's rows lie at 0 .. n of the sums
-        row0 += r0;
-        result(r, 0, o % pieces, c0);
-        row0 -= r0;
-      }
-      if (r0 + fit < rows) {
-        __syncthreads();
-        clear();
-      }
-    }
-    return;
-  }
-
   // column groups of the wave: one, or (short reductions) `rounds` of them
   const int tiles = (width + WC * CT * cols - 1) / (WC * CT * cols);
   const int it0 = LOOP ? nt * p.rounds : nt, it1 = LOOP ? min(it0 + p.rounds, tiles) : nt + 1;
   const bool one = LOOP && last - first <= BS;              // x of the whole reduction stays
-  Block f;
+  Block f[AHEAD];
 #pragma unroll
   for (int b = 0; b < BS; ++b)
 #pragma unroll
@@ -546,37 +474,54 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
 #pragma unroll
       for (int m = 0; m < 4; ++m) xv[b][i][m] = u32x4{0, 0, 0, 0};
   columns((it0 * WC + wc) * CT * cols);
-  if (first < last) {
-    load_codes(f, first);
-    load_x(first);
+  if (first < last) load_codes(f[0], first);
+  __builtin_amdgcn_sched_barrier(0);         // the codes first: x may hang on the rows' indices
+  // places past the chunk's rows hold zeros or the first row again: nothing of theirs is written
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    int r = row0 + (16 * i + lr < rows ? 16 * i + lr : 0);
+    if (p.a_rows) {
+      r = p.a_rows[r];
+      r = (r >= 0 && r < p.src_rows) ? r : 0;
+    }
+    x[i] = static_cast<const uint8_t*>(p.a) + static_cast<int64_t>(r) * K * 2 + (TR ? 16 : 64) * lg;
   }
+  if (first < last) load_x(first);
+#pragma unroll
+  for (int d = 1; d < AHEAD; ++d)
+    if (first + d * BS < last) load_codes(f[d], first + d * BS);
   u32x4 xp[BS][RT][4];
   for (int it = it0; it < it1; ++it) {
     const int c0 = (it * WC + wc) * CT * cols;
-    for (int t = first; t < last; t += BS) {
-      // the block leaves the registers that the next one's loads come into
-      uint32_t sq[SW][4], zq[ZW][4];
-      unpack(f, sq, zq);
-      if (!one || it == it0) {
+    for (int t0 = first; t0 < last; t0 += AHEAD * BS) {
 #pragma unroll
-        for (int b = 0; b < BS; ++b)
+      for (int d = 0; d < AHEAD; ++d) {
+        const int t = t0 + d * BS;
+        if (t >= last) break;
+        // the block leaves the registers that the next one's loads come into
+        uint32_t sq[SW][4], zq[ZW][4];
+        unpack(f[d], sq, zq);
+        if (!one || it == it0) {
 #pragma unroll
-          for (int i = 0; i < RT; ++i)
+          for (int b = 0; b < BS; ++b)
 #pragma unroll
-            for (int m = 0; m < 4; ++m) xp[b][i][m] = i4_pairs(xv[b][i][m]);
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+              for (int m = 0; m < 4; ++m) xp[b][i][m] = i4_pairs(xv[b][i][m]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (t + BS < last) load_x(t + BS);
+        if (t + AHEAD * BS < last) {
+          load_codes(f[d], t + AHEAD * BS);
+        } else if (LOOP && it + 1 < it1) {
+          columns(((it + 1) * WC + wc) * CT * cols);
+          load_codes(f[d], first);
+          if (!one) load_x(first);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int b = 0; b < BS; ++b) products(xp[b], b, sq, zq);
       }
-      __builtin_amdgcn_sched_barrier(0);
-      if (t + BS < last) {
-        load_codes(f, t + BS);
-        load_x(t + BS);
-      } else if (LOOP && it + 1 < it1) {
-        columns(((it + 1) * WC + wc) * CT * cols);
-        load_codes(f, first);
-        if (!one) load_x(first);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int b = 0; b < BS; ++b) products(xp[b], b, sq, zq);
     }
     leave();
     if constexpr (LOOP) {
@@ -605,12 +550,7 @@ static hipError_t i4_start(Int4Params p, int gated, int out32, hipStream_t strea
   p.n_tiles = (i4_tiles(shape, p.N, gated) + p.rounds - 1) / p.rounds;
   const int64_t blocks = i4_blocks(shape, p.E, p.N, p.m_total, gated);
   if (blocks == 0) return hipSuccess;
-  size_t lds = 0;
-  if (shape.xlds) {                          // rows of x that a workgroup holds
-    p.xrows = static_cast<int>(i4_rows(p.E, p.m_total, p.rows_hint));
-    lds = static_cast<size_t>(i4_xbytes(p.xrows, p.K));
-  }
-  hipLaunchKernelGGL((k_int4_gemv<F16, GROUP, ZEROS, SHAPE>), dim3(static_cast<unsigned>(blocks)), dim3(64 * shape.wk * shape.wc), lds,
+  hipLaunchKernelGGL((k_int4_gemv<F16, GROUP, ZEROS, SHAPE>), dim3(static_cast<unsigned>(blocks)), dim3(64 * shape.wk * shape.wc), 0,
                      stream, p, gated, out32);
   return hipGetLastError();
 }

@@ -195,7 +195,7 @@ struct Int4Params {
   int src_rows;
   int act;
   int rows_hint;
-  int n_tiles, rounds, xrows;   // set by the launcher
+  int n_tiles, rounds;     // set by the launcher
   void* out;
 };
 int64_t int4_gemv_threads(int E, int N, int K, int64_t m_total, int64_t hint, int gated);   // of the launch
