@@ -143,8 +143,8 @@ struct ScoredParams {
   float* topk_w;
   float* scores;           // [T, E] or nullptr
   // set by the launcher
-  int need_all;            // every expert's score is needed
-  int vec;                 // rows can be read 4 values at a time
+  int narrow;              // 16-bit logits
+  int vec, vec_bias, vec_scores;   // rows can be read or written 4 values at a time
   int lanes_per_group;     // a power of two, or 0: groups by way of LDS
   int lds_token;           // doubles of LDS a token
 };
@@ -159,7 +159,7 @@ struct ScoredGradParams {
   const float* d_scores;   // or nullptr
   int64_t d_scores_ld;     // E, or 0: one row for all tokens
   void* dlogits;
-  int vec;                 // set by the launcher
+  int vec, vec_d, vec_out; // set by the launcher, as above
 };
 hipError_t launch_route_scored(const ScoredParams& p, int dtype, int* counts, int* offsets, int* perm_src_token,
                                int* perm_of_assignment, float* perm_weight, void* ws, hipStream_t stream);
