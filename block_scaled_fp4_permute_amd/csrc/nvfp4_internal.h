@@ -146,7 +146,7 @@ struct ScoredParams {
   int narrow;              // 16-bit logits
   int vec, vec_bias, vec_scores;   // rows can be read or written 4 values at a time
   int lanes_per_group;     // a power of two, or 0: groups by way of LDS
-  int lds_token;           // doubles of LDS a token
+  int lds_wave;            // doubles of LDS a wave
 };
 struct ScoredGradParams {
   const void* logits;

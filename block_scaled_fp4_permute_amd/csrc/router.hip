@@ -13,7 +13,10 @@
 // float32 step are ordered as the definition orders them, and results do not
 // depend on how a float32 exponential rounds.  The kernels choose by float32 keys
 // first, and take float64 ones for every expert only where two values that matter
-// lie within the float32 keys' error of each other.  An expert is closed if its logit is
+// lie within the float32 keys' error of each other.  A launch finds its code in no
+// instruction cache, and a wave that runs through 12 KB of it once waits some 10 us
+// for its lines: what is rare, or long in float64, is a loop over few instructions.
+// An expert is closed if its logit is
 // -inf or NaN, or its key -inf or NaN; closed ones are taken, by id and with
 // weight 0, only where a token has fewer open ones than it needs.
 #include "nvfp4_internal.h"
@@ -168,15 +171,33 @@ __device__ __forceinline__ double rt_exp(double x) {
   y = fma(y, r, 1.0);
   return ldexp(y, static_cast<int>(n));
 }
-__device__ __forceinline__ double rt_sigmoid(float l) { return 1.0 / (1.0 + rt_exp(-static_cast<double>(l))); }
 
-// the two largest of what two lanes hold
-template <typename T>
-__device__ __forceinline__ void top2_merge(T& a1, T& a2, T b1, T b2) {
-  const T low = a1 < b1 ? a1 : b1;
-  a1 = a1 < b1 ? b1 : a1;
-  a2 = a2 < b2 ? b2 : a2;
-  a2 = a2 < low ? low : a2;
+// the two largest (a1 >= a2) of what two lanes hold
+__device__ __forceinline__ void top2_merge(float& a1, float& a2, float b1, float b2) {
+  a2 = fmaxf(fmaxf(fminf(a1, b1), a2), b2);
+  a1 = fmaxf(a1, b1);
+}
+// ... over `s` (a power of two) neighbouring lanes
+__device__ __forceinline__ void top2_lanes(float& a1, float& a2, int s) {
+  auto with = [&](uint32_t b1, uint32_t b2) __attribute__((always_inline)) {
+    top2_merge(a1, a2, __uint_as_float(b1), __uint_as_float(b2));
+  };
+  if (s > 1) with(dpp_u32<kDppXor1>(__float_as_uint(a1)), dpp_u32<kDppXor1>(__float_as_uint(a2)));
+  if (s > 2) with(dpp_u32<kDppXor2>(__float_as_uint(a1)), dpp_u32<kDppXor2>(__float_as_uint(a2)));
+  if (s > 4) with(dpp_u32<kDppHalfMirror>(__float_as_uint(a1)), dpp_u32<kDppHalfMirror>(__float_as_uint(a2)));
+  if (s > 8) with(dpp_u32<kDppMirror>(__float_as_uint(a1)), dpp_u32<kDppMirror>(__float_as_uint(a2)));
+  if (s > 16) {
+    uint32_t b1, b2;
+    a1 = __uint_as_float(rt_row_pair(__float_as_uint(a1), b1));
+    a2 = __uint_as_float(rt_row_pair(__float_as_uint(a2), b2));
+    with(b1, b2);
+  }
+  if (s > 32) {
+    uint32_t b1, b2;
+    a1 = __uint_as_float(rt_half_pair(__float_as_uint(a1), b1));
+    a2 = __uint_as_float(rt_half_pair(__float_as_uint(a2), b2));
+    with(b1, b2);
+  }
 }
 
 __device__ __forceinline__ void rt_lds_step() {
@@ -185,144 +206,233 @@ __device__ __forceinline__ void rt_lds_step() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Which groups stay.  key(c): of the lane's expert c, above `shut` if open; T: float
-// with `near` (set if two groups' values lie within tol + |value| 2^-18), or double
-// (near: never).  Returns a bit for each of the lane's experts that went with its
-// group.  lds: (E + 2 n_group) doubles of the token's own where no lanes' borders
-// follow the groups'.
-template <int LPT, int NE, typename T, typename K>
-__device__ __forceinline__ uint64_t scored_groups(const ScoredParams& p, K key, T shut, T tol, double* lds_bytes, bool& near) {
-  const T none = -static_cast<T>(__builtin_huge_valf());
+// Which groups stay, by float32 keys (key(c): of the lane's expert c, -inf if there is
+// none).  near: set if the last group that stays and the first that goes are within
+// tol + |value| 2^-22.  Returns a bit for each of the lane's experts that stays.  lds:
+// E + 2 n_group floats of the token's own, where no lanes' borders follow the groups'.
+template <int LPT, int NE, typename K>
+__device__ __forceinline__ uint32_t scored_groups(const ScoredParams& p, K key, float tol, float* lds, bool& near) {
+  const float none = -__builtin_huge_valf();
   const int l = threadIdx.x & (LPT - 1);
   const int e0 = l * NE;
   const int gs = p.E / p.n_group;
-  auto value = [&](T a1, T a2) __attribute__((always_inline)) { return p.group_top == 2 && a2 > none ? a1 + a2 : a1; };
-  auto beats = [&](T o, int h, T v, int g) __attribute__((always_inline)) {
-    if (h != g && fabs(o - v) <= tol + fabs(v) * static_cast<T>(0x1p-18) && o > none && v > none) near = true;
-    return o > v || (o == v && h < g);
-  };
+  auto value = [&](float a1, float a2) __attribute__((always_inline)) { return p.group_top == 2 ? a1 + a2 : a1; };
+  float last = -none, next = none;          // of the groups that stay, and that go
+  uint32_t stays = 0;
   if (p.lanes_per_group) {
     const int s = p.lanes_per_group;
-    T a1 = none, a2 = none;
+    float a1 = none, a2 = none;
 #pragma unroll
     for (int c = 0; c < NE; ++c) {
-      const T k = key(c);
-      top2_merge(a1, a2, k > shut ? k : none, none);
+      const float k = key(c);
+      a2 = __builtin_amdgcn_fmed3f(a1, a2, k);
+      a1 = fmaxf(a1, k);
     }
-    for (int d = 1; d < s; d <<= 1) {
-      const T b1 = __shfl_xor(a1, d), b2 = __shfl_xor(a2, d);
-      top2_merge(a1, a2, b1, b2);
-    }
-    const T v = value(a1, a2);
+    top2_lanes(a1, a2, s);
+    const float v = value(a1, a2);
     const int g = l / s;
     int rank = 0;
-    for (int h = 0; h < p.n_group; ++h) rank += beats(__shfl(v, h * s, LPT), h, v, g) ? 1 : 0;
-    if (g >= p.n_group) near = false;
-    return rank < p.topk_group ? 0ull : ~0ull;
-  }
-  // keys by way of LDS, a group's behind those of the one before it and a gap (no bank twice)
-  T* lds = reinterpret_cast<T*>(lds_bytes);
-  T* val = lds + p.E + p.n_group;
+    for (int h0 = 0; h0 < p.n_group; h0 += 4) {              // four exchanges at a time
+      float o[4];
 #pragma unroll
-  for (int c = 0; c < NE; ++c) {
-    const int e = e0 + c;
-    if (e < p.E) lds[e + e / gs] = key(c);
-  }
-  rt_lds_step();
-  for (int g = l; g < p.n_group; g += LPT) {
-    T a1 = none, a2 = none;
-    for (int i = 0; i < gs; ++i) {
-      const T o = lds[g * (gs + 1) + i];
-      top2_merge(a1, a2, o > shut ? o : none, none);
+      for (int i = 0; i < 4; ++i) o[i] = __shfl(v, min(h0 + i, p.n_group - 1) * s, LPT);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rank += h0 + i < p.n_group && o[i] > v ? 1 : 0;
     }
-    val[g] = value(a1, a2);
-  }
-  rt_lds_step();
-  for (int g = l; g < p.n_group; g += LPT) {
-    const T v = val[g];
-    int rank = 0;
-    for (int h = 0; h < p.n_group; ++h) rank += beats(val[h], h, v, g) ? 1 : 0;
-    lds[g * (gs + 1) + gs] = rank < p.topk_group ? 1 : 0;   // in the gap behind the group
-  }
-  rt_lds_step();
-  uint64_t gone = 0;
-#pragma unroll
-  for (int c = 0; c < NE; ++c) {
-    const int e = e0 + c;
-    if (e < p.E && lds[(e / gs) * (gs + 1) + gs] == 0) gone |= 1ull << c;
-  }
-  rt_lds_step();                            // the same words are written again
-  return gone;
-}
-
-// The choice by float64 keys: k rounds of the best that is left, ties to the lower id
-// (a lane's best is its first, and lanes hold ascending ids).  Lanes meet on the
-// float32 roundings (rounding keeps the order), and only a tie there looks at the
-// float64 keys.  Lane j gets the j-th.
-template <int LPT, int NE, typename B>
-__device__ __forceinline__ void choose_exact(const ScoredParams& p, const float (&x)[NE], B bias, double top, double z, double* lds,
-                                             int& my_id, bool& my_open) {
-  const int l = threadIdx.x & (LPT - 1);
-  const int e0 = l * NE;
-  double key[NE];
-#pragma unroll
-  for (int c = 0; c < NE; ++c) {
-    key[c] = static_cast<double>(rt_finite(x[c]));
-    if (p.bias || p.n_group > 1) {
-      key[c] = p.softmax ? rt_exp(key[c] - top) / z : rt_sigmoid(rt_finite(x[c]));
-      if (p.bias) key[c] += static_cast<double>(bias(c));
+    if (g < p.n_group) {
+      if (rank < p.topk_group) {
+        stays = ~0u;
+        last = v;
+      } else {
+        next = v;
+      }
     }
-    if (!rt_open(x[c]) || !(key[c] > kNone)) key[c] = kClosed;
-  }
-  uint64_t gone = 0;
-  if (p.n_group > 1) {
-    bool near = false;
-    gone = scored_groups<LPT, NE, double>(p, [&](int c) __attribute__((always_inline)) { return key[c]; }, kClosed, -1.0, lds, near);
-  }
-#pragma unroll
-  for (int c = 0; c < NE; ++c) {
-    if (!p.bias) key[c] = rt_open(x[c]) ? static_cast<double>(rt_finite(x[c])) : kClosed;
-    if (((gone >> c) & 1) || e0 + c >= p.E) key[c] = kNone;
-  }
-  double best = kNone;
-  int bid = 0;
-  auto rescan = [&]() __attribute__((always_inline)) {
-    best = kNone;
-    bid = e0;
+    // equal values at the border all stay, and are then too many
+    near |= __popcll(seg_ballot<LPT>(g < p.n_group && stays != 0)) != p.topk_group * s;
+  } else {
+    // keys by way of LDS, a group's behind those of the one before it and a gap (no bank twice)
+    float* const val = lds + p.E + p.n_group;
 #pragma unroll
     for (int c = 0; c < NE; ++c) {
-      const bool more = key[c] > best;
-      best = more ? key[c] : best;
-      bid = more ? e0 + c : bid;
+      const int e = e0 + c;
+      if (e < p.E) lds[e + e / gs] = key(c);
     }
-  };
-  rescan();
-  const int base = (threadIdx.x & 63) & ~(LPT - 1);
-  for (int j = 0; j < p.k; ++j) {
-    const float h = static_cast<float>(best);
-    bool mine = h == seg_max<LPT>(h);
-    uint64_t who = seg_ballot<LPT>(mine);
-    if (__any((who & (who - 1)) != 0)) {
-      const double b = mine ? best : kNone;
-      const double m = seg_max<LPT>(b);      // by every lane of the wave
-      mine = mine && b == m;
-      who = seg_ballot<LPT>(mine);
+    rt_lds_step();
+    for (int g = l; g < p.n_group; g += LPT) {
+      float a1 = none, a2 = none;
+      for (int i = 0; i < gs; ++i) {
+        const float k = lds[g * (gs + 1) + i];
+        a2 = __builtin_amdgcn_fmed3f(a1, a2, k);
+        a1 = fmaxf(a1, k);
+      }
+      val[g] = value(a1, a2);
     }
-    const int w = __builtin_ctzll(who);
-    const int packed = __shfl(bid | (best > kClosed ? 1 << 30 : 0), base + w);
-    if (l == j) {
-      my_id = packed & 0xFFFF;
-      my_open = (packed >> 30) != 0;
+    rt_lds_step();
+    int count = 0;
+    for (int g = l; g < p.n_group; g += LPT) {
+      const float v = val[g];
+      int rank = 0;
+      for (int h = 0; h < p.n_group; ++h) rank += val[h] > v ? 1 : 0;
+      const bool in = rank < p.topk_group;
+      count += in ? 1 : 0;
+      lds[g * (gs + 1) + gs] = in ? 1.0f : 0.0f;             // in the gap behind the group
+      last = in ? fminf(last, v) : last;
+      next = in ? next : fmaxf(next, v);
     }
-    if (l == w) {
+    rt_lds_step();
 #pragma unroll
-      for (int c = 0; c < NE; ++c) key[c] = bid == e0 + c ? kNone : key[c];
-      rescan();
+    for (int c = 0; c < NE; ++c) {
+      const int e = e0 + c;
+      if (e < p.E && lds[(e / gs) * (gs + 1) + gs] != 0.0f) stays |= 1u << c;
     }
+    rt_lds_step();                          // the same words are written again
+    near |= seg_sum<LPT>(static_cast<float>(count)) != static_cast<float>(p.topk_group);
   }
+  last = -seg_max<LPT>(-last);
+  next = seg_max<LPT>(next);
+  near |= last - next <= tol + fabsf(last) * 0x1p-22f;
+  return stays;
 }
 
-// float32 bits in an order of unsigned integers
+// Scores of all experts in float64 by N lanes, four neighbours at a time: f(i, x, s) for
+// i to i + 3, closed ones (and those past E) with score 0.  Returns the softmax's sum
+// (1 for a sigmoid).  Four chains of float64 steps a lane hide their latency; all 16 of a
+// row at once are 6 KB of code, which costs a cold launch more than the loop.
+template <int N, int DT, typename F>
+__device__ __forceinline__ double scores64(const ScoredParams& p, size_t row, int l, double top, F f) {
+  double z = 1.0;
+  for (int pass = p.softmax ? 0 : 1; pass < 2; ++pass) {
+    double sum = 0.0;
+    for (int i = 4 * l; i < p.E; i += 4 * N) {
+      float x[4];
+      double s[4];
+      rt_load_row<DT, 4>(p.logits, row, i, p.E, p.vec, x);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const double v = static_cast<double>(rt_finite(x[c]));
+        const double e = rt_exp(p.softmax ? v - top : -v);
+        s[c] = rt_open(x[c]) ? (p.softmax ? e : 1.0 / (1.0 + e)) : 0.0;
+        sum += s[c];
+      }
+      if (pass == 0) continue;
+      if (p.softmax) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[c] /= z;
+      }
+      f(i, x, s);
+    }
+    if (pass == 0) {
+      z = seg_sum<N>(sum);
+      z = z > 0.0 ? z : 1.0;
+    }
+  }
+  return z;
+}
+
+// The choice by float64 keys, one token on the whole wave: k rounds of the best that is
+// left, ties to the lower id.  Lane l holds experts l, l + 64, ... in LDS (E + 2 n_group
+// doubles of the wave's own).  Lanes meet on the float32 roundings of their best (rounding
+// keeps the order), and only a tie there looks at the float64 keys and ids.  list[j] gets
+// the j-th, with bit 30 set if it is open.
+template <int DT>
+__device__ __forceinline__ void choose_exact(const ScoredParams& p, int t, double* lds, int* list) {
+  const int l = threadIdx.x & 63;
+  const size_t row = static_cast<size_t>(t) * p.E;
+  const int gs = p.n_group > 1 ? p.E / p.n_group : p.E;
+  double top = 0.0;
+  if (p.softmax) {
+    float m = -__builtin_huge_valf();
+    for (int i = l; i < p.E; i += 64) {
+      const float x = rt_load<DT>(p.logits, row + i);
+      m = rt_open(x) ? fmaxf(m, rt_finite(x)) : m;
+    }
+    m = seg_max<64>(m);
+    top = rt_open(m) ? m : 0.0f;
+  }
+  auto at = [&](int e) __attribute__((always_inline)) { return e + (p.n_group > 1 ? e / gs : 0); };
+  if (p.bias || p.n_group > 1) {
+    scores64<64, DT>(p, row, l, top, [&](int i, const float (&x)[4], const double (&s)[4]) __attribute__((always_inline)) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (i + c >= p.E) break;
+        const double v = s[c] + (p.bias ? static_cast<double>(p.bias[i + c]) : 0.0);
+        lds[at(i + c)] = rt_open(x[c]) && v > kNone ? v : kClosed;
+      }
+    });
+  }
+  rt_lds_step();
+  double* const val = lds + p.E + p.n_group;
+  if (p.n_group > 1) {
+    // the lanes of a group (a power of two) take its keys in turn and join theirs
+    int parts = 1;
+    while (2 * parts * p.n_group <= 64) parts *= 2;
+    const int g = l / parts;
+    double a1 = kNone, a2 = kNone;
+    auto add = [&](double b1, double b2) __attribute__((always_inline)) {
+      a2 = fmax(fmin(a1, b1), fmax(a2, b2));
+      a1 = fmax(a1, b1);
+    };
+    for (int i = l % parts; i < gs; i += parts) {
+      const double k = g < p.n_group ? lds[g * (gs + 1) + i] : kNone;
+      add(k > kClosed ? k : kNone, kNone);
+    }
+    for (int d = 1; d < parts; d *= 2) {
+      const double b1 = __shfl_xor(a1, d), b2 = __shfl_xor(a2, d);
+      add(b1, b2);
+    }
+    if (g < p.n_group && l % parts == 0) val[g] = p.group_top == 2 && a2 > kNone ? a1 + a2 : a1;
+    rt_lds_step();
+    for (int g = l; g < p.n_group; g += 64) {
+      int rank = 0;
+      for (int h = 0; h < p.n_group; ++h) rank += val[h] > val[g] || (val[h] == val[g] && h < g) ? 1 : 0;
+      lds[g * (gs + 1) + gs] = rank < p.topk_group ? 1.0 : 0.0;
+    }
+    rt_lds_step();
+  }
+  for (int i = l; i < p.E; i += 64) {
+    if (!p.bias) {
+      const float x = rt_load<DT>(p.logits, row + i);
+      lds[at(i)] = rt_open(x) ? static_cast<double>(rt_finite(x)) : kClosed;
+    }
+    if (p.n_group > 1 && lds[(i / gs) * (gs + 1) + gs] == 0.0) lds[at(i)] = kNone;
+  }
+  rt_lds_step();
+  double best = kNone;
+  int id = 0x7fffffff;
+  auto scan = [&]() __attribute__((always_inline)) {
+    best = kNone;
+    id = 0x7fffffff;
+    for (int i = l; i < p.E; i += 64) {
+      const double k = lds[at(i)];
+      if (k > best) {
+        best = k;
+        id = i;
+      }
+    }
+  };
+  scan();
+  for (int j = 0; j < p.k; ++j) {
+    const float h = static_cast<float>(best);
+    const float m = seg_max<64>(h);
+    uint64_t who = __ballot(h == m);
+    if (who & (who - 1)) {
+      const double b = h == m ? best : kNone;
+      const double most = seg_max<64>(b);    // by every lane of the wave
+      const uint32_t first = seg_reduce<64>(h == m && b == most ? static_cast<uint32_t>(id) : 0xffffffffu,
+                                            [](uint32_t a, uint32_t b) __attribute__((always_inline)) { return a < b ? a : b; });
+      who = __ballot(h == m && b == most && static_cast<uint32_t>(id) == first);
+    }
+    const int w = __builtin_ctzll(who);
+    if (l == w) {
+      list[j] = id | (best > kClosed ? 1 << 30 : 0);
+      lds[at(id)] = kNone;
+      scan();
+    }
+  }
+  rt_lds_step();
+}
+
+// float32 bits in an order of unsigned integers (0 below all numbers)
 __device__ __forceinline__ uint32_t rt_order(float f) {
   const uint32_t u = __float_as_uint(f);
   return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
@@ -331,206 +441,231 @@ __device__ __forceinline__ float rt_unorder(uint32_t u) {
   return __uint_as_float(u ^ (static_cast<uint32_t>(static_cast<int32_t>(~u) >> 31) | 0x80000000u));
 }
 
-// The choice by float32 keys.  An expert's key is an unsigned integer, its place in
-// the lane in the low bits (so the key loses log2(NE) bits): a lane's best of NE is a
-// few three-way maxima.  Returns 0 (for a whole wave) where the float32 keys do not
-// settle which experts or groups are chosen, 1 where they settle all, 2 where the
-// order of the k chosen is open.  list: 32 ints of the token's own.
+// v[0 .. N) in descending order: Batcher's odd-even merge sort (two instructions an exchange)
+template <int N>
+__device__ __forceinline__ void rt_sort(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const uint32_t a = v[i + j], b = v[i + j + k];
+            v[i + j] = a > b ? a : b;
+            v[i + j + k] = a > b ? b : a;
+          }
+}
+
+// The choice by float32 keys, of tokens whose logits (and biases) are all finite.
+// list (32 ints of the token's own) gets n candidates, k or a few more, that hold the
+// k chosen.  Returns n; order: the float32 keys do not settle their order; near: nor,
+// with up to LPT candidates, that they are all, or which groups stay, or a value is not
+// finite.
+//
+// An expert's key is an unsigned integer with its place in the lane in the low bits
+// (so the key loses log2(NE) bits).  Each lane sorts its own, and then the lanes
+// compare their first ones and one of them drops it, k times and on until a key is
+// clearly smaller: 1 instruction a key and round in place of 4 for a search through
+// all.
 //
 // Errors: a sigmoid from v_exp_f32 and v_rcp_f32 is off by at most 2^-22 (s (1 - s)
 // (|x| + 2) 2^-24 + 3 s 2^-24), a softmax by p (|x - max| + 30) 2^-24 (sums of 16 and
 // over 6 levels, exp, quotient), which is below 2^-18 max p (|x - max| p <= 0.37 max
 // p); the bias adds 2^-24 |key|, the lost bits |key| 2^-19 for 16 places.  Two keys
-// within twice that, tol + |key| 2^-18, are not settled, group values within twice
-// as much.
+// within twice that, tol + |key| 2^-18, are not settled; group values, of keys with
+// all their bits, within 2 tol + |value| 2^-22.
 template <int LPT, int NE>
 __device__ __forceinline__ int choose_fast(const ScoredParams& p, const float (&x)[NE], const float (&bias)[NE], float top, float z,
-                                           double* lds, int* list, int& my_id, bool& my_open) {
+                                           float* lds, int* list, bool& order, bool& near) {
   constexpr uint32_t LOW = NE <= 4 ? 3 : 15;
   static_assert(NE <= 16, "the place takes 4 bits");
   const int l = threadIdx.x & (LPT - 1);
   const int e0 = l * NE;
+  const bool full = p.E == LPT * NE;
   float key[NE];
   float big = 1.0f;                          // of a sigmoid
+  float odd = 0.0f;                          // NaN if any value is not finite
+#pragma unroll
+  for (int c = 0; c < NE; ++c) odd = full || e0 + c < p.E ? fmaf(x[c], 0.0f, odd) : odd;
   if (p.bias || p.n_group > 1) {
     if (p.softmax) big = __builtin_amdgcn_rcpf(z);                      // the largest p
 #pragma unroll
-    for (int c = 0; c < NE; ++c) {
-      const float a = rt_finite(x[c]);
-      key[c] = p.softmax ? __builtin_amdgcn_exp2f((a - top) * 1.44269504f) * big
-                         : __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(a * -1.44269504f));
-      if (p.bias) key[c] += bias[c];
+    for (int c = 0; c < NE; ++c)
+      key[c] = p.softmax ? __builtin_amdgcn_exp2f((x[c] - top) * 1.44269504f) * big
+                         : __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x[c] * -1.44269504f));
+    if (p.bias) {
+#pragma unroll
+      for (int c = 0; c < NE; ++c) {
+        odd = full || e0 + c < p.E ? fmaf(bias[c], 0.0f, odd) : odd;
+        key[c] += bias[c];
+      }
     }
-  } else {
-#pragma unroll
-    for (int c = 0; c < NE; ++c) key[c] = rt_finite(x[c]);
   }
+  near = odd != 0.0f;                        // NaN
   const float none = -__builtin_huge_valf();
-#pragma unroll
-  for (int c = 0; c < NE; ++c) key[c] = rt_open(x[c]) && key[c] > none ? key[c] : none;
   const float tol = p.softmax ? big * 0x1p-16f : 0x1p-20f;
-  bool near = false;
-  uint64_t gone = 0;
+  uint32_t keep = ~0u;
   if (p.n_group > 1)
-    gone = scored_groups<LPT, NE, float>(p, [&](int c) __attribute__((always_inline)) { return key[c]; }, none, 2.0f * tol, lds, near);
-  // by logits: the keys are exact (and 16-bit ones keep all their bits)
+    keep = scored_groups<LPT, NE>(p, [&](int c) __attribute__((always_inline)) { return full || e0 + c < p.E ? key[c] : none; },
+                                  2.0f * tol, lds, near);
+  if (!full) keep &= e0 >= p.E ? 0u : p.E - e0 >= 32 ? ~0u : (1u << (p.E - e0)) - 1;
+  // by logits: the keys are exact, and 16-bit ones keep all their bits
   const bool exact = !p.bias && p.narrow;
   uint32_t el[NE];
 #pragma unroll
   for (int c = 0; c < NE; ++c) {
-    const float k = p.bias ? key[c] : rt_finite(x[c]);
-    const bool open = key[c] > none;
-    el[c] = ((open ? rt_order(k) & ~LOW : LOW + 1) | (LOW - c));        // closed ones below every open
-    if (((gone >> c) & 1) || e0 + c >= p.E) el[c] = 0;
+    const uint32_t there = static_cast<uint32_t>(static_cast<int32_t>(keep << (31 - c)) >> 31);
+    el[c] = ((rt_order(p.bias ? key[c] : x[c]) & ~LOW) | (LOW - c)) & there;
   }
-  bool order = false;
+  rt_sort<NE>(el);
+  order = false;
   float before = __builtin_huge_valf();
-  for (int j = 0; j <= p.k; ++j) {           // and the first that is not chosen
-    uint32_t best = 0;
-#pragma unroll
-    for (int c = 0; c < NE; ++c) best = el[c] > best ? el[c] : best;
-    const uint32_t t = best & ~LOW;
+  int n = 0;
+  bool more = true;
+  for (int j = 0; __any(more); ++j) {
+    const uint32_t t = el[0] & ~LOW;
     const uint32_t m = seg_reduce<LPT>(t, [](uint32_t a, uint32_t b) __attribute__((always_inline)) { return a > b ? a : b; });
     const float v = rt_unorder(m);
-    // closed and absent ones (m <= LOW + 1) are in their order already
-    const bool close = !exact && m > LOW + 1 && before - v <= (p.bias ? tol : 0.0f) + fabsf(v) * 0x1p-18f;
-    if (j < p.k) order |= close;
-    else near |= close;
-    before = m > LOW + 1 ? v : __builtin_huge_valf();
-    const int w = __builtin_ctzll(seg_ballot<LPT>(t == m));
-    const uint32_t gone_el = l == w ? best : 0;
-    if (j < p.k && l == w) list[j] = e0 + static_cast<int>(LOW - (best & LOW)) + (m > LOW + 1 ? 1 << 30 : 0);
+    const bool close = !exact && m != 0 && before - v <= (p.bias ? tol : 0.0f) + fabsf(v) * 0x1p-18f;
+    before = v;
+    more = more && (j < p.k || close);
+    if (more && j >= (LPT < 32 ? LPT : 32)) {
+      near = true;
+      more = false;
+    }
+    order |= more && close;
+    n += more ? 1 : 0;
+    const bool mine = l == __builtin_ctzll(seg_ballot<LPT>(t == m));
+    if (mine && more) list[j] = (e0 + static_cast<int>(LOW - (el[0] & LOW))) | (1 << 30);
 #pragma unroll
-    for (int c = 0; c < NE; ++c) el[c] = el[c] == gone_el ? 0 : el[c];
+    for (int c = 0; c < NE - 1; ++c) el[c] = mine ? el[c + 1] : el[c];
+    if (mine) el[NE - 1] = 0;
   }
-  if (__any(near)) return 0;
-  rt_lds_step();
-  const int packed = l < p.k ? list[l] : 0;
-  my_id = packed & 0xFFFF;
-  my_open = (packed >> 30) != 0;
-  return __any(order) ? 2 : 1;
+  near = seg_ballot<LPT>(near) != 0;         // over the token's lanes
+  return n;
 }
 
-// One token on LPT lanes, expert l * NE + c in register c of lane l.  Writes ids,
-// weights and (if wanted) scores; lane j < k returns the j-th choice and its weight.
-// lds: of the token's own, for groups (scored_groups); list: 32 ints of its own.  Lanes
-// of a token past T take part on the last token's values and write nothing.
+// One token on LPT lanes, expert l * NE + c in register c of lane l (NE 0: none, the
+// float64 choice at once).  Writes ids, weights and (if wanted) scores.  Returns the place
+// among the k chosen of the expert and weight that the lane holds, or k.  lds: lds_wave
+// doubles of the wave's own; list: 32 ints of the token's own.  Lanes of a token past T
+// take part on the last token's values and write nothing.
 template <int LPT, int NE, int DT>
-__device__ __forceinline__ void scored_token(const ScoredParams& p, int t, bool live, double* lds, int* list, int& my_id, float& my_w) {
+__device__ __forceinline__ int scored_token(const ScoredParams& p, int t, bool live, double* lds, int* list, int& my_id, float& my_w) {
   const int l = threadIdx.x & (LPT - 1);
-  const int e0 = l * NE;
   const size_t row = static_cast<size_t>(t) * p.E;
-  float x[NE];
-  rt_load_row<DT, NE>(p.logits, row, e0, p.E, p.vec, x);
-  constexpr bool FAST = NE <= 16;
-  float bias[FAST ? NE : 1];
-  if constexpr (FAST) {
+  double top = 0.0, z = 0.0;
+  int n = p.k;
+  bool order = false, near = true;
+  if constexpr (NE > 0) {
+    const int e0 = l * NE;
+    float x[NE], bias[NE];
+    rt_load_row<DT, NE>(p.logits, row, e0, p.E, p.vec, x);
     if (p.bias) rt_load_row<0, NE>(p.bias, 0, e0, p.E, p.vec_bias, bias);
-  }
-  const bool by_key = p.bias || p.n_group > 1;
-  double top = 0.0, z = 1.0;
-  if (p.softmax) {
-    float m = -__builtin_huge_valf();
+    float zf = 1.0f;
+    if (p.softmax) {
+      float m = -__builtin_huge_valf();
 #pragma unroll
-    for (int c = 0; c < NE; ++c) m = rt_open(x[c]) ? fmaxf(m, rt_finite(x[c])) : m;
+      for (int c = 0; c < NE; ++c) m = rt_open(x[c]) ? fmaxf(m, rt_finite(x[c])) : m;
+      m = seg_max<LPT>(m);
+      top = rt_open(m) ? m : 0.0f;
+      if (p.bias || p.n_group > 1) {
+        zf = 0.0f;
+#pragma unroll
+        for (int c = 0; c < NE; ++c)
+          zf += rt_open(x[c]) ? __builtin_amdgcn_exp2f((rt_finite(x[c]) - static_cast<float>(top)) * 1.44269504f) : 0.0f;
+        zf = seg_sum<LPT>(zf);
+        zf = zf > 0.0f ? zf : 1.0f;
+      }
+    }
+    n = choose_fast<LPT, NE>(p, x, bias, static_cast<float>(top), zf,
+                             reinterpret_cast<float*>(lds) + ((threadIdx.x & 63) / LPT) * (p.E + 2 * p.n_group), list, order, near);
+  } else if (p.softmax) {
+    float m = -__builtin_huge_valf();
+    for (int i = l; i < p.E; i += LPT) {
+      const float x = rt_load<DT>(p.logits, row + i);
+      m = rt_open(x) ? fmaxf(m, rt_finite(x)) : m;
+    }
     m = seg_max<LPT>(m);
     top = rt_open(m) ? m : 0.0f;
   }
-  auto sum64 = [&]() __attribute__((always_inline)) {
-    double sum = 0.0;
-#pragma unroll
-    for (int c = 0; c < NE; ++c) sum += rt_open(x[c]) ? rt_exp(static_cast<double>(rt_finite(x[c])) - top) : 0.0;
-    sum = seg_sum<LPT>(sum);
-    z = sum > 0.0 ? sum : 1.0;
-  };
-  const bool have_z = p.softmax && (p.scores || !p.renormalize);
-  if (have_z) sum64();
-  if (p.scores && live) {
-    float s[NE];
-#pragma unroll
-    for (int c = 0; c < NE; ++c) {
-      const float a = rt_open(x[c]) ? rt_finite(x[c]) : 0.0f;
-      const double v = p.softmax ? rt_exp(static_cast<double>(a) - top) / z : rt_sigmoid(a);
-      s[c] = rt_open(x[c]) ? static_cast<float>(v) : 0.0f;
-    }
-    rt_store_row<NE>(p.scores, row, e0, p.E, p.vec_scores, s);
+  // the tokens of the wave that are not settled, one after the other on all its lanes
+  rt_lds_step();
+  const int base = (threadIdx.x & 63) & ~(LPT - 1);
+  for (uint64_t rest = __ballot(near && l == 0); rest; rest &= rest - 1) {
+    const int at = __builtin_ctzll(rest);
+    choose_exact<DT>(p, __builtin_amdgcn_readlane(t, at), lds, list + (at - base) / LPT * 32);
   }
+  if (near) {
+    n = p.k;
+    order = false;
+  }
+  rt_lds_step();
+  if (p.scores || (p.softmax && (!p.renormalize || (p.bias && __any(order)))))
+    z = scores64<LPT, DT>(p, row, l, top, [&](int i, const float (&)[4], const double (&s)[4]) __attribute__((always_inline)) {
+      if (!p.scores || !live) return;
+      const float v[4] = {static_cast<float>(s[0]), static_cast<float>(s[1]), static_cast<float>(s[2]), static_cast<float>(s[3])};
+      rt_store_row<4>(p.scores, row, i, p.E, p.vec_scores, v);
+    });
 
-  bool my_open = false;
-  my_id = 0;
-  int settled = 0;
-  if constexpr (FAST) {
-    float zf = static_cast<float>(z);
-    if (p.softmax && by_key && !have_z) {
-      zf = 0.0f;
-#pragma unroll
-      for (int c = 0; c < NE; ++c)
-        zf += rt_open(x[c]) ? __builtin_amdgcn_exp2f((rt_finite(x[c]) - static_cast<float>(top)) * 1.44269504f) : 0.0f;
-      zf = seg_sum<LPT>(zf);
-      zf = zf > 0.0f ? zf : 1.0f;
+  // the candidates' scores, one a lane.  Renormalised softmax: relative to the largest
+  // candidate's logit, which divides out; renormalised sigmoids of logits below -500
+  // times exp(-largest), likewise: scores that would underflow together keep their ratios
+  const int packed = l < n ? list[l] : 0;
+  my_id = packed & 0xFFFF;
+  const bool open = l < n && (packed >> 30) != 0;
+  const float xj = open ? rt_finite(rt_load<DT>(p.logits, row + my_id)) : 0.0f;
+  const float most = seg_max<LPT>(open ? xj : -__builtin_huge_valf());
+  const bool low = !p.softmax && p.renormalize && most < -500.0f;
+  const double from = p.softmax && p.renormalize && open ? static_cast<double>(most) : top;
+  double u = rt_exp(p.softmax ? static_cast<double>(xj) - from : -static_cast<double>(xj));
+  if (!p.softmax) u = 1.0 / (1.0 + u);
+  else if (!p.renormalize) u /= z;
+  int place = l < n ? l : p.k;
+  if (__any(order)) {
+    // in the order of the float64 keys, ties to the lower id
+    double key = static_cast<double>(xj);
+    if (p.bias && p.softmax) key = p.renormalize ? rt_exp(key - top) / z : u;
+    else if (p.bias) key = u;
+    if (p.bias) key += static_cast<double>(p.bias[my_id]);
+    if (!open) key = kClosed;
+    int rank = 0;
+    for (int i = 0; i < (LPT < 32 ? LPT : 32); ++i) {
+      const double o = __shfl(key, i, LPT);
+      const int oid = __shfl(l < n ? my_id : 0x7fffffff, i, LPT);
+      rank += oid != 0x7fffffff && (o > key || (o == key && oid < my_id)) ? 1 : 0;
     }
-    settled = choose_fast<LPT, NE>(p, x, bias, static_cast<float>(top), zf, lds, list, my_id, my_open);
+    if (order) place = l < n ? rank : p.k;
   }
-  if (settled != 1) {
-    if (p.softmax && by_key && !have_z) sum64();
-    if (settled == 0) {
-      choose_exact<LPT, NE>(p, x, [&](int c) __attribute__((always_inline)) {
-        if constexpr (FAST) return bias[c];
-        else return e0 + c < p.E ? p.bias[e0 + c] : 0.0f;
-      }, top, z, lds, my_id, my_open);
-    } else {
-      // the chosen in the order of their float64 keys, ties to the lower id
-      const float xj = rt_finite(rt_load<DT>(p.logits, row + my_id));
-      double key = static_cast<double>(xj);
-      if (p.bias) key = (p.softmax ? rt_exp(key - top) / z : rt_sigmoid(xj)) + static_cast<double>(p.bias[my_id]);
-      if (!my_open) key = kClosed;
-      int rank = 0;
-      for (int i = 0; i < p.k; ++i) {
-        const double o = __shfl(key, i, LPT);
-        const int id = __shfl(my_id, i, LPT);
-        rank += (o > key || (o == key && id < my_id)) ? 1 : 0;
-      }
-      rt_lds_step();
-      if (l < p.k) list[rank] = my_id | (my_open ? 1 << 30 : 0);
-      rt_lds_step();
-      const int packed = l < p.k ? list[l] : 0;
-      my_id = packed & 0xFFFF;
-      my_open = (packed >> 30) != 0;
-    }
-  }
-
-  // weights of the chosen: their scores again, one a lane.  Renormalised, relative to
-  // the largest of the chosen logits (sigmoid: times exp(-b), b = min(largest, 0)):
-  // the factor divides out, and scores that would underflow together keep their ratios
-  double u = 0.0;
-  my_open = my_open && l < p.k;
-  const float xj = rt_finite(rt_load<DT>(p.logits, row + my_id));
+  if (low) u = 1.0 / (rt_exp(most) + rt_exp(open ? static_cast<double>(most) - static_cast<double>(xj) : 0.0));
+  u = open && place < p.k ? u : 0.0;
   if (p.renormalize) {
-    const float m = seg_max<LPT>(my_open ? xj : -__builtin_huge_valf());
-    const double b = p.softmax ? m : fminf(m, 0.0f), d = my_open ? b - static_cast<double>(xj) : 0.0;
-    u = my_open ? (p.softmax ? rt_exp(-d) : 1.0 / (rt_exp(b) + rt_exp(d))) : 0.0;
     const double s = seg_sum<LPT>(u);
     u = s > 0.0 ? u / s : 0.0;
-  } else if (my_open) {
-    u = p.softmax ? rt_exp(static_cast<double>(xj) - top) / z : rt_sigmoid(xj);
   }
   my_w = static_cast<float>(u * static_cast<double>(p.scale));
-  if (live && l < p.k) {
-    const size_t at = static_cast<size_t>(t) * p.k + l;
+  if (live && place < p.k) {
+    const size_t at = static_cast<size_t>(t) * p.k + place;
     p.topk_ids[at] = my_id;
     p.topk_w[at] = my_w;
   }
+  return place;
 }
 
+constexpr int rt_threads(int ne) { return ne ? 256 : 64; }    // without registers a token takes up to 34 KB of LDS
 template <int LPT, int NE, int DT>
-__global__ __launch_bounds__(256) void k_route_scored(const ScoredParams p) {
+__global__ __launch_bounds__(rt_threads(NE)) void k_route_scored(const ScoredParams p) {
   extern __shared__ double lds[];
-  __shared__ int list[256 / LPT][32];
+  constexpr int kTokens = rt_threads(NE) / LPT;
+  __shared__ int list[kTokens][32];
   const int sub = threadIdx.x / LPT;
-  const int t = blockIdx.x * (256 / LPT) + sub;
+  const int t = blockIdx.x * kTokens + sub;
   int id;
   float w;
-  scored_token<LPT, NE, DT>(p, min(t, p.T - 1), t < p.T, lds + static_cast<size_t>(sub) * p.lds_token, list[sub], id, w);
+  scored_token<LPT, NE, DT>(p, min(t, p.T - 1), t < p.T, lds + static_cast<size_t>(threadIdx.x >> 6) * p.lds_wave, list[sub], id, w);
 }
 
 // ------------------------------------------------------------------ few tokens: routing and permutation in one launch
@@ -542,10 +677,9 @@ template <int NE, int DT>
 __global__ __launch_bounds__(1024) void k_route_small(const ScoredParams p, int* __restrict__ counts, int* __restrict__ offsets,
                                                       int* __restrict__ src, int* __restrict__ row_of, float* __restrict__ row_w) {
   extern __shared__ double lds[];
-  __shared__ int cnt[4096];
+  __shared__ int cnt[256];                 // E <= 256
   __shared__ int ids[kSmallRows];
   __shared__ float ws[kSmallRows];
-  __shared__ int wave_sum[16];
   __shared__ int list[16][32];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n = p.T * p.k;
@@ -553,10 +687,10 @@ __global__ __launch_bounds__(1024) void k_route_small(const ScoredParams p, int*
   for (int t = wave; t < p.T; t += 16) {
     int id;
     float w;
-    scored_token<64, NE, DT>(p, t, true, lds + static_cast<size_t>(wave) * p.lds_token, list[wave], id, w);
-    if (lane < p.k) {
-      ids[t * p.k + lane] = id;
-      ws[t * p.k + lane] = w;
+    const int place = scored_token<64, NE, DT>(p, t, true, lds + static_cast<size_t>(wave) * p.lds_wave, list[wave], id, w);
+    if (place < p.k) {
+      ids[t * p.k + place] = id;
+      ws[t * p.k + place] = w;
     }
   }
   __syncthreads();
@@ -567,35 +701,34 @@ __global__ __launch_bounds__(1024) void k_route_small(const ScoredParams p, int*
     atomicAdd(&cnt[id], 1);
   }
   __syncthreads();
-  // thread t owns 4 neighbouring experts
-  int c[4], sum = 0;
+  // one wave, 4 neighbouring experts a lane
+  if (wave == 0) {
+    int c[4], sum = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = 4 * tid + i;
-    c[i] = e < p.E ? cnt[e] : 0;
-    sum += c[i];
-  }
-  int incl = sum;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(incl, d);
-    if (lane >= d) incl += v;
-  }
-  if (lane == 63) wave_sum[wave] = incl;
-  __syncthreads();
-  int run = incl - sum;
-  for (int w = 0; w < wave; ++w) run += wave_sum[w];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = 4 * tid + i;
-    if (e < p.E) {
-      counts[e] = c[i];
-      offsets[e] = run;
-      cnt[e] = run;
+    for (int i = 0; i < 4; ++i) {
+      const int e = 4 * lane + i;
+      c[i] = e < p.E ? cnt[e] : 0;
+      sum += c[i];
     }
-    run += c[i];
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(incl, d);
+      if (lane >= d) incl += v;
+    }
+    int run = incl - sum;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = 4 * lane + i;
+      if (e < p.E) {
+        counts[e] = c[i];
+        offsets[e] = run;
+        cnt[e] = run;
+      }
+      run += c[i];
+    }
+    if (lane == 0) offsets[p.E] = n;
   }
-  if (tid == 0) offsets[p.E] = n;
   __syncthreads();
   if (tid < n) {
     const int r = cnt[ids[tid]] + rank;
@@ -770,16 +903,23 @@ static int rt_lanes_per_group(int E, int n_group, int ne) {
   return (s & (s - 1)) == 0 ? s : 0;
 }
 
+// doubles of LDS a wave: the float64 choice's of one token, or the float32 one's of each of its tokens
+static int rt_lds_wave(const ScoredParams& p, int lpt) {
+  const int one = p.E + 2 * p.n_group;
+  return p.n_group > 1 && !p.lanes_per_group && lpt < 64 ? (64 / lpt * one + 1) / 2 : one;
+}
+
 template <int LPT, int NE>
 static hipError_t rt_start(ScoredParams p, int dtype, hipStream_t stream) {
-  p.lanes_per_group = rt_lanes_per_group(p.E, p.n_group, NE);
-  p.lds_token = p.n_group > 1 && !p.lanes_per_group ? p.E + 2 * p.n_group : 0;
-  constexpr int kTokens = 256 / LPT;
+  constexpr int kThreads = rt_threads(NE);
+  p.lanes_per_group = NE ? rt_lanes_per_group(p.E, p.n_group, NE ? NE : 1) : 0;
+  p.lds_wave = rt_lds_wave(p, LPT);
+  constexpr int kTokens = kThreads / LPT;
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(p.T) + kTokens - 1) / kTokens));
-  const size_t lds = static_cast<size_t>(kTokens) * p.lds_token * sizeof(double);
-  if (dtype == 0) hipLaunchKernelGGL((k_route_scored<LPT, NE, 0>), grid, dim3(256), lds, stream, p);
-  else if (dtype == 1) hipLaunchKernelGGL((k_route_scored<LPT, NE, 1>), grid, dim3(256), lds, stream, p);
-  else hipLaunchKernelGGL((k_route_scored<LPT, NE, 2>), grid, dim3(256), lds, stream, p);
+  const size_t lds = static_cast<size_t>(kThreads / 64) * p.lds_wave * sizeof(double);
+  if (dtype == 0) hipLaunchKernelGGL((k_route_scored<LPT, NE, 0>), grid, dim3(kThreads), lds, stream, p);
+  else if (dtype == 1) hipLaunchKernelGGL((k_route_scored<LPT, NE, 1>), grid, dim3(kThreads), lds, stream, p);
+  else hipLaunchKernelGGL((k_route_scored<LPT, NE, 2>), grid, dim3(kThreads), lds, stream, p);
   return hipGetLastError();
 }
 
@@ -787,8 +927,8 @@ template <int NE>
 static hipError_t rt_start_small(ScoredParams p, int dtype, int* counts, int* offsets, int* src, int* row_of, float* row_w,
                                  hipStream_t stream) {
   p.lanes_per_group = rt_lanes_per_group(p.E, p.n_group, NE);
-  p.lds_token = p.n_group > 1 && !p.lanes_per_group ? p.E + 2 * p.n_group : 0;
-  const size_t lds = static_cast<size_t>(16) * p.lds_token * sizeof(double);
+  p.lds_wave = rt_lds_wave(p, 64);
+  const size_t lds = static_cast<size_t>(16) * p.lds_wave * sizeof(double);
   if (dtype == 0)
     hipLaunchKernelGGL((k_route_small<NE, 0>), dim3(1), dim3(1024), lds, stream, p, counts, offsets, src, row_of, row_w);
   else if (dtype == 1)
@@ -805,14 +945,13 @@ hipError_t launch_route_scored(const ScoredParams& q, int dtype, int* counts, in
   p.vec = p.E % 4 == 0 && reinterpret_cast<uintptr_t>(p.logits) % (dtype == 0 ? 16 : 8) == 0;
   p.vec_bias = p.E % 4 == 0 && reinterpret_cast<uintptr_t>(p.bias) % 16 == 0;
   p.vec_scores = p.E % 4 == 0 && reinterpret_cast<uintptr_t>(p.scores) % 16 == 0;
-  if (p.T <= 16 && p.T * p.k <= kSmallRows && p.E <= 512)
-    return p.E <= 256 ? rt_start_small<4>(p, dtype, counts, offsets, src, row_of, row_w, stream)
-                      : rt_start_small<8>(p, dtype, counts, offsets, src, row_of, row_w, stream);
+  if (p.T <= 16 && p.T * p.k <= kSmallRows && p.E <= 256)
+    return rt_start_small<4>(p, dtype, counts, offsets, src, row_of, row_w, stream);
   hipError_t err;
   if (rt_narrow(p.T, p.E, p.k)) err = p.E <= 64 ? rt_start<16, 4>(p, dtype, stream) : rt_start<16, 16>(p, dtype, stream);
   else if (p.E <= 256) err = rt_start<64, 4>(p, dtype, stream);
   else if (p.E <= 1024) err = rt_start<64, 16>(p, dtype, stream);
-  else err = rt_start<64, 64>(p, dtype, stream);
+  else err = rt_start<64, 0>(p, dtype, stream);
   if (err != hipSuccess) return err;
   return launch_permute(p.topk_ids, p.topk_w, p.T, p.E, p.k, counts, offsets, src, row_of, row_w, ws, stream);
 }
