@@ -15,11 +15,14 @@ namespace nvfp4 {
 // A group with a NaN or an infinity, or whose scale overflows its type, gets scale
 // NaN, codes 8 (zeros: codes and z 0).
 //
-// One pass: GROUP / 8 lanes hold a group, 8 values each.  The quotient is
-// x * (1 / s) except where that lands within 2^-14 of a tie: |x / s| < 32, so the
-// product is off by less than 32 * 3 * 2^-24 < 2^-17, and only there can it decide
-// otherwise than the divided one.  Below 2^-100 the reciprocal could leave
-// float32's range, and the group is divided throughout.
+// One pass: 8 lanes (4 of a group of 32) hold a group, 8 values each or two times 8.
+// As much bound by instructions as by memory, so a code costs six: the quotient
+// x * (1 / s) plus 1.5 * 2^23 + z in one rounding is the code in the low bits, after a
+// clamp; its distance from x * (1 / s) tells a quotient next to a tie.  Only within 2^-16
+// of one can the product, off by less than |x / s| (2^-23 + 2^-24) < 24 * 1.5 * 2^-23 <
+// 2^-17 (rcp: 1 ulp), decide otherwise than the divided one, and the lane then divides.
+// Below 2^-100 the reciprocal could leave float32's range, and the group is divided
+// throughout.
 template <int DT>
 struct I4Piece {
   u32x4 w[DT == 0 ? 2 : 1];
@@ -32,32 +35,40 @@ struct I4Piece {
   }
 };
 
-// over the L (4, 8 or 16) lanes of a group
+// over the L (4 or 8) lanes of a group
 template <int L>
 __device__ __forceinline__ float i4_max(float v) {
   v = __builtin_elementwise_maximum(v, __uint_as_float(dpp_u32<kDppXor1>(__float_as_uint(v))));
   v = __builtin_elementwise_maximum(v, __uint_as_float(dpp_u32<kDppXor2>(__float_as_uint(v))));
   if constexpr (L >= 8) v = __builtin_elementwise_maximum(v, __uint_as_float(dpp_u32<kDppHalfMirror>(__float_as_uint(v))));
-  if constexpr (L >= 16) v = __builtin_elementwise_maximum(v, __uint_as_float(dpp_u32<kDppMirror>(__float_as_uint(v))));
   return v;
 }
+
+constexpr int i4_pieces(int group) { return group == 128 ? 2 : 1; }       // of 8 values a lane
 
 template <int DT, int GROUP, bool ZEROS, bool SF16>
 __global__ __launch_bounds__(256) void k_int4_quantize(const void* __restrict__ x, int64_t pieces, uint32_t* __restrict__ codes,
                                                        uint16_t* __restrict__ scales, uint8_t* __restrict__ zeros) {
-  constexpr int L = GROUP / 8;
+  constexpr int P = i4_pieces(GROUP), L = GROUP / 8 / P;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= pieces) return;                  // whole groups
-  I4Piece<DT> v;
-  const u32x4* src = static_cast<const u32x4*>(x) + i * (DT == 0 ? 2 : 1);
-  v.w[0] = __builtin_nontemporal_load(src);
-  if constexpr (DT == 0) v.w[1] = __builtin_nontemporal_load(src + 1);
+  if (i * P >= pieces) return;              // whole groups
+  const int64_t i0 = P == 1 ? i : i / L * (P * L) + i % L;  // the lane's pieces are L apart
+  I4Piece<DT> v[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const u32x4* src = static_cast<const u32x4*>(x) + (i0 + p * L) * (DT == 0 ? 2 : 1);
+    v[p].w[0] = __builtin_nontemporal_load(src);
+    if constexpr (DT == 0) v[p].w[1] = __builtin_nontemporal_load(src + 1);
+  }
   float hi = 0.0f, lo = 0.0f;               // lo: of -x
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float a = v.at(k);
-    hi = __builtin_elementwise_maximum(hi, ZEROS ? a : fabsf(a));
-    if constexpr (ZEROS) lo = __builtin_elementwise_maximum(lo, -a);
+  for (int p = 0; p < P; ++p) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float a = v[p].at(k);
+      hi = __builtin_elementwise_maximum(hi, ZEROS ? a : fabsf(a));
+      if constexpr (ZEROS) lo = __builtin_elementwise_maximum(lo, -a);
+    }
   }
   hi = i4_max<L>(hi);
   if constexpr (ZEROS) lo = i4_max<L>(lo);
@@ -82,26 +93,44 @@ __global__ __launch_bounds__(256) void k_int4_quantize(const void* __restrict__ 
     s = 1.0f;
     bits = SF16 ? 0x7E00 : 0x7FC0;
   }
-  const bool fast = s > 0x1p-100f;
-  const float inv = 1.0f / s;
-  const float z = ZEROS ? fminf(rintf(lo / s), 15.0f) : 8.0f;
-  float r[8];
-  bool tie = !fast;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float t = v.at(k) * inv;
-    r[k] = rintf(t);
-    tie |= fabsf(t - r[k]) > 0.5f - 0x1p-14f;
+  constexpr float kBase = 0x1.8p23f;
+  constexpr float kTie = 0.5f - 0x1p-16f;
+  const float inv = __builtin_amdgcn_rcpf(s);
+  float z = 8.0f;
+  float off = 0.0f;                         // the largest distance of a quotient from its rounding
+  if constexpr (ZEROS) {
+    const float t = lo * inv;
+    z = rintf(t);
+    off = fabsf(t - z);
+    z = fminf(z, 15.0f);
   }
-  if (tie) {
+  const float base = kBase + z;
+  float q[P][8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) r[k] = rintf(v.at(k) / s);
+  for (int p = 0; p < P; ++p) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      q[p][k] = fmaf(v[p].at(k), inv, base);
+      off = fmaxf(off, fabsf(fmaf(v[p].at(k), inv, base - q[p][k])));
+    }
   }
-  uint32_t w = 0;
+  if (off > kTie || s <= 0x1p-100f) {
+    if constexpr (ZEROS) z = fminf(rintf(lo / s), 15.0f);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) w |= static_cast<uint32_t>(fminf(fmaxf(r[k] + z, 0.0f), 15.0f)) << (4 * k);
-  if (!finite) w = ZEROS ? 0u : 0x88888888u;
-  codes[i] = w;
+    for (int p = 0; p < P; ++p) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) q[p][k] = rintf(v[p].at(k) / s) + (kBase + z);
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    // kBase's own bits, shifted with the codes, reach bit 31 by the third code
+    uint32_t w = 0u - (0x4B400000u + (0x4B400000u << 4) + (0x4B400000u << 8));
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w += __float_as_uint(__builtin_amdgcn_fmed3f(q[p][k], kBase, kBase + 15.0f)) << (4 * k);
+    if (!finite) w = ZEROS ? 0u : 0x88888888u;
+    codes[i0 + p * L] = w;
+  }
   if (threadIdx.x % L == 0) {
     scales[i / L] = bits;
     if constexpr (ZEROS) zeros[i / L] = finite ? static_cast<uint8_t>(z) : 0;
@@ -137,7 +166,8 @@ template <int DT, int GROUP, bool ZEROS, bool SF16>
 static hipError_t i4_quantize(const void* x, int64_t pieces, uint32_t* codes, uint16_t* scales, uint8_t* zeros, hipStream_t stream) {
   for (int64_t i = 0; i < pieces; i += kI4Most) {
     const int64_t n = pieces - i < kI4Most ? pieces - i : kI4Most;
-    hipLaunchKernelGGL((k_int4_quantize<DT, GROUP, ZEROS, SF16>), dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream,
+    constexpr int per = 256 * i4_pieces(GROUP);
+    hipLaunchKernelGGL((k_int4_quantize<DT, GROUP, ZEROS, SF16>), dim3(static_cast<unsigned>((n + per - 1) / per)), dim3(256), 0, stream,
                        static_cast<const uint8_t*>(x) + i * (DT == 0 ? 32 : 16), n, codes + i, scales + i / (GROUP / 8),
                        ZEROS ? zeros + i / (GROUP / 8) : nullptr);
     const hipError_t err = hipGetLastError();
