@@ -353,11 +353,14 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
   auto products = [&](const u32x4 (&xp)[RT][4], int b, const uint32_t (&sq)[SW][4], const uint32_t (&zq)[ZW][4])
       __attribute__((always_inline)) {
     float4v off[RT][GS];
+    auto offset = [&](int m) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
+      for (int i = 0; i < RT; ++i)
         off[i][m / MS] = TT::mfma(xp[i][m], fixed, m % MS ? off[i][m / MS] : float4v{0, 0, 0, 0});
+    };
+    if constexpr (RT == 1)                   // for four row tiles a group at a time: registers
+#pragma unroll
+      for (int m = 0; m < 4; ++m) offset(m);
     u32x4 c[CT];
 #pragma unroll
     for (int j = 0; j < CT; ++j) {
@@ -367,6 +370,9 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
     // the tiles' products in turn: neighbouring ones do not wait for each other
 #pragma unroll
     for (int g = 0; g < GS; ++g) {
+      if constexpr (RT > 1)
+#pragma unroll
+        for (int m = 0; m < MS; ++m) offset(g * MS + m);
       float4v d[RT][CT];
 #pragma unroll
       for (int m = 0; m < MS; ++m)
@@ -459,7 +465,8 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) red[wk][wc][16 * i + 4 * lg + u][16 * j + lr] = acc[i][j][u];
   };
-  const int pieces = gated ? CT : 2 * CT;                   // of 8 columns, of a wave's columns
+  constexpr int kLog = CT == 4 ? 2 : CT == 2 ? 1 : 0;
+  const int pieces = kLog + (gated ? 0 : 1);                // log2: of 8 columns, of a wave's columns
   clear();
 
   // column groups of the wave: one, or (short reductions) `rounds` of them
@@ -474,6 +481,17 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
 #pragma unroll
       for (int m = 0; m < 4; ++m) xv[b][i][m] = u32x4{0, 0, 0, 0};
   columns((it0 * WC + wc) * CT * cols);
+  // the wave's next columns; whole ones lie alike
+  auto advance = [&](int it) __attribute__((always_inline)) {
+    const int c1 = (it + 1) * WC * CT * cols, step = WC * CT * cols;
+    if (c1 <= width) {
+      qb += static_cast<int64_t>(step) * (K / 2);
+      sb += static_cast<int64_t>(step) * groups * 2;
+      if constexpr (ZEROS) zb += static_cast<int64_t>(step) * groups;
+    } else {
+      columns((it * WC + wc) * CT * cols);
+    }
+  };
   if (first < last) load_codes(f[0], first);
   __builtin_amdgcn_sched_barrier(0);         // the codes first: x may hang on the rows' indices
   // places past the chunk's rows hold zeros or the first row again: nothing of theirs is written
@@ -514,7 +532,7 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
         if (t + AHEAD * BS < last) {
           load_codes(f[d], t + AHEAD * BS);
         } else if (LOOP && it + 1 < it1) {
-          columns(((it + 1) * WC + wc) * CT * cols);
+          advance(it + 1);
           load_codes(f[d], first);
           if (!one) load_x(first);
         }
@@ -529,15 +547,15 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      for (int o = lane; o < pieces * rows; o += 64) result(o / pieces, wc, o % pieces, c0);
+      for (int o = lane; o < rows << pieces; o += 64) result(o >> pieces, wc, o & ((1 << pieces) - 1), c0);
       clear();
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
     } else {
       __syncthreads();
-      for (int o = threadIdx.x; o < WC * pieces * rows; o += 64 * WK * WC) {
-        const int w = o / pieces % WC;
-        result(o / (pieces * WC), w, o % pieces, (it * WC + w) * CT * cols);
+      for (int o = threadIdx.x; o < WC * rows << pieces; o += 64 * WK * WC) {
+        const int w = (o >> pieces) % WC;
+        result((o >> pieces) / WC, w, o & ((1 << pieces) - 1), (it * WC + w) * CT * cols);
       }
     }
   }
