@@ -85,16 +85,19 @@ constexpr int kI4Step = 128;               // codes of a weight row per wave and
 struct Int4Shape {
   int rt, ct, wk, wc, bs, ahead;
 };
-constexpr Int4Shape kI4Shapes[] = {{1, 2, 8, 1, 2, 3}, {1, 4, 4, 1, 2, 1}, {1, 4, 1, 4, 2, 1}, {4, 2, 4, 1, 1, 1}, {1, 1, 8, 1, 2, 3}};
+constexpr Int4Shape kI4Shapes[] = {{1, 2, 8, 1, 2, 3}, {1, 4, 4, 1, 2, 1}, {1, 4, 1, 4, 2, 1}, {2, 2, 1, 4, 2, 1}, {1, 1, 8, 1, 2, 3}};
 
 static inline int i4_tiles(const Int4Shape& s, int N, int gated) {
   const int width = gated ? N / 2 : N, per = (gated ? 8 : 16) * s.ct * s.wc;
   return (width + per - 1) / per;
 }
-// Which of them, by rows of one expert (the hint, or what m_total gives each expert
-// that can have any), the length of the reduction, and tasks:
-//   3  more than 16 rows
+// Which of them, by the length of the reduction, rows of one expert (the hint, or what
+// m_total gives each expert that can have any) and tasks.
 //   2  reductions of up to 512: a wave's own, over several column groups
+//   3  and two row tiles a wave above 16 rows (256 experts, 256 -> 6144: 32 rows 75 us
+//      against 101, 128 rows 255 against 403); longer reductions stay with 16 rows a
+//      workgroup, and the chunks of an expert read its weights at about the same time,
+//      from L2 (6144 -> 2 x 256, 64 rows: 359 us; two row tiles 444, four 433)
 //   1  four tiles a wave from a workgroup a CU on (64 tokens, 6144 -> 2 x 256: 80 us
 //      against 120 in shape 0; 8 tokens 27 against 37)
 //   0  else, twice the waves for the same columns (2 tokens: 17 us against 19; dense
@@ -103,8 +106,7 @@ static inline int i4_tiles(const Int4Shape& s, int N, int gated) {
 static inline int i4_choice(int E, int N, int K, int64_t m_total, int64_t hint, int gated) {
   const int64_t experts = E < m_total ? E : m_total;
   const int64_t share = experts ? (m_total + experts - 1) / experts : 0;
-  if ((hint > share ? hint : share) > 16) return 3;
-  if (K <= 512) return 2;
+  if (K <= 512) return (hint > share ? hint : share) > 16 ? 3 : 2;
   if (experts * i4_tiles(kI4Shapes[1], N, gated) >= 256) return 1;
   return experts * i4_tiles(kI4Shapes[0], N, gated) >= 256 ? 0 : 4;
 }
@@ -349,6 +351,7 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
           }
     }
   };
+  constexpr bool EARLY = RT == 1;            // x is asked for a block ahead, registers allowing
   float4v acc[RT][CT];
   auto products = [&](const u32x4 (&xp)[RT][4], int b, const uint32_t (&sq)[SW][4], const uint32_t (&zq)[ZW][4])
       __attribute__((always_inline)) {
@@ -358,7 +361,7 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
       for (int i = 0; i < RT; ++i)
         off[i][m / MS] = TT::mfma(xp[i][m], fixed, m % MS ? off[i][m / MS] : float4v{0, 0, 0, 0});
     };
-    if constexpr (RT == 1)                   // for four row tiles a group at a time: registers
+    if constexpr (RT == 1)                   // for two row tiles a group at a time: registers
 #pragma unroll
       for (int m = 0; m < 4; ++m) offset(m);
     u32x4 c[CT];
@@ -504,7 +507,7 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
     }
     x[i] = static_cast<const uint8_t*>(p.a) + static_cast<int64_t>(r) * K * 2 + (TR ? 16 : 64) * lg;
   }
-  if (first < last) load_x(first);
+  if (EARLY && first < last) load_x(first);
 #pragma unroll
   for (int d = 1; d < AHEAD; ++d)
     if (first + d * BS < last) load_codes(f[d], first + d * BS);
@@ -520,6 +523,7 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
         uint32_t sq[SW][4], zq[ZW][4];
         unpack(f[d], sq, zq);
         if (!one || it == it0) {
+          if constexpr (!EARLY) load_x(t);
 #pragma unroll
           for (int b = 0; b < BS; ++b)
 #pragma unroll
@@ -528,13 +532,13 @@ void k_int4_gemv(const Int4Params p, int gated, int out32) {
               for (int m = 0; m < 4; ++m) xp[b][i][m] = i4_pairs(xv[b][i][m]);
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (t + BS < last) load_x(t + BS);
+        if (EARLY && t + BS < last) load_x(t + BS);
         if (t + AHEAD * BS < last) {
           load_codes(f[d], t + AHEAD * BS);
         } else if (LOOP && it + 1 < it1) {
           advance(it + 1);
           load_codes(f[d], first);
-          if (!one) load_x(first);
+          if (EARLY && !one) load_x(first);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll

@@ -661,9 +661,9 @@ int int4_dequantize(const uint8_t* codes, const void* scales, const uint8_t* zer
  * order.  Any N (gated: even); K % group == 0; E <= 4096; zeros entries above 15
  * count as they are.  Activations finite (a row with an infinity or a NaN gives
  * NaNs in its own results only).  Any number of rows gives the product; from some
- * 64 rows an expert int4_dequantize and the 16-bit products are faster.  Size limits
- * (NVFP4MOE_ERR_UNSUPPORTED beyond them) as there, and fewer than 2^32 threads in
- * all. */
+ * 160 rows an expert int4_dequantize and the 16-bit products are faster.  Size limits
+ * (NVFP4MOE_ERR_UNSUPPORTED beyond them) as there, fewer than 2^32 threads in all,
+ * and gated (N/2 + 64) * (K/2) < 2^32 - 64. */
 typedef struct nvfp4moe_int4_gemv_args {
   const void* a;              /* [a_rows_total, K], 16-byte aligned */
   int32_t dtype;              /* NVFP4MOE_BF16 or NVFP4MOE_F16: of a, b_scales and 16-bit results */

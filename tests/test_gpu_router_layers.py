@@ -35,7 +35,7 @@ def test_int4_layer(T):
     w = quantize_expert_weights_int4(w_gu, w_dn, 64, T % 2 == 1)
     router = _router(E)
     layer = INT4MoELayer(T, H, I, E, k, DEV, router)
-    assert layer.wide == (T * k > 64 * E)
+    assert layer.wide == (T * k > layer.most_rows * E)
     out = layer.forward(logits, x, w).double().cpu().numpy()
     ids, wt, _, _ = R.route(logits.cpu().numpy(), k, "sigmoid", router.bias.cpu().numpy(), 4, 2, 2, True, 2.5)
     vals = [Q.dequantize(q.codes.cpu().numpy(), q.scales.float().cpu().numpy(), None if q.zeros is None else q.zeros.cpu().numpy(), 64)
