@@ -1319,8 +1319,8 @@ def moe_unpermute_combine_backward(dout, y, perm_of_assignment, topk_w, *, need_
                                    dy=None, d_topk_w=None, stream=None):
     """Gradients of moe_unpermute_combine from dout [T, H]: (dy [rows, H] in y's
     type, d_topk_w float32 [T, k]); None where not needed.  topk_w float32 [T, k];
-    perm_of_assignment as in the forward call (None: row t*k + j), its entries all
-    different.  Rows of a new dy that no entry names are zero."""
+    perm_of_assignment as in the forward call (None: row t*k + j), its entries in
+    [0, rows) and all different.  Rows of a new dy that no entry names are zero."""
     import torch
     if dout.dim() != 2 or y.dim() != 2 or topk_w.dim() != 2:
         raise ValueError("dout must be [T, H], y [rows, H] and topk_w [T, k]")
