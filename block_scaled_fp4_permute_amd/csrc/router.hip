@@ -471,12 +471,12 @@ __device__ __forceinline__ void rt_sort(uint32_t (&v)[N]) {
 // clearly smaller: 1 instruction a key and round in place of 4 for a search through
 // all.
 //
-// Errors: a sigmoid from v_exp_f32 and v_rcp_f32 is off by at most 2^-22 (s (1 - s)
-// (|x| + 2) 2^-24 + 3 s 2^-24), a softmax by p (|x - max| + 30) 2^-24 (sums of 16 and
-// over 6 levels, exp, quotient), which is below 2^-18 max p (|x - max| p <= 0.37 max
-// p); the bias adds 2^-24 |key|, the lost bits |key| 2^-19 for 16 places.  Two keys
-// within twice that, tol + |key| 2^-18, are not settled; group values, of keys with
-// all their bits, within 2 tol + |value| 2^-22.
+// Errors, in steps of 2^-24: a sigmoid from v_exp_f32 and v_rcp_f32 (1 ulp each) is off
+// by s (1 - s) (|x| + 2) + 3 s < 3.2, a softmax by p (|x - max| + 35) (exp; sums of 16
+// and over 6 levels; quotient), which is below 36 max p as |x - max| p <= 0.37 max p; the
+// bias adds |key|, the lost bits |key| 2^5 for 16 places.  So two keys further apart than
+// tol + |key| 2^-18, tol 8 steps or 128 max p, are in order, and so are group values, of
+// up to two keys with all their bits, further apart than 2 tol + |value| 2^-22.
 template <int LPT, int NE>
 __device__ __forceinline__ int choose_fast(const ScoredParams& p, const float (&x)[NE], const float (&bias)[NE], float top, float z,
                                            float* lds, int* list, bool& order, bool& near) {
@@ -506,7 +506,7 @@ __device__ __forceinline__ int choose_fast(const ScoredParams& p, const float (&
   }
   near = odd != 0.0f;                        // NaN
   const float none = -__builtin_huge_valf();
-  const float tol = p.softmax ? big * 0x1p-16f : 0x1p-20f;
+  const float tol = p.softmax ? big * 0x1p-17f : 0x1p-21f;
   uint32_t keep = ~0u;
   if (p.n_group > 1)
     keep = scored_groups<LPT, NE>(p, [&](int c) __attribute__((always_inline)) { return full || e0 + c < p.E ? key[c] : none; },
@@ -760,7 +760,7 @@ __global__ __launch_bounds__(256) void k_route_scored_grad(const ScoredGradParam
   if (p.d_scores) {
     rt_load_row<0, NE>(p.d_scores, static_cast<size_t>(t) * p.d_scores_ld, e0, p.E, p.vec_d, q);
 #pragma unroll
-    for (int c = 0; c < NE; ++c) q[c] = e0 + c < p.E ? q[c] : 0.0f;
+    for (int c = 0; c < NE; ++c) q[c] = rt_open(x[c]) ? q[c] : 0.0f;     // a closed score is 0 whatever the logits
   } else {
 #pragma unroll
     for (int c = 0; c < NE; ++c) q[c] = 0.0f;

@@ -174,6 +174,31 @@ def test_gradient_of_foreign_ids(kind, renormalize):
     assert (np.abs(got - want) <= tol).all()
 
 
+@pytest.mark.parametrize("E", [24, 256])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+def test_gradients_at_closed_experts_are_not_read(E, kind, renormalize, bad):
+    """What the scores of closed logits and the weights of closed choices get is nothing, NaN and
+    infinities too; the row's other gradients stay."""
+    r = np.random.default_rng(E)
+    T, k = 40, 6
+    l = r.standard_normal((T, E)).astype(np.float32)
+    l[:, 1::3] = -INF
+    l[::2, 0] = NAN
+    l[5, 4:] = -INF                             # fewer open ones than k: closed ones are chosen
+    l[6] = -INF
+    c = (T, E, k, kind, False, (1, 1, 1), renormalize, "f32")
+    ids, w, s, o = _want(l.astype(np.float64), c, None)
+    dw, ds = r.standard_normal((T, k)).astype(np.float32), r.standard_normal((T, E)).astype(np.float32)
+    want, tol = R.route_grad(dw, l, ids, o, kind, renormalize, 2.5, ds)
+    ds[~o] = bad
+    dw[~o[np.arange(T)[:, None], ids]] = bad
+    got = m.moe_route_scored_backward(up(dw), up(l), up(ids), score=KIND[kind], renormalize=renormalize, scale=2.5, d_scores=up(ds))
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert (err <= tol).all()
+
+
 def test_default_is_the_plain_softmax_router():
     l = torch.randn((300, 96), device=DEV)
     a, b = m.moe_route_scored(l, 7), m.moe_route_permute(l, 7)
