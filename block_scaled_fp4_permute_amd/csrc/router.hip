@@ -329,16 +329,15 @@ __device__ __forceinline__ double scores64(const ScoredParams& p, size_t row, in
   return z;
 }
 
-// The choice by float64 keys, one token on the whole wave: k rounds of the best that is
-// left, ties to the lower id.  Lane l holds experts l, l + 64, ... in LDS (E + 2 n_group
-// doubles of the wave's own).  Lanes meet on the float32 roundings of their best (rounding
-// keeps the order), and only a tie there looks at the float64 keys and ids.  list[j] gets
-// the j-th, with bit 30 set if it is open.
+// Float64 keys of one token by the whole wave, expert e at lds[rt_at(p, e)] (E + 2 n_group
+// doubles of the wave's own; closed experts kClosed).  Returns a bit for each group that
+// stays.
+__device__ __forceinline__ int rt_at(const ScoredParams& p, int e) { return p.n_group > 1 ? e + e / (p.E / p.n_group) : e; }
 template <int DT>
-__device__ __forceinline__ void choose_exact(const ScoredParams& p, int t, double* lds, int* list) {
+__device__ __forceinline__ uint64_t exact_groups(const ScoredParams& p, int t, double* lds) {
   const int l = threadIdx.x & 63;
   const size_t row = static_cast<size_t>(t) * p.E;
-  const int gs = p.n_group > 1 ? p.E / p.n_group : p.E;
+  const int gs = p.E / p.n_group;
   double top = 0.0;
   if (p.softmax) {
     float m = -__builtin_huge_valf();
@@ -349,52 +348,62 @@ __device__ __forceinline__ void choose_exact(const ScoredParams& p, int t, doubl
     m = seg_max<64>(m);
     top = rt_open(m) ? m : 0.0f;
   }
-  auto at = [&](int e) __attribute__((always_inline)) { return e + (p.n_group > 1 ? e / gs : 0); };
   if (p.bias || p.n_group > 1) {
     scores64<64, DT>(p, row, l, top, [&](int i, const float (&x)[4], const double (&s)[4]) __attribute__((always_inline)) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         if (i + c >= p.E) break;
         const double v = s[c] + (p.bias ? static_cast<double>(p.bias[i + c]) : 0.0);
-        lds[at(i + c)] = rt_open(x[c]) && v > kNone ? v : kClosed;
+        lds[rt_at(p, i + c)] = rt_open(x[c]) && v > kNone ? v : kClosed;
       }
     });
   }
   rt_lds_step();
+  if (p.n_group == 1) return ~0ull;
   double* const val = lds + p.E + p.n_group;
-  if (p.n_group > 1) {
-    // the lanes of a group (a power of two) take its keys in turn and join theirs
-    int parts = 1;
-    while (2 * parts * p.n_group <= 64) parts *= 2;
-    const int g = l / parts;
-    double a1 = kNone, a2 = kNone;
-    auto add = [&](double b1, double b2) __attribute__((always_inline)) {
-      a2 = fmax(fmin(a1, b1), fmax(a2, b2));
-      a1 = fmax(a1, b1);
-    };
-    for (int i = l % parts; i < gs; i += parts) {
-      const double k = g < p.n_group ? lds[g * (gs + 1) + i] : kNone;
-      add(k > kClosed ? k : kNone, kNone);
-    }
-    for (int d = 1; d < parts; d *= 2) {
-      const double b1 = __shfl_xor(a1, d), b2 = __shfl_xor(a2, d);
-      add(b1, b2);
-    }
-    if (g < p.n_group && l % parts == 0) val[g] = p.group_top == 2 && a2 > kNone ? a1 + a2 : a1;
-    rt_lds_step();
-    for (int g = l; g < p.n_group; g += 64) {
-      int rank = 0;
-      for (int h = 0; h < p.n_group; ++h) rank += val[h] > val[g] || (val[h] == val[g] && h < g) ? 1 : 0;
-      lds[g * (gs + 1) + gs] = rank < p.topk_group ? 1.0 : 0.0;
-    }
-    rt_lds_step();
+  // the lanes of a group (a power of two) take its keys in turn and join theirs
+  int parts = 1;
+  while (2 * parts * p.n_group <= 64) parts *= 2;
+  const int g = l / parts;
+  double a1 = kNone, a2 = kNone;
+  auto add = [&](double b1, double b2) __attribute__((always_inline)) {
+    a2 = fmax(fmin(a1, b1), fmax(a2, b2));
+    a1 = fmax(a1, b1);
+  };
+  for (int i = l % parts; i < gs; i += parts) {
+    const double k = g < p.n_group ? lds[g * (gs + 1) + i] : kNone;
+    add(k > kClosed ? k : kNone, kNone);
   }
+  for (int d = 1; d < parts; d *= 2) {
+    const double b1 = __shfl_xor(a1, d), b2 = __shfl_xor(a2, d);
+    add(b1, b2);
+  }
+  if (g < p.n_group && l % parts == 0) val[g] = p.group_top == 2 && a2 > kNone ? a1 + a2 : a1;
+  rt_lds_step();
+  const double mine = val[l < p.n_group ? l : 0];
+  int rank = 0;
+  for (int h = 0; h < p.n_group; ++h) rank += val[h] > mine || (val[h] == mine && h < l) ? 1 : 0;
+  rt_lds_step();                            // the same words are written again
+  return __ballot(l < p.n_group && rank < p.topk_group);
+}
+
+// The choice by float64 keys, one token on the whole wave: k rounds of the best that is
+// left, ties to the lower id.  Lane l holds experts l, l + 64, ... in LDS.  Lanes meet on
+// the float32 roundings of their best (rounding keeps the order), and only a tie there
+// looks at the float64 keys and ids.  list[j] gets the j-th, with bit 30 set if it is open.
+template <int DT>
+__device__ __forceinline__ void choose_exact(const ScoredParams& p, int t, double* lds, int* list) {
+  const int l = threadIdx.x & 63;
+  const size_t row = static_cast<size_t>(t) * p.E;
+  const int gs = p.E / p.n_group;
+  const uint64_t stay = exact_groups<DT>(p, t, lds);
   for (int i = l; i < p.E; i += 64) {
+    double* const k = lds + rt_at(p, i);
     if (!p.bias) {
       const float x = rt_load<DT>(p.logits, row + i);
-      lds[at(i)] = rt_open(x) ? static_cast<double>(rt_finite(x)) : kClosed;
+      *k = rt_open(x) ? static_cast<double>(rt_finite(x)) : kClosed;
     }
-    if (p.n_group > 1 && lds[(i / gs) * (gs + 1) + gs] == 0.0) lds[at(i)] = kNone;
+    if (p.n_group > 1 && !((stay >> (i / gs)) & 1)) *k = kNone;
   }
   rt_lds_step();
   double best = kNone;
@@ -403,7 +412,7 @@ __device__ __forceinline__ void choose_exact(const ScoredParams& p, int t, doubl
     best = kNone;
     id = 0x7fffffff;
     for (int i = l; i < p.E; i += 64) {
-      const double k = lds[at(i)];
+      const double k = lds[rt_at(p, i)];
       if (k > best) {
         best = k;
         id = i;
@@ -425,7 +434,7 @@ __device__ __forceinline__ void choose_exact(const ScoredParams& p, int t, doubl
     const int w = __builtin_ctzll(who);
     if (l == w) {
       list[j] = id | (best > kClosed ? 1 << 30 : 0);
-      lds[at(id)] = kNone;
+      lds[rt_at(p, id)] = kNone;
       scan();
     }
   }
@@ -477,9 +486,9 @@ __device__ __forceinline__ void rt_sort(uint32_t (&v)[N]) {
 // bias adds |key|, the lost bits |key| 2^5 for 16 places.  So two keys further apart than
 // tol + |key| 2^-18, tol 8 steps or 128 max p, are in order, and so are group values, of
 // up to two keys with all their bits, further apart than 2 tol + |value| 2^-22.
-template <int LPT, int NE>
-__device__ __forceinline__ int choose_fast(const ScoredParams& p, const float (&x)[NE], const float (&bias)[NE], float top, float z,
-                                           float* lds, int* list, bool& order, bool& near) {
+template <int LPT, int NE, int DT>
+__device__ __forceinline__ int choose_fast(const ScoredParams& p, int t, const float (&x)[NE], const float (&bias)[NE], float top,
+                                           float z, double* lds, int* list, bool& order, bool& near) {
   constexpr uint32_t LOW = NE <= 4 ? 3 : 15;
   static_assert(NE <= 16, "the place takes 4 bits");
   const int l = threadIdx.x & (LPT - 1);
@@ -504,13 +513,27 @@ __device__ __forceinline__ int choose_fast(const ScoredParams& p, const float (&
       }
     }
   }
-  near = odd != 0.0f;                        // NaN
+  near = seg_ballot<LPT>(!(odd == 0.0f)) != 0;               // NaN
   const float none = -__builtin_huge_valf();
   const float tol = p.softmax ? big * 0x1p-17f : 0x1p-21f;
   uint32_t keep = ~0u;
-  if (p.n_group > 1)
+  if (p.n_group > 1) {
+    const int base = (threadIdx.x & 63) & ~(LPT - 1);
+    bool close = false;
     keep = scored_groups<LPT, NE>(p, [&](int c) __attribute__((always_inline)) { return full || e0 + c < p.E ? key[c] : none; },
-                                  2.0f * tol, lds, near);
+                                  2.0f * tol, reinterpret_cast<float*>(lds) + base / LPT * (p.E + 2 * p.n_group), close);
+    close = seg_ballot<LPT>(close) != 0 && !near;
+    // such tokens of the wave one after the other, on all its lanes
+    for (uint64_t rest = __ballot(close && l == 0); rest; rest &= rest - 1) {
+      const int at = __builtin_ctzll(rest);
+      const uint64_t stay = exact_groups<DT>(p, __builtin_amdgcn_readlane(t, at), lds);
+      if (base != at) continue;
+      keep = 0;
+      const int gs = p.E / p.n_group;
+#pragma unroll 1
+      for (int c = 0; c < NE; ++c) keep |= e0 + c < p.E && ((stay >> ((e0 + c) / gs)) & 1) ? 1u << c : 0u;
+    }
+  }
   if (!full) keep &= e0 >= p.E ? 0u : p.E - e0 >= 32 ? ~0u : (1u << (p.E - e0)) - 1;
   // by logits: the keys are exact, and 16-bit ones keep all their bits
   const bool exact = !p.bias && p.narrow;
@@ -526,8 +549,8 @@ __device__ __forceinline__ int choose_fast(const ScoredParams& p, const float (&
   int n = 0;
   bool more = true;
   for (int j = 0; __any(more); ++j) {
-    const uint32_t t = el[0] & ~LOW;
-    const uint32_t m = seg_reduce<LPT>(t, [](uint32_t a, uint32_t b) __attribute__((always_inline)) { return a > b ? a : b; });
+    const uint32_t first = el[0] & ~LOW;
+    const uint32_t m = seg_reduce<LPT>(first, [](uint32_t a, uint32_t b) __attribute__((always_inline)) { return a > b ? a : b; });
     const float v = rt_unorder(m);
     const bool close = !exact && m != 0 && before - v <= (p.bias ? tol : 0.0f) + fabsf(v) * 0x1p-18f;
     before = v;
@@ -538,7 +561,7 @@ __device__ __forceinline__ int choose_fast(const ScoredParams& p, const float (&
     }
     order |= more && close;
     n += more ? 1 : 0;
-    const bool mine = l == __builtin_ctzll(seg_ballot<LPT>(t == m));
+    const bool mine = l == __builtin_ctzll(seg_ballot<LPT>(first == m));
     if (mine && more) list[j] = (e0 + static_cast<int>(LOW - (el[0] & LOW))) | (1 << 30);
 #pragma unroll
     for (int c = 0; c < NE - 1; ++c) el[c] = mine ? el[c + 1] : el[c];
@@ -581,8 +604,7 @@ __device__ __forceinline__ int scored_token(const ScoredParams& p, int t, bool l
         zf = zf > 0.0f ? zf : 1.0f;
       }
     }
-    n = choose_fast<LPT, NE>(p, x, bias, static_cast<float>(top), zf,
-                             reinterpret_cast<float*>(lds) + ((threadIdx.x & 63) / LPT) * (p.E + 2 * p.n_group), list, order, near);
+    n = choose_fast<LPT, NE, DT>(p, t, x, bias, static_cast<float>(top), zf, lds, list, order, near);
   } else if (p.softmax) {
     float m = -__builtin_huge_valf();
     for (int i = l; i < p.E; i += LPT) {
