@@ -16,7 +16,8 @@ namespace nvfp4 {
 // NaN, codes 8 (zeros: codes and z 0).
 //
 // One pass: 8 lanes (4 of a group of 32) hold a group, 8 values each or two times 8.
-// As much bound by instructions as by memory, so a code costs six: the quotient
+// As much bound by instructions as by memory (256 x 512 x 6144 in bf16, groups of 128: 382
+// us, 5.3 TB/s; 459 with eleven instructions a code and 8 values a lane), so a code costs six: the quotient
 // x * (1 / s) plus 1.5 * 2^23 + z in one rounding is the code in the low bits, after a
 // clamp; its distance from x * (1 / s) tells a quotient next to a tie.  Only within 2^-16
 // of one can the product, off by less than |x / s| (2^-23 + 2^-24) < 24 * 1.5 * 2^-23 <
@@ -137,6 +138,8 @@ __global__ __launch_bounds__(256) void k_int4_quantize(const void* __restrict__ 
   }
 }
 
+// The inverse, 8 codes a lane: bound by memory (the same weights 387 us, 5.2 TB/s, most of it
+// the values written).  16-bit values are rounded once, from an exact product.
 template <int GROUP, bool ZEROS, bool SF16, bool OUT32>
 __global__ __launch_bounds__(256) void k_int4_dequantize(const uint32_t* __restrict__ codes, const uint16_t* __restrict__ scales,
                                                          const uint8_t* __restrict__ zeros, int64_t pieces, void* __restrict__ out) {

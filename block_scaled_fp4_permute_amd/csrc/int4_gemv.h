@@ -20,6 +20,9 @@
 // swaps each of 32 and 16 lanes), so that one matrix instruction takes 32
 // neighbouring codes, of one group.  Within 8 codes the pairs are (i, i + 4), as
 // the shifts give them; x is permuted alike.
+//
+// Reached: 256 experts, 2 rows each, 6144 -> 2 x 256 (417 MB) 67 to 73 us, 5.7 to 6.2
+// TB/s; 8 rows each, 256 -> 6144 (240 MB) 55 to 58, 4.2; one token (13 MB) 9.
 #pragma once
 
 #include <type_traits>
@@ -93,16 +96,18 @@ static inline int i4_tiles(const Int4Shape& s, int N, int gated) {
 }
 // Which of them, by the length of the reduction, rows of one expert (the hint, or what
 // m_total gives each expert that can have any) and tasks.
-//   2  reductions of up to 512: a wave's own, over several column groups
+//   2  reductions of up to 512: a wave's own, over several column groups (256 experts, 8
+//      rows, 256 -> 6144: 54 us; 217 in shape 1)
 //   3  and two row tiles a wave above 16 rows (256 experts, 256 -> 6144: 32 rows 75 us
 //      against 101, 128 rows 255 against 403); longer reductions stay with 16 rows a
 //      workgroup, and the chunks of an expert read its weights at about the same time,
 //      from L2 (6144 -> 2 x 256, 64 rows: 359 us; two row tiles 444, four 433)
-//   1  four tiles a wave from a workgroup a CU on (64 tokens, 6144 -> 2 x 256: 80 us
-//      against 120 in shape 0; 8 tokens 27 against 37)
-//   0  else, twice the waves for the same columns (2 tokens: 17 us against 19; dense
-//      8192 x 8192, 3 rows: 20 against 27)
-//   4  and one tile a wave where even those leave CUs without a workgroup
+//   1  four tiles a wave from a workgroup a CU on (64 tokens, 6144 -> 2 x 256: 67 us
+//      against 128 in shape 0; 4 tokens 15 against 21)
+//   0  else, twice the waves for the same columns (2 tokens: 12 us against 15; dense
+//      8192 x 8192, 3 rows: 16 against 22)
+//   4  and one tile a wave where even those leave CUs without a workgroup (one token:
+//      9.3 us against 10.6; 2 tokens 16.0 against 11.8)
 static inline int i4_choice(int E, int N, int K, int64_t m_total, int64_t hint, int gated) {
   const int64_t experts = E < m_total ? E : m_total;
   const int64_t share = experts ? (m_total + experts - 1) / experts : 0;
@@ -111,7 +116,8 @@ static inline int i4_choice(int E, int N, int K, int64_t m_total, int64_t hint, 
   return experts * i4_tiles(kI4Shapes[0], N, gated) >= 256 ? 0 : 4;
 }
 // Column groups of a wave, one after the other (short reductions): some 2048
-// workgroups (256 experts, 8 rows, 256 -> 6144: 63 us; 70 with 1024 of them, 80 with 8192)
+// workgroups (256 experts, 8 rows, 256 -> 6144, before other steps: 63 us; 70 with 1024 of
+// them, 80 with 8192)
 static inline int i4_rounds(const Int4Shape& s, int E, int N, int64_t m_total, int gated) {
   if (s.wk > 1) return 1;
   const int64_t chunks = m_total / (16 * s.rt) + (E < m_total ? E : m_total);

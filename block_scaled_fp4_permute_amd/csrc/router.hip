@@ -12,13 +12,19 @@
 // Everything that decides a choice is float64: keys that differ by less than a
 // float32 step are ordered as the definition orders them, and results do not
 // depend on how a float32 exponential rounds.  The kernels choose by float32 keys
-// first, and take float64 ones for every expert only where two values that matter
-// lie within the float32 keys' error of each other.  A launch finds its code in no
-// instruction cache, and a wave that runs through 12 KB of it once waits some 10 us
-// for its lines: what is rare, or long in float64, is a loop over few instructions.
-// An expert is closed if its logit is
-// -inf or NaN, or its key -inf or NaN; closed ones are taken, by id and with
-// weight 0, only where a token has fewer open ones than it needs.
+// first, and take float64 ones only where two values that matter lie within the
+// float32 keys' error of each other: of the candidates for their order, of one
+// token's experts for its groups, of all of a token's choice where a value is not
+// finite or more than 16 or 32 candidates are that close.
+// Bound by latency up to some 8192 tokens and by instructions beyond (float64 where
+// scores are wanted).  A launch finds its code in no instruction cache, and a wave
+// that runs through 12 KB of it once waits some 10 us for its lines: what is rare, or
+// long in float64, is a loop over few instructions.  Top-8 of 256 in 8 groups with a
+// bias, float32: 256 tokens 7 us, 4096 9, 16384 15 to 17 (read at 4.86 TB/s: 3.5),
+// with scores 27.
+// An expert is closed if its logit is -inf or NaN, or its key -inf or NaN; closed
+// ones are taken, by id and with weight 0, only where a token has fewer open ones
+// than it needs.
 #include "nvfp4_internal.h"
 
 namespace nvfp4 {
@@ -693,7 +699,8 @@ __global__ __launch_bounds__(rt_threads(NE)) void k_route_scored(const ScoredPar
 // ------------------------------------------------------------------ few tokens: routing and permutation in one launch
 // One workgroup: wave w routes tokens w, w + 16, ...; then every assignment counts
 // the earlier ones of its expert (n <= kSmallRows: a walk over LDS), and a scan of
-// the experts' counts places the rows.  Bound by latency: four launches otherwise.
+// the experts' counts places the rows.  Bound by latency: 7.5 us for one token, against
+// 7 + 4 + 3.5 in the three launches of more.
 static constexpr int kSmallRows = 256;
 template <int NE, int DT>
 __global__ __launch_bounds__(1024) void k_route_small(const ScoredParams p, int* __restrict__ counts, int* __restrict__ offsets,
@@ -767,7 +774,8 @@ __global__ __launch_bounds__(1024) void k_route_small(const ScoredParams p, int*
 // the logits then get
 //   sigmoid (1 - s_e) (c_e + s_e q_e),   softmax c_e - s_e sum(c) + s_e (q_e - sum(s q))
 // with q the scores' own gradient.  Nothing is divided by a small score that way.
-// All in float32: one read of logits (and q), one write of the gradient.
+// All in float32: one read of logits (and q), one write of the gradient.  16384 tokens,
+// 256 experts, float32 with q: 14 us for 50 MB (3.6 TB/s); 2051 tokens in bf16 6.
 template <int LPT, int NE, int DT>
 __global__ __launch_bounds__(256) void k_route_scored_grad(const ScoredGradParams p) {
   const int t0 = blockIdx.x * (256 / LPT) + threadIdx.x / LPT;
@@ -914,7 +922,8 @@ __global__ __launch_bounds__(256) void k_route_scored_grad(const ScoredGradParam
 
 // ------------------------------------------------------------------ host side
 // 16 lanes a token where its experts fit 16 registers a lane and there are tokens
-// enough to fill the chip that way: the rounds then serve 4 tokens a wave.
+// enough to fill the chip that way: the rounds then serve 4 tokens a wave (256 tokens
+// 8.4 us against 7.1 on 64 lanes, 2047 9.0 against 9.6).
 static bool rt_narrow(int T, int E, int k) { return E <= 256 && k <= 16 && T >= 2048; }
 
 // lanes of a group if groups end between lanes and a butterfly joins them, else 0 (by way of LDS)

@@ -181,7 +181,8 @@ int moe_route_permute(const float* logits, int32_t T, int32_t E, int32_t k,
  *   weights  the chosen scores u_j, as they are or (renormalize) u_j / sum(u), times
  *            `scale`, rounded to float32 once
  * Scores, keys and weights are float64 up to there, so near-equal keys are ordered
- * as defined.  An expert is closed if its logit is -inf or NaN, or its key -inf or
+ * as defined (values that differ by float64's own rounding, as sums of a group's keys
+ * can, may come in either order).  An expert is closed if its logit is -inf or NaN, or its key -inf or
  * NaN (a bias of -inf takes it out).  Closed experts have score 0 in a softmax,
  * count nothing in their group (a group without an open expert comes last), and
  * are chosen, by ascending id and with weight 0, only where the groups that stay
@@ -659,8 +660,9 @@ int int4_dequantize(const uint8_t* codes, const void* scales, const uint8_t* zer
  * in dtype or float32; gated (N = 2I, rows [0, I) gate): h[p, i] = act(y[p, i]) *
  * y[p, I + i] [m_total, I] in dtype.  Exact products, float32 sums in a fixed
  * order.  Any N (gated: even); K % group == 0; E <= 4096; zeros entries above 15
- * count as they are.  Activations finite (a row with an infinity or a NaN gives
- * NaNs in its own results only).  Any number of rows gives the product; from some
+ * count as they are.  Activations finite, and small enough that 31 sum(|a|) over a
+ * group stays in float32's range (a row with an infinity or a NaN gives NaNs in its
+ * own results only).  Any number of rows gives the product; from some
  * 160 rows an expert int4_dequantize and the 16-bit products are faster.  Size limits
  * (NVFP4MOE_ERR_UNSUPPORTED beyond them) as there, fewer than 2^32 threads in all,
  * and gated (N/2 + 64) * (K/2) < 2^32 - 64. */
