@@ -16,14 +16,18 @@ namespace nvfp4 {
 // NaN, codes 8 (zeros: codes and z 0).
 //
 // One pass: 8 lanes (4 of a group of 32) hold a group, 8 values each or two times 8.
-// As much bound by instructions as by memory (256 x 512 x 6144 in bf16, groups of 128: 382
-// us, 5.3 TB/s; 459 with eleven instructions a code and 8 values a lane), so a code costs six: the quotient
-// x * (1 / s) plus 1.5 * 2^23 + z in one rounding is the code in the low bits, after a
-// clamp; its distance from x * (1 / s) tells a quotient next to a tie.  Only within 2^-16
-// of one can the product, off by less than |x / s| (2^-23 + 2^-24) < 24 * 1.5 * 2^-23 <
-// 2^-17 (rcp: 1 ulp), decide otherwise than the divided one, and the lane then divides.
-// Below 2^-100 the reciprocal could leave float32's range, and the group is divided
-// throughout.
+// Bound by memory where instructions are few (256 x 512 x 6144 in bf16, groups of 128: 308
+// us, 6.6 TB/s; 402 with true divisions wherever x * (1 / s) lands next to a tie, which a
+// group of bf16 values does often enough).  So the divisions share their reciprocal:
+// with y the correctly rounded 1 / s and t = x y, t + (x - t s) y rounds to the quotient.
+//   y: rcp is 1 ulp off, and one Newton step leaves 2^-46; s has at most 11 bits, so 1 / s
+//   is 2^-36 at least from where its rounding changes
+//   quotient: the remainder x - t s is exact, what is left 2^-46 off; a place where the
+//   rounding changes is an odd number M of 25 bits, and x = S M has no solution in 24
+//   bits, so x / s is 2^-36 at least from any
+// Below 2^-100 the remainder could leave float32's range, and the group is divided.  The
+// quotient's rounding to an integer is an addition of 1.5 * 2^23, whose low bits are the
+// code after a clamp.
 template <int DT>
 struct I4Piece {
   u32x4 w[DT == 0 ? 2 : 1];
@@ -95,33 +99,27 @@ __global__ __launch_bounds__(256) void k_int4_quantize(const void* __restrict__ 
     bits = SF16 ? 0x7E00 : 0x7FC0;
   }
   constexpr float kBase = 0x1.8p23f;
-  constexpr float kTie = 0.5f - 0x1p-16f;
-  const float inv = __builtin_amdgcn_rcpf(s);
+  float y = __builtin_amdgcn_rcpf(s);
+  y = fmaf(fmaf(-s, y, 1.0f), y, y);
+  auto quotient = [&](float v) __attribute__((always_inline)) {
+    const float t = v * y;
+    return fmaf(fmaf(-t, s, v), y, t);
+  };
   float z = 8.0f;
-  float off = 0.0f;                         // the largest distance of a quotient from its rounding
-  if constexpr (ZEROS) {
-    const float t = lo * inv;
-    z = rintf(t);
-    off = fabsf(t - z);
-    z = fminf(z, 15.0f);
-  }
-  const float base = kBase + z;
+  if constexpr (ZEROS) z = fminf(rintf(quotient(lo)), 15.0f);
   float q[P][8];
 #pragma unroll
-  for (int p = 0; p < P; ++p) {
+  for (int p = 0; p < P; ++p)
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      q[p][k] = fmaf(v[p].at(k), inv, base);
-      off = fmaxf(off, fabsf(fmaf(v[p].at(k), inv, base - q[p][k])));
+      const float t = quotient(v[p].at(k));
+      q[p][k] = (ZEROS ? rintf(t) : t) + (kBase + z);        // z may be odd, and then a tie's other side even
     }
-  }
-  if (off > kTie || s <= 0x1p-100f) {
+  if (s <= 0x1p-100f) {
     if constexpr (ZEROS) z = fminf(rintf(lo / s), 15.0f);
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
+    for (int p = 0; p < P; ++p)
 #pragma unroll
       for (int k = 0; k < 8; ++k) q[p][k] = rintf(v[p].at(k) / s) + (kBase + z);
-    }
   }
 #pragma unroll
   for (int p = 0; p < P; ++p) {
