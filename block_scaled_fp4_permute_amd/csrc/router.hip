@@ -490,7 +490,8 @@ __device__ __forceinline__ void rt_sort(uint32_t (&v)[N]) {
 // by s (1 - s) (|x| + 2) + 3 s < 3.2, a softmax by p (|x - max| + 35) (exp; sums of 16
 // and over 6 levels; quotient), which is below 36 max p as |x - max| p <= 0.37 max p; the
 // bias adds |key|, the lost bits |key| 2^5 for 16 places.  So two keys further apart than
-// tol + |key| 2^-18, tol 8 steps or 128 max p, are in order, and so are group values, of
+// tol + |key| 2^-18, tol 8 steps or 128 max p, are in order (logits as keys if they differ
+// at all), and so are group values, of
 // up to two keys with all their bits, further apart than 2 tol + |value| 2^-22.
 template <int LPT, int NE, int DT>
 __device__ __forceinline__ int choose_fast(const ScoredParams& p, int t, const float (&x)[NE], const float (&bias)[NE], float top,
@@ -541,13 +542,14 @@ __device__ __forceinline__ int choose_fast(const ScoredParams& p, int t, const f
     }
   }
   if (!full) keep &= e0 >= p.E ? 0u : p.E - e0 >= 32 ? ~0u : (1u << (p.E - e0)) - 1;
-  // by logits: the keys are exact, and 16-bit ones keep all their bits
+  // by logits: the keys are exact but for the lost bits, and 16-bit ones keep theirs.  The
+  // addition makes a zero of either sign the same one
   const bool exact = !p.bias && p.narrow;
   uint32_t el[NE];
 #pragma unroll
   for (int c = 0; c < NE; ++c) {
     const uint32_t there = static_cast<uint32_t>(static_cast<int32_t>(keep << (31 - c)) >> 31);
-    el[c] = ((rt_order(p.bias ? key[c] : x[c]) & ~LOW) | (LOW - c)) & there;
+    el[c] = ((rt_order((p.bias ? key[c] : x[c]) + 0.0f) & ~LOW) | (LOW - c)) & there;
   }
   rt_sort<NE>(el);
   order = false;
@@ -558,7 +560,7 @@ __device__ __forceinline__ int choose_fast(const ScoredParams& p, int t, const f
     const uint32_t first = el[0] & ~LOW;
     const uint32_t m = seg_reduce<LPT>(first, [](uint32_t a, uint32_t b) __attribute__((always_inline)) { return a > b ? a : b; });
     const float v = rt_unorder(m);
-    const bool close = !exact && m != 0 && before - v <= (p.bias ? tol : 0.0f) + fabsf(v) * 0x1p-18f;
+    const bool close = !exact && m != 0 && before - v <= (p.bias ? tol + fabsf(v) * 0x1p-18f : 0.0f);
     before = v;
     more = more && (j < p.k || close);
     if (more && j >= (LPT < 32 ? LPT : 32)) {

@@ -188,8 +188,8 @@ int moe_route_permute(const float* logits, int32_t T, int32_t E, int32_t k,
  * are chosen, by ascending id and with weight 0, only where the groups that stay
  * have fewer than k open ones; a row without any open expert has weights 0.  +inf
  * counts as the largest float32.
- * Outputs, permutation and workspace as for moe_route_permute; `scores` (nullable)
- * receives s as float32, 0 where the logit is -inf or NaN.  Limits as there, and
+ * Outputs, permutation and workspace as for moe_route_permute, none of them over the
+ * logits or the bias; `scores` (nullable) receives s as float32, 0 where the logit is -inf or NaN.  Limits as there, and
  * n_group divides E, n_group <= 64, k <= topk_group * E / n_group,
  * group_top <= E / n_group. */
 typedef struct nvfp4moe_route_args {

@@ -234,3 +234,16 @@ def test_weights_above_4_gib(N, K):
     q = m.int4_quantize(v)
     last, sc, _ = Q.quantize(v[0, N - 1:].float().cpu().numpy(), 128, False, "bf16")
     assert np.array_equal(q.codes[0, N - 1:].cpu().numpy(), last)
+
+
+def test_no_rows_and_rows_of_no_expert():
+    w = m.int4_quantize(torch.randn((3, 40, 64), device=DEV), 32, True, torch.bfloat16)
+    off = torch.zeros(4, dtype=torch.int32, device=DEV)
+    for rows in (0, 5):
+        x = torch.randn((rows, 64), device=DEV).to(torch.bfloat16)
+        assert m.int4_grouped_gemv(x, w, off, m_total=0).shape == (0, 40)
+        assert m.int4_grouped_gemv(x, w, off, m_total=0, gated=True).shape == (0, 20)
+    # rows that belong to no expert stay as they are
+    out = torch.full((5, 40), 3.0, device=DEV)
+    m.int4_grouped_gemv(x, w, off, m_total=5, out=out)
+    assert (out == 3).all()

@@ -110,3 +110,17 @@ def test_permutation_around_its_sizes(E, n):
             assert np.array_equal(a.cpu().numpy(), b)
         assert (got.perm_weight == 1).all()
         del got
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("groups", [(1, 1, 1), (8, 4, 2)], ids=str)
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("T", [5, 64, 2100])
+def test_zeros_of_either_sign_are_one_value(T, bias, groups, dtype):
+    r = np.random.default_rng(T)
+    l = torch.from_numpy(np.where(r.random((T, 64)) < 0.5, np.float32(-0.0), np.float32(0.0))).to(F[dtype])
+    l[::3, ::9] = 1.0
+    b = np.where(r.random(64) < 0.5, np.float32(-0.0), np.float32(0.0)).astype(np.float32) if bias else None
+    got = m.moe_route_scored(l.to(DEV), 6, score=m.SCORE_SIGMOID, bias=None if b is None else up(b), n_group=groups[0],
+                             topk_group=groups[1], group_top=groups[2])
+    _same(got, l.double().numpy(), 6, "sigmoid", b, groups, 64)
