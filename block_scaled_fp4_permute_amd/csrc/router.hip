@@ -925,8 +925,10 @@ __global__ __launch_bounds__(256) void k_route_scored_grad(const ScoredGradParam
 // ------------------------------------------------------------------ host side
 // 16 lanes a token where its experts fit 16 registers a lane and there are tokens
 // enough to fill the chip that way: the rounds then serve 4 tokens a wave (256 tokens
-// 8.4 us against 7.1 on 64 lanes, 2047 9.0 against 9.6).
-static bool rt_narrow(int T, int E, int k) { return E <= 256 && k <= 16 && T >= 2048; }
+// 8.4 us against 7.1 on 64 lanes, 2047 9.0 against 9.6; with float64 scores of all
+// experts 2051 tokens 12.4 against 11.0 and in bf16 13.0 against 9.1, 4096 13.8 against
+// 14.6, 8192 16.6 against 23.7).
+static bool rt_narrow(int T, int E, int k, bool scores) { return E <= 256 && k <= 16 && T >= (scores ? 4096 : 2048); }
 
 // lanes of a group if groups end between lanes and a butterfly joins them, else 0 (by way of LDS)
 static int rt_lanes_per_group(int E, int n_group, int ne) {
@@ -981,7 +983,8 @@ hipError_t launch_route_scored(const ScoredParams& q, int dtype, int* counts, in
   if (p.T <= 16 && p.T * p.k <= kSmallRows && p.E <= 256)
     return rt_start_small<4>(p, dtype, counts, offsets, src, row_of, row_w, stream);
   hipError_t err;
-  if (rt_narrow(p.T, p.E, p.k)) err = p.E <= 64 ? rt_start<16, 4>(p, dtype, stream) : rt_start<16, 16>(p, dtype, stream);
+  const bool scores = p.scores || (p.softmax && !p.renormalize);
+  if (rt_narrow(p.T, p.E, p.k, scores)) err = p.E <= 64 ? rt_start<16, 4>(p, dtype, stream) : rt_start<16, 16>(p, dtype, stream);
   else if (p.E <= 256) err = rt_start<64, 4>(p, dtype, stream);
   else if (p.E <= 1024) err = rt_start<64, 16>(p, dtype, stream);
   else err = rt_start<64, 0>(p, dtype, stream);
@@ -1005,7 +1008,7 @@ hipError_t launch_route_scored_grad(const ScoredGradParams& q, int dtype, hipStr
   p.vec = p.E % 4 == 0 && reinterpret_cast<uintptr_t>(p.logits) % four == 0;
   p.vec_d = p.E % 4 == 0 && reinterpret_cast<uintptr_t>(p.d_scores) % 16 == 0;
   p.vec_out = p.E % 4 == 0 && reinterpret_cast<uintptr_t>(p.dlogits) % four == 0;
-  if (rt_narrow(p.T, p.E, p.k)) return p.E <= 64 ? rt_start_grad<16, 4>(p, dtype, stream) : rt_start_grad<16, 16>(p, dtype, stream);
+  if (rt_narrow(p.T, p.E, p.k, false)) return p.E <= 64 ? rt_start_grad<16, 4>(p, dtype, stream) : rt_start_grad<16, 16>(p, dtype, stream);
   if (p.E <= 256) return rt_start_grad<64, 4>(p, dtype, stream);
   if (p.E <= 1024) return rt_start_grad<64, 16>(p, dtype, stream);
   return rt_start_grad<64, 64>(p, dtype, stream);

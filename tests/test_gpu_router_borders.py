@@ -11,7 +11,7 @@ import block_scaled_fp4_permute_amd as m
 from oracle import moe as OM
 from oracle import router as R
 from tests.gpu_common import DEV, up
-from tests.test_gpu_router import F, KIND
+from tests.test_gpu_router import F, KIND, _call, _check, _edge_rows, _logits, _want
 
 pytestmark = pytest.mark.gpu
 
@@ -124,3 +124,34 @@ def test_zeros_of_either_sign_are_one_value(T, bias, groups, dtype):
     got = m.moe_route_scored(l.to(DEV), 6, score=m.SCORE_SIGMOID, bias=None if b is None else up(b), n_group=groups[0],
                              topk_group=groups[1], group_top=groups[2])
     _same(got, l.double().numpy(), 6, "sigmoid", b, groups, 64)
+
+
+@pytest.mark.parametrize("c", [
+    (4095, 256, 8, "sigmoid", True, (8, 4, 2), True, "f32"),        # the last on 64 lanes a token with scores
+    (4096, 256, 8, "sigmoid", True, (8, 4, 2), True, "f32"),
+    (4099, 256, 16, "softmax", False, (1, 1, 1), False, "bf16"),
+    (4101, 61, 5, "softmax", True, (1, 1, 1), True, "f16"),
+    (4097, 96, 6, "sigmoid", True, (12, 4, 2), False, "f32"),
+    (4098, 250, 8, "softmax", True, (5, 3, 1), False, "f32"),
+], ids=str)
+def test_scores_of_many_tokens(c):
+    _, t, l, bias = _logits(c)
+    got, scores = _call(t, c, bias, save_scores=True)
+    _check(got, scores, _want(l, c, bias), c[2], c[1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("groups", [(1, 1, 1), (8, 3, 2)], ids=str)
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+def test_edge_rows_of_many_tokens(bias, kind, groups, dtype):
+    t = torch.from_numpy(_edge_rows(72, dtype != "f32")).to(F[dtype])
+    b = None
+    if bias:
+        b = (np.random.default_rng(3).standard_normal(72) * 0.01).astype(np.float32)
+        b[3], b[5], b[9] = -np.inf, np.nan, np.inf
+    for renormalize in (True, False):
+        c = (len(t), 72, 6, kind, bias, groups, renormalize, dtype)
+        ids, w, s, _ = _want(t.double().numpy(), c, b)
+        got, scores = _call(t.repeat(200, 1), c, b, save_scores=True)
+        _check(got, scores, (np.tile(ids, (200, 1)), np.tile(w, (200, 1)), np.tile(s, (200, 1)), None), 6, 72)
