@@ -305,15 +305,18 @@ def _dtype_code(t):
 
 def _dtype_any(t, name):
     import torch
-    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name}: expected float32, bfloat16 or float16, got {t.dtype}")
-    return code
+    if t.dtype == torch.float32:
+        return F32
+    if t.dtype == torch.bfloat16:
+        return BF16
+    if t.dtype == torch.float16:
+        return F16
+    raise TypeError(f"{name}: expected float32, bfloat16 or float16, got {t.dtype}")
 
 
 def _need_shape(t, shape, dtype, name, device):
     _need(t, dtype, name, device)
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name}: expected {list(shape)}, got {list(t.shape)}")
 
 
@@ -332,6 +335,11 @@ class Routing:
 def _new_routing(T, E, k, dev, stream):
     import torch
     i32, f32 = torch.int32, torch.float32
+    if stream is None:
+        # of another tensor's type and device: a fifth less than by naming them
+        ids, w, n = _empty((T, k), i32, dev), _empty((T, k), f32, dev), T * k
+        new = ids.new_empty
+        return Routing(ids, w, new(E), new(E + 1), new(n), new(n), w.new_empty(n))
     new = _new_result
     return Routing(new((T, k), i32, dev, stream), new((T, k), f32, dev, stream), new(E, i32, dev, stream),
                    new(E + 1, i32, dev, stream), new(T * k, i32, dev, stream), new(T * k, i32, dev, stream),
@@ -420,9 +428,9 @@ def moe_route_scored_backward(d_topk_w, logits, topk_ids, *, score: int = SCORE_
         ld = E if d_scores.dim() == 2 else 0
         _need_shape(d_scores, (T, E) if ld else (E,), torch.float32, "d_scores", dev)
     dlogits = _result(dlogits, (T, E), logits.dtype, logits, "dlogits", stream)
-    args = RouteGradArgs(logits=logits.data_ptr(), dtype=code, T=T, E=E, k=k, score=score, renormalize=int(renormalize),
-                         scale=scale, bias=_ptr(bias), topk_ids=topk_ids.data_ptr(), d_topk_w=d_topk_w.data_ptr(),
-                         d_scores=_ptr(d_scores), d_scores_ld=ld, dlogits=dlogits.data_ptr())
+    # in the order of the fields
+    args = RouteGradArgs(logits.data_ptr(), code, T, E, k, score, int(renormalize), scale, _ptr(bias), topk_ids.data_ptr(),
+                         d_topk_w.data_ptr(), _ptr(d_scores), ld, dlogits.data_ptr())
     _call(dev, stream, lib().moe_route_scored_backward, ctypes.byref(args))
     return dlogits
 
