@@ -1188,9 +1188,10 @@ def _need_int4(q, name, dev):
     if q.group not in (32, 64, 128):
         raise ValueError(f"{name}: group {q.group} (32, 64 or 128)")
     _need(q.codes, torch.uint8, name + ".codes", dev)
-    shape = tuple(q.codes.shape[:-1]) + (2 * q.codes.shape[-1] // q.group,)
-    if 2 * q.codes.shape[-1] % q.group:
-        raise ValueError(f"{name}: {2 * q.codes.shape[-1]} columns, not a multiple of the group of {q.group}")
+    *lead, half = q.codes.shape
+    if 2 * half % q.group:
+        raise ValueError(f"{name}: {2 * half} columns, not a multiple of the group of {q.group}")
+    shape = (*lead, 2 * half // q.group)
     _need_shape(q.scales, shape, q.scales.dtype, name + ".scales", dev)
     if q.zeros is not None:
         _need_shape(q.zeros, shape, torch.uint8, name + ".zeros", dev)
@@ -1214,14 +1215,15 @@ def int4_quantize(x, group: int = 128, zeros: bool = False, scale_dtype=None, ou
         dtype = scale_dtype or (torch.bfloat16 if code == F32 else x.dtype)
         if dtype not in (torch.bfloat16, torch.float16):
             raise TypeError(f"scale_dtype: expected bfloat16 or float16, got {dtype}")
-        lead, gs = tuple(x.shape[:-1]), cols // group
-        out = INT4Tensor(_result(None, lead + (cols // 2,), torch.uint8, x, "out.codes", stream),
-                         _result(None, lead + (gs,), dtype, x, "out.scales", stream),
-                         _result(None, lead + (gs,), torch.uint8, x, "out.zeros", stream) if zeros else None, group)
-    elif out.group != group or tuple(out.codes.shape) != tuple(x.shape[:-1]) + (cols // 2,) or \
-            (out.zeros is not None) != zeros or (scale_dtype is not None and out.scales.dtype != scale_dtype):
-        raise ValueError("out does not match x, group, zeros and scale_dtype")
-    scode = _need_int4(out, "out", dev)
+        scode = BF16 if dtype == torch.bfloat16 else F16
+        lead, gs, u8 = x.shape[:-1], cols // group, torch.uint8
+        out = INT4Tensor(_new_result((*lead, cols // 2), u8, dev, stream), _new_result((*lead, gs), dtype, dev, stream),
+                         _new_result((*lead, gs), u8, dev, stream) if zeros else None, group)
+    else:
+        if out.group != group or out.codes.shape != (*x.shape[:-1], cols // 2) or (out.zeros is not None) != zeros or \
+                (scale_dtype is not None and out.scales.dtype != scale_dtype):
+            raise ValueError("out does not match x, group, zeros and scale_dtype")
+        scode = _need_int4(out, "out", dev)
     if x.numel() == 0:
         return out
     _call(dev, stream, lib().int4_quantize, x.data_ptr(), code, x.numel() // cols, cols, group, scode,
