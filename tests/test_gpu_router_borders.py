@@ -155,3 +155,35 @@ def test_edge_rows_of_many_tokens(bias, kind, groups, dtype):
         ids, w, s, _ = _want(t.double().numpy(), c, b)
         got, scores = _call(t.repeat(200, 1), c, b, save_scores=True)
         _check(got, scores, (np.tile(ids, (200, 1)), np.tile(w, (200, 1)), np.tile(s, (200, 1)), None), 6, 72)
+
+
+@pytest.mark.parametrize("T", [5, 300, 2100, 4100])
+@pytest.mark.parametrize("weights", [True, False], ids=["perm_weight", "none"])
+def test_given_outputs(T, weights):
+    """Results, scores and a workspace of the caller's, four bytes off any alignment and between guards;
+    the workspace holds another call's rest."""
+    E, k = 64, 4
+    c = (T, E, k, "sigmoid", True, (8, 4, 2), True, "f32")
+    _, t, l, bias = _logits(c)
+    guard = []
+
+    def block(*shape, dtype=torch.int32):
+        n = int(np.prod(shape))
+        whole = torch.full((n + 12,), 77, dtype=dtype, device=DEV)
+        guard.append((whole, n))
+        return whole[5:5 + n].view(shape)
+
+    out = m.Routing(block(T, k), block(T, k, dtype=torch.float32), block(E), block(E + 1), block(T * k), block(T * k),
+                    block(T * k, dtype=torch.float32) if weights else None)
+    scores = block(T, E, dtype=torch.float32)
+    ws = torch.full((m.lib().moe_route_permute_workspace_size(T, E, k),), 255, dtype=torch.uint8, device=DEV)
+    x = block(T, E, dtype=torch.float32)
+    x.copy_(t)
+    got, s = m.moe_route_scored(x, k, score=m.SCORE_SIGMOID, bias=up(bias), n_group=8, topk_group=4, group_top=2, scale=2.5,
+                                scores=scores, out=out, workspace=ws)
+    assert got is out and s is scores
+    whole = m.Routing(*[getattr(out, f) for f in ("topk_ids", "topk_w", "counts", "offsets", "perm_src_token", "perm_of_assignment")],
+                      out.perm_weight if weights else _call(t, c, bias).perm_weight)
+    _check(whole, scores, _want(l, c, bias), k, E)
+    for w, n in guard:
+        assert (w[:5] == 77).all() and (w[5 + n:] == 77).all()
