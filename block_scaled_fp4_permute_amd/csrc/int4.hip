@@ -77,7 +77,8 @@ __global__ __launch_bounds__(256) void k_int4_quantize(const void* __restrict__ 
   }
   hi = i4_max<L>(hi);
   if constexpr (ZEROS) lo = i4_max<L>(lo);
-  const float raw = ZEROS ? (hi + lo) * (1.0f / 15.0f) : hi * (1.0f / 7.0f);
+  float raw = ZEROS ? (hi + lo) * (1.0f / 15.0f) : hi * (1.0f / 7.0f);
+  asm("" : "+v"(raw));                      // a float32 product: one with the conversion to f16 in it rounds but once
   uint16_t bits;
   float s;
   if constexpr (SF16) {

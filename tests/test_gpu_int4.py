@@ -247,3 +247,27 @@ def test_no_rows_and_rows_of_no_expert():
     out = torch.full((5, 40), 3.0, device=DEV)
     m.int4_grouped_gemv(x, w, off, m_total=5, out=out)
     assert (out == 3).all()
+
+
+@pytest.mark.parametrize("zeros", [False, True], ids=["symmetric", "zeros"])
+@pytest.mark.parametrize("st", ["bf16", "f16"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_quantise_whole_range(group, dtype, st, zeros):
+    """Groups of any exponent, values of one size or many, quotients on ties; the scale rounds twice, to
+    float32 and to its type (7 n 2^-25 by 1/7 is n 2^-25 in float32, halfway between two f16 values)."""
+    r = np.random.default_rng(group)
+    n = 3000
+    e = r.integers(*((-24, 15) if dtype == "f16" else (-140, 126)), (n, 1))
+    x = r.standard_normal((n, group)) * np.exp2(e - r.integers(0, 12, (n, group)) * (np.arange(n)[:, None] % 3 == 0))
+    h = n // 2
+    x[:h] = np.round(x[:h] / np.abs(x[:h]).max(1, keepdims=True) * 14) / 2 * np.exp2(e[:h])
+    x[:200, 0] = (15 if zeros else 7) * 2.0 ** -25 * np.arange(200)
+    x[:200, 1:] = x[:200, :1] * r.random((200, group - 1))
+    with np.errstate(over="ignore"):
+        t = torch.from_numpy(x.astype(np.float32)).to(F[dtype])
+    got = m.int4_quantize(t.to(DEV), group, zeros, F[st])
+    codes, scales, z = Q.quantize(t.float().numpy(), group, zeros, st)
+    assert np.array_equal(got.scales.float().cpu().numpy(), scales, equal_nan=True)
+    assert np.array_equal(got.codes.cpu().numpy(), codes)
+    assert not zeros or np.array_equal(got.zeros.cpu().numpy(), z)
