@@ -213,9 +213,11 @@ __device__ __forceinline__ void rt_lds_step() {
 }
 
 // Which groups stay, by float32 keys (key(c): of the lane's expert c, -inf if there is
-// none).  near: set if the last group that stays and the first that goes are within
-// tol + |value| 2^-22.  Returns a bit for each of the lane's experts that stays.  lds:
-// E + 2 n_group floats of the token's own, where no lanes' borders follow the groups'.
+// none).  near: set if a group that stays and one that goes could change places: their
+// values, each with the error that its own keys give it (tol + the keys' sizes, which may
+// be far above that of a sum they cancel in, times 3.125 2^-24), are not clear of each
+// other.  Returns a bit for each of the lane's experts that stays.  lds: E + 2 n_group
+// floats of the token's own, where no lanes' borders follow the groups'.
 template <int LPT, int NE, typename K>
 __device__ __forceinline__ uint32_t scored_groups(const ScoredParams& p, K key, float tol, float* lds, bool& near) {
   const float none = -__builtin_huge_valf();
@@ -223,7 +225,10 @@ __device__ __forceinline__ uint32_t scored_groups(const ScoredParams& p, K key, 
   const int e0 = l * NE;
   const int gs = p.E / p.n_group;
   auto value = [&](float a1, float a2) __attribute__((always_inline)) { return p.group_top == 2 ? a1 + a2 : a1; };
-  float last = -none, next = none;          // of the groups that stay, and that go
+  auto error = [&](float a1, float a2) __attribute__((always_inline)) {
+    return fmaf(p.group_top == 2 ? fabsf(a1) + fabsf(a2) : fabsf(a1), 0x1.9p-23f, tol);
+  };
+  float last = -none, next = none;          // the least that a group that stays, and the most that one that goes, may be worth
   uint32_t stays = 0;
   if (p.lanes_per_group) {
     const int s = p.lanes_per_group;
@@ -235,7 +240,7 @@ __device__ __forceinline__ uint32_t scored_groups(const ScoredParams& p, K key, 
       a1 = fmaxf(a1, k);
     }
     top2_lanes(a1, a2, s);
-    const float v = value(a1, a2);
+    const float v = value(a1, a2), err = error(a1, a2);
     const int g = l / s;
     int rank = 0;
     for (int h0 = 0; h0 < p.n_group; h0 += 4) {              // four exchanges at a time
@@ -248,10 +253,11 @@ __device__ __forceinline__ uint32_t scored_groups(const ScoredParams& p, K key, 
     if (g < p.n_group) {
       if (rank < p.topk_group) {
         stays = ~0u;
-        last = v;
+        last = v - err;
       } else {
-        next = v;
+        next = v + err;
       }
+      near |= !(err < -none);                // a sum beyond float32's range
     }
     // equal values at the border all stay, and are then too many
     near |= __popcll(seg_ballot<LPT>(g < p.n_group && stays != 0)) != p.topk_group * s;
@@ -272,6 +278,7 @@ __device__ __forceinline__ uint32_t scored_groups(const ScoredParams& p, K key, 
         a1 = fmaxf(a1, k);
       }
       val[g] = value(a1, a2);
+      lds[g * (gs + 1) + gs] = error(a1, a2);                // in the gap behind the group
     }
     rt_lds_step();
     int count = 0;
@@ -280,10 +287,12 @@ __device__ __forceinline__ uint32_t scored_groups(const ScoredParams& p, K key, 
       int rank = 0;
       for (int h = 0; h < p.n_group; ++h) rank += val[h] > v ? 1 : 0;
       const bool in = rank < p.topk_group;
+      const float err = lds[g * (gs + 1) + gs];
       count += in ? 1 : 0;
-      lds[g * (gs + 1) + gs] = in ? 1.0f : 0.0f;             // in the gap behind the group
-      last = in ? fminf(last, v) : last;
-      next = in ? next : fmaxf(next, v);
+      lds[g * (gs + 1) + gs] = in ? 1.0f : 0.0f;             // the error's place, read by this lane alone
+      last = in ? fminf(last, v - err) : last;
+      next = in ? next : fmaxf(next, v + err);
+      near |= !(err < -none);
     }
     rt_lds_step();
 #pragma unroll
@@ -296,7 +305,7 @@ __device__ __forceinline__ uint32_t scored_groups(const ScoredParams& p, K key, 
   }
   last = -seg_max<LPT>(-last);
   next = seg_max<LPT>(next);
-  near |= last - next <= tol + fabsf(last) * 0x1p-22f;
+  near |= !(last > next);
   return stays;
 }
 
@@ -491,8 +500,11 @@ __device__ __forceinline__ void rt_sort(uint32_t (&v)[N]) {
 // and over 6 levels; quotient), which is below 36 max p as |x - max| p <= 0.37 max p; the
 // bias adds |key|, the lost bits |key| 2^5 for 16 places.  So two keys further apart than
 // tol + |key| 2^-18, tol 8 steps or 128 max p, are in order (logits as keys if they differ
-// at all), and so are group values, of
-// up to two keys with all their bits, further apart than 2 tol + |value| 2^-22.
+// at all).  A group's value, of up to two keys a with all their bits, is off by twice 3.2
+// steps or 36 max p, by sum |a| for the keys' additions and, at most as much each, for
+// their own and that of the bound: below tol + 3.125 sum |a| steps (the k-th largest of
+// keys that are off by an error that grows with their size is off by that at its own).
+// A masked group of -1e9, say, thus makes nothing near but its like.
 template <int LPT, int NE, int DT>
 __device__ __forceinline__ int choose_fast(const ScoredParams& p, int t, const float (&x)[NE], const float (&bias)[NE], float top,
                                            float z, double* lds, int* list, bool& order, bool& near) {
@@ -528,7 +540,7 @@ __device__ __forceinline__ int choose_fast(const ScoredParams& p, int t, const f
     const int base = (threadIdx.x & 63) & ~(LPT - 1);
     bool close = false;
     keep = scored_groups<LPT, NE>(p, [&](int c) __attribute__((always_inline)) { return full || e0 + c < p.E ? key[c] : none; },
-                                  2.0f * tol, reinterpret_cast<float*>(lds) + base / LPT * (p.E + 2 * p.n_group), close);
+                                  tol, reinterpret_cast<float*>(lds) + base / LPT * (p.E + 2 * p.n_group), close);
     close = seg_ballot<LPT>(close) != 0 && !near;
     // such tokens of the wave one after the other, on all its lanes
     for (uint64_t rest = __ballot(close && l == 0); rest; rest &= rest - 1) {
