@@ -654,25 +654,23 @@ __device__ __forceinline__ int scored_token(const ScoredParams& p, int t, bool l
     });
 
   // the candidates' scores, one a lane.  Renormalised softmax: relative to the largest
-  // candidate's logit, which divides out; renormalised sigmoids of logits below -500
-  // times exp(-largest), likewise: scores that would underflow together keep their ratios
+  // chosen logit, which divides out; renormalised sigmoids of logits below -500 times
+  // exp(-largest), likewise: scores that would underflow together keep their ratios.
+  // (A candidate that is not chosen may have a logit hundreds above them, where keys tie.)
   const int packed = l < n ? list[l] : 0;
   my_id = packed & 0xFFFF;
   const bool open = l < n && (packed >> 30) != 0;
   const float xj = open ? rt_finite(rt_load<DT>(p.logits, row + my_id)) : 0.0f;
-  const float most = seg_max<LPT>(open ? xj : -__builtin_huge_valf());
-  const bool low = !p.softmax && p.renormalize && most < -500.0f;
-  const double from = p.softmax && p.renormalize && open ? static_cast<double>(most) : top;
-  double u = rt_exp(p.softmax ? static_cast<double>(xj) - from : -static_cast<double>(xj));
-  if (!p.softmax) u = 1.0 / (1.0 + u);
-  else if (!p.renormalize) u /= z;
+  const bool ratios = p.softmax && p.renormalize;
+  double u = 0.0;
+  if (!ratios || (p.bias && __any(order))) {
+    u = rt_exp(p.softmax ? static_cast<double>(xj) - top : -static_cast<double>(xj));
+    u = p.softmax ? u / z : 1.0 / (1.0 + u);
+  }
   int place = l < n ? l : p.k;
   if (__any(order)) {
     // in the order of the float64 keys, ties to the lower id
-    double key = static_cast<double>(xj);
-    if (p.bias && p.softmax) key = p.renormalize ? rt_exp(key - top) / z : u;
-    else if (p.bias) key = u;
-    if (p.bias) key += static_cast<double>(p.bias[my_id]);
+    double key = p.bias ? u + static_cast<double>(p.bias[my_id]) : static_cast<double>(xj);
     if (!open) key = kClosed;
     int rank = 0;
     for (int i = 0; i < (LPT < 32 ? LPT : 32); ++i) {
@@ -682,8 +680,12 @@ __device__ __forceinline__ int scored_token(const ScoredParams& p, int t, bool l
     }
     if (order) place = l < n ? rank : p.k;
   }
-  if (low) u = 1.0 / (rt_exp(most) + rt_exp(open ? static_cast<double>(most) - static_cast<double>(xj) : 0.0));
-  u = open && place < p.k ? u : 0.0;
+  const bool chosen = open && place < p.k;
+  const float most = seg_max<LPT>(chosen ? xj : -__builtin_huge_valf());
+  if (ratios) u = rt_exp(chosen ? static_cast<double>(xj) - static_cast<double>(most) : 0.0);
+  else if (p.renormalize && most < -500.0f)
+    u = 1.0 / (rt_exp(most) + rt_exp(chosen ? static_cast<double>(most) - static_cast<double>(xj) : 0.0));
+  u = chosen ? u : 0.0;
   if (p.renormalize) {
     const double s = seg_sum<LPT>(u);
     u = s > 0.0 ? u / s : 0.0;
