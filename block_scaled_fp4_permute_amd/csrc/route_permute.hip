@@ -350,9 +350,15 @@ __global__ __launch_bounds__(256) void k_scatter(const int* __restrict__ ids, co
 // One workgroup of 1024 threads per chunk.  Each sums every chunk's histogram (from
 // L2: 128 chunks of 256 experts are 128 KB) into the experts' totals and the part of
 // them that lies in earlier chunks, scans the totals, and places its own 1024
-// assignments.  16384 tokens, top-8 of 256: 5 us in place of 12 (k_scan) + 5
+// assignments.  16384 tokens, top-8 of 256: 7 us in place of 12 (k_scan) + 5
 // (k_scatter).
-static constexpr int kPlaceChunks = 256;   // the histograms are read once for each chunk
+// Each of the chunks' workgroups reads every histogram, chunks^2 E words (1 GB at the limit
+// with 4096 experts), and yet wins up to the limit whatever E, the more the larger both
+// are (moe_route_permute of top-8, us, so / by k_scan and k_scatter): 61 experts, 16 chunks
+// 16.5 / 16.8, 256 chunks 46 / 66; 256 experts 19.3 / 19.2 and 64 / 84; 513 experts 24.5 /
+// 24.9 and 121 / 128; 1024 experts 29.8 / 30.5 and 156 / 177; 4095 experts 177 / 209 and
+// 1106 / 1620; 4096 experts 133 / 167 and 1032 / 1588.
+static constexpr int kPlaceChunks = 256;
 static constexpr int kPlaceBatch = 8;
 __global__ __launch_bounds__(1024) void k_place(const int* __restrict__ ids, const float* __restrict__ topk_w,
                                                 const int* __restrict__ local_rank, const int* __restrict__ chunk_hist,
@@ -395,6 +401,7 @@ __global__ __launch_bounds__(1024) void k_place(const int* __restrict__ ids, con
       *reinterpret_cast<int4*>(&pre[part * E + e]) = b;
     }
   } else {
+    // as many round trips: a chunk at a time 513 experts and 256 chunks took 163 us, 121 now
     width = (E + 63) & ~63;
     parts = width <= 1024 ? 1024 / width : 1;
     for (int e0 = 0; e0 < E; e0 += 1024) {
@@ -402,10 +409,17 @@ __global__ __launch_bounds__(1024) void k_place(const int* __restrict__ ids, con
       const int e = width <= 1024 ? tid % width : e0 + tid;
       if (part >= parts || e >= E) continue;
       int t = 0, b = 0;
-      for (int c = part; c < nchunks; c += parts) {
-        const int v = chunk_hist[static_cast<size_t>(c) * E + e];
-        t += v;
-        b += c < chunk ? v : 0;
+      for (int c0 = part; c0 < nchunks; c0 += kPlaceBatch * parts) {
+        int v[kPlaceBatch];
+#pragma unroll
+        for (int j = 0; j < kPlaceBatch; ++j)
+          v[j] = chunk_hist[static_cast<size_t>(min(c0 + j * parts, nchunks - 1)) * E + e];
+#pragma unroll
+        for (int j = 0; j < kPlaceBatch; ++j) {
+          const int c = c0 + j * parts;
+          t += c < nchunks ? v[j] : 0;
+          b += c < chunk ? v[j] : 0;
+        }
       }
       tot[part * width + e] = t;            // part 0 alone where width > 1024
       pre[part * width + e] = b;
