@@ -1,7 +1,7 @@
 // The router with scores, and the gradient of its logits.
 //
-//   scores    sigmoid s_e = 1 / (1 + exp(-l_e)), or softmax over the token's open
-//             experts
+//   scores    sigmoid s_e = 1 / (1 + exp(-l_e)), or softmax over the token's
+//             experts whose logits are neither -inf nor NaN, whatever their bias
 //   choice    by key_e = s_e + bias_e among the topk_group best of n_group groups
 //             of neighbouring experts (a group's value: the sum of its group_top
 //             largest keys); without a bias by the logit, which has the scores'
@@ -22,8 +22,8 @@
 // long in float64, is a loop over few instructions.  Top-8 of 256 in 8 groups with a
 // bias, float32: 256 tokens 7 us, 4096 9, 16384 15 to 17 (read at 4.86 TB/s: 3.5),
 // with scores 27.
-// An expert is closed if its logit is -inf or NaN, or its key -inf or NaN; closed
-// ones are taken, by id and with weight 0, only where a token has fewer open ones
+// An expert is closed to the choice if its logit is -inf or NaN, or its key -inf or NaN;
+// closed ones are taken, by id and with weight 0, only where a token has fewer open ones
 // than it needs.
 #include "nvfp4_internal.h"
 
@@ -806,7 +806,7 @@ __global__ __launch_bounds__(256) void k_route_scored_grad(const ScoredGradParam
   if (p.d_scores) {
     rt_load_row<0, NE>(p.d_scores, static_cast<size_t>(t) * p.d_scores_ld, e0, p.E, p.vec_d, q);
 #pragma unroll
-    for (int c = 0; c < NE; ++c) q[c] = rt_open(x[c]) ? q[c] : 0.0f;     // a closed score is 0 whatever the logits
+    for (int c = 0; c < NE; ++c) q[c] = rt_open(x[c]) ? q[c] : 0.0f;     // the score of -inf or NaN is 0 whatever the others
   } else {
 #pragma unroll
     for (int c = 0; c < NE; ++c) q[c] = 0.0f;

@@ -78,7 +78,7 @@ typedef enum nvfp4moe_activation {
 
 /* scores of moe_route_scored */
 typedef enum nvfp4moe_score {
-  NVFP4MOE_SCORE_SOFTMAX = 0,    /* softmax over the token's open experts */
+  NVFP4MOE_SCORE_SOFTMAX = 0,    /* softmax over the token's logits (-inf and NaN left out) */
   NVFP4MOE_SCORE_SIGMOID = 1     /* 1 / (1 + exp(-l)) */
 } nvfp4moe_score;
 
@@ -170,7 +170,8 @@ int moe_route_permute(const float* logits, int32_t T, int32_t E, int32_t k,
  * moe_route_permute with the choices of a trained router (the router of
  * "Discovering SM120-Specific CUTLASS MoE Kernels", section "Input Knowledge
  * Required", whose form the pages leave open):
- *   scores   s [T, E] of the logits l (float32, bf16 or f16), by `score`
+ *   scores   s [T, E] of the logits l (float32, bf16 or f16), by `score`, whatever
+ *            the bias; 0 where the logit is -inf or NaN
  *   keys     s + bias[e] (the balance bias enters the choice, not the weights)
  *   groups   the E experts are n_group groups of neighbours; a group's value is the
  *            sum of its group_top (1 or 2) largest keys; the topk_group best stay
@@ -178,18 +179,19 @@ int moe_route_permute(const float* logits, int32_t T, int32_t E, int32_t k,
  *   choice   the k largest keys of the groups that stay, descending, ties to the
  *            lower id; without a bias by the logits themselves (the scores' order
  *            without their saturation)
- *   weights  the chosen scores u_j, as they are or (renormalize) u_j / sum(u), times
- *            `scale`, rounded to float32 once
+ *   weights  the chosen scores u_j, as they are or (renormalize) u_j / sum(u), also
+ *            where the scores underflow together, times `scale`, rounded to float32 once
  * Scores, keys and weights are float64 up to there, so near-equal keys are ordered
  * as defined (values that differ by float64's own rounding, as sums of a group's keys
- * can, may come in either order).  An expert is closed if its logit is -inf or NaN, or its key -inf or
- * NaN (a bias of -inf takes it out).  Closed experts have score 0 in a softmax,
- * count nothing in their group (a group without an open expert comes last), and
- * are chosen, by ascending id and with weight 0, only where the groups that stay
- * have fewer than k open ones; a row without any open expert has weights 0.  +inf
- * counts as the largest float32.
+ * can, may come in either order).  An expert is closed to the choice if its logit is
+ * -inf or NaN, or its key -inf or NaN.  Closed experts count nothing in their group (a
+ * group without an open expert comes last), and are chosen, by ascending id and with
+ * weight 0, only where the groups that stay have fewer than k open ones; a row without
+ * any open expert has weights 0.  A bias of -inf or NaN closes an expert to the choice
+ * alone: its score and its share of a softmax's sum remain, and its logit's gradient.
+ * +inf counts as the largest float32.
  * Outputs, permutation and workspace as for moe_route_permute, none of them over the
- * logits or the bias; `scores` (nullable) receives s as float32, 0 where the logit is -inf or NaN.  Limits as there, and
+ * logits or the bias; `scores` (nullable) receives s as float32.  Limits as there, and
  * n_group divides E, n_group <= 64, k <= topk_group * E / n_group,
  * group_top <= E / n_group. */
 typedef struct nvfp4moe_route_args {
@@ -218,7 +220,7 @@ int moe_route_scored(const nvfp4moe_route_args* args, void* workspace, size_t wo
  * d_scores, that of the scores (a balance loss): [T, E] with d_scores_ld = E, or one
  * row for all tokens with d_scores_ld = 0.  logits, topk_ids and the options are
  * those of the forward call (bias: only its -inf and NaN matter).  The choice and
- * the bias have no gradient; closed logits get 0.  Ids outside [0, E) are left out;
+ * the bias have no gradient; logits of -inf or NaN get 0.  Ids outside [0, E) are left out;
  * an id that stands twice in a row counts twice.  dlogits has the logits' type;
  * float32 arithmetic, rounded once. */
 typedef struct nvfp4moe_route_grad_args {
