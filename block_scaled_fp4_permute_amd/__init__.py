@@ -1325,23 +1325,29 @@ def moe_unpermute_combine(y, perm_of_assignment, topk_w, T: int, k: int, out=Non
     return out
 
 
-def moe_unpermute_combine_backward(dout, y, perm_of_assignment, topk_w, *, need_dy: bool = True, need_dw: bool = True,
-                                   dy=None, d_topk_w=None, stream=None):
+def moe_unpermute_combine_backward(dout, y, perm_of_assignment, topk_w, *, k: int | None = None, need_dy: bool = True,
+                                   need_dw: bool = True, dy=None, d_topk_w=None, stream=None):
     """Gradients of moe_unpermute_combine from dout [T, H]: (dy [rows, H] in y's
-    type, d_topk_w float32 [T, k]); None where not needed.  topk_w float32 [T, k];
-    perm_of_assignment as in the forward call (None: row t*k + j), its entries in
-    [0, rows) and all different.  Rows of a new dy that no entry names are zero."""
+    type, d_topk_w float32 [T, k]); None where not needed.  topk_w float32 [T, k], or
+    None for a plain sum (weights of 1) of k rows a token; perm_of_assignment as in
+    the forward call (None: row t*k + j), its entries in [0, rows) and all different.
+    Rows of a new dy that no entry names are zero."""
     import torch
-    if dout.dim() != 2 or y.dim() != 2 or topk_w.dim() != 2:
+    if dout.dim() != 2 or y.dim() != 2 or (topk_w is not None and topk_w.dim() != 2):
         raise ValueError("dout must be [T, H], y [rows, H] and topk_w [T, k]")
+    if k is None:
+        if topk_w is None:
+            raise ValueError("k is needed without topk_w")
+        k = topk_w.shape[1]
     if not (need_dy or need_dw):
         raise ValueError("neither dy nor d_topk_w is needed")
     dev = y.device
     y_code, d_code = _dtype_code(y), _dtype_code(dout)
     _need(y, y.dtype, "y", dev)
     _need(dout, dout.dtype, "dout", dev)
-    (T, H), k, rows = dout.shape, topk_w.shape[1], y.shape[0]
-    _need_shape(topk_w, (T, k), torch.float32, "topk_w", dev)
+    (T, H), rows = dout.shape, y.shape[0]
+    if topk_w is not None:
+        _need_shape(topk_w, (T, k), torch.float32, "topk_w", dev)
     if y.shape[1] != H:
         raise ValueError("operand shapes disagree")
     if perm_of_assignment is not None:
@@ -1358,7 +1364,7 @@ def moe_unpermute_combine_backward(dout, y, perm_of_assignment, topk_w, *, need_
         dy = None
     d_topk_w = _result(d_topk_w, (T, k), torch.float32, y, "d_topk_w", stream) if need_dw else None
     _call(dev, stream, lib().moe_unpermute_combine_backward, dout.data_ptr(), d_code, y.data_ptr(), y_code, rows,
-          _ptr(perm_of_assignment), topk_w.data_ptr(), T, k, H, _ptr(dy), _ptr(d_topk_w))
+          _ptr(perm_of_assignment), _ptr(topk_w), T, k, H, _ptr(dy), _ptr(d_topk_w))
     return dy, d_topk_w
 
 
