@@ -59,15 +59,18 @@ class Router:
         """The options that the gradient takes too."""
         return dict(score=self.score, bias=self.bias, renormalize=self.renormalize, scale=self.scale)
 
-    def route(self, logits, k, out=None, workspace=None, stream=None):
-        return moe_route_scored(logits, k, n_group=self.n_group, topk_group=self.topk_group, group_top=self.group_top,
-                                out=out, workspace=workspace, stream=stream, **self.weights())
+    def route(self, logits, k, out=None, workspace=None, stream=None, scores=None) -> Routing:
+        """scores: float32 [T, E] to receive those of all experts."""
+        r = moe_route_scored(logits, k, n_group=self.n_group, topk_group=self.topk_group, group_top=self.group_top,
+                             out=out, workspace=workspace, stream=stream, scores=scores, **self.weights())
+        return r if scores is None else r[0]
 
 
-def _route(layer, logits: torch.Tensor, stream) -> Routing:
-    """A layer's routing, by its Router if it has one."""
-    if layer.router is not None:
-        return layer.router.route(logits, layer.k, out=layer.routing, workspace=layer.route_ws, stream=stream)
+def _route(layer, logits: torch.Tensor, stream, scores: torch.Tensor | None = None) -> Routing:
+    """A layer's routing, by its Router if it has one; the plain one's scores are the default Router's."""
+    if layer.router is not None or scores is not None:
+        return (layer.router or Router()).route(logits, layer.k, out=layer.routing, workspace=layer.route_ws, stream=stream,
+                                                scores=scores)
     return moe_route_permute(logits, layer.k, out=layer.routing, workspace=layer.route_ws, stream=stream)
 
 
@@ -630,16 +633,18 @@ class MoELayer16:
         # address of the gu that belongs to self.h and self.routing; only to refuse other gradients with
         self._gu_of_h = None
 
-    def route(self, logits: torch.Tensor, stream=None) -> Routing:
+    def route(self, logits: torch.Tensor, stream=None, scores: torch.Tensor | None = None) -> Routing:
+        """scores: float32 [T, E] to receive the router's, for a balance loss."""
         self._gu_of_h = None
-        return _route(self, logits, stream)
+        return _route(self, logits, stream, scores)
 
     def forward(self, logits: torch.Tensor, x: torch.Tensor, w_gu: torch.Tensor, w_dn: torch.Tensor,
-                stream=None, gu: torch.Tensor | None = None) -> torch.Tensor:
-        """One layer step, bf16 [T, H]; gu: as for expert_rows, for backward."""
+                stream=None, gu: torch.Tensor | None = None, scores: torch.Tensor | None = None) -> torch.Tensor:
+        """One layer step, bf16 [T, H]; gu: as for expert_rows, for backward; scores:
+        as for route (their gradient is backward's d_scores)."""
         if self.dtype == torch.float16:
             raise TypeError("forward: the combine takes bfloat16 rows, not float16 ones (use route and expert_rows)")
-        r = self.route(logits, stream)
+        r = self.route(logits, stream, scores)
         self.expert_rows(x, w_gu, w_dn, gu=gu, stream=stream)
         return moe_unpermute_combine(self.y2, r.perm_of_assignment, r.topk_w, self.T, self.k, out=self.out,
                                      stream=stream)
@@ -681,7 +686,7 @@ class MoELayer16:
                  w_dn: torch.Tensor, d_scores: torch.Tensor | None = None, stream=None):
         """Gradients from dout [T, H] (bf16 or float32) of the last forward call,
         whose gu and inputs these are: (dlogits, dx, dw_gu, dw_dn).  d_scores: the
-        gradient of the router's scores (a balance loss), as for
+        gradient of the router's scores (a balance loss on forward's `scores`), as for
         moe_route_scored_backward.  Refused as in expert_rows_backward; bf16
         weights only."""
         from . import moe_route_scored_backward, moe_unpermute_combine_backward
