@@ -2,7 +2,8 @@
 //   dy[row(t, j)] = w[t, j] dout[t]   (rounded once to y's type)
 //   dw[t, j] = <dout[t], y[row(t, j)]>   (float32 sums in a fixed order)
 // in one pass: every row of y is read once, every row of dy written once, both past the
-// caches.  Bound by memory: 16384 tokens, top-8, 6144 wide, bf16 (3.4 GB) 677 us, 5.05 TB/s.
+// caches.  Bound by memory: 16384 tokens, top-8, 6144 wide, bf16 (3.4 GB) 675 to 690 us, 5.0
+// TB/s; in float32 (6.8 GB) 1456, 4.7 TB/s, and 4096 tokens 1024 wide 50, 5.8 TB/s.
 #include "nvfp4_internal.h"
 
 namespace nvfp4 {
@@ -120,12 +121,16 @@ static hipError_t cg_start(const CombineGradParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// A wave for two of a token's rows up to 4 KB of bf16 a row, else the workgroup for four:
+// A wave for two of a token's rows up to 2048 wide, else the workgroup for four:
 // top-8 in bf16, us, wave / workgroup
 //   H 512, 2048 tokens 7.9 / 11.2, 16384 tokens 44 / 83;  H 1024, 16384 tokens 99 / 151
 //   H 2048, 1024 tokens 12.4 / 14.5, 4096 tokens 44.7 / 46.0, 16384 tokens 245 / 231
 //   H 6144, 255 tokens 12.2 / 9.8, 2048 tokens 65 / 68, 4096 tokens 193 / 174, 16384 tokens 697 / 692
 // (a workgroup for one row each: 13.0, 85, 176 and 693 there)
+// in float32, where rows have twice the bytes and either side of the limit is within 8 %
+//   H 512, 16384 tokens 108 / 129;  H 1024, 255 tokens 4.7 / 5.2, 16384 tokens 254 / 239
+//   H 2048, 255 tokens 6.3 / 7.6, 4096 tokens 114 / 105, 16384 tokens 497 / 481
+//   H 4096, 255 tokens 12.7 / 15.0, 4096 tokens 259 / 249;  H 6144, 16384 tokens 1485 / 1461
 template <int DT, int YT>
 static hipError_t cg_launch(const CombineGradParams& p, hipStream_t stream) {
   return p.H <= 2048 ? cg_start<DT, YT, 64, 2>(p, stream) : cg_start<DT, YT, 256, 4>(p, stream);

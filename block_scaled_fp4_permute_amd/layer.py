@@ -129,7 +129,10 @@ def quantize_expert_weights(w_gu: torch.Tensor, w_dn: torch.Tensor) -> ExpertWei
 
 
 class MoELayer:
-    """Preallocated NVFP4 MoE layer for T tokens."""
+    """Preallocated NVFP4 MoE layer for T tokens.  Without a Router, routing and the
+    quantisation of x share their launches; with one they have their own (2048
+    tokens, 256 experts, 6144 wide: 33 us, with the default Router 42, with 8
+    groups 44 to 47, of a step of 323)."""
 
     def __init__(self, T: int, H: int, I: int, E: int, k: int, device, swiglu: str = "fused",
                  combine: str = "gather", ffn: str = "one_launch", router: Router | None = None):
