@@ -18,11 +18,11 @@
 // finite or more than 16 or 32 candidates are that close.
 // Bound by latency: one chain of dependent steps a token (sort, then k rounds of
 // exchanges), in one round of waves up to 16384 tokens, where neither memory (1.0 TB/s)
-// nor the vector units (38 % busy; 47 with float64 scores) are full.  A launch finds its code in no instruction cache, and a wave
-// that runs through 12 KB of it once waits some 10 us for its lines: what is rare, or
-// long in float64, is a loop over few instructions.  Top-8 of 256 in 8 groups with a
-// bias, float32: 256 tokens 7 us, 4096 9, 16384 15 to 17 (read at 4.86 TB/s: 3.5),
-// with scores 27.
+// nor the vector units (38 % busy; 47 with float64 scores) are full.  A launch finds
+// its code in no instruction cache, and a wave that runs through 12 KB of it once waits
+// some 10 us for its lines: what is rare, or long in float64, is a loop over few
+// instructions.  Top-8 of 256 in 8 groups with a bias, float32: 256 tokens 7 us, 4096 9,
+// 16384 15 to 17 (read at 4.86 TB/s: 3.5), with scores 26 to 27.
 // An expert is closed to the choice if its logit is -inf or NaN, or its key -inf or NaN;
 // closed ones are taken, by id and with weight 0, only where a token has fewer open ones
 // than it needs.

@@ -3,10 +3,9 @@ a value far smaller than the rounding of either, so float32 keys order groups wr
 where float64 ones do not.  Ids exactly as oracle/router.py has them."""
 import numpy as np
 import pytest
-import torch
 
 import block_scaled_fp4_permute_amd as m
-from tests.gpu_common import DEV, up
+from tests.gpu_common import up
 from tests.test_gpu_router import KIND
 from tests.test_gpu_router_borders import _same
 
